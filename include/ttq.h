@@ -290,6 +290,133 @@ int ttq_qmatmul(const ttq_params* prm, const uint8_t* codes,
                 const void* X, const void* B, const void* A, float* Y,
                 void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- low-rank adapters of many requests ----------------------------------
+ * Beside a shared projection, whose low-rank term B (A X) is one for all rows,
+ * each row of a batch may add a pair of its own, held in a set of n_adapters:
+ *   Y[t] = base[t] + scale[e] B_e (A_e x_t),   e = index[t].
+ * Of prm only d, d_out, T and rank are read: rank is that of every pair
+ * (smaller ones padded with zeros), a multiple of 8 up to 128; d is a multiple
+ * of 8 (TTQ_EUNSUPPORTED otherwise).
+ *   X      [T][d] bf16           A   [n_adapters][rank][d] bf16
+ *   B      [n_adapters][d_out][rank] bf16
+ *   scale  optional [n_adapters] float32 (1 without)
+ *   index  [T] int32 on the device; a row whose index lies outside
+ *          [0, n_adapters) has no pair: Y[t] = base[t]
+ *   base   optional [T][d_out] float32, e.g. what ttq_linear or ttq_qmatmul
+ *          gave (0 without); may be Y itself, but not otherwise overlap it
+ *   Y      [T][d_out] float32
+ *   workspace of at least ttq_adapters_workspace_bytes
+ * Both products accumulate in float32 and A_e x_t enters the second one with
+ * all its 24 bits.  n_adapters = 0 copies base.  X, A and B are 16-byte
+ * aligned, the rest as for ttq_linear; the same error rules. */
+int ttq_adapters_workspace_bytes(const ttq_params* prm, int64_t n_adapters,
+                                 size_t* bytes);
+int ttq_adapters(const ttq_params* prm, int64_t n_adapters, const void* X,
+                 const void* A, const void* B, const float* scale,
+                 const int32_t* index, const float* base, float* Y,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- a mixture-of-experts layer from stored codes ------------------------
+ * The decode step of a layer whose MLP is `experts` gated MLPs, each kept as
+ * ttq_quantize leaves its weights, for a few tokens (T <= 128):
+ *   l_e = router[e] . x_t               scores, summed in float64
+ *   chosen: the top_k largest scores, equal ones by the lower index, NaN last
+ *   w_j = exp(l_j - max) / sum of it over the chosen experts
+ *         (TTQ_MOE_RENORMALIZE) or over all of them (without)
+ *   h   = silu(gate) * up,  gate and up rows of (m + s q) D^{-1/2} times x_t
+ *   Y[t] = sum_j w_j (down rows of expert j times h)
+ *   T, d, ff       tokens, channels of the layer, width of an expert; d and ff
+ *                  multiples of group (and rows of whole 16 bytes of codes)
+ *   experts, top_k up to 256 and 16; top_k <= experts
+ *   bits, group, qformat   of all stored codes, as for ttq_quantize
+ *   X        [T][d] bf16; router [experts][d] bf16
+ *   gu_*     gate rows, then up rows: codes [experts][2 ff][row_bytes(d)],
+ *            scales, mins [experts][2 ff][d/group], dhalf_inv [experts][d]
+ *   dn_*     codes [experts][d][row_bytes(ff)], scales, mins
+ *            [experts][d][ff/group], dhalf_inv [experts][ff]
+ *   Y        [T][d] float32
+ *   ids_out, weights_out   optional [T][top_k] int32 / float32, best first
+ *   workspace of at least ttq_moe_workspace_bytes
+ * The contractions accumulate in float32, with x D^{-1/2} and h D^{-1/2} in
+ * all their 24 bits.  Larger T, experts or top_k are TTQ_EUNSUPPORTED.  X,
+ * router, codes, dhalf_inv and Y are 16-byte aligned, the rest their type's;
+ * the error rules of ttq_linear. */
+#define TTQ_MOE_RENORMALIZE 1u
+typedef struct ttq_moe_params {
+  int64_t T;
+  int64_t d;
+  int64_t ff;
+  int32_t experts;
+  int32_t top_k;
+  int32_t bits;
+  int32_t group;
+  uint32_t flags;
+  uint32_t qformat;
+} ttq_moe_params;
+int ttq_moe_workspace_bytes(const ttq_moe_params* prm, size_t* bytes);
+int ttq_moe(const ttq_moe_params* prm, const void* X, const void* router,
+            const uint8_t* gu_codes, const float* gu_scales,
+            const float* gu_mins, const float* gu_dhalf_inv,
+            const uint8_t* dn_codes, const float* dn_scales,
+            const float* dn_mins, const float* dn_dhalf_inv, float* Y,
+            int32_t* ids_out, float* weights_out, void* workspace,
+            size_t workspace_bytes, void* stream);
+
+/* ---- a cache quantized as it is written ----------------------------------
+ * The quantizer of ttq_quantize applied to rows as they are produced, such as
+ * the K and V rows of a decoder ("Test-time quantization: quantising on the
+ * fly with no calibration dataset", lo0 blog: KV-cache scales derived on the
+ * fly by the same logic).  A cache has n_slots rows of d channels (all heads
+ * of a token, K and V side by side or in two caches), each stored as a weight
+ * row of ttq_quantize is: `bits` wide codes packed in ttq_packed_row_bytes,
+ * and float32 scales and mins per group:
+ *   codes [n_slots][row_bytes], scales, mins [n_slots][d/group].
+ * Formats and the float32 code decision are those of TTQ_QF_*, except that a
+ * scale is the group's range times the float32 nearest to 1/N (1/Z for
+ * TTQ_QF_SYM, 1/448 for TTQ_QF_FP8) instead of the range divided by it (at
+ * most one unit in the last place away).
+ * With dhalf, the D^{1/2} of each channel (e.g. dhalf_out of ttq_quantize for
+ * the prompt's queries), the codes are those of x D^{1/2}; reading with
+ * dhalf_inv = 1 / dhalf undoes it.
+ * Of prm only d, T, bits, group and qformat are read.
+ *
+ * ttq_cache_write quantizes T rows: row t of X goes to cache row slots[t].
+ *   x_type   TTQ_BF16 or TTQ_F32
+ *   X        [T] rows of d values, ldx >= d elements apart (a column range of
+ *            a wider matrix is fine); 16-byte aligned, as is every row
+ *   dhalf    optional [d] float32
+ *   slots    [T] int64 on the device; a row whose slot lies outside
+ *            [0, n_slots) is not written (padding: -1).  The other slots of a
+ *            call must be distinct: of a slot named twice the stored row may
+ *            be a mixture of both.
+ * A group that holds an infinity or a NaN, or whose range is no finite
+ * float32, reads back as NaN; a scale below 2^-126 counts as 0.
+ *
+ * ttq_cache_read gives rows 0 .. lens[i] - 1 of n_seq sequences as out[i][t],
+ * out being [n_seq][T][d] of out_type (TTQ_BF16: rounded once).  Cache rows
+ * are grouped in pages of page_tokens (a power of two up to 4096); row t of
+ * sequence i is cache row pages[i][t / page_tokens] * page_tokens
+ * + t % page_tokens.  pages [n_seq][max_pages] and lens [n_seq] are int32 on
+ * the device.  A length past T or past the pages is cut to them, a negative
+ * one is 0.  Rows behind a sequence's length, and rows whose page lies outside
+ * the cache, are left as they were.
+ *   dhalf_inv  optional [d] float32; out 16-byte aligned
+ * Neither call needs a workspace.  Alignment: X, dhalf, dhalf_inv, codes and
+ * out 16 bytes, the rest their type's.  Error rules as for ttq_linear
+ * (TTQ_EALIGN also for an ldx that breaks the row alignment). */
+#define TTQ_BF16 0
+#define TTQ_F32 1
+int ttq_cache_write(const ttq_params* prm, int64_t n_slots, int32_t x_type,
+                    const void* X, int64_t ldx, const float* dhalf,
+                    const int64_t* slots, uint8_t* codes, float* scales,
+                    float* mins, void* stream);
+int ttq_cache_read(const ttq_params* prm, int64_t n_slots, int64_t n_seq,
+                   int64_t max_pages, int32_t page_tokens, const int32_t* pages,
+                   const int32_t* lens, const uint8_t* codes,
+                   const float* scales, const float* mins,
+                   const float* dhalf_inv, int32_t out_type, void* out,
+                   void* stream);
+
 /* Human-readable text of a status code (static storage). */
 const char* ttq_status_string(int status);
 

@@ -56,6 +56,17 @@ EXPORTS = {
                                                    _c.POINTER(_c.c_size_t)]),
     "ttq_lowrank_pca": (_c.c_int, [_vp, _c.c_int32, _vp, _vp, _vp, _vp, _vp,
                                    _vp, _vp, _c.c_size_t, _vp]),
+    "ttq_adapters_workspace_bytes": (_c.c_int, [_vp, _c.c_int64,
+                                                _c.POINTER(_c.c_size_t)]),
+    "ttq_adapters": (_c.c_int, [_vp, _c.c_int64, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _vp, _vp, _c.c_size_t, _vp]),
+    "ttq_moe_workspace_bytes": (_c.c_int, [_vp, _c.POINTER(_c.c_size_t)]),
+    "ttq_moe": (_c.c_int, [_vp] * 15 + [_c.c_size_t, _vp]),
+    "ttq_cache_write": (_c.c_int, [_vp, _c.c_int64, _c.c_int32, _vp, _c.c_int64,
+                                   _vp, _vp, _vp, _vp, _vp, _vp]),
+    "ttq_cache_read": (_c.c_int, [_vp, _c.c_int64, _c.c_int64, _c.c_int64,
+                                  _c.c_int32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _c.c_int32, _vp, _vp]),
     "ttq_status_string": (_c.c_char_p, [_c.c_int]),
     "ttq_last_hip_error": (_c.c_int, []),
     "ttq_stream_read": (_c.c_int, [_vp, _c.c_int64, _vp, _vp]),
@@ -80,6 +91,20 @@ class ttq_params(ctypes.Structure):
         ("p", ctypes.c_double),
         ("lambda_", ctypes.c_double),
         ("alpha", ctypes.c_double),
+        ("flags", ctypes.c_uint32),
+        ("qformat", ctypes.c_uint32),
+    ]
+
+
+class ttq_moe_params(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64),
+        ("d", ctypes.c_int64),
+        ("ff", ctypes.c_int64),
+        ("experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("bits", ctypes.c_int32),
+        ("group", ctypes.c_int32),
         ("flags", ctypes.c_uint32),
         ("qformat", ctypes.c_uint32),
     ]
@@ -530,6 +555,253 @@ def ttq_qmatmul(codes, scales, mins, dhalf_inv, X, B=None, A=None, *,
     if st != TTQ_OK:
         raise TTQError(st, "ttq_qmatmul")
     return Y
+
+
+# --------------------------------------------- one decode step from codes
+TTQ_BF16 = 0
+TTQ_F32 = 1
+TTQ_MOE_RENORMALIZE = 1
+
+
+def _elem_type(t, name) -> int:
+    import torch
+    dt = getattr(t, "dtype", None)
+    if dt is torch.bfloat16:
+        return TTQ_BF16
+    if dt is torch.float32:
+        return TTQ_F32
+    raise TypeError(f"{name} must be a torch.Tensor of torch.bfloat16 or "
+                    f"torch.float32, got {dt if dt is not None else type(t)}")
+
+
+def _enqueue(where, dev, fn, *args):
+    """Call a library entry point with the tensors' device current."""
+    import torch
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st != TTQ_OK:
+        raise TTQError(st, where)
+
+
+def _step_workspace(dev, stream, need_key, query):
+    """_workspace, but a buffer of its own for a call that is being captured:
+    it then lives in the graph's memory, and no other graph or stream has it."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(int(query()), 256), dtype=torch.uint8, device=dev)
+    return _workspace(dev, stream, need_key, query)
+
+
+def ttq_adapters_workspace_bytes(prm: ttq_params, n_adapters: int) -> int:
+    out = ctypes.c_size_t(0)
+    st = load_library().ttq_adapters_workspace_bytes(
+        ctypes.byref(prm), int(n_adapters), ctypes.byref(out))
+    if st != TTQ_OK:
+        raise TTQError(st, "ttq_adapters_workspace_bytes")
+    return int(out.value)
+
+
+def ttq_adapters(X, A, B, index, *, scale=None, base=None, Y=None,
+                 workspace=None, stream=None):
+    """Y[t] = base[t] + scale[e] B[e] (A[e] x_t) with e = index[t]: low-rank
+    adapters of many requests beside a shared projection (see include/ttq.h).
+
+    X [T, d], A [n, r, d] and B [n, d_out, r] are bfloat16, ``scale`` [n] and
+    ``base`` [T, d_out] float32, ``index`` [T] int32 (outside 0 .. n - 1: no
+    pair).  ``base`` is what ttq_linear, ttq_linear_batched (flattened),
+    ttq_linear_segmented or ttq_qmatmul gave for X; ``Y=base`` adds in place.
+    """
+    import torch
+    T, d = X.shape
+    n, r, _ = A.shape
+    d_out = B.shape[1]
+    dev = X.device
+    if dev.type != "cuda":
+        raise ValueError("X must be a GPU tensor")
+    _check(X, "X", torch.bfloat16, (T, d), dev)
+    _check(A, "A", torch.bfloat16, (n, r, d), dev)
+    _check(B, "B", torch.bfloat16, (n, d_out, r), dev)
+    _check(index, "index", torch.int32, (T,), dev)
+    _check(scale, "scale", torch.float32, (n,), dev)
+    _check(base, "base", torch.float32, (T, d_out), dev)
+    if Y is None:
+        Y = torch.empty((T, d_out), dtype=torch.float32, device=dev)
+    _check(Y, "Y", torch.float32, (T, d_out), dev)
+    prm, key = _params(d, d_out, T, r, 4, 32, 2.0, 0.0, 0.0, 0, "asym")
+    if stream is None:
+        stream = _current_stream(dev)
+    if workspace is None:
+        workspace = _step_workspace(dev, stream, ("adapters", key),
+                                    lambda: ttq_adapters_workspace_bytes(prm, n))
+    _enqueue("ttq_adapters", dev, load_library().ttq_adapters,
+             ctypes.byref(prm), n, _ptr(X), _ptr(A), _ptr(B), _ptr(scale),
+             _ptr(index), _ptr(base), _ptr(Y), _ptr(workspace),
+             workspace.numel(), stream)
+    return Y
+
+
+def make_moe_params(*, T: int, d: int, ff: int, experts: int, top_k: int,
+                    bits: int, group: int, renormalize: bool = True,
+                    qformat="asym") -> ttq_moe_params:
+    return ttq_moe_params(int(T), int(d), int(ff), int(experts), int(top_k),
+                          int(bits), int(group),
+                          TTQ_MOE_RENORMALIZE if renormalize else 0,
+                          qformat_code(qformat))
+
+
+def ttq_moe_workspace_bytes(prm: ttq_moe_params) -> int:
+    out = ctypes.c_size_t(0)
+    st = load_library().ttq_moe_workspace_bytes(ctypes.byref(prm), ctypes.byref(out))
+    if st != TTQ_OK:
+        raise TTQError(st, "ttq_moe_workspace_bytes")
+    return int(out.value)
+
+
+_MOE = {}
+
+
+def _moe_params(T, d, ff, E, k, bits, group, renormalize, qformat):
+    """The parameter block and packed row bytes of one shape, kept (bounded)."""
+    key = (T, d, ff, E, k, bits, group, bool(renormalize), qformat)
+    got = _MOE.get(key)
+    if got is None:
+        if len(_MOE) > 4096:
+            _MOE.clear()
+            _NEED.clear()
+        prm = make_moe_params(T=T, d=d, ff=ff, experts=E, top_k=k, bits=bits,
+                              group=group, renormalize=renormalize,
+                              qformat=qformat)
+        ttq_moe_workspace_bytes(prm)  # raises for what the library refuses
+        got = _MOE[key] = (prm, key, _row_bytes(d, bits, group),
+                           _row_bytes(ff, bits, group))
+    return got
+
+
+def ttq_moe(X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv, dn_codes,
+            dn_scales, dn_mins, dn_dhalf_inv, *, top_k: int, bits: int,
+            group: int, renormalize: bool = True, Y=None, ids_out=None,
+            weights_out=None, workspace=None, stream=None, qformat="asym"):
+    """Y[T, d] = a mixture-of-experts layer for a few tokens X [T, d], its
+    experts' projections being codes stored by ttq_quantize (see
+    include/ttq.h): gate rows followed by up rows in gu_* [E, 2 ff, ...], down
+    rows in dn_* [E, d, ...], dhalf_inv [E, d] and [E, ff]; router [E, d]
+    bfloat16.  ``ids_out`` and ``weights_out`` [T, top_k] receive the chosen
+    experts (int32, best first) and their weights (float32)."""
+    import torch
+    T, d = X.shape
+    E, ff = dn_dhalf_inv.shape
+    dev = X.device
+    if dev.type != "cuda":
+        raise ValueError("X must be a GPU tensor")
+    prm, key, rb, rf = _moe_params(T, d, ff, E, top_k, bits, group,
+                                   renormalize, qformat)
+    _check(X, "X", torch.bfloat16, (T, d), dev)
+    _check(router, "router", torch.bfloat16, (E, d), dev)
+    _check(gu_codes, "gu_codes", torch.uint8, (E, 2 * ff, rb), dev)
+    _check(gu_scales, "gu_scales", torch.float32, (E, 2 * ff, d // group), dev)
+    _check(gu_mins, "gu_mins", torch.float32, (E, 2 * ff, d // group), dev)
+    _check(gu_dhalf_inv, "gu_dhalf_inv", torch.float32, (E, d), dev)
+    _check(dn_codes, "dn_codes", torch.uint8, (E, d, rf), dev)
+    _check(dn_scales, "dn_scales", torch.float32, (E, d, ff // group), dev)
+    _check(dn_mins, "dn_mins", torch.float32, (E, d, ff // group), dev)
+    _check(dn_dhalf_inv, "dn_dhalf_inv", torch.float32, (E, ff), dev)
+    if Y is None:
+        Y = torch.empty((T, d), dtype=torch.float32, device=dev)
+    _check(Y, "Y", torch.float32, (T, d), dev)
+    _check(ids_out, "ids_out", torch.int32, (T, top_k), dev)
+    _check(weights_out, "weights_out", torch.float32, (T, top_k), dev)
+    if stream is None:
+        stream = _current_stream(dev)
+    if workspace is None:
+        workspace = _step_workspace(dev, stream, ("moe", key),
+                                    lambda: ttq_moe_workspace_bytes(prm))
+    _enqueue("ttq_moe", dev, load_library().ttq_moe, ctypes.byref(prm),
+             _ptr(X), _ptr(router), _ptr(gu_codes), _ptr(gu_scales),
+             _ptr(gu_mins), _ptr(gu_dhalf_inv), _ptr(dn_codes),
+             _ptr(dn_scales), _ptr(dn_mins), _ptr(dn_dhalf_inv), _ptr(Y),
+             _ptr(ids_out), _ptr(weights_out), _ptr(workspace),
+             workspace.numel(), stream)
+    return Y
+
+
+def _check_cache(codes, scales, mins, d, bits, group):
+    import torch
+    n_slots, dev = codes.shape[0], codes.device
+    if dev.type != "cuda":
+        raise ValueError("codes must be a GPU tensor")
+    rb = _row_bytes(d, bits, group)
+    G = d // group
+    _check(codes, "codes", torch.uint8, (n_slots, rb), dev)
+    _check(scales, "scales", torch.float32, (n_slots, G), dev)
+    _check(mins, "mins", torch.float32, (n_slots, G), dev)
+    return n_slots, dev
+
+
+def ttq_cache_write(X, slots, codes, scales, mins, *, bits: int, group: int,
+                    dhalf=None, qformat="asym", stream=None):
+    """Quantize the rows of X [T, d] (bfloat16 or float32; rows may lie apart,
+    e.g. the K and V columns of a wider matrix) into the cache rows
+    ``slots`` [T] (int64; a negative one is padding and not written).
+
+    The cache is (codes [n_slots, row_bytes] uint8, scales and mins [n_slots,
+    d / group] float32), updated in place; with ``dhalf`` [d] the codes are
+    those of x D^{1/2} (see include/ttq.h).
+    """
+    import torch
+    T, d = X.shape
+    n_slots, dev = _check_cache(codes, scales, mins, d, bits, group)
+    x_type = _elem_type(X, "X")
+    if X.device != dev:
+        raise ValueError(f"X must be on {dev}, got {X.device}")
+    if d > 1 and X.stride(1) != 1:
+        raise ValueError("X must have contiguous rows")
+    ldx = X.stride(0) if T > 1 else d
+    _check(slots, "slots", torch.int64, (T,), dev)
+    _check(dhalf, "dhalf", torch.float32, (d,), dev)
+    prm, _ = _params(d, 1, T, 0, bits, group, 2.0, 0.0, 0.0, 0, qformat)
+    if stream is None:
+        stream = _current_stream(dev)
+    _enqueue("ttq_cache_write", dev, load_library().ttq_cache_write,
+             ctypes.byref(prm), n_slots, x_type, _ptr(X), ldx, _ptr(dhalf),
+             _ptr(slots), _ptr(codes), _ptr(scales), _ptr(mins), stream)
+
+
+def ttq_cache_read(codes, scales, mins, pages, lens, *, bits: int, group: int,
+                   page_tokens: int, out=None, T=None, d=None, dhalf_inv=None,
+                   dtype=None, qformat="asym", stream=None):
+    """Read sequences back from a cache: out [n_seq, T, d] (bfloat16 or
+    float32), row t of sequence i from page ``pages[i, t // page_tokens]``.
+
+    ``pages`` [n_seq, max_pages] and ``lens`` [n_seq] are int32.  Rows behind a
+    sequence's length are left as they were; without ``out`` a tensor of zeros
+    for ``T`` rows of ``d`` channels is made (default: all pages, the channels
+    of the stored groups; ``dtype`` bfloat16 by default).
+    """
+    import torch
+    n_seq, max_pages = pages.shape
+    if out is None:
+        d = scales.shape[1] * group if d is None else d
+        T = max_pages * page_tokens if T is None else T
+        out = torch.zeros((n_seq, T, d), dtype=dtype or torch.bfloat16,
+                          device=codes.device)
+    _, T, d = out.shape
+    n_slots, dev = _check_cache(codes, scales, mins, d, bits, group)
+    out_type = _elem_type(out, "out")
+    _check(out, "out", out.dtype, (n_seq, T, d), dev)
+    _check(pages, "pages", torch.int32, (n_seq, max_pages), dev)
+    _check(lens, "lens", torch.int32, (n_seq,), dev)
+    _check(dhalf_inv, "dhalf_inv", torch.float32, (d,), dev)
+    prm, _ = _params(d, 1, T, 0, bits, group, 2.0, 0.0, 0.0, 0, qformat)
+    if stream is None:
+        stream = _current_stream(dev)
+    _enqueue("ttq_cache_read", dev, load_library().ttq_cache_read,
+             ctypes.byref(prm), n_slots, n_seq, max_pages, page_tokens,
+             _ptr(pages), _ptr(lens), _ptr(codes), _ptr(scales), _ptr(mins),
+             _ptr(dhalf_inv), out_type, _ptr(out), stream)
+    return out
 
 
 # ------------------------------------------------- low-rank factors by PCA

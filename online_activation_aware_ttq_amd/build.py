@@ -37,6 +37,9 @@ SOURCES = [
     "k_segment.hip",
     "k_pca.hip",
     "k_stream.hip",
+    "k_cache.hip",
+    "k_adapters.hip",
+    "k_moe.hip",
     "ttq_api.cpp",
 ]
 

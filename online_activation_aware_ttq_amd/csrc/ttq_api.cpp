@@ -24,6 +24,8 @@ constexpr int64_t kMaxDout = int64_t(1) << 22;
 constexpr int64_t kMaxT = int64_t(1) << 22;
 constexpr int64_t kMaxR = 4096;
 constexpr int64_t kMaxElems = int64_t(1) << 34;
+constexpr int64_t kMaxSeq = 65535;  // sequences of one cache read (grid y)
+constexpr int64_t kMaxCacheOut = int64_t(1) << 37;  // elements it writes
 // two-phase path: workspace for the dequantized weights of several requests
 constexpr int64_t kMaxWhatBytes = int64_t(4) << 30;
 constexpr int kFusedMaxT = 128;
@@ -245,7 +247,8 @@ const char* kKernelNames[K_NUM_KINDS] = {
     "quant_what", "gemm_mfma", "lowrank_z", "gemv_t1", "splitk_reduce",
     "qgemv", "dequant", "qfused", "lowrank_zsum", "gemm_quant", "seg_copy",
     "pca_skinny", "pca_psum", "pca_chol", "pca_trsm", "pca_residual",
-    "pca_complete", "stream_read"};
+    "pca_complete", "stream_read", "cache_write", "cache_read",
+    "adapters_shrink", "adapters_expand", "moe_route", "moe_up", "moe_down", "moe_sum"};
 
 hipEvent_t take_event() {
   if (!g_timing.pool.empty()) {
@@ -1155,6 +1158,257 @@ int pca_impl(const ttq_params* prm, int32_t iters, const void* W,
   return run(K_LR_RESIDUAL, s, [&](const Launch& L) { return launch_lr_residual(ra, (int)n, L); });
 }
 
+// ------------------------------------------- adapters of many requests
+// (k_adapters.hip).  Reads d, d_out, T and rank (of each pair); bits, group,
+// p, lambda, alpha, the path flags and qformat are not read.
+constexpr int64_t kMaxAdapterRank = 128;
+constexpr int64_t kMaxAdapters = int64_t(1) << 20;
+
+int validate_adapters(const ttq_params* prm, int64_t n) {
+  if (!prm) return TTQ_ENULL;
+  if (n < 0 || n > kMaxAdapters) return TTQ_EINVAL;
+  if (prm->d < 1 || prm->d > kMaxD) return TTQ_EINVAL;
+  if (prm->d_out < 0 || prm->d_out > kMaxDout) return TTQ_EINVAL;
+  if (prm->T < 0 || prm->T > kMaxT) return TTQ_EINVAL;
+  if (prm->rank < 1) return TTQ_EINVAL;
+  if (prm->T * prm->d > kMaxElems || prm->T * prm->d_out > kMaxElems) return TTQ_EINVAL;
+  if (prm->rank % 8 != 0 || prm->rank > kMaxAdapterRank) return TTQ_EUNSUPPORTED;
+  if (prm->d % 8 != 0) return TTQ_EUNSUPPORTED;  // 16-byte loads of its rows
+  return TTQ_OK;
+}
+
+struct AdaptersPlan {
+  int slots = 1;      // distinct pairs of a 16-token tile with workgroups of their own
+  int nks = 1;        // channel ranges of the first product
+  int64_t kc = 0;
+  size_t total = 0;
+};
+
+AdaptersPlan make_adapters_plan(const ttq_params* prm) {
+  AdaptersPlan P;
+  const int64_t tiles = std::max<int64_t>(1, (prm->T + 15) / 16);
+  P.slots = (int)std::max<int64_t>(1, std::min({int64_t(16), prm->T, 1024 / tiles}));
+  // ranges of at least 512 channels, about two workgroups per compute unit
+  int64_t nks = std::min((prm->d + 511) / 512, std::max<int64_t>(1, 512 / (tiles * P.slots)));
+  nks = std::min<int64_t>(nks, 8);
+  P.kc = (prm->d + nks * 128 - 1) / (nks * 128) * 128;
+  P.nks = (int)((prm->d + P.kc - 1) / P.kc);
+  P.total = sizeof(float) * P.nks * prm->T * prm->rank;
+  return P;
+}
+
+int adapters_impl(const ttq_params* prm, int64_t n, const void* X,
+                  const void* A, const void* B, const float* scale,
+                  const int32_t* index, const float* base, float* Y,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  int st = validate_adapters(prm, n);
+  if (st != TTQ_OK) return st;
+  const int64_t T = prm->T, dout = prm->d_out;
+  if (T == 0 || dout == 0) return TTQ_OK;
+  if (!Y || !index) return TTQ_ENULL;
+  if (n > 0 && (!X || !A || !B)) return TTQ_ENULL;
+  if (misaligned(X, 16) || misaligned(A, 16) || misaligned(B, 16) ||
+      misaligned(scale, 4) || misaligned(index, 4) || misaligned(base, 4) ||
+      misaligned(Y, 4) || misaligned(workspace, 256))
+    return TTQ_EALIGN;
+  const AdaptersPlan P = make_adapters_plan(prm);
+  if (!workspace) return TTQ_ENULL;
+  if (workspace_bytes < P.total) return TTQ_EWORKSPACE;
+  if (inject_hip_error()) return TTQ_EHIP;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  AdaptersArgs a{};
+  a.X = static_cast<const bf16_t*>(X);
+  a.A = static_cast<const bf16_t*>(A);
+  a.B = static_cast<const bf16_t*>(B);
+  a.scale = scale; a.index = index; a.base = base; a.Y = Y;
+  a.S = static_cast<float*>(workspace);
+  a.T = T; a.n = n; a.d = prm->d; a.d_out = dout; a.rank = prm->rank;
+  a.kc = P.kc; a.nks = P.nks;
+  a.vec = dout % 4 == 0 && !misaligned(Y, 16) && !misaligned(base, 16);
+  if (n > 0) {
+    st = run(K_AD_SHRINK, s, [&](const Launch& L) { return launch_ad_shrink(a, P.slots, L); });
+    if (st != TTQ_OK) return st;
+  }
+  return run(K_AD_EXPAND, s, [&](const Launch& L) { return launch_ad_expand(a, P.slots, L); });
+}
+
+// ------------------------------------------- mixture of experts
+// (k_moe.hip)
+struct MoePlan {
+  int64_t gu_rb = 0, dn_rb = 0;
+  size_t off_ids = 0, off_w = 0, off_h = 0, off_yp = 0, total = 0;
+};
+
+int validate_moe(const ttq_moe_params* prm, MoePlan* P) {
+  if (!prm) return TTQ_ENULL;
+  if (prm->d < 1 || prm->d > kMaxD || prm->ff < 1 || prm->ff > kMaxD) return TTQ_EINVAL;
+  if (prm->T < 0 || prm->T > kMaxT || prm->experts < 1 || prm->top_k < 1) return TTQ_EINVAL;
+  if (prm->top_k > prm->experts) return TTQ_EINVAL;
+  if (prm->bits < 1 || prm->bits > 8 || prm->qformat > TTQ_QF_FP8) return TTQ_EINVAL;
+  if (prm->qformat == TTQ_QF_SYM && prm->bits < 2) return TTQ_EINVAL;
+  if (prm->qformat == TTQ_QF_FP8 && prm->bits != 8) return TTQ_EINVAL;
+  if (prm->group <= 0 || prm->d % prm->group != 0 || prm->ff % prm->group != 0)
+    return TTQ_EINVAL;
+  if (prm->flags & ~TTQ_MOE_RENORMALIZE) return TTQ_EINVAL;
+  if (prm->d * prm->ff > kMaxElems) return TTQ_EINVAL;
+  if (prm->group != 32 && prm->group != 64 && prm->group != 128 && prm->group != 256)
+    return TTQ_EUNSUPPORTED;
+  if (prm->T > kMoeMaxT || prm->experts > kMoeMaxE || prm->top_k > kMoeMaxK)
+    return TTQ_EUNSUPPORTED;
+  const int cb = container_bits(prm->bits);
+  if (prm->d * cb % 128 != 0 || prm->ff * cb % 128 != 0) return TTQ_EUNSUPPORTED;
+  P->gu_rb = prm->d * cb / 8;
+  P->dn_rb = prm->ff * cb / 8;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  const int64_t pairs = prm->T * prm->top_k;
+  P->off_ids = take(sizeof(int32_t) * pairs);
+  P->off_w = take(sizeof(float) * pairs);
+  P->off_h = take(sizeof(uint16_t) * pairs * 3 * prm->ff);
+  P->off_yp = take(sizeof(float) * pairs * prm->d);
+  P->total = off;
+  return TTQ_OK;
+}
+
+int moe_impl(const ttq_moe_params* prm, const void* X, const void* router,
+             const uint8_t* gu_codes, const float* gu_scales,
+             const float* gu_mins, const float* gu_dhalf_inv,
+             const uint8_t* dn_codes, const float* dn_scales,
+             const float* dn_mins, const float* dn_dhalf_inv, float* Y,
+             int32_t* ids_out, float* weights_out, void* workspace,
+             size_t workspace_bytes, void* stream) {
+  MoePlan P;
+  int st = validate_moe(prm, &P);
+  if (st != TTQ_OK) return st;
+  if (prm->T == 0) return TTQ_OK;
+  if (!X || !router || !Y || !gu_codes || !gu_scales || !gu_mins || !gu_dhalf_inv ||
+      !dn_codes || !dn_scales || !dn_mins || !dn_dhalf_inv || !workspace)
+    return TTQ_ENULL;
+  if (misaligned(X, 16) || misaligned(router, 16) || misaligned(gu_codes, 16) ||
+      misaligned(dn_codes, 16) || misaligned(gu_dhalf_inv, 16) ||
+      misaligned(dn_dhalf_inv, 16) || misaligned(gu_scales, 4) ||
+      misaligned(gu_mins, 4) || misaligned(dn_scales, 4) || misaligned(dn_mins, 4) ||
+      misaligned(Y, 16) || misaligned(ids_out, 4) || misaligned(weights_out, 4) ||
+      misaligned(workspace, 256))
+    return TTQ_EALIGN;
+  if (workspace_bytes < P.total) return TTQ_EWORKSPACE;
+  if (inject_hip_error()) return TTQ_EHIP;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  MoeArgs a{};
+  a.X = static_cast<const bf16_t*>(X);
+  a.router = static_cast<const bf16_t*>(router);
+  a.T = prm->T; a.d = prm->d; a.ff = prm->ff;
+  a.E = prm->experts; a.k = prm->top_k;
+  a.renorm = (prm->flags & TTQ_MOE_RENORMALIZE) != 0;
+  a.ids = ids_out ? ids_out : reinterpret_cast<int32_t*>(ws + P.off_ids);
+  a.w = weights_out ? weights_out : reinterpret_cast<float*>(ws + P.off_w);
+  a.gu = gu_codes; a.gu_rb = P.gu_rb; a.gu_s = gu_scales; a.gu_m = gu_mins;
+  a.gu_dhi = gu_dhalf_inv;
+  a.dn = dn_codes; a.dn_rb = P.dn_rb; a.dn_s = dn_scales; a.dn_m = dn_mins;
+  a.dn_dhi = dn_dhalf_inv;
+  a.gshift = __builtin_ctz((unsigned)prm->group);
+  a.H = reinterpret_cast<bf16_t*>(ws + P.off_h);
+  a.Yp = reinterpret_cast<float*>(ws + P.off_yp);
+  a.Y = Y;
+  a.qf = (int)prm->qformat;
+  const int cb = container_bits(prm->bits);
+  st = run(K_MOE_ROUTE, s, [&](const Launch& L) { return launch_moe_route(a, L); });
+  if (st != TTQ_OK) return st;
+  st = run(K_MOE_UP, s, [&](const Launch& L) { return launch_moe_up(a, prm->group, cb, L); });
+  if (st != TTQ_OK) return st;
+  st = run(K_MOE_DOWN, s, [&](const Launch& L) { return launch_moe_down(a, prm->group, cb, L); });
+  if (st != TTQ_OK) return st;
+  return run(K_MOE_SUM, s, [&](const Launch& L) { return launch_moe_sum(a, L); });
+}
+
+// ------------------------------------------- cache of quantized rows
+// (k_cache.hip).  d: channels of a row; T: rows to write, or rows of room per
+// sequence to read into; d_out, rank, p, lambda, alpha and the path flags are
+// not read.
+int validate_cache(const ttq_params* prm, int64_t n_slots, ttq_params* q,
+                   int64_t* rb) {
+  if (!prm) return TTQ_ENULL;
+  *q = quantize_view(prm);
+  q->d_out = 1;
+  q->p = 2.0;
+  q->lambda = q->alpha = 0.0;
+  const int st = validate_packed(prm, *q, rb);
+  if (st != TTQ_OK) return st;
+  if (n_slots < 0 || n_slots > kMaxElems) return TTQ_EINVAL;
+  return TTQ_OK;
+}
+
+int cache_write_impl(const ttq_params* prm, int64_t n_slots, int32_t x_type,
+                     const void* X, int64_t ldx, const float* dhalf,
+                     const int64_t* slots, uint8_t* codes, float* scales,
+                     float* mins, void* stream) {
+  ttq_params q;
+  int64_t rb = 0;
+  const int st = validate_cache(prm, n_slots, &q, &rb);
+  if (st != TTQ_OK) return st;
+  if (x_type != TTQ_BF16 && x_type != TTQ_F32) return TTQ_EINVAL;
+  if (q.T > 0 && (ldx < q.d || ldx > kMaxElems)) return TTQ_EINVAL;
+  if (q.T == 0 || n_slots == 0) return TTQ_OK;
+  if (!X || !slots || !codes || !scales || !mins) return TTQ_ENULL;
+  if (misaligned(X, 16) || misaligned(dhalf, 16) || misaligned(slots, 8) ||
+      misaligned(codes, 16) || misaligned(scales, 4) || misaligned(mins, 4) ||
+      ldx % (x_type == TTQ_F32 ? 4 : 8) != 0)
+    return TTQ_EALIGN;
+  if (inject_hip_error()) return TTQ_EHIP;
+  CacheWriteArgs a{};
+  a.X = X; a.ldx = ldx; a.x_f32 = x_type == TTQ_F32; a.dh = dhalf;
+  a.slots = slots; a.codes = codes; a.s = scales; a.m = mins;
+  a.T = q.T; a.C = q.d; a.n_slots = n_slots; a.row_bytes = rb;
+  a.Nf = (float)((1 << q.bits) - 1);
+  a.rN = 1.0f / (q.qformat == TTQ_QF_FP8 ? 448.0f
+                 : q.qformat == TTQ_QF_SYM ? (float)((1 << (q.bits - 1)) - 1) : a.Nf);
+  a.cb = container_bits(q.bits);
+  a.qf = (int)q.qformat;
+  return run(K_CACHE_WRITE, static_cast<hipStream_t>(stream),
+             [&](const Launch& L) { return launch_cache_write(a, q.group, L); });
+}
+
+int cache_read_impl(const ttq_params* prm, int64_t n_slots, int64_t n_seq,
+                    int64_t max_pages, int32_t page_tokens,
+                    const int32_t* pages, const int32_t* lens,
+                    const uint8_t* codes, const float* scales,
+                    const float* mins, const float* dhalf_inv,
+                    int32_t out_type, void* out, void* stream) {
+  ttq_params q;
+  int64_t rb = 0;
+  const int st = validate_cache(prm, n_slots, &q, &rb);
+  if (st != TTQ_OK) return st;
+  if (n_seq < 0 || n_seq > kMaxSeq) return TTQ_EINVAL;
+  if (max_pages < 0 || max_pages > kMaxT) return TTQ_EINVAL;
+  if (page_tokens < 1) return TTQ_EINVAL;
+  if (out_type != TTQ_BF16 && out_type != TTQ_F32) return TTQ_EINVAL;
+  if (page_tokens > 4096 || (page_tokens & (page_tokens - 1)) != 0)
+    return TTQ_EUNSUPPORTED;
+  if (n_seq * q.T > 0 && n_seq * q.T > kMaxCacheOut / q.d) return TTQ_EINVAL;
+  if (q.T == 0 || n_seq == 0 || max_pages == 0 || n_slots == 0) return TTQ_OK;
+  if (!pages || !lens || !codes || !scales || !mins || !out) return TTQ_ENULL;
+  if (misaligned(pages, 4) || misaligned(lens, 4) || misaligned(codes, 16) ||
+      misaligned(scales, 4) || misaligned(mins, 4) || misaligned(dhalf_inv, 16) ||
+      misaligned(out, 16))
+    return TTQ_EALIGN;
+  if (inject_hip_error()) return TTQ_EHIP;
+  CacheReadArgs a{};
+  a.codes = codes; a.s = scales; a.m = mins; a.dhi = dhalf_inv;
+  a.pages = pages; a.lens = lens; a.out = out; a.out_f32 = out_type == TTQ_F32;
+  a.n_seq = n_seq; a.max_pages = max_pages; a.T = q.T; a.C = q.d;
+  a.n_slots = n_slots; a.row_bytes = rb;
+  a.pshift = __builtin_ctz((unsigned)page_tokens);
+  a.gshift = __builtin_ctz((unsigned)q.group);
+  a.qf = (int)q.qformat;
+  return run(K_CACHE_READ, static_cast<hipStream_t>(stream),
+             [&](const Launch& L) { return launch_cache_read(a, container_bits(q.bits), L); });
+}
+
 // ------------------------------------------- allocation-free entry point
 // Scratch for callers that cannot allocate: one array per GPU, held until the
 // process ends.  Host code never uses the array's name as an address (on the
@@ -1319,6 +1573,63 @@ int ttq_lowrank_pca(const ttq_params* prm, int32_t iters, const void* W,
                     size_t workspace_bytes, void* stream) {
   return pca_impl(prm, iters, W, X, Omega, B_out, A_out, Wres_out, workspace,
                   workspace_bytes, stream);
+}
+
+int ttq_adapters_workspace_bytes(const ttq_params* prm, int64_t n_adapters,
+                                 size_t* bytes) {
+  if (!bytes) return TTQ_ENULL;
+  const int st = validate_adapters(prm, n_adapters);
+  if (st != TTQ_OK) return st;
+  *bytes = make_adapters_plan(prm).total;
+  return TTQ_OK;
+}
+
+int ttq_adapters(const ttq_params* prm, int64_t n_adapters, const void* X,
+                 const void* A, const void* B, const float* scale,
+                 const int32_t* index, const float* base, float* Y,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  return adapters_impl(prm, n_adapters, X, A, B, scale, index, base, Y,
+                       workspace, workspace_bytes, stream);
+}
+
+int ttq_moe_workspace_bytes(const ttq_moe_params* prm, size_t* bytes) {
+  if (!bytes) return TTQ_ENULL;
+  MoePlan P;
+  const int st = validate_moe(prm, &P);
+  if (st != TTQ_OK) return st;
+  *bytes = P.total;
+  return TTQ_OK;
+}
+
+int ttq_moe(const ttq_moe_params* prm, const void* X, const void* router,
+            const uint8_t* gu_codes, const float* gu_scales,
+            const float* gu_mins, const float* gu_dhalf_inv,
+            const uint8_t* dn_codes, const float* dn_scales,
+            const float* dn_mins, const float* dn_dhalf_inv, float* Y,
+            int32_t* ids_out, float* weights_out, void* workspace,
+            size_t workspace_bytes, void* stream) {
+  return moe_impl(prm, X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv,
+                  dn_codes, dn_scales, dn_mins, dn_dhalf_inv, Y, ids_out,
+                  weights_out, workspace, workspace_bytes, stream);
+}
+
+int ttq_cache_write(const ttq_params* prm, int64_t n_slots, int32_t x_type,
+                    const void* X, int64_t ldx, const float* dhalf,
+                    const int64_t* slots, uint8_t* codes, float* scales,
+                    float* mins, void* stream) {
+  return cache_write_impl(prm, n_slots, x_type, X, ldx, dhalf, slots, codes,
+                          scales, mins, stream);
+}
+
+int ttq_cache_read(const ttq_params* prm, int64_t n_slots, int64_t n_seq,
+                   int64_t max_pages, int32_t page_tokens, const int32_t* pages,
+                   const int32_t* lens, const uint8_t* codes,
+                   const float* scales, const float* mins,
+                   const float* dhalf_inv, int32_t out_type, void* out,
+                   void* stream) {
+  return cache_read_impl(prm, n_slots, n_seq, max_pages, page_tokens, pages,
+                         lens, codes, scales, mins, dhalf_inv, out_type, out,
+                         stream);
 }
 
 const char* ttq_status_string(int status) {

@@ -40,6 +40,14 @@ enum KernelKind {
   K_LR_RESIDUAL,       // PCA: W - B A in bf16
   K_PCA_COMPLETE,      // PCA: completion of a rank-deficient basis
   K_STREAM_READ,       // plain read of device memory (measurement ceiling)
+  K_CACHE_WRITE,       // rows quantized into a cache
+  K_CACHE_READ,        // rows of a cache read back
+  K_AD_SHRINK,         // adapters: A_e x per row
+  K_AD_EXPAND,         // adapters: base + c_e B_e (A_e x)
+  K_MOE_ROUTE,         // experts: scores, the chosen ones and their weights
+  K_MOE_UP,            // experts: gate and up products, silu(g) u
+  K_MOE_DOWN,          // experts: down products
+  K_MOE_SUM,           // experts: weighted sum of a row's experts
   K_NUM_KINDS
 };
 
@@ -61,6 +69,29 @@ __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ unsigned f2bf(float f) {
   return (unsigned)__builtin_bit_cast(unsigned short, (__bf16)f);
+}
+
+// Eight float32 values as three bf16 planes whose sum is each value exactly
+// (8 significant bits a plane, cut off rather than rounded; below 2^-109 the
+// last bits are lost to bf16's exponent range).  An infinity or NaN becomes
+// NaN, unless INF keeps infinities in the first plane.
+template <bool INF = false>
+__device__ __forceinline__ void split24(const float (&v)[8], u32x4 (&pl)[3]) {
+  unsigned h[8], m[8], lo[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    h[i] = __float_as_uint(v[i]) & 0xffff0000u;
+    float r = v[i] - __uint_as_float(h[i]);
+    if (INF) r = v[i] == __uint_as_float(h[i]) ? 0.f : r;
+    m[i] = __float_as_uint(r) & 0xffff0000u;
+    lo[i] = __float_as_uint(r - __uint_as_float(m[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    pl[0][i] = __builtin_amdgcn_perm(h[2 * i + 1], h[2 * i], 0x07060302u);
+    pl[1][i] = __builtin_amdgcn_perm(m[2 * i + 1], m[2 * i], 0x07060302u);
+    pl[2][i] = __builtin_amdgcn_perm(lo[2 * i + 1], lo[2 * i], 0x07060302u);
+  }
 }
 
 // Raw buffer loads: a resource descriptor bounds the addressable range, and a
@@ -652,6 +683,85 @@ int lowrank_z_splits(int64_t M, int64_t d, int rp, int slice);
 inline size_t lowrank_z_part_bytes(int64_t M, int64_t d, int rp, int slice) {
   return (size_t)lowrank_z_splits(M, d, rp, slice) * M * rp * sizeof(float);
 }
+
+// ---- low-rank adapters of many requests (k_adapters.hip)
+struct AdaptersArgs {
+  const bf16_t* X;        // [T][d]
+  const bf16_t* A;        // [n][rank][d]
+  const bf16_t* B;        // [n][d_out][rank]
+  const float* scale;     // optional [n]
+  const int32_t* index;   // [T]; outside [0, n): no pair
+  const float* base;      // optional [T][d_out], may be Y
+  float* Y;               // [T][d_out]
+  float* S;               // [nks][T][rank] partial sums of A_e x
+  int64_t T, n, d, d_out, rank;
+  int64_t kc;             // channels per range, a multiple of 32
+  int nks;                // ranges
+  int vec;                // 16-byte accesses to base and Y
+};
+// slots: distinct pairs of a tile that get workgroups of their own
+hipError_t launch_ad_shrink(const AdaptersArgs& a, int slots, const Launch& L);
+hipError_t launch_ad_expand(const AdaptersArgs& a, int slots, const Launch& L);
+
+// ---- mixture of experts from stored codes (k_moe.hip)
+struct MoeArgs {
+  const bf16_t* X;        // [T][d]
+  const bf16_t* router;   // [E][d]
+  int64_t T, d, ff;
+  int E, k, renorm;
+  int32_t* ids;           // [T][k] chosen experts, best first
+  float* w;               // [T][k] their weights
+  // stored codes of the experts: gate rows then up rows [E][2 ff], and down
+  // rows [E][d]
+  const uint8_t* gu; int64_t gu_rb;
+  const float* gu_s; const float* gu_m; const float* gu_dhi;
+  const uint8_t* dn; int64_t dn_rb;
+  const float* dn_s; const float* dn_m; const float* dn_dhi;
+  int gshift;             // log2 of the group
+  bf16_t* H;              // [T k][3][ff] planes of silu(g) u D^{-1/2}
+  float* Yp;              // [T k][d] weighted expert outputs
+  float* Y;               // [T][d]
+  int qf;
+};
+hipError_t launch_moe_route(const MoeArgs& a, const Launch& L);
+hipError_t launch_moe_up(const MoeArgs& a, int group, int cb, const Launch& L);
+hipError_t launch_moe_down(const MoeArgs& a, int group, int cb, const Launch& L);
+hipError_t launch_moe_sum(const MoeArgs& a, const Launch& L);
+constexpr int kMoeMaxT = 128, kMoeMaxE = 256, kMoeMaxK = 16;
+
+// ---- a cache quantized as it is written (k_cache.hip)
+struct CacheWriteArgs {
+  const void* X;          // [T][ldx], bf16 or float32
+  int64_t ldx;
+  int x_f32;
+  const float* dh;        // optional [C] D^{1/2}
+  const int64_t* slots;   // [T] cache rows; outside [0, n_slots): not written
+  uint8_t* codes;         // [n_slots][row_bytes]
+  float* s;               // [n_slots][C / group]
+  float* m;
+  int64_t T, C, n_slots, row_bytes;
+  float Nf;               // 2^bits - 1
+  float rN;               // 1 / N (1 / Z for QF_SYM, 1 / 448 for QF_FP8)
+  int cb;                 // container bits
+  int qf;                 // quantizer format (QFmt)
+};
+hipError_t launch_cache_write(const CacheWriteArgs& a, int group, const Launch& L);
+
+struct CacheReadArgs {
+  const uint8_t* codes;
+  const float* s;
+  const float* m;
+  const float* dhi;       // optional [C] D^{-1/2}
+  const int32_t* pages;   // [n_seq][max_pages]
+  const int32_t* lens;    // [n_seq]
+  void* out;              // [n_seq][T][C], bf16 or float32
+  int out_f32;
+  int64_t n_seq, max_pages, T, C, n_slots, row_bytes;
+  int pshift;             // log2 of the rows per page
+  int gshift;             // log2 of the group
+  int qf;                 // QF_FP8: E4M3 codes; any other format: integer codes
+};
+hipError_t launch_cache_read(const CacheReadArgs& a, int cb, const Launch& L);
 
 // Plain streaming read (measurement ceiling of the one-token projection):
 // one workgroup per kStreamReadBlockBytes, one XOR per workgroup to sink.

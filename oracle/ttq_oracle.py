@@ -79,6 +79,7 @@ __all__ = [
     "encode_intzp_fp32",
     "encode_fp8_fp32",
     "quantize_format",
+    "cache_rows",
     "reconstruct_format",
     "format_offsets",
     "format_levels",
@@ -583,6 +584,45 @@ def quantize_format(W32, dh32, bits: int, group: int, fmt: str) -> dict:
         v, s = encode_fp8_fp32(W32, dh32, group)
         return dict(codes=e4m3_encode(v), s=s)
     raise ValueError(f"unknown format {fmt!r}")
+
+
+def cache_rows(X32, dh32, bits: int, group: int, fmt: str) -> dict:
+    """What a quantized cache stores of float32 rows X: the quantizers above on
+    u = fl(x * dh32), with s = fl(range * fl(1 / n)) (n = N, Z or 448) in place
+    of fl(range / n), and s = 0 where that is below 2^-126.  Returns codes
+    (uint8), s and off (float32 [rows, G]) and the float64 values off + s code
+    (E4M3 codes: s times the value) the stored terms stand for.  Finite rows
+    whose ranges do not overflow."""
+    f = np.float32
+    u, rows, d = _grouped_u32(X32, dh32, group)
+    N, Z = f(2 ** bits - 1), f(2 ** (bits - 1) - 1)
+    mn, mx = u.min(axis=2), u.max(axis=2)
+    lo, hi = np.minimum(mn, f(0)), np.maximum(mx, f(0))
+    span, n = {"asym": (mx - mn, N), "intzp": (hi - lo, N), "sym": (np.maximum(-mn, mx), Z),
+               "fp8": (np.maximum(-mn, mx), f(E4M3_MAX))}[fmt]
+    s = span * (f(1) / n)
+    s = np.where(s < f(2.0 ** -126), f(0), s)
+    inv = _inv32(s)[:, :, None]
+    if fmt == "asym":
+        q = np.clip(np.rint((u - mn[:, :, None]) * inv), f(0), N)
+        off = mn
+    elif fmt == "sym":
+        q = np.clip(np.rint(u * inv), -Z, Z) + Z
+        off = -(Z * s)
+    elif fmt == "intzp":
+        z = np.rint(lo * inv[:, :, 0])
+        q = np.clip(np.rint(u * inv) - z[:, :, None], f(0), N)
+        off = z * s
+    else:
+        v = e4m3_round(np.clip(u * inv, -f(E4M3_MAX), f(E4M3_MAX)).astype(np.float64))
+        off = np.zeros_like(s)
+    s64 = s.astype(np.float64)[:, :, None]
+    if fmt == "fp8":
+        codes, values = e4m3_encode(v.reshape(rows, d)), s64 * v
+    else:
+        codes = q.astype(np.uint8).reshape(rows, d)
+        values = off.astype(np.float64)[:, :, None] + s64 * q.astype(np.float64)
+    return dict(codes=codes, s=s, off=off, values=values.reshape(rows, d))
 
 
 def reconstruct_format(codes, s, bits: int, group: int, fmt: str, m=None,
