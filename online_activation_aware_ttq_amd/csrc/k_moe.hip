@@ -10,15 +10,30 @@
 // where a product with stored codes is, per group g of a row,
 //   s_g sum_{i in g} q_i x'_i + m_g sum_{i in g} x'_i,   x' = x D^{-1/2}.
 //
-// The codes are exact in bf16 and x' enters as three bf16 planes that sum to
-// it (split24), so the products are as exact as float32 ones, on the matrix
-// cores; the group sums of x' come from the same planes against ones.
+// The codes are exact in bf16, and x' is the sum of three bf16 planes
+// (split24), so float32 accumulation on the matrix cores is as exact as
+// float32 products.  The planes are COLUMNS of the products: an expert that n
+// tokens chose has 3 n of them, 16 to a matrix instruction, and a token's three
+// results are added at the end.  One token then costs one instruction per 32
+// channels and 16 rows, not three, and 5 tokens no more than one.
+#include <algorithm>
+
 #include "codes.h"
 #include "ttq_internal.h"
 
 namespace ttq {
 
 namespace {
+
+// The order in which the expansion of 8 codes leaves their channels: that of
+// the bytes which hold them (1: 4-bit containers, even codes first; 2: 2-bit
+// containers, channel i beside i + 4; 0: as they are).
+__host__ __device__ constexpr int order_of(int cb, bool f8) {
+  return f8 ? 0 : cb == 4 ? 1 : cb == 2 ? 2 : 0;
+}
+__host__ __device__ constexpr int code_order(int order, int i) {
+  return order == 1 ? (i < 4 ? 2 * i : 2 * (i - 4) + 1) : order == 2 ? i / 2 + 4 * (i % 2) : i;
+}
 
 // ------------------------------------------------------------- routing
 // does expert a (score la) come before expert b?
@@ -28,29 +43,82 @@ __device__ __forceinline__ bool before(double la, int a, double lb, int b) {
   return la > lb || (la == lb && a < b);
 }
 
-// One workgroup per token: 16 waves take the experts in turn, then every
-// expert's rank is counted against all others.
+// one wave's part of a score: channels c0 + 8 l + step i, below d
+__device__ __forceinline__ double score_part(const bf16_t* x, const bf16_t* r, int64_t c0,
+                                             int64_t step, int64_t d) {
+  double s0 = 0.0, s1 = 0.0;
+  // four steps' loads at a time (past the end: the same channels, not added)
+  for (int64_t c = c0; c < d; c += 4 * step) {
+    u32x4 xv[4], rv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t ci = c + i * step < d ? c + i * step : c;
+      xv[i] = *(const u32x4*)(x + ci);
+      rv[i] = *(const u32x4*)(r + ci);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c + i * step >= d) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s0 += (double)(bf16lo(xv[i][j]) * bf16lo(rv[i][j]));
+        s1 += (double)(bf16hi(xv[i][j]) * bf16hi(rv[i][j]));
+      }
+    }
+  }
+  return s0 + s1;
+}
+__device__ __forceinline__ double wave_sum(double s) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+  return s;
+}
+
+// scores of many experts: a wave per (token, expert)
+__global__ __launch_bounds__(256) void k_moe_score(MoeArgs a) {
+  const int l = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t t = blockIdx.y;
+  if (e >= a.E) return;
+  const double s = wave_sum(score_part(a.X + t * a.d, a.router + (int64_t)e * a.d, l * 8, 512, a.d));
+  if (l == 0) a.score[t * a.E + e] = s;
+}
+
+// Where piece (of 8 channels) c / 8 of a row of planes lies, and in which
+// order its channels: a lane of the products holds a contiguous quarter of a
+// group's codes, 8 for each matrix instruction, in the order their expansion
+// leaves them in (code_order).  Rows are [group][plane][GS].
+__host__ __device__ constexpr int64_t plane_piece(int64_t c, int gs) {
+  const int64_t g = c / gs, i = c % gs, q = i / (gs / 4), k = i % (gs / 4) / 8;
+  return g * 3 * gs + k * 32 + q * 8;
+}
+
+// One workgroup per token: the scores (its own, when few), every expert's rank
+// by counting those before it, the weights, and x' of the chosen ones as
+// planes.
+template <int ORDER>
 __global__ __launch_bounds__(1024) void k_moe_route(MoeArgs a) {
   __shared__ double score[kMoeMaxE];
+  __shared__ double part[16];
   __shared__ int rank[kMoeMaxE];
   __shared__ int chosen[kMoeMaxK];
   const int tid = threadIdx.x, l = tid & 63, w = tid >> 6;
   const int64_t t = blockIdx.x;
   const bf16_t* x = a.X + t * a.d;
-  for (int e = w; e < a.E; e += 16) {
-    const bf16_t* r = a.router + (int64_t)e * a.d;
-    double s = 0.0;
-    for (int64_t c = l * 8; c < a.d; c += 512) {
-      const u32x4 xv = *(const u32x4*)(x + c), rv = *(const u32x4*)(r + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s += (double)(bf16lo(xv[i]) * bf16lo(rv[i]));
-        s += (double)(bf16hi(xv[i]) * bf16hi(rv[i]));
-      }
+  if (a.score) {
+    if (tid < a.E) score[tid] = a.score[t * a.E + tid];
+  } else if (a.E <= 8) {  // two waves an expert
+    const int e = w >> 1;
+    if (e < a.E) {
+      const double s = wave_sum(score_part(x, a.router + (int64_t)e * a.d, (w & 1) * 512 + l * 8, 1024, a.d));
+      if (l == 0) part[w] = s;
     }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
-    if (l == 0) score[e] = s;
+    __syncthreads();
+    if (tid < a.E) score[tid] = part[2 * tid] + part[2 * tid + 1];
+  } else {
+    for (int e = w; e < a.E; e += 16) {
+      const double s = wave_sum(score_part(x, a.router + (int64_t)e * a.d, l * 8, 512, a.d));
+      if (l == 0) score[e] = s;
+    }
   }
   if (tid < a.E) rank[tid] = 0;
   __syncthreads();
@@ -71,6 +139,25 @@ __global__ __launch_bounds__(1024) void k_moe_route(MoeArgs a) {
       for (int j = 0; j < a.E; ++j) sum += expf((float)(score[j] - top));
     a.ids[t * a.k + tid] = e;
     a.w[t * a.k + tid] = expf((float)(score[e] - top)) / sum;
+  }
+  const int np = (int)(a.d / 8);
+  for (int i = tid; i < a.k * np; i += 1024) {
+    const int j = i / np;
+    const int64_t c = (int64_t)(i % np) * 8;
+    const u32x4 xv = *(const u32x4*)(x + c);
+    const float* dhi = a.gu_dhi + (int64_t)chosen[j] * a.d + c;
+    const f32x4 h0 = *(const f32x4*)dhi, h1 = *(const f32x4*)(dhi + 4);
+    const float v[8] = {bf16lo(xv.x) * h0.x, bf16hi(xv.x) * h0.y, bf16lo(xv.y) * h0.z,
+                        bf16hi(xv.y) * h0.w, bf16lo(xv.z) * h1.x, bf16hi(xv.z) * h1.y,
+                        bf16lo(xv.w) * h1.z, bf16hi(xv.w) * h1.w};
+    float u[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) u[b] = v[code_order(ORDER, b)];
+    u32x4 pl[3];
+    split24(u, pl);
+    bf16_t* dst = a.Xp + (t * a.k + j) * 3 * a.d + plane_piece(c, a.gs);
+#pragma unroll
+    for (int b = 0; b < 3; ++b) *(u32x4*)(dst + b * a.gs) = pl[b];
   }
 }
 
@@ -118,184 +205,431 @@ __device__ __forceinline__ u32x4 codes_bf16(u32x2 raw) {
     return u32x4{p[0], p[1], p[2], p[3]};
   }
 }
-// the channel (of 8) at place i of that operand
-template <int CB, bool F8>
-constexpr int code_order(int i) {
-  if (!F8 && CB == 4) return i < 4 ? 2 * i : 2 * (i - 4) + 1;
-  if (!F8 && CB == 2) return i / 2 + 4 * (i % 2);
-  return i;
+
+// The expert of blockIdx.y and the choices (pairs) that name it, in order, in
+// list[]: n of them (0: none).  Up to 64 choices: the blockIdx.y-th distinct
+// expert of them in order of appearance; more: expert blockIdx.y itself.  Every
+// wave finds them for itself and writes the same list, so no barrier is needed.
+struct Mine {
+  int e, n;
+};
+__host__ inline int expert_slots(int64_t P, int E) {
+  return P <= 64 ? (int)std::min(P, (int64_t)E) : E;
+}
+__device__ __forceinline__ Mine my_expert(const MoeArgs& a, int16_t* list) {
+  const int l = threadIdx.x & 63;
+  const int P = (int)a.T * a.k, slot = blockIdx.y;
+  const uint64_t below = (1ull << l) - 1ull;
+  if (P <= 64) {
+    const int id = l < P ? a.ids[l] : -1;
+    uint64_t left = __ballot(l < P);
+    int e = 0;
+    uint64_t same = 0;
+    for (int i = 0; i <= slot; ++i) {
+      if (!left) return Mine{0, 0};
+      e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+      same = __ballot(id == e);
+      left &= ~same;
+    }
+    if (id == e) list[__builtin_popcountll(same & below)] = (int16_t)l;
+    return Mine{e, (int)__builtin_popcountll(same)};
+  }
+  int n = 0;
+  for (int i0 = 0; i0 < P; i0 += 256) {
+    int id[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = i0 + i * 64 + l;
+      id[i] = at < P ? a.ids[at] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t m = __ballot(id[i] == slot);
+      if (id[i] == slot) list[n + __builtin_popcountll(m & below)] = (int16_t)(i0 + i * 64 + l);
+      n += __builtin_popcountll(m);
+    }
+  }
+  return Mine{slot, n};
 }
 
-// One expert's rows against the tokens that chose it, 16 at a time.
-// UP: rows are RT/2 blocks of 16 gate rows and the RT/2 up rows beside them,
-// x' is formed from X, and the result is silu(g) u D^{-1/2} as planes; else
-// RT blocks of down rows, x' is those planes, and the result is the expert's
-// weighted output.  The four waves of a workgroup take the groups in turn and
-// add up in LDS in wave order.
-constexpr int MW = 4;
+// The rows of one kind of projection of one expert as the products read them.
+struct Rows {
+  __amdgpu_buffer_rsrc_t c0, c1;  // codes of the first and second kind of row
+};
+template <int RB, bool UP>
+__device__ __forceinline__ Rows expert_rows(const MoeArgs& a, int e, int64_t row0) {
+  const int64_t N = UP ? a.ff : a.d, rb = UP ? a.gu_rb : a.dn_rb;
+  const int64_t nrow = max((int64_t)0, min((int64_t)RB * 16, N - row0));
+  const int64_t erow = (int64_t)e * (UP ? 2 * a.ff : a.d) + min(row0, N - 1);
+  const uint8_t* codes = UP ? a.gu : a.dn;
+  Rows r;
+  // bounded buffers: rows past the last read zeros
+  r.c0 = make_rsrc(codes + erow * rb, (uint32_t)(nrow * rb));
+  r.c1 = UP ? make_rsrc(codes + (erow + a.ff) * rb, (uint32_t)(nrow * rb)) : r.c0;
+  return r;
+}
 
-template <int CB, bool F8, int GS, int RT, bool UP>
-__global__ __launch_bounds__(MW * 64) void k_moe_proj(MoeArgs a) {
+// The scales and offsets of `rows` rows of one kind from row0 on, scale groups
+// [g0, g0 + ng), to LDS as sm[row][group] (an odd pitch: 16 rows of a read in
+// 16 banks): rows are contiguous in memory, so each is fetched once.
+__device__ __forceinline__ void stage_scales(float2* sm, int pitch, const float* s, const float* m,
+                                             int64_t row0, int rows, int64_t nrow, int64_t Gs,
+                                             int64_t g0, int ng) {
+  for (int i = threadIdx.x; i < rows * ng; i += blockDim.x) {
+    const int r = i / ng, g = i % ng;
+    const int64_t at = (row0 + min((int64_t)r, nrow - 1)) * Gs + g0 + g;
+    sm[r * pitch + g] = float2{s[at], m[at]};
+  }
+}
+
+// The codes come in slots of SB bytes of each row: a wave loads whole lines of
+// its RT * 16 rows (16 bytes a lane, SB / 16 lanes a row) into registers, and
+// puts them in its own part of LDS, from where the products read the pieces
+// their lanes need.  (Read in place, a lane's piece of a group makes 64-byte
+// requests, and with those the kernel stayed at 3.4 TB/s whatever its tiles.)
+// In LDS the 16-byte pieces of row r are swapped by r / 2, which puts the 16
+// rows of a read on all banks.
+template <int CB, int GS>
+struct Slot {
+  static constexpr int SB = CB == 1 ? 64 : 128;
+  static constexpr int SG = SB * 8 / CB / GS;   // groups
+  static constexpr int LPR = SB / 16;           // lanes a row
+  static constexpr int RPI = 64 / LPR;          // rows a load
+};
+template <int CB, int GS, int RT>
+struct Stage {
+  u32x4 c[RT * 16 / Slot<CB, GS>::RPI];
+};
+template <int CB, int GS, int RT, int RB>
+__device__ __forceinline__ void load_codes_of(Stage<CB, GS, RT>& st, const Rows& r, int64_t rb,
+                                              int slot, int l) {
+  using S = Slot<CB, GS>;
+  constexpr int PER = RB * 16 / S::RPI;  // loads of one kind of row
+#pragma unroll
+  for (int i = 0; i < RT * 16 / S::RPI; ++i)
+    st.c[i] = buf_load16(i < PER ? r.c0 : r.c1,
+                         (uint32_t)(((i % PER) * S::RPI + l / S::LPR) * rb + l % S::LPR * 16),
+                         (uint32_t)(slot * S::SB));
+}
+template <int CB, int GS, int RT>
+__device__ __forceinline__ void put_codes(const Stage<CB, GS, RT>& st, uint8_t* lds, int l) {
+  using S = Slot<CB, GS>;
+#pragma unroll
+  for (int i = 0; i < RT * 16 / S::RPI; ++i) {
+    const int row = i * S::RPI + l / S::LPR;
+    *(u32x4*)(lds + row * S::SB + ((l % S::LPR) ^ (row >> 1 & (S::LPR - 1))) * 16) = st.c[i];
+  }
+}
+// the lane's quarter of group j of a slot, row block r
+template <int CB, int GS>
+__device__ __forceinline__ GroupCodes<CB, GS> get_codes(const uint8_t* lds, int r, int j, int lr, int q) {
+  using S = Slot<CB, GS>;
+  constexpr int NB = GroupCodes<CB, GS>::NB;
+  const int row = r * 16 + lr, at = j * (GS * CB / 8) + q * NB;
+  const int swz = row >> 1 & (S::LPR - 1);
+  const uint8_t* base = lds + row * S::SB;
+  GroupCodes<CB, GS> c;
+  if constexpr (NB >= 16) {
+#pragma unroll
+    for (int i = 0; i < NB / 16; ++i) {
+      const u32x4 v = *(const u32x4*)(base + ((at / 16 + i) ^ swz) * 16);
+      c.w[4 * i] = v.x; c.w[4 * i + 1] = v.y; c.w[4 * i + 2] = v.z; c.w[4 * i + 3] = v.w;
+    }
+  } else {
+    const uint8_t* p = base + ((at / 16) ^ swz) * 16 + at % 16;
+    if constexpr (NB == 8) {
+      const u32x2 v = *(const u32x2*)p;
+      c.w[0] = v.x;
+      c.w[1] = v.y;
+    } else if constexpr (NB == 4) {
+      c.w[0] = *(const unsigned*)p;
+    } else if constexpr (NB == 2) {
+      c.w[0] = *(const uint16_t*)p;
+    } else {
+      c.w[0] = *p;
+    }
+  }
+  return c;
+}
+
+// group j of a slot: RT row blocks against NB * 16 columns of planes x
+template <int CB, bool F8, int GS, int RT, int NB>
+__device__ __forceinline__ void use_group(const uint8_t* lds, int j, const u32x4 (&x)[GS / 32][NB],
+                                          const float2* sm, int pitch, int lr, int q,
+                                          f32x4 (&acc)[RT][NB]) {
+  const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  f32x4 sx[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    sx[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < GS / 32; ++k)
+      sx[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[k][b]),
+                                                     __builtin_bit_cast(bf16x8, ones), sx[b], 0, 0, 0);
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const float2 sc = sm[r * 16 * pitch];
+    const GroupCodes<CB, GS> c = get_codes<CB, GS>(lds, r, j, lr, q);
+    f32x4 p[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) p[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < GS / 32; ++k) {
+      const u32x4 cq = codes_bf16<CB, F8>(step_codes<CB, GS>(c, k));
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        p[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[k][b]),
+                                                      __builtin_bit_cast(bf16x8, cq), p[b], 0, 0, 0);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[r][b][i] = fmaf(sc.x, p[b][i], fmaf(sc.y, sx[b][i], acc[r][b][i]));
+  }
+}
+
+// slots s0, s0 + step, ... below s1 (groups below G), the next one's loads in
+// flight while one is contracted; sm: the lane's row of the staged scales,
+// whose first group is gs0.  stage() puts them there while the first codes are
+// on their way.
+template <int CB, bool F8, int GS, int RT, int RB, int NB, class F>
+__device__ __forceinline__ void contract(const Rows& r, const bf16_t* const (&col)[NB], int64_t rb,
+                                         int s0, int s1, int step, int G, uint8_t* lds,
+                                         const float2* sm, int pitch, int gs0, int gdiv, int l,
+                                         f32x4 (&acc)[RT][NB], F&& stage) {
+  using S = Slot<CB, GS>;
   constexpr int NKS = GS / 32;
-  __shared__ unsigned have[kMoeMaxE / 32];
+  const int lr = l & 15, q = l >> 4;
+  Stage<CB, GS, RT> st;
+  load_codes_of<CB, GS, RT, RB>(st, r, rb, s0, l);
+  __builtin_amdgcn_sched_barrier(0);
+  stage();
+  for (int s = s0; s < s1; s += step) {
+    put_codes<CB, GS, RT>(st, lds, l);
+    // the planes come from L2 and are asked for ahead of the next codes, so
+    // that they are not waited for behind them
+    constexpr int XG = S::SG * NKS * NB <= 12 ? S::SG : S::SG * NKS * NB <= 24 ? S::SG / 2 : 1;
+    u32x4 x[XG][NKS][NB];
+    auto planes = [&](int j) {
+      const int gg = min(s * S::SG + j, G - 1);  // (a group past the end is not used)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int k = 0; k < NKS; ++k)
+          x[j % XG][k][b] = *(const u32x4*)(col[b] + (int64_t)gg * 3 * GS + k * 32 + q * 8);
+    };
+#pragma unroll
+    for (int j = 0; j < XG; ++j) planes(j);
+    __builtin_amdgcn_sched_barrier(0);
+    load_codes_of<CB, GS, RT, RB>(st, r, rb, s + step, l);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < S::SG; ++j) {
+      const int g = s * S::SG + j;
+      if (j > 0 && j % XG == 0) {
+#pragma unroll
+        for (int i = 0; i < XG; ++i) planes(j + i);
+      }
+      if (j == 0 || g < G)  // uniform
+        use_group<CB, F8, GS, RT, NB>(lds, j, x[j % XG], sm + ((g >> gdiv) - gs0), pitch, lr, q, acc);
+    }
+  }
+}
+
+// silu(g) u D^{-1/2} as the planes of the down product
+template <int ORDER>
+__device__ __forceinline__ void store_hidden(const MoeArgs& a, int64_t p, int64_t row, float gate,
+                                             float up, float dhi) {
+  const float h = gate / (1.f + expf(-gate)) * up * dhi;
+  const unsigned hi = __float_as_uint(h) & 0xffff0000u;
+  const float r1 = h - __uint_as_float(hi);
+  const unsigned mid = __float_as_uint(r1) & 0xffff0000u;
+  const unsigned lo = __float_as_uint(r1 - __uint_as_float(mid));
+  int at = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (code_order(ORDER, j) == (int)(row & 7)) at = j;
+  bf16_t* dst = a.H + p * 3 * a.ff + plane_piece(row & ~(int64_t)7, a.gs) + at;
+  dst[0] = (bf16_t)(hi >> 16);
+  dst[a.gs] = (bf16_t)(mid >> 16);
+  dst[2 * a.gs] = (bf16_t)(lo >> 16);
+}
+
+// One expert's rows against the tokens that chose it, NB * 16 columns at a
+// time.  The W waves are KS ranges of groups (taken in turn) by W / KS blocks
+// of rows.  UP: a block is RT/2 * 16 gate rows and the up rows beside them, and
+// the result goes to H; else RT * 16 down rows, and the weighted result to Yp.
+template <int CB, bool F8, int GS, int RT, int NB, int W, int KS, bool UP>
+__global__ __launch_bounds__(W * 64) void k_moe_proj(MoeArgs a) {
+  constexpr int RB = UP ? RT / 2 : RT;
+  constexpr int ORDER = order_of(CB, F8);
   __shared__ int16_t list[kMoeMaxT];
-  __shared__ int count;
-  __shared__ f32x4 red[MW][RT][64];
+  // the waves' slots of codes and the staged scales, then (in their place) the
+  // products [column][row]
+  extern __shared__ __attribute__((aligned(16))) float dyn[];
+  float(*red)[RT][NB][16][17] = reinterpret_cast<float(*)[RT][NB][16][17]>(dyn);
   const int tid = threadIdx.x, l = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = l & 15, q = l >> 4;
-  const int P = (int)a.T * a.k;
+  const Mine mine = my_expert(a, list);
+  const int n = mine.n, e = mine.e;
+  if (n == 0) return;  // uniform
 
-  // the blockIdx.y-th expert that any token chose, and the choices that name it
-  if (tid < kMoeMaxE / 32) have[tid] = 0u;
-  __syncthreads();
-  for (int i = tid; i < P; i += MW * 64) atomicOr(&have[a.ids[i] >> 5], 1u << (a.ids[i] & 31));
-  __syncthreads();
-  int e = -1;
-  for (int i = 0, left = blockIdx.y; i < kMoeMaxE / 32; ++i) {
-    unsigned b = have[i];
-    const int c = __builtin_popcount(b);
-    if (left < c) {
-      while (left--) b &= b - 1u;
-      e = i * 32 + __builtin_ctz(b);
-      break;
-    }
-    left -= c;
-  }
-  if (e < 0) return;  // uniform
-  if (w == 0) {
-    int n = 0;
-    for (int i0 = 0; i0 < P; i0 += 64) {
-      const bool mine = i0 + l < P && a.ids[i0 + l] == e;
-      const uint64_t m = __ballot(mine);
-      if (mine) list[n + __builtin_popcountll(m & ((1ull << l) - 1ull))] = (int16_t)(i0 + l);
-      n += __builtin_popcountll(m);
-    }
-    if (l == 0) count = n;
-  }
-  __syncthreads();
-  const int n = count;
+  const int64_t N = UP ? a.ff : a.d, rb = UP ? a.gu_rb : a.dn_rb;
+  const int G = (int)((UP ? a.d : a.ff) / GS);
+  const int gdiv = a.gshift - __builtin_ctz((unsigned)GS);
+  const int64_t row0 = ((int64_t)blockIdx.x * (W / KS) + w / KS) * (RB * 16);
+  const Rows rows = expert_rows<RB, UP>(a, e, row0);
+  const bf16_t* xp = UP ? a.Xp : a.H;
+  const int64_t K3 = 3 * (UP ? a.d : a.ff);
+  constexpr int WR = RB * 16 * (W / KS);  // rows (of one kind) of the workgroup
+  const int64_t wrow0 = (int64_t)blockIdx.x * WR, wn = min((int64_t)WR, N - wrow0);
+  const int64_t erow = (int64_t)e * (UP ? 2 * a.ff : a.d) + wrow0;
+  const int64_t Gs = (UP ? a.d : a.ff) >> a.gshift;
+  const float* ss = UP ? a.gu_s : a.dn_s;
+  const float* mm = UP ? a.gu_m : a.dn_m;
+  // scale groups staged at a time; the lane's first row there: its row block's
+  // rows (of both kinds) are 16 RT rows one after another
+  const int pitch = a.pitch;
+  constexpr int SLOT = RT * 16 * Slot<CB, GS>::SB;
+  uint8_t* slot = reinterpret_cast<uint8_t*>(dyn) + w * SLOT;
+  float2* sm = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(dyn) + W * SLOT);
+  const float2* sml = sm + ((w / KS) * RT * 16 + lr) * pitch;
 
-  const int64_t K = UP ? a.d : a.ff, N = UP ? a.ff : a.d;  // channels, rows (of each kind)
-  const int64_t rb = UP ? a.gu_rb : a.dn_rb;
-  const int64_t Gs = K >> a.gshift;  // scales per row
-  const int G = (int)(K / GS);
-  constexpr int RB = UP ? RT / 2 : RT;  // row blocks of one kind
-  const int64_t row0 = (int64_t)blockIdx.x * RB * 16;
-  const int64_t nrow = min((int64_t)RB * 16, N - row0);
-  const int64_t erow = (int64_t)e * (UP ? 2 * a.ff : a.d) + row0;  // first row among all experts'
-  const uint8_t* codes = UP ? a.gu : a.dn;
-  const float* sp = UP ? a.gu_s : a.dn_s;
-  const float* mp = UP ? a.gu_m : a.dn_m;
-  // one bounded buffer per kind of row: rows past the last read zeros
-  const __amdgpu_buffer_rsrc_t c0 = make_rsrc(codes + erow * rb, (uint32_t)(nrow * rb));
-  const __amdgpu_buffer_rsrc_t c1 = UP ? make_rsrc(codes + (erow + a.ff) * rb, (uint32_t)(nrow * rb)) : c0;
-  int64_t srow[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int64_t in = (r % RB) * 16 + lr;
-    srow[r] = (erow + (r / RB) * a.ff + min(in, nrow - 1)) * Gs;
-  }
-  const float* dhi = UP ? a.gu_dhi + (int64_t)e * a.d : nullptr;
-  const int gsub = __builtin_ctz((unsigned)GS);
+  // a thread's row is the same in every turn of the last loop below; its factor
+  // is asked for ahead of the codes
+  static_assert(W * 64 % WR == 0, "rows of a workgroup");
+  const int rr = tid % WR;
+  const int64_t row = wrow0 + rr;
+  const float dhi = UP && row < N ? a.dn_dhi[(int64_t)e * a.ff + row] : 0.f;
 
-  for (int tb = 0; tb < n; tb += 16) {
-    // columns past the last repeat the first (never stored)
-    const int pick = list[tb + lr < n ? tb + lr : tb];
-    const bf16_t* xsrc = UP ? a.X + (int64_t)(pick / a.k) * a.d : a.H + (int64_t)pick * 3 * a.ff;
-    f32x4 acc[RT];
+  // tokens of a pass: their columns are 3 j, 3 j + 1, 3 j + 2
+  constexpr int TP = NB * 16 / 3;
+  for (int t0 = 0; t0 < n; t0 += TP) {
+    const int here = min(TP, n - t0);
+    const bf16_t* col[NB];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int g = w; g < G; g += MW) {
-      GroupCodes<CB, GS> cv[RT];
-      float s[RT], m[RT];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        load_codes<CB, GS>(cv[r], r < RB ? c0 : c1,
-                           (uint32_t)(((r % RB) * 16 + lr) * rb + q * GroupCodes<CB, GS>::NB),
-                           (uint32_t)((int64_t)g * GS * CB / 8));
-        const int64_t gi = srow[r] + (((int64_t)g << gsub) >> a.gshift);
-        s[r] = sp[gi];
-        m[r] = mp[gi];
-      }
-      f32x4 Pr[RT], Sx = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int r = 0; r < RT; ++r) Pr[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < NKS; ++k) {
-        const int64_t c = (int64_t)g * GS + q * (GS / 4) + k * 8;
-        u32x4 pl[3];
-        if constexpr (UP) {
-          const u32x4 xv = *(const u32x4*)(xsrc + c);
-          const f32x4 h0 = *(const f32x4*)(dhi + c), h1 = *(const f32x4*)(dhi + c + 4);
-          const float v[8] = {bf16lo(xv.x) * h0.x, bf16hi(xv.x) * h0.y, bf16lo(xv.y) * h0.z,
-                              bf16hi(xv.y) * h0.w, bf16lo(xv.z) * h1.x, bf16hi(xv.z) * h1.y,
-                              bf16lo(xv.w) * h1.z, bf16hi(xv.w) * h1.w};
-          float u[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) u[i] = v[code_order<CB, F8>(i)];
-          split24(u, pl);
-        } else {
-          // (the planes are stored in the operand's order)
-#pragma unroll
-          for (int i = 0; i < 3; ++i) pl[i] = *(const u32x4*)(xsrc + i * a.ff + c);
-        }
-        const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-          Sx = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, pl[i]),
-                                                      __builtin_bit_cast(bf16x8, ones), Sx, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const u32x4 cq = codes_bf16<CB, F8>(step_codes<CB, GS>(cv[r], k));
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            Pr[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, pl[i]),
-                                                           __builtin_bit_cast(bf16x8, cq), Pr[r], 0, 0, 0);
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(s[r], Pr[r][i], fmaf(m[r], Sx[i], acc[r][i]));
+    for (int b = 0; b < NB; ++b) {
+      // columns past the last repeat the first (never stored)
+      const int c = b * 16 + lr < 3 * here ? b * 16 + lr : 0;
+      col[b] = xp + (int64_t)list[t0 + c / 3] * K3 + (c % 3) * GS;
     }
+    f32x4 acc[RT][NB];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) red[w][r][l] = acc[r];
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[r][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    constexpr int SG = Slot<CB, GS>::SG;
+    for (int gs0 = 0; gs0 < Gs; gs0 += a.ngs) {
+      const int ng = min(a.ngs, (int)Gs - gs0);
+      const int g1 = min(G, (gs0 + ng) << gdiv);
+      contract<CB, F8, GS, RT, RB, NB>(
+          rows, col, rb, (gs0 << gdiv) / SG + w % KS, (g1 + SG - 1) / SG, KS, g1, slot, sml, pitch,
+          gs0, gdiv, l, acc, [&] {
+            if (gs0 > 0) __syncthreads();
+            for (int b = 0; b < W / KS; ++b)
+              for (int kind = 0; kind < (UP ? 2 : 1); ++kind)
+                stage_scales(sm + (b * RT + kind * RB) * 16 * pitch, pitch, ss, mm,
+                             erow + kind * a.ff + min((int64_t)b * RB * 16, wn - 1), RB * 16,
+                             max((int64_t)1, wn - b * RB * 16), Gs, gs0, ng);
+            __syncthreads();
+          });
+    }
+    // lane l of a product holds row l & 15 and columns 4 (l >> 4) + i
     __syncthreads();
-    // lane ll of block r holds row r * 16 + (ll & 15), columns 4 (ll >> 4) + i
-    for (int i = tid; i < RB * 256; i += MW * 64) {
-      const int r = i >> 8, ll = i & 63, c = (i >> 6) & 3;
-      const int col = tb + (ll >> 4) * 4 + c;
-      const int64_t row = row0 + r * 16 + (ll & 15);
-      if (col >= n || row >= N) continue;
-      auto sum = [&](int rr) {
-        float v = red[0][rr][ll][c];
 #pragma unroll
-        for (int ww = 1; ww < MW; ++ww) v += red[ww][rr][ll][c];
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[w][r][b][q * 4 + i][lr] = acc[r][b][i];
+    __syncthreads();
+    for (int i = tid; i < here * WR; i += W * 64) {
+      const int j = i / WR;
+      const int wb = rr / (RB * 16), ri = rr % (RB * 16);
+      if (row >= N) continue;
+      auto value = [&](int r) {
+        float v = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int pl = 0; pl < 3; ++pl) {
+            const int c = 3 * j + pl;
+            v += red[wb * KS + ks][r][c >> 4][c & 15][ri & 15];
+          }
         return v;
       };
-      const int64_t p = list[col];
-      if constexpr (UP) {
-        const float gate = sum(r), up = sum(RB + r);
-        const float h = gate / (1.f + expf(-gate)) * up * a.dn_dhi[(int64_t)e * a.ff + row];
-        const unsigned hi = __float_as_uint(h) & 0xffff0000u;
-        const float r1 = h - __uint_as_float(hi);
-        const unsigned mid = __float_as_uint(r1) & 0xffff0000u;
-        const unsigned lo = __float_as_uint(r1 - __uint_as_float(mid));
-        // in the order of the down product's operand
-        int at = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (code_order<CB, F8>(j) == (int)(row & 7)) at = j;
-        bf16_t* dst = a.H + p * 3 * a.ff + (row & ~(int64_t)7) + at;
-        dst[0] = (bf16_t)(hi >> 16);
-        dst[a.ff] = (bf16_t)(mid >> 16);
-        dst[2 * a.ff] = (bf16_t)(lo >> 16);
-      } else {
-        a.Yp[p * a.d + row] = a.w[p] * sum(r);
-      }
+      const int64_t p = list[t0 + j];
+      if constexpr (UP)
+        store_hidden<ORDER>(a, p, row, value(ri >> 4), value(RB + (ri >> 4)), dhi);
+      else
+        a.Yp[p * a.d + row] = a.w[p] * value(ri >> 4);
     }
     __syncthreads();
+  }
+}
+
+// The down products and their weighted sum of ONE token: a workgroup owns 16
+// rows of all its k experts, the waves being experts by ranges of groups.
+template <int CB, bool F8, int GS, int W>
+__global__ __launch_bounds__(W * 64) void k_moe_down_one(MoeArgs a) {
+  __shared__ float red[W][3][17];
+  extern __shared__ __attribute__((aligned(16))) float dyn[];
+  const int l = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  constexpr int SG = Slot<CB, GS>::SG, SLOT = 16 * Slot<CB, GS>::SB;
+  uint8_t* slot = reinterpret_cast<uint8_t*>(dyn) + w * SLOT;
+  float2* sm = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(dyn) + W * SLOT);
+  const int lr = l & 15, q = l >> 4;
+  const int64_t row0 = (int64_t)blockIdx.x * 16;
+  const int G = (int)(a.ff / GS);
+  const int gdiv = a.gshift - __builtin_ctz((unsigned)GS);
+  const int64_t Gs = a.ff >> a.gshift;
+  const int KS = max(1, W / a.k);  // waves an expert
+  const int EP = W / KS;           // experts at a time
+  const int pitch = a.pitch;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < a.k; j0 += EP) {
+    const int j = j0 + w / KS;
+    const bool live = j < a.k;
+    f32x4 acc[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
+    for (int gs0 = 0; gs0 < Gs; gs0 += a.ngs) {
+      const int ng = min(a.ngs, (int)Gs - gs0);
+      const int g1 = min(G, (gs0 + ng) << gdiv);
+      // (waves with no expert of their own in this turn go along with the last)
+      const int jj = min(j, a.k - 1);
+      const Rows rows = expert_rows<1, false>(a, a.ids[jj], row0);
+      const bf16_t* const col[1] = {a.H + (int64_t)jj * 3 * a.ff + (lr < 3 ? lr : 0) * GS};
+      contract<CB, F8, GS, 1, 1, 1>(
+          rows, col, a.dn_rb, (gs0 << gdiv) / SG + w % KS, live ? (g1 + SG - 1) / SG : 0, KS, g1, slot,
+          sm + ((w / KS) % EP * 16 + lr) * pitch, pitch, gs0, gdiv, l, acc, [&] {
+            if (j0 > 0 || gs0 > 0) __syncthreads();
+            for (int b = 0; b < EP && j0 + b < a.k; ++b)
+              stage_scales(sm + b * 16 * pitch, pitch, a.dn_s, a.dn_m,
+                           (int64_t)a.ids[j0 + b] * a.d + row0, 16, a.d - row0, Gs, gs0, ng);
+            __syncthreads();
+          });
+    }
+    if (live) {
+      const float wj = a.w[j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = fmaf(wj, acc[0][0][i], sum[i]);
+    }
+  }
+  if (q == 0) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) red[w][i][lr] = sum[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < 16 && row0 + threadIdx.x < a.d) {
+    float y = 0.f;
+#pragma unroll
+    for (int ww = 0; ww < W; ++ww)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) y += red[ww][i][threadIdx.x];
+    a.Y[row0 + threadIdx.x] = y;
   }
 }
 
@@ -308,44 +642,80 @@ __global__ __launch_bounds__(256) void k_moe_sum(MoeArgs a) {
   *(f32x4*)(a.Y + i) = y;
 }
 
-template <int CB, bool F8, bool UP>
-hipError_t launch_proj(const MoeArgs& a, int group, const Launch& L) {
-  constexpr int RT = 4;
+template <int CB, bool F8, int GS, bool UP>
+hipError_t launch_proj(const MoeArgs& a, const Launch& L) {
   const int64_t N = UP ? a.ff : a.d;
-  const int64_t per = 16 * (UP ? RT / 2 : RT);
-  const int slots = (int)(a.T * a.k < a.E ? a.T * a.k : a.E);
-  const dim3 grid((unsigned)((N + per - 1) / per), (unsigned)slots), blk(MW * 64);
-  switch (group) {
-    case 32: return ext_launch(k_moe_proj<CB, F8, 32, RT, UP>, grid, blk, 0, L, a);
-    case 64: return ext_launch(k_moe_proj<CB, F8, 64, RT, UP>, grid, blk, 0, L, a);
-    // a group of 256 is two halves with one scale
-    case 128: case 256: return ext_launch(k_moe_proj<CB, F8, 128, RT, UP>, grid, blk, 0, L, a);
-    default: return hipErrorInvalidValue;
+  const int slots = expert_slots(a.T * a.k, a.E);
+  const int64_t Gs = (UP ? a.d : a.ff) >> a.gshift;
+  // LDS: the waves' slots, and `rows` rows of staged scales, up to kStage bytes
+  // of them at a time (an odd number of float2 a row, whole slots' groups); the
+  // products later, in their place
+  constexpr int kStage = 40 * 1024;
+  using S = Slot<CB, GS>;
+  MoeArgs b = a;
+  auto lds = [&](int rows, int slots, size_t products) {
+    b.ngs = (int)std::min(Gs, (int64_t)kStage / (rows * 8) / S::SG * S::SG);
+    b.pitch = b.ngs | 1;
+    return (uint32_t)std::max((size_t)slots * 16 * S::SB + (size_t)rows * b.pitch * 8, products);
+  };
+  auto go = [&](auto kernel, int RT, int NB, int W, int KS) {
+    const int rows = RT * 16 * (W / KS), per = UP ? rows / 2 : rows;
+    const uint32_t bytes = lds(rows, W * RT, (size_t)W * RT * NB * 16 * 17 * 4);
+    return ext_launch(kernel, dim3((unsigned)((N + per - 1) / per), (unsigned)slots), dim3(W * 64),
+                      bytes, L, b);
+  };
+  if (!UP && a.T == 1) {
+    constexpr int W = 8;
+    const uint32_t bytes = lds(16 * (W / std::max(1, W / a.k)), W, 0);
+    return ext_launch(k_moe_down_one<CB, F8, GS, W>, dim3((unsigned)((N + 15) / 16)),
+                      dim3(W * 64), bytes, L, b);
   }
+  // columns an expert can expect: 16 of them are 5 tokens
+  if (a.T * a.k <= 5 * (int64_t)a.E) return go(k_moe_proj<CB, F8, GS, 4, 1, 4, 4, UP>, 4, 1, 4, 4);
+  return go(k_moe_proj<CB, F8, GS, 4, 3, 4, 2, UP>, 4, 3, 4, 2);
 }
 
 template <bool UP>
-hipError_t launch_cb(const MoeArgs& a, int group, int cb, const Launch& L) {
-  if (a.qf == QF_FP8) return cb == 8 ? launch_proj<8, true, UP>(a, group, L) : hipErrorInvalidValue;
+hipError_t launch_cb(const MoeArgs& a, int cb, const Launch& L) {
+#define TTQ_MOE_GS(CBV, F8)                                       \
+  switch (a.gs) {                                                 \
+    case 32: return launch_proj<CBV, F8, 32, UP>(a, L);           \
+    case 64: return launch_proj<CBV, F8, 64, UP>(a, L);           \
+    case 128: return launch_proj<CBV, F8, 128, UP>(a, L);         \
+    default: return hipErrorInvalidValue;                         \
+  }
+  if (a.qf == QF_FP8) {
+    if (cb != 8) return hipErrorInvalidValue;
+    TTQ_MOE_GS(8, true)
+  }
   switch (cb) {
-    case 1: return launch_proj<1, false, UP>(a, group, L);
-    case 2: return launch_proj<2, false, UP>(a, group, L);
-    case 4: return launch_proj<4, false, UP>(a, group, L);
-    case 8: return launch_proj<8, false, UP>(a, group, L);
+    case 1: TTQ_MOE_GS(1, false)
+    case 2: TTQ_MOE_GS(2, false)
+    case 4: TTQ_MOE_GS(4, false)
+    case 8: TTQ_MOE_GS(8, false)
     default: return hipErrorInvalidValue;
   }
+#undef TTQ_MOE_GS
 }
 
 }  // namespace
 
-hipError_t launch_moe_route(const MoeArgs& a, const Launch& L) {
-  return ext_launch(k_moe_route, dim3((unsigned)a.T), dim3(1024), 0, L, a);
+hipError_t launch_moe_score(const MoeArgs& a, const Launch& L) {
+  return ext_launch(k_moe_score, dim3((unsigned)((a.E + 3) / 4), (unsigned)a.T), dim3(256), 0, L, a);
 }
-hipError_t launch_moe_up(const MoeArgs& a, int group, int cb, const Launch& L) {
-  return launch_cb<true>(a, group, cb, L);
+hipError_t launch_moe_route(const MoeArgs& a, int cb, const Launch& L) {
+  const dim3 grid((unsigned)a.T), blk(1024);
+  switch (order_of(cb, a.qf == QF_FP8)) {
+    case 1: return ext_launch(k_moe_route<1>, grid, blk, 0, L, a);
+    case 2: return ext_launch(k_moe_route<2>, grid, blk, 0, L, a);
+    default: return ext_launch(k_moe_route<0>, grid, blk, 0, L, a);
+  }
 }
-hipError_t launch_moe_down(const MoeArgs& a, int group, int cb, const Launch& L) {
-  return launch_cb<false>(a, group, cb, L);
+hipError_t launch_moe_up(const MoeArgs& a, int cb, const Launch& L) {
+  return launch_cb<true>(a, cb, L);
+}
+hipError_t launch_moe_down(const MoeArgs& a, int cb, const Launch& L) {
+  return launch_cb<false>(a, cb, L);
 }
 hipError_t launch_moe_sum(const MoeArgs& a, const Launch& L) {
   return ext_launch(k_moe_sum, dim3((unsigned)((a.T * a.d / 4 + 255) / 256)), dim3(256), 0, L, a);

@@ -248,7 +248,7 @@ const char* kKernelNames[K_NUM_KINDS] = {
     "qgemv", "dequant", "qfused", "lowrank_zsum", "gemm_quant", "seg_copy",
     "pca_skinny", "pca_psum", "pca_chol", "pca_trsm", "pca_residual",
     "pca_complete", "stream_read", "cache_write", "cache_read",
-    "adapters_shrink", "adapters_expand", "moe_route", "moe_up", "moe_down", "moe_sum"};
+    "adapters_shrink", "adapters_expand", "moe_score", "moe_route", "moe_up", "moe_down", "moe_sum"};
 
 hipEvent_t take_event() {
   if (!g_timing.pool.empty()) {
@@ -1236,8 +1236,12 @@ int adapters_impl(const ttq_params* prm, int64_t n, const void* X,
 // (k_moe.hip)
 struct MoePlan {
   int64_t gu_rb = 0, dn_rb = 0;
-  size_t off_ids = 0, off_w = 0, off_h = 0, off_yp = 0, total = 0;
+  bool score = false;  // scores by a launch of their own
+  size_t off_ids = 0, off_w = 0, off_score = 0, off_xp = 0, off_h = 0, off_yp = 0,
+         total = 0;
 };
+// one workgroup per token takes up to this many router weights itself
+constexpr int64_t kMoeRouteElems = 65536;
 
 int validate_moe(const ttq_moe_params* prm, MoePlan* P) {
   if (!prm) return TTQ_ENULL;
@@ -1268,8 +1272,11 @@ int validate_moe(const ttq_moe_params* prm, MoePlan* P) {
   const int64_t pairs = prm->T * prm->top_k;
   P->off_ids = take(sizeof(int32_t) * pairs);
   P->off_w = take(sizeof(float) * pairs);
+  P->score = prm->experts * prm->d > kMoeRouteElems;
+  if (P->score) P->off_score = take(sizeof(double) * prm->T * prm->experts);
+  P->off_xp = take(sizeof(uint16_t) * pairs * 3 * prm->d);
   P->off_h = take(sizeof(uint16_t) * pairs * 3 * prm->ff);
-  P->off_yp = take(sizeof(float) * pairs * prm->d);
+  if (prm->T > 1) P->off_yp = take(sizeof(float) * pairs * prm->d);
   P->total = off;
   return TTQ_OK;
 }
@@ -1312,17 +1319,24 @@ int moe_impl(const ttq_moe_params* prm, const void* X, const void* router,
   a.dn = dn_codes; a.dn_rb = P.dn_rb; a.dn_s = dn_scales; a.dn_m = dn_mins;
   a.dn_dhi = dn_dhalf_inv;
   a.gshift = __builtin_ctz((unsigned)prm->group);
+  a.gs = std::min(prm->group, 128);
+  a.score = P.score ? reinterpret_cast<double*>(ws + P.off_score) : nullptr;
+  a.Xp = reinterpret_cast<bf16_t*>(ws + P.off_xp);
   a.H = reinterpret_cast<bf16_t*>(ws + P.off_h);
   a.Yp = reinterpret_cast<float*>(ws + P.off_yp);
   a.Y = Y;
   a.qf = (int)prm->qformat;
   const int cb = container_bits(prm->bits);
-  st = run(K_MOE_ROUTE, s, [&](const Launch& L) { return launch_moe_route(a, L); });
+  if (P.score) {
+    st = run(K_MOE_SCORE, s, [&](const Launch& L) { return launch_moe_score(a, L); });
+    if (st != TTQ_OK) return st;
+  }
+  st = run(K_MOE_ROUTE, s, [&](const Launch& L) { return launch_moe_route(a, cb, L); });
   if (st != TTQ_OK) return st;
-  st = run(K_MOE_UP, s, [&](const Launch& L) { return launch_moe_up(a, prm->group, cb, L); });
+  st = run(K_MOE_UP, s, [&](const Launch& L) { return launch_moe_up(a, cb, L); });
   if (st != TTQ_OK) return st;
-  st = run(K_MOE_DOWN, s, [&](const Launch& L) { return launch_moe_down(a, prm->group, cb, L); });
-  if (st != TTQ_OK) return st;
+  st = run(K_MOE_DOWN, s, [&](const Launch& L) { return launch_moe_down(a, cb, L); });
+  if (st != TTQ_OK || a.T == 1) return st;  // (one token's experts are summed there)
   return run(K_MOE_SUM, s, [&](const Launch& L) { return launch_moe_sum(a, L); });
 }
 

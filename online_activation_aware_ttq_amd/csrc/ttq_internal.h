@@ -44,6 +44,7 @@ enum KernelKind {
   K_CACHE_READ,        // rows of a cache read back
   K_AD_SHRINK,         // adapters: A_e x per row
   K_AD_EXPAND,         // adapters: base + c_e B_e (A_e x)
+  K_MOE_SCORE,         // experts: scores
   K_MOE_ROUTE,         // experts: scores, the chosen ones and their weights
   K_MOE_UP,            // experts: gate and up products, silu(g) u
   K_MOE_DOWN,          // experts: down products
@@ -718,14 +719,19 @@ struct MoeArgs {
   const uint8_t* dn; int64_t dn_rb;
   const float* dn_s; const float* dn_m; const float* dn_dhi;
   int gshift;             // log2 of the group
-  bf16_t* H;              // [T k][3][ff] planes of silu(g) u D^{-1/2}
-  float* Yp;              // [T k][d] weighted expert outputs
+  int ngs, pitch;         // scale groups staged at a time, and their pitch (set by the launchers)
+  int gs;                 // channels of a step of the products: min(group, 128)
+  double* score;          // [T][E], or null: the routing kernel takes them itself
+  bf16_t* Xp;             // [T k] rows of x' as planes (see k_moe.hip), 3 d each
+  bf16_t* H;              // [T k] rows of silu(g) u D^{-1/2} as planes, 3 ff each
+  float* Yp;              // [T k][d] weighted expert outputs (T > 1)
   float* Y;               // [T][d]
   int qf;
 };
-hipError_t launch_moe_route(const MoeArgs& a, const Launch& L);
-hipError_t launch_moe_up(const MoeArgs& a, int group, int cb, const Launch& L);
-hipError_t launch_moe_down(const MoeArgs& a, int group, int cb, const Launch& L);
+hipError_t launch_moe_score(const MoeArgs& a, const Launch& L);
+hipError_t launch_moe_route(const MoeArgs& a, int cb, const Launch& L);
+hipError_t launch_moe_up(const MoeArgs& a, int cb, const Launch& L);
+hipError_t launch_moe_down(const MoeArgs& a, int cb, const Launch& L);
 hipError_t launch_moe_sum(const MoeArgs& a, const Launch& L);
 constexpr int kMoeMaxT = 128, kMoeMaxE = 256, kMoeMaxK = 16;
 
