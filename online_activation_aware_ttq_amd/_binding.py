@@ -634,7 +634,7 @@ def ttq_adapters(X, A, B, index, *, scale=None, base=None, Y=None,
     if stream is None:
         stream = _current_stream(dev)
     if workspace is None:
-        workspace = _step_workspace(dev, stream, ("adapters", key),
+        workspace = _step_workspace(dev, stream, ("adapters", key, n),
                                     lambda: ttq_adapters_workspace_bytes(prm, n))
     _enqueue("ttq_adapters", dev, load_library().ttq_adapters,
              ctypes.byref(prm), n, _ptr(X), _ptr(A), _ptr(B), _ptr(scale),

@@ -13,12 +13,14 @@
 // product as three bf16 planes that sum to it exactly (split24), so the result
 // is as exact as float32 products would be, on the matrix cores.
 //
-// Both work on tiles of 16 consecutive tokens.  A tile's distinct pairs are
-// found by ballots over its 16 indices, and each workgroup takes the tile's
-// j-th pair: the rows that name another one are not loaded, and their columns
-// of the product not stored.  So every pair is read once per tile that uses
-// it, whatever the order of the requests, with no sorting pass, and a tile of
-// one request's prompt is one ordinary matrix product.
+// Both work on tiles of consecutive tokens (128 of a decode batch, 64 of
+// prompts).  A tile's distinct pairs are found by ballots over its indices, and
+// a workgroup gathers the rows that name the j-th of them, 16 to a matrix
+// instruction: every pair is read once per tile that uses it, whatever the
+// order of the requests and with no sorting pass, and a tile of one request's
+// prompt is one ordinary matrix product.
+#include <algorithm>
+
 #include "ttq_internal.h"
 
 namespace ttq {
@@ -27,211 +29,504 @@ namespace {
 
 constexpr int AW = 4;  // waves per workgroup
 
-struct TilePair {
-  int e;              // the j-th distinct pair of the tile, -1: it has fewer
-  unsigned rows;      // the tile's rows that name it
-  unsigned none;      // the tile's rows that name no pair
+// The distinct pairs of the tile at t0 (TC * 64 tokens) that a workgroup takes,
+// one after another, and the rows that name them.  A decode step (TC = 2): the
+// pair of row blockIdx.y, if no earlier row names it.  Prompts, whose tiles
+// have few: every gridDim.y-th distinct one.  The rows that name no pair go
+// with the first workgroup.  Uniform; every wave writes the same list of rows,
+// so none waits for another: list[0, n) name pair e, list[n, all) none.
+template <int TC>
+struct TilePairs {
+  int idx[TC];
+  uint64_t left[TC], none[TC];  // rows not yet taken, rows that name no pair
+  int e, n, all;
+
+  __device__ __forceinline__ TilePairs(const AdaptersArgs& a, int64_t t0) {
+    const int l = threadIdx.x & 63;
+#pragma unroll
+    for (int c = 0; c < TC; ++c) {
+      const int64_t t = t0 + c * 64 + l;
+      const int i = t < a.T ? a.index[t] : -1;
+      idx[c] = i < a.n ? i : -1;
+      left[c] = __ballot(idx[c] >= 0);
+      none[c] = __ballot(t < a.T && idx[c] < 0);
+    }
+    if (TC == 1) {
+      for (int i = 0; i < (int)blockIdx.y; ++i) skip();
+    } else {  // only the rows that name what row blockIdx.y does, if it is their first
+      const int j = blockIdx.y;
+      uint64_t same[TC];
+      const int pick = lane_index(j);
+      int first = -1;
+#pragma unroll
+      for (int c = TC - 1; c >= 0; --c) {
+        same[c] = __ballot(idx[c] == pick);
+        if (same[c]) first = c * 64 + __builtin_ctzll(same[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < TC; ++c) left[c] = pick >= 0 && first == j ? same[c] : 0;
+    }
+    if (blockIdx.y != 0) {
+#pragma unroll
+      for (int c = 0; c < TC; ++c) none[c] = 0;
+    }
+  }
+  __device__ __forceinline__ int lane_index(int row) const {
+    int i = 0;
+#pragma unroll
+    for (int c = 0; c < TC; ++c)
+      if (row / 64 == c) i = __builtin_amdgcn_readlane(idx[c], row % 64);
+    return i;
+  }
+  // the next pair's rows leave left[]; returns them in same[]
+  __device__ __forceinline__ int skip(uint64_t* rows = nullptr) {
+    int i = -1;
+#pragma unroll
+    for (int c = TC - 1; c >= 0; --c)
+      if (left[c]) i = __builtin_amdgcn_readlane(idx[c], __builtin_ctzll(left[c]));
+#pragma unroll
+    for (int c = 0; c < TC; ++c) {
+      const uint64_t same = i < 0 ? 0 : __ballot(idx[c] == i);
+      left[c] &= ~same;
+      if (rows) rows[c] = same;
+    }
+    return i;
+  }
+  // false: nothing is left
+  __device__ __forceinline__ bool next(uint8_t* list, bool with_none) {
+    const int l = threadIdx.x & 63;
+    const uint64_t below = (1ull << l) - 1ull;
+    uint64_t same[TC];
+    e = skip(same);
+    n = 0;
+#pragma unroll
+    for (int c = 0; c < TC; ++c) {
+      if (same[c] >> l & 1u) list[n + __builtin_popcountll(same[c] & below)] = (uint8_t)(c * 64 + l);
+      n += __builtin_popcountll(same[c]);
+    }
+    all = n;
+    if (with_none) {
+#pragma unroll
+      for (int c = 0; c < TC; ++c) {
+        if (none[c] >> l & 1u) list[all + __builtin_popcountll(none[c] & below)] = (uint8_t)(c * 64 + l);
+        all += __builtin_popcountll(none[c]);
+        none[c] = 0;
+      }
+    }
+    for (int i = 1; i < (TC == 1 ? (int)gridDim.y : 1); ++i) skip();  // the other workgroups'
+    return all > 0;
+  }
 };
 
-// (uniform over the wave: every lane looks at token l & 15)
-__device__ __forceinline__ TilePair tile_pair(const int32_t* index, int64_t T, int64_t n,
-                                              int64_t t0, int j) {
-  const int lr = threadIdx.x & 15;
-  const int64_t t = t0 + lr;
-  const int idx = t < T ? index[t] : -1;
-  const bool ok = idx >= 0 && idx < n;
-  unsigned left = (unsigned)__ballot(ok) & 0xffffu;
-  const unsigned in = t0 + 16 <= T ? 0xffffu : (1u << (int)(T - t0)) - 1u;
-  TilePair p{-1, 0u, in & ~left};
-  while (left) {
-    const int e = __builtin_amdgcn_readlane(idx, __builtin_ctz(left));
-    const unsigned same = (unsigned)__ballot(ok && idx == e) & 0xffffu;
-    if (j-- == 0) {
-      p.e = e;
-      p.rows = same;
-      break;
-    }
-    left &= ~same;
-  }
-  return p;
-}
-
-// S partials: workgroup (tile, j, range) of AW waves, which take the range's
-// 32-channel steps in turn and add up in LDS in wave order.  NR: 16-row
-// blocks of A_e.
-template <int NR>
+// S partials: workgroup (tile, its pairs, range) of AW waves, which take the range's
+// 32-channel steps in turn and add up in LDS in wave order.  NR: 16-row blocks
+// of A_e; NB: 16-token blocks of a pass over the range.
+template <int TC, int NR, int NB>
 __global__ __launch_bounds__(AW * 64) void k_ad_shrink(AdaptersArgs a) {
   __shared__ f32x4 red[AW - 1][NR][64];
-  const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
+  __shared__ uint8_t list[TC * 64];
+  const int l = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int lr = l & 15, q = l >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * 16;
-  const int ks = blockIdx.z;
-  const int64_t k0 = ks * a.kc, k1 = min(a.d, k0 + a.kc);
-  for (int j = blockIdx.y; j < 16; j += gridDim.y) {
-    const TilePair p = tile_pair(a.index, a.T, a.n, t0, j);
-    if (p.e < 0) break;  // uniform over the workgroup
+  const int64_t t0 = (int64_t)blockIdx.x * TC * 64;
+  const int64_t k0 = blockIdx.z * a.kc, k1 = min(a.d, k0 + a.kc);
+  TilePairs<TC> r(a, t0);
+  while (r.next(list, false)) {  // uniform over the workgroup
     const __amdgpu_buffer_rsrc_t ar =
-        make_rsrc(a.A + (int64_t)p.e * a.rank * a.d, (uint32_t)(a.rank * a.d * 2));
+        make_rsrc(a.A + (int64_t)r.e * a.rank * a.d, (uint32_t)(a.rank * a.d * 2));
     const __amdgpu_buffer_rsrc_t xr =
-        make_rsrc(a.X + t0 * a.d, (uint32_t)(min((int64_t)16, a.T - t0) * a.d * 2));
-    const uint32_t xoff = (p.rows >> lr & 1u) ? (uint32_t)(lr * a.d * 2) : kOutOfRange;
-    f32x4 acc[NR];
+        make_rsrc(a.X + t0 * a.d, (uint32_t)(min((int64_t)TC * 64, a.T - t0) * a.d * 2));
+    for (int b0 = 0; b0 < r.n; b0 += NB * 16) {
+      uint32_t xoff[NB];
 #pragma unroll
-    for (int n = 0; n < NR; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int64_t k = k0 + w * 32; k < k1; k += AW * 32) {
-      // channels past the range (a multiple of 8 wide) read zeros
-      const uint32_t c = k + q * 8 < k1 ? (uint32_t)(k + q * 8) * 2 : kOutOfRange;
-      const u32x4 xv = buf_load16(xr, min(xoff + c, kOutOfRange), 0);
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        const uint32_t row = (uint32_t)((n * 16 + lr) * a.d * 2);
-        const u32x4 av = buf_load16(ar, min(row + c, kOutOfRange), 0);
-        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8, xv), __builtin_bit_cast(bf16x8, av), acc[n], 0, 0, 0);
+      for (int b = 0; b < NB; ++b) {
+        const int i = b0 + b * 16 + lr;
+        xoff[b] = i < r.n ? (uint32_t)(list[i] * a.d * 2) : kOutOfRange;
       }
-    }
-    if (w > 0) {
+      f32x4 acc[NB][NR];
 #pragma unroll
-      for (int n = 0; n < NR; ++n) red[w - 1][n][l] = acc[n];
-    }
-    __syncthreads();
-    if (w == 0) {
-      // lane l of a 16 x 16 product holds column l & 15 and rows 4 (l >> 4) + i
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int n = 0; n < NR; ++n) {
+        for (int n = 0; n < NR; ++n) acc[b][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // U steps' loads at a time, the next ones in flight while these multiply
+      constexpr int U = NR * NB > 4 ? 1 : 2;
+      u32x4 xv[2][U][NB], av[2][U][NR];
+      auto load = [&](int s, int64_t k) {
 #pragma unroll
-        for (int ww = 0; ww < AW - 1; ++ww) acc[n] += red[ww][n][l];
-        const int col = n * 16 + lr;
+        for (int u = 0; u < U; ++u) {
+          // channels past the range (a multiple of 8 wide) read zeros
+          const int64_t kk = k + u * (AW * 32) + q * 8;
+          const uint32_t c = kk < k1 ? (uint32_t)kk * 2 : kOutOfRange;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col < a.rank && (p.rows >> (q * 4 + i) & 1u))
-            a.S[((int64_t)ks * a.T + t0 + q * 4 + i) * a.rank + col] = acc[n][i];
-      }
-    }
-    __syncthreads();
-  }
-}
-
-// Y: workgroup (tile, j, block of 16 * OT outputs per wave).  NK: 32-column
-// steps of the rank.
-constexpr int OT = 4;
-
-template <int NK>
-__global__ __launch_bounds__(AW * 64) void k_ad_expand(AdaptersArgs a) {
-  const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int lr = l & 15, q = l >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * 16, t = t0 + lr;
-  const int64_t o0 = ((int64_t)blockIdx.z * AW + w) * (OT * 16);
-  if (o0 >= a.d_out) return;
-  for (int j = blockIdx.y; j < 16; j += gridDim.y) {
-    const TilePair p = tile_pair(a.index, a.T, a.n, t0, j);
-    // rows that name no pair go with the first one
-    const unsigned rows = j == 0 ? p.rows | p.none : p.rows;
-    if (!rows) break;
-    const bool mine = rows >> lr & 1u, live = p.rows >> lr & 1u;
-    f32x4 acc[OT];
+          for (int n = 0; n < NR; ++n)
+            av[s][u][n] = buf_load16(ar, min((uint32_t)((n * 16 + lr) * a.d * 2) + c, kOutOfRange), 0);
 #pragma unroll
-    for (int o = 0; o < OT; ++o) acc[o] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float c = 0.f;
-    if (p.e >= 0) {
-      c = a.scale ? a.scale[p.e] : 1.f;
-      const __amdgpu_buffer_rsrc_t br =
-          make_rsrc(a.B + (int64_t)p.e * a.d_out * a.rank, (uint32_t)(a.d_out * a.rank * 2));
-      u32x4 bv[OT][NK];
-#pragma unroll
-      for (int o = 0; o < OT; ++o)
-#pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          const int64_t row = o0 + o * 16 + lr;
-          const int col = k * 32 + q * 8;
-          bv[o][k] = buf_load16(br, row < a.d_out && col < a.rank
-                                        ? (uint32_t)((row * a.rank + col) * 2) : kOutOfRange, 0);
+          for (int b = 0; b < NB; ++b) xv[s][u][b] = buf_load16(xr, min(xoff[b] + c, kOutOfRange), 0);
         }
+      };
+      auto use = [&](int s) {
 #pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        const int col = k * 32 + q * 8;
-        float s[8];
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = 0.f;
-        if (live && col < a.rank) {
-          for (int ks = 0; ks < a.nks; ++ks) {
-            const float* sp = a.S + ((int64_t)ks * a.T + t) * a.rank + col;
-            const f32x4 s0 = *(const f32x4*)sp, s1 = *(const f32x4*)(sp + 4);
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+              acc[b][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8, xv[s][u][b]), __builtin_bit_cast(bf16x8, av[s][u][n]),
+                  acc[b][n], 0, 0, 0);
+      };
+      constexpr int64_t STEP = U * AW * 32;
+      int64_t k = k0 + w * 32;
+      load(0, k);
+      __builtin_amdgcn_sched_barrier(0);
+      for (; k < k1; k += 2 * STEP) {
+        load(1, k + STEP);
+        __builtin_amdgcn_sched_barrier(0);
+        use(0);
+        __builtin_amdgcn_sched_barrier(0);
+        load(0, k + 2 * STEP);
+        __builtin_amdgcn_sched_barrier(0);
+        use(1);  // (past the range: zeros)
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if (b0 + b * 16 >= r.n) break;  // uniform
+        if (w > 0) {
+#pragma unroll
+          for (int n = 0; n < NR; ++n) red[w - 1][n][l] = acc[b][n];
+        }
+        __syncthreads();
+        if (w == 0) {
+          // lane l of a 16 x 16 product holds column l & 15 and rows 4 (l >> 4) + i
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+#pragma unroll
+            for (int ww = 0; ww < AW - 1; ++ww) acc[b][n] += red[ww][n][l];
+            const int col = n * 16 + lr;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              s[i] += s0[i];
-              s[4 + i] += s1[i];
+              const int at = b0 + b * 16 + q * 4 + i;
+              if (col < a.rank && at < r.n)
+                a.S[((int64_t)blockIdx.z * a.T + t0 + list[at]) * a.rank + col] = acc[b][n][i];
             }
           }
         }
-        u32x4 pl[3];
-        split24<true>(s, pl);
-#pragma unroll
-        for (int o = 0; o < OT; ++o)
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            acc[o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bv[o][k]),
-                                                            __builtin_bit_cast(bf16x8, pl[i]),
-                                                            acc[o], 0, 0, 0);
+        __syncthreads();
       }
     }
-    // lane l holds token l & 15, outputs 4 (l >> 4) + i of each block
-    if (mine) {
+  }
+}
+
+// sum of the partials of 8 columns of S, in range order
+__device__ __forceinline__ void sum_parts(const AdaptersArgs& a, const float* sp, float (&s)[8]) {
+  f32x4 v[4][2];
 #pragma unroll
-      for (int o = 0; o < OT; ++o) {
-        const int64_t col = o0 + o * 16 + q * 4;
-        const float* bp = a.base ? a.base + t * a.d_out + col : nullptr;
-        float* yp = a.Y + t * a.d_out + col;
-        if (a.vec && col < a.d_out) {
-          f32x4 b = {0.f, 0.f, 0.f, 0.f};
-          if (bp) b = *(const f32x4*)bp;
+  for (int i = 0; i < 4; ++i) {
+    const float* p = sp + (int64_t)min(i, a.nks - 1) * a.T * a.rank;
+    v[i][0] = *(const f32x4*)p;
+    v[i][1] = *(const f32x4*)(p + 4);
+  }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) b[i] = live ? fmaf(c, acc[o][i], b[i]) : b[i];
-          *(f32x4*)yp = b;
+  for (int i = 0; i < 4; ++i) {
+    if (i >= a.nks) break;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      s[x] += v[i][0][x];
+      s[4 + x] += v[i][1][x];
+    }
+  }
+}
+
+// Y of a decode step: workgroup (pair, outputs).  Its waves share the planes of
+// 16 of the pair's rows and take 16 * OT outputs each at a time, B_e and base of
+// the next ones in flight while these multiply.  (One turn per workgroup spent
+// most of its time on the way to its first loads: 61 us for 64 pairs of rank
+// 64 on 4096 -> 11008.)  NK: 32-column steps of the rank.
+constexpr int OT = 2;
+
+template <int NK>
+__global__ __launch_bounds__(AW * 64, NK <= 2 ? 2 : 1) void k_ad_expand_step(AdaptersArgs a) {
+  __shared__ u32x4 planes[NK][3][64];
+  __shared__ uint8_t list[128];
+  const int tid = threadIdx.x, l = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = l & 15, q = l >> 4;
+  TilePairs<2> r(a, 0);
+  if (!r.next(list, true)) return;  // uniform over the workgroup
+  const bool pair = r.e >= 0;
+  const __amdgpu_buffer_rsrc_t br =
+      make_rsrc(a.B + (int64_t)max(r.e, 0) * a.d_out * a.rank,
+                pair ? (uint32_t)(a.d_out * a.rank * 2) : 0u);
+  const float c = !pair ? 0.f : a.scale ? a.scale[r.e] : 1.f;
+  const int64_t o0 = ((int64_t)blockIdx.z * AW + w) * (OT * 16);
+  const int64_t ostep = (int64_t)gridDim.z * AW * (OT * 16);
+  for (int b0 = 0; b0 < r.all; b0 += 16) {
+    const int at = b0 + lr;
+    const bool mine = at < r.all, live = at < r.n;
+    const int64_t t = list[min(at, r.all - 1)];
+    const float* bp = a.base ? a.base + t * a.d_out + q * 4 : nullptr;
+    float* yp = a.Y + t * a.d_out + q * 4;
+    struct Turn {
+      u32x4 b[OT][NK];
+      f32x4 y[OT];  // lane l holds token l & 15 and outputs 4 (l >> 4) + i of each 16
+    };
+    auto load = [&](Turn& u, int64_t o) {
+#pragma unroll
+      for (int i = 0; i < OT; ++i) {
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          const int64_t row = o + i * 16 + lr;
+          const int col = k * 32 + q * 8;
+          u.b[i][k] = buf_load16(br, row < a.d_out && col < a.rank
+                                         ? (uint32_t)((row * a.rank + col) * 2) : kOutOfRange, 0);
+        }
+        u.y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int64_t col = o + i * 16 + q * 4;
+        if (!bp || !mine) continue;
+        if (a.vec) {
+          if (col < a.d_out) u.y[i] = *(const f32x4*)(bp + o + i * 16);
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (col + i < a.d_out) {
-              const float b = bp ? bp[i] : 0.f;
-              yp[i] = live ? fmaf(c, acc[o][i], b) : b;
-            }
+          for (int x = 0; x < 4; ++x)
+            if (col + x < a.d_out) u.y[i][x] = bp[o + i * 16 + x];
         }
       }
+    };
+    auto use = [&](Turn& u, int64_t o) {
+      f32x4 acc[OT];
+#pragma unroll
+      for (int i = 0; i < OT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < NK; ++k)
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          const u32x4 pl = planes[k][x][l];
+#pragma unroll
+          for (int i = 0; i < OT; ++i)
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, u.b[i][k]),
+                                                            __builtin_bit_cast(bf16x8, pl), acc[i],
+                                                            0, 0, 0);
+        }
+      if (!mine) return;
+#pragma unroll
+      for (int i = 0; i < OT; ++i) {
+        const int64_t col = o + i * 16 + q * 4;
+        if (live) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) u.y[i][x] = fmaf(c, acc[i][x], u.y[i][x]);
+        }
+        if (a.vec) {
+          if (col < a.d_out) *(f32x4*)(yp + o + i * 16) = u.y[i];
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (col + x < a.d_out) yp[o + i * 16 + x] = u.y[i][x];
+        }
+      }
+    };
+    Turn u0, u1;
+    load(u0, o0);
+    // a thread sums the partials of 4 columns of a row
+    if (b0 > 0) __syncthreads();
+    for (int i = tid; i < NK * 128; i += AW * 64) {
+      const int sr = i / (NK * 8), sc = i % (NK * 8) * 4;
+      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+      if (b0 + sr < r.n && sc < a.rank) {
+        const float* sp = a.S + (int64_t)list[b0 + sr] * a.rank + sc;
+        f32x4 v[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) v[p] = *(const f32x4*)(sp + (int64_t)min(p, a.nks - 1) * a.T * a.rank);
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          if (p < a.nks) s += v[p];
+      }
+      const float s8[8] = {s.x, s.y, s.z, s.w, 0.f, 0.f, 0.f, 0.f};
+      u32x4 pl[3];
+      split24<true>(s8, pl);
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+        reinterpret_cast<u32x2*>(&planes[sc / 32][x][sc % 32 / 8 * 16 + sr])[sc / 4 % 2] =
+            u32x2{pl[x].x, pl[x].y};
     }
+    __syncthreads();
+    for (int64_t o = o0; o < a.d_out; o += 2 * ostep) {
+      load(u1, o + ostep);  // (past the outputs: nothing is read)
+      use(u0, o);
+      load(u0, o + 2 * ostep);
+      if (o + ostep < a.d_out) use(u1, o + ostep);
+    }
+  }
+}
+
+// Y of prompts: workgroup (tile, its pairs, outputs).  The planes of up to 64 gathered rows' S go
+// to LDS, once for the workgroup's four waves, which take 16 * OT outputs at a
+// time.
+template <int TC, int NK>
+__global__ __launch_bounds__(AW * 64) void k_ad_expand(AdaptersArgs a) {
+  // [block of 16 rows][step][plane][lane]: a wave's read is 1 KiB in a row
+  __shared__ u32x4 planes[4][NK][3][64];
+  __shared__ uint8_t list[TC * 64];
+  const int tid = threadIdx.x, l = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = l & 15, q = l >> 4;
+  const int64_t t0 = (int64_t)blockIdx.x * TC * 64;
+  TilePairs<TC> r(a, t0);
+  while (r.next(list, true)) {  // uniform over the workgroup
+    const float c = r.e < 0 ? 0.f : a.scale ? a.scale[r.e] : 1.f;
+    const __amdgpu_buffer_rsrc_t br =
+        make_rsrc(a.B + (int64_t)max(r.e, 0) * a.d_out * a.rank,
+                  r.e < 0 ? 0u : (uint32_t)(a.d_out * a.rank * 2));
+    // the first outputs' factors are asked for ahead of S
+    const int64_t ostep = (int64_t)gridDim.z * AW * (OT * 16);
+    int64_t o0 = ((int64_t)blockIdx.z * AW + w) * (OT * 16);
+    u32x4 bv[OT][NK];
+    auto load_b = [&](int64_t o) {
+#pragma unroll
+      for (int i = 0; i < OT; ++i)
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          const int64_t row = o + i * 16 + lr;
+          const int col = k * 32 + q * 8;
+          bv[i][k] = buf_load16(br, row < a.d_out && col < a.rank
+                                        ? (uint32_t)((row * a.rank + col) * 2) : kOutOfRange, 0);
+        }
+    };
+    load_b(o0);
+    for (int b0 = 0; b0 < r.all; b0 += 64) {
+      // S of 64 rows: wave w takes rows b0 + 16 w ..
+      if (b0 > 0) __syncthreads();
+      if (b0 + w * 16 < r.all) {
+        const int at = b0 + w * 16 + lr;
+        const int64_t t = t0 + list[min(at, r.all - 1)];
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          const int col = k * 32 + q * 8;
+          float s[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] = 0.f;
+          if (at < r.n && col < a.rank) sum_parts(a, a.S + t * a.rank + col, s);
+          u32x4 pl[3];
+          split24<true>(s, pl);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) planes[w][k][i][l] = pl[i];
+        }
+      }
+      __syncthreads();
+      const int nb = min(4, (r.all - b0 + 15) / 16);
+      // lane l holds token l & 15 and outputs 4 (l >> 4) + i of each 16; the
+      // next block's part of base is in flight while one is computed
+      f32x4 y[OT], yn[OT];
+      auto load_y = [&](f32x4 (&v)[OT], int64_t o, int b) {
+        const int at = b0 + b * 16 + lr;
+        const float* bp = a.base + (t0 + list[min(at, r.all - 1)]) * a.d_out + o + q * 4;
+#pragma unroll
+        for (int i = 0; i < OT; ++i) {
+          v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+          const int64_t col = o + i * 16 + q * 4;
+          if (!a.base || at >= r.all) continue;
+          if (a.vec) {
+            if (col < a.d_out) v[i] = *(const f32x4*)(bp + i * 16);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (col + x < a.d_out) v[i][x] = bp[i * 16 + x];
+          }
+        }
+      };
+      if (o0 < a.d_out) load_y(y, o0, 0);
+      for (int64_t o = o0; o < a.d_out; o += ostep) {
+        for (int b = 0; b < nb; ++b) {
+          const int at = b0 + b * 16 + lr;
+          const bool mine = at < r.all, live = at < r.n;
+          float* yp = a.Y + (t0 + list[min(at, r.all - 1)]) * a.d_out + o + q * 4;
+          if (b + 1 < nb) load_y(yn, o, b + 1);
+          else if (o + ostep < a.d_out) load_y(yn, o + ostep, 0);
+          f32x4 acc[OT];
+#pragma unroll
+          for (int i = 0; i < OT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < NK; ++k) {
+            u32x4 pl[3];
+#pragma unroll
+            for (int x = 0; x < 3; ++x) pl[x] = planes[b][k][x][l];
+#pragma unroll
+            for (int i = 0; i < OT; ++i)
+#pragma unroll
+              for (int x = 0; x < 3; ++x)
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, bv[i][k]), __builtin_bit_cast(bf16x8, pl[x]), acc[i],
+                    0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < OT; ++i) {
+            const int64_t col = o + i * 16 + q * 4;
+            if (live) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) y[i][x] = fmaf(c, acc[i][x], y[i][x]);
+            }
+            if (mine && a.vec) {
+              if (col < a.d_out) *(f32x4*)(yp + i * 16) = y[i];
+            } else if (mine) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (col + x < a.d_out) yp[i * 16 + x] = y[i][x];
+            }
+            y[i] = yn[i];
+          }
+        }
+        // the next outputs' factors, or the first ones again for the next rows
+        const bool more = o + ostep < a.d_out;
+        if (more || (b0 + 64 < r.all && ostep < a.d_out)) load_b(more ? o + ostep : o0);
+      }
+    }
+    __syncthreads();
   }
 }
 
 }  // namespace
 
 hipError_t launch_ad_shrink(const AdaptersArgs& a, int slots, const Launch& L) {
-  const int64_t tiles = (a.T + 15) / 16;
+  const bool step = a.T <= kAdStepTokens;
+  const int64_t tiles = (a.T + (step ? 127 : 63)) / (step ? 128 : 64);
   if (tiles == 0 || a.n == 0) return hipSuccess;
   const dim3 grid((unsigned)tiles, (unsigned)slots, (unsigned)a.nks), blk(AW * 64);
+#define TTQ_AD_SHRINK(NR)                                                         \
+  return step ? ext_launch(k_ad_shrink<2, NR, 1>, grid, blk, 0, L, a)             \
+              : ext_launch(k_ad_shrink<1, NR, NR <= 4 ? 4 : 2>, grid, blk, 0, L, a);
   switch ((a.rank + 15) / 16) {
-    case 1: return ext_launch(k_ad_shrink<1>, grid, blk, 0, L, a);
-    case 2: return ext_launch(k_ad_shrink<2>, grid, blk, 0, L, a);
-    case 3: return ext_launch(k_ad_shrink<3>, grid, blk, 0, L, a);
-    case 4: return ext_launch(k_ad_shrink<4>, grid, blk, 0, L, a);
-    case 5: case 6: return ext_launch(k_ad_shrink<6>, grid, blk, 0, L, a);
-    case 7: case 8: return ext_launch(k_ad_shrink<8>, grid, blk, 0, L, a);
+    case 1: TTQ_AD_SHRINK(1)
+    case 2: TTQ_AD_SHRINK(2)
+    case 3: case 4: TTQ_AD_SHRINK(4)
+    case 5: case 6: TTQ_AD_SHRINK(6)
+    case 7: case 8: TTQ_AD_SHRINK(8)
     default: return hipErrorInvalidValue;
   }
+#undef TTQ_AD_SHRINK
 }
 
 hipError_t launch_ad_expand(const AdaptersArgs& a, int slots, const Launch& L) {
-  const int64_t tiles = (a.T + 15) / 16;
-  const int64_t blocks = (a.d_out + AW * OT * 16 - 1) / (AW * OT * 16);
+  const bool step = a.T <= kAdStepTokens;
+  const int64_t tiles = (a.T + (step ? 127 : 63)) / (step ? 128 : 64);
+  const int64_t per = AW * OT * 16;
+  int64_t blocks = (a.d_out + per - 1) / per;
   if (tiles == 0 || blocks == 0) return hipSuccess;
+  // several blocks of outputs a workgroup, while that leaves enough of them for
+  // the chip (prompts: two per compute unit; decode steps, of whose workgroups
+  // some have no pair, eight)
+  blocks = std::max<int64_t>(1, std::min(blocks, step ? 2048 / a.T : 512 / tiles));
   const dim3 grid((unsigned)tiles, (unsigned)slots, (unsigned)blocks), blk(AW * 64);
+#define TTQ_AD_EXPAND(NK)                                                 \
+  return step ? ext_launch(k_ad_expand_step<NK>, grid, blk, 0, L, a)      \
+              : ext_launch(k_ad_expand<1, NK>, grid, blk, 0, L, a);
   switch ((a.rank + 31) / 32) {
-    case 0:  // no pairs at all
-    case 1: return ext_launch(k_ad_expand<1>, grid, blk, 0, L, a);
-    case 2: return ext_launch(k_ad_expand<2>, grid, blk, 0, L, a);
-    case 3: return ext_launch(k_ad_expand<3>, grid, blk, 0, L, a);
-    case 4: return ext_launch(k_ad_expand<4>, grid, blk, 0, L, a);
+    case 1: TTQ_AD_EXPAND(1)
+    case 2: TTQ_AD_EXPAND(2)
+    case 3: TTQ_AD_EXPAND(3)
+    case 4: TTQ_AD_EXPAND(4)
     default: return hipErrorInvalidValue;
   }
+#undef TTQ_AD_EXPAND
 }
 
 }  // namespace ttq

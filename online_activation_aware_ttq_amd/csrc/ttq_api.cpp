@@ -1178,19 +1178,22 @@ int validate_adapters(const ttq_params* prm, int64_t n) {
 }
 
 struct AdaptersPlan {
-  int slots = 1;      // distinct pairs of a 16-token tile with workgroups of their own
+  int slots = 1;      // distinct pairs of a tile with workgroups of their own
   int nks = 1;        // channel ranges of the first product
   int64_t kc = 0;
   size_t total = 0;
 };
 
-AdaptersPlan make_adapters_plan(const ttq_params* prm) {
+AdaptersPlan make_adapters_plan(const ttq_params* prm, int64_t n) {
   AdaptersPlan P;
-  const int64_t tiles = std::max<int64_t>(1, (prm->T + 15) / 16);
-  P.slots = (int)std::max<int64_t>(1, std::min({int64_t(16), prm->T, 1024 / tiles}));
+  const bool step = prm->T <= kAdStepTokens;
+  const int64_t tiles = step ? 1 : (prm->T + 63) / 64;
+  // a decode step: a workgroup per row, those of a pair's first row work; tiles
+  // of prompts, which have few pairs: one, and more where there are few tiles
+  P.slots = (int)std::max<int64_t>(1, step ? prm->T : std::min<int64_t>({4, n, 64 / tiles}));
   // ranges of at least 512 channels, about two workgroups per compute unit
-  int64_t nks = std::min((prm->d + 511) / 512, std::max<int64_t>(1, 512 / (tiles * P.slots)));
-  nks = std::min<int64_t>(nks, 8);
+  int64_t nks = std::min((prm->d + 511) / 512, std::max<int64_t>(1, (step ? 1024 : 512) / (tiles * P.slots)));
+  nks = std::min<int64_t>(nks, 4);
   P.kc = (prm->d + nks * 128 - 1) / (nks * 128) * 128;
   P.nks = (int)((prm->d + P.kc - 1) / P.kc);
   P.total = sizeof(float) * P.nks * prm->T * prm->rank;
@@ -1211,7 +1214,7 @@ int adapters_impl(const ttq_params* prm, int64_t n, const void* X,
       misaligned(scale, 4) || misaligned(index, 4) || misaligned(base, 4) ||
       misaligned(Y, 4) || misaligned(workspace, 256))
     return TTQ_EALIGN;
-  const AdaptersPlan P = make_adapters_plan(prm);
+  const AdaptersPlan P = make_adapters_plan(prm, n);
   if (!workspace) return TTQ_ENULL;
   if (workspace_bytes < P.total) return TTQ_EWORKSPACE;
   if (inject_hip_error()) return TTQ_EHIP;
@@ -1594,7 +1597,7 @@ int ttq_adapters_workspace_bytes(const ttq_params* prm, int64_t n_adapters,
   if (!bytes) return TTQ_ENULL;
   const int st = validate_adapters(prm, n_adapters);
   if (st != TTQ_OK) return st;
-  *bytes = make_adapters_plan(prm).total;
+  *bytes = make_adapters_plan(prm, n_adapters).total;
   return TTQ_OK;
 }
 

@@ -697,9 +697,12 @@ struct AdaptersArgs {
   float* S;               // [nks][T][rank] partial sums of A_e x
   int64_t T, n, d, d_out, rank;
   int64_t kc;             // channels per range, a multiple of 32
-  int nks;                // ranges
+  int nks;                // ranges, at most 4
   int vec;                // 16-byte accesses to base and Y
 };
+// batches of up to this many rows are one tile (decode steps), longer ones go
+// in tiles of 64
+constexpr int64_t kAdStepTokens = 128;
 // slots: distinct pairs of a tile that get workgroups of their own
 hipError_t launch_ad_shrink(const AdaptersArgs& a, int slots, const Launch& L);
 hipError_t launch_ad_expand(const AdaptersArgs& a, int slots, const Launch& L);

@@ -57,6 +57,14 @@ def test_adapter_arguments():
     assert adapters(p, ws_bytes=need - 1) == ttq.TTQ_EWORKSPACE
 
 
+def test_adapters_workspace_of_every_size():
+    for T in (0, 1, 127, 128, 129, 4096, 100000):
+        for n in (0, 1, 1000):
+            for d in (8, 512, 1 << 17):
+                need = ttq.ttq_adapters_workspace_bytes(aprm(T=T, d=d), n)
+                assert (need == 0) == (T == 0) and need <= 8 * T * 16 * 4
+
+
 def test_adapters_nothing_to_do():
     nul = dict(X=None, A=None, B=None, index=None, Y=None, ws=None)
     assert adapters(aprm(T=0), **nul) == ttq.TTQ_OK
