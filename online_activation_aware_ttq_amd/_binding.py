@@ -574,25 +574,78 @@ def _elem_type(t, name) -> int:
                     f"torch.float32, got {dt if dt is not None else type(t)}")
 
 
+# A decode step makes many small calls, so these entry points keep their host
+# time short: what a shape implies (parameter block, expected types and shapes,
+# workspace need) is worked out once per shape, and a call only compares.
+_PLANS = {}
+
+
+def _plan(key, make):
+    plan = _PLANS.get(key)
+    if plan is None:
+        if len(_PLANS) > 4096:
+            _PLANS.clear()
+        plan = _PLANS[key] = make()
+    return plan
+
+
+def _expect(tensors, want, dev):
+    """Raise unless every tensor (None: absent) is as its (name, dtype, shape)
+    says, contiguous and on ``dev``; returns their addresses."""
+    di = dev.index
+    ptrs = []
+    for t, (name, dtype, shape) in zip(tensors, want):
+        if t is None:
+            ptrs.append(None)
+            continue
+        try:
+            ok = (t.dtype is dtype and t.shape == shape and t.get_device() == di
+                  and t.is_contiguous())
+        except AttributeError:
+            ok = False
+        if not ok:
+            _check(t, name, dtype, shape, dev)
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+_several = None  # more than one device
+
+
 def _enqueue(where, dev, fn, *args):
     """Call a library entry point with the tensors' device current."""
+    global _several
     import torch
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        st = fn(*args)
-    else:
+    if _several is None:
+        _several = torch.cuda.device_count() > 1
+    if _several and dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             st = fn(*args)
+    else:
+        st = fn(*args)
     if st != TTQ_OK:
         raise TTQError(st, where)
 
 
-def _step_workspace(dev, stream, need_key, query):
-    """_workspace, but a buffer of its own for a call that is being captured:
-    it then lives in the graph's memory, and no other graph or stream has it."""
+def _gpu(t, name):
+    """Device of ``t``, which has to be a GPU tensor."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    return dev
+
+
+def _step_workspace(dev, stream, need):
+    """The stream's kept buffer (see _workspace), but one of its own for a call
+    that is being captured: it then lives in the graph's memory, and no other
+    graph or stream has it."""
     import torch
-    if torch.cuda.is_current_stream_capturing():
-        return torch.empty(max(int(query()), 256), dtype=torch.uint8, device=dev)
-    return _workspace(dev, stream, need_key, query)
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    buf = _SCRATCH.get((dev.index, stream))
+    if buf is not None and buf.numel() >= need:
+        return buf
+    return _workspace(dev, stream, None, lambda: need)
 
 
 def ttq_adapters_workspace_bytes(prm: ttq_params, n_adapters: int) -> int:
@@ -618,27 +671,27 @@ def ttq_adapters(X, A, B, index, *, scale=None, base=None, Y=None,
     T, d = X.shape
     n, r, _ = A.shape
     d_out = B.shape[1]
-    dev = X.device
-    if dev.type != "cuda":
-        raise ValueError("X must be a GPU tensor")
-    _check(X, "X", torch.bfloat16, (T, d), dev)
-    _check(A, "A", torch.bfloat16, (n, r, d), dev)
-    _check(B, "B", torch.bfloat16, (n, d_out, r), dev)
-    _check(index, "index", torch.int32, (T,), dev)
-    _check(scale, "scale", torch.float32, (n,), dev)
-    _check(base, "base", torch.float32, (T, d_out), dev)
+    dev = _gpu(X, "X")
+
+    def make():
+        bf, f32 = torch.bfloat16, torch.float32
+        prm = make_params(d=d, d_out=d_out, T=T, rank=r, bits=4, group=32, p=2.0,
+                          lam=0.0, alpha=0.0)
+        return prm, max(256, ttq_adapters_workspace_bytes(prm, n)), (
+            ("X", bf, (T, d)), ("A", bf, (n, r, d)), ("B", bf, (n, d_out, r)),
+            ("scale", f32, (n,)), ("index", torch.int32, (T,)),
+            ("base", f32, (T, d_out)), ("Y", f32, (T, d_out)))
+
+    prm, need, want = _plan(("adapters", T, d, n, r, d_out), make)
     if Y is None:
         Y = torch.empty((T, d_out), dtype=torch.float32, device=dev)
-    _check(Y, "Y", torch.float32, (T, d_out), dev)
-    prm, key = _params(d, d_out, T, r, 4, 32, 2.0, 0.0, 0.0, 0, "asym")
+    ptrs = _expect((X, A, B, scale, index, base, Y), want, dev)
     if stream is None:
         stream = _current_stream(dev)
     if workspace is None:
-        workspace = _step_workspace(dev, stream, ("adapters", key, n),
-                                    lambda: ttq_adapters_workspace_bytes(prm, n))
+        workspace = _step_workspace(dev, stream, need)
     _enqueue("ttq_adapters", dev, load_library().ttq_adapters,
-             ctypes.byref(prm), n, _ptr(X), _ptr(A), _ptr(B), _ptr(scale),
-             _ptr(index), _ptr(base), _ptr(Y), _ptr(workspace),
+             ctypes.byref(prm), n, *ptrs, workspace.data_ptr(),
              workspace.numel(), stream)
     return Y
 
@@ -660,26 +713,6 @@ def ttq_moe_workspace_bytes(prm: ttq_moe_params) -> int:
     return int(out.value)
 
 
-_MOE = {}
-
-
-def _moe_params(T, d, ff, E, k, bits, group, renormalize, qformat):
-    """The parameter block and packed row bytes of one shape, kept (bounded)."""
-    key = (T, d, ff, E, k, bits, group, bool(renormalize), qformat)
-    got = _MOE.get(key)
-    if got is None:
-        if len(_MOE) > 4096:
-            _MOE.clear()
-            _NEED.clear()
-        prm = make_moe_params(T=T, d=d, ff=ff, experts=E, top_k=k, bits=bits,
-                              group=group, renormalize=renormalize,
-                              qformat=qformat)
-        ttq_moe_workspace_bytes(prm)  # raises for what the library refuses
-        got = _MOE[key] = (prm, key, _row_bytes(d, bits, group),
-                           _row_bytes(ff, bits, group))
-    return got
-
-
 def ttq_moe(X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv, dn_codes,
             dn_scales, dn_mins, dn_dhalf_inv, *, top_k: int, bits: int,
             group: int, renormalize: bool = True, Y=None, ids_out=None,
@@ -693,51 +726,46 @@ def ttq_moe(X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv, dn_codes,
     import torch
     T, d = X.shape
     E, ff = dn_dhalf_inv.shape
-    dev = X.device
-    if dev.type != "cuda":
-        raise ValueError("X must be a GPU tensor")
-    prm, key, rb, rf = _moe_params(T, d, ff, E, top_k, bits, group,
-                                   renormalize, qformat)
-    _check(X, "X", torch.bfloat16, (T, d), dev)
-    _check(router, "router", torch.bfloat16, (E, d), dev)
-    _check(gu_codes, "gu_codes", torch.uint8, (E, 2 * ff, rb), dev)
-    _check(gu_scales, "gu_scales", torch.float32, (E, 2 * ff, d // group), dev)
-    _check(gu_mins, "gu_mins", torch.float32, (E, 2 * ff, d // group), dev)
-    _check(gu_dhalf_inv, "gu_dhalf_inv", torch.float32, (E, d), dev)
-    _check(dn_codes, "dn_codes", torch.uint8, (E, d, rf), dev)
-    _check(dn_scales, "dn_scales", torch.float32, (E, d, ff // group), dev)
-    _check(dn_mins, "dn_mins", torch.float32, (E, d, ff // group), dev)
-    _check(dn_dhalf_inv, "dn_dhalf_inv", torch.float32, (E, ff), dev)
+    dev = _gpu(X, "X")
+
+    def make():
+        prm = make_moe_params(T=T, d=d, ff=ff, experts=E, top_k=top_k, bits=bits,
+                              group=group, renormalize=renormalize,
+                              qformat=qformat)
+        need = max(256, ttq_moe_workspace_bytes(prm))
+        bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+        rb, rf = (_row_bytes(c, bits, group) for c in (d, ff))
+        gu, dn = (E, 2 * ff, d // group), (E, d, ff // group)
+        return prm, need, (
+            ("X", bf, (T, d)), ("router", bf, (E, d)),
+            ("gu_codes", u8, (E, 2 * ff, rb)), ("gu_scales", f32, gu),
+            ("gu_mins", f32, gu), ("gu_dhalf_inv", f32, (E, d)),
+            ("dn_codes", u8, (E, d, rf)), ("dn_scales", f32, dn),
+            ("dn_mins", f32, dn), ("dn_dhalf_inv", f32, (E, ff)),
+            ("Y", f32, (T, d)), ("ids_out", torch.int32, (T, top_k)),
+            ("weights_out", f32, (T, top_k)))
+
+    prm, need, want = _plan(("moe", T, d, ff, E, top_k, bits, group,
+                             bool(renormalize), qformat), make)
     if Y is None:
         Y = torch.empty((T, d), dtype=torch.float32, device=dev)
-    _check(Y, "Y", torch.float32, (T, d), dev)
-    _check(ids_out, "ids_out", torch.int32, (T, top_k), dev)
-    _check(weights_out, "weights_out", torch.float32, (T, top_k), dev)
+    ptrs = _expect((X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv,
+                    dn_codes, dn_scales, dn_mins, dn_dhalf_inv, Y, ids_out,
+                    weights_out), want, dev)
     if stream is None:
         stream = _current_stream(dev)
     if workspace is None:
-        workspace = _step_workspace(dev, stream, ("moe", key),
-                                    lambda: ttq_moe_workspace_bytes(prm))
-    _enqueue("ttq_moe", dev, load_library().ttq_moe, ctypes.byref(prm),
-             _ptr(X), _ptr(router), _ptr(gu_codes), _ptr(gu_scales),
-             _ptr(gu_mins), _ptr(gu_dhalf_inv), _ptr(dn_codes),
-             _ptr(dn_scales), _ptr(dn_mins), _ptr(dn_dhalf_inv), _ptr(Y),
-             _ptr(ids_out), _ptr(weights_out), _ptr(workspace),
-             workspace.numel(), stream)
+        workspace = _step_workspace(dev, stream, need)
+    _enqueue("ttq_moe", dev, load_library().ttq_moe, ctypes.byref(prm), *ptrs,
+             workspace.data_ptr(), workspace.numel(), stream)
     return Y
 
 
-def _check_cache(codes, scales, mins, d, bits, group):
-    import torch
-    n_slots, dev = codes.shape[0], codes.device
-    if dev.type != "cuda":
-        raise ValueError("codes must be a GPU tensor")
-    rb = _row_bytes(d, bits, group)
-    G = d // group
-    _check(codes, "codes", torch.uint8, (n_slots, rb), dev)
-    _check(scales, "scales", torch.float32, (n_slots, G), dev)
-    _check(mins, "mins", torch.float32, (n_slots, G), dev)
-    return n_slots, dev
+def _cache_params(T, d, bits, group, qformat):
+    """Parameter block and packed row bytes of a cache of d channels."""
+    prm = make_params(d=d, d_out=1, T=T, bits=bits, group=group, p=2.0, lam=0.0,
+                      alpha=0.0, qformat=qformat)
+    return prm, ttq_packed_row_bytes(prm)
 
 
 def ttq_cache_write(X, slots, codes, scales, mins, *, bits: int, group: int,
@@ -752,21 +780,31 @@ def ttq_cache_write(X, slots, codes, scales, mins, *, bits: int, group: int,
     """
     import torch
     T, d = X.shape
-    n_slots, dev = _check_cache(codes, scales, mins, d, bits, group)
+    n_slots = codes.shape[0]
+    dev = _gpu(codes, "codes")
     x_type = _elem_type(X, "X")
     if X.device != dev:
         raise ValueError(f"X must be on {dev}, got {X.device}")
     if d > 1 and X.stride(1) != 1:
         raise ValueError("X must have contiguous rows")
     ldx = X.stride(0) if T > 1 else d
-    _check(slots, "slots", torch.int64, (T,), dev)
-    _check(dhalf, "dhalf", torch.float32, (d,), dev)
-    prm, _ = _params(d, 1, T, 0, bits, group, 2.0, 0.0, 0.0, 0, qformat)
+
+    def make():
+        f32 = torch.float32
+        prm, rb = _cache_params(T, d, bits, group, qformat)
+        return prm, (
+            ("dhalf", f32, (d,)), ("slots", torch.int64, (T,)),
+            ("codes", torch.uint8, (n_slots, rb)),
+            ("scales", f32, (n_slots, d // group)),
+            ("mins", f32, (n_slots, d // group)))
+
+    prm, want = _plan(("write", T, d, n_slots, bits, group, qformat), make)
+    ptrs = _expect((dhalf, slots, codes, scales, mins), want, dev)
     if stream is None:
         stream = _current_stream(dev)
     _enqueue("ttq_cache_write", dev, load_library().ttq_cache_write,
-             ctypes.byref(prm), n_slots, x_type, _ptr(X), ldx, _ptr(dhalf),
-             _ptr(slots), _ptr(codes), _ptr(scales), _ptr(mins), stream)
+             ctypes.byref(prm), n_slots, x_type, X.data_ptr(), ldx, *ptrs,
+             stream)
 
 
 def ttq_cache_read(codes, scales, mins, pages, lens, *, bits: int, group: int,
@@ -788,19 +826,29 @@ def ttq_cache_read(codes, scales, mins, pages, lens, *, bits: int, group: int,
         out = torch.zeros((n_seq, T, d), dtype=dtype or torch.bfloat16,
                           device=codes.device)
     _, T, d = out.shape
-    n_slots, dev = _check_cache(codes, scales, mins, d, bits, group)
+    n_slots = codes.shape[0]
+    dev = _gpu(codes, "codes")
     out_type = _elem_type(out, "out")
-    _check(out, "out", out.dtype, (n_seq, T, d), dev)
-    _check(pages, "pages", torch.int32, (n_seq, max_pages), dev)
-    _check(lens, "lens", torch.int32, (n_seq,), dev)
-    _check(dhalf_inv, "dhalf_inv", torch.float32, (d,), dev)
-    prm, _ = _params(d, 1, T, 0, bits, group, 2.0, 0.0, 0.0, 0, qformat)
+
+    def make():
+        f32, i32 = torch.float32, torch.int32
+        prm, rb = _cache_params(T, d, bits, group, qformat)
+        return prm, (
+            ("pages", i32, (n_seq, max_pages)), ("lens", i32, (n_seq,)),
+            ("codes", torch.uint8, (n_slots, rb)),
+            ("scales", f32, (n_slots, d // group)),
+            ("mins", f32, (n_slots, d // group)), ("dhalf_inv", f32, (d,)),
+            ("out", (torch.bfloat16, f32)[out_type], (n_seq, T, d)))
+
+    prm, want = _plan(("read", T, d, n_slots, n_seq, max_pages, out_type, bits,
+                       group, qformat), make)
+    *ptrs, po = _expect((pages, lens, codes, scales, mins, dhalf_inv, out), want,
+                        dev)
     if stream is None:
         stream = _current_stream(dev)
     _enqueue("ttq_cache_read", dev, load_library().ttq_cache_read,
-             ctypes.byref(prm), n_slots, n_seq, max_pages, page_tokens,
-             _ptr(pages), _ptr(lens), _ptr(codes), _ptr(scales), _ptr(mins),
-             _ptr(dhalf_inv), out_type, _ptr(out), stream)
+             ctypes.byref(prm), n_slots, n_seq, max_pages, page_tokens, *ptrs,
+             out_type, po, stream)
     return out
 
 

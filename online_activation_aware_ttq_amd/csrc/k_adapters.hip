@@ -359,6 +359,143 @@ __global__ __launch_bounds__(AW * 64, NK <= 2 ? 2 : 1) void k_ad_expand_step(Ada
   }
 }
 
+// Both products of a small decode step in one launch: workgroup (pair, outputs)
+// forms its pair's S itself, from A_e in L2.  That costs every workgroup the
+// whole of A_e, and saves a launch and the way of S through memory; see
+// ad_one_launch for where it pays.
+constexpr int SW = 8;        // waves
+constexpr int ST = 2;        // turns of 16 * OT outputs a wave
+
+template <int NK>
+__global__ __launch_bounds__(SW * 64) void k_ad_step(AdaptersArgs a) {
+  constexpr int NR = 2 * NK, PITCH = 32 * NK + 4;
+  __shared__ float part[SW][16][PITCH];
+  __shared__ u32x4 planes[NK][3][64];
+  __shared__ uint8_t list[128];
+  const int tid = threadIdx.x, l = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = l & 15, q = l >> 4;
+  TilePairs<2> r(a, 0);
+  if (!r.next(list, true)) return;  // uniform over the workgroup
+  const bool pair = r.e >= 0;
+  const __amdgpu_buffer_rsrc_t br =
+      make_rsrc(a.B + (int64_t)max(r.e, 0) * a.d_out * a.rank,
+                pair ? (uint32_t)(a.d_out * a.rank * 2) : 0u);
+  const __amdgpu_buffer_rsrc_t ar =
+      make_rsrc(a.A + (int64_t)max(r.e, 0) * a.rank * a.d, pair ? (uint32_t)(a.rank * a.d * 2) : 0u);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.X, (uint32_t)(a.T * a.d * 2));
+  const int64_t o0 = ((int64_t)blockIdx.z * SW + w) * (ST * OT * 16);
+  u32x4 bv[ST * OT][NK];
+#pragma unroll
+  for (int i = 0; i < ST * OT; ++i)
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      const int64_t row = o0 + i * 16 + lr;
+      const int col = k * 32 + q * 8;
+      bv[i][k] = buf_load16(br, row < a.d_out && col < a.rank
+                                    ? (uint32_t)((row * a.rank + col) * 2) : kOutOfRange, 0);
+    }
+  const float c = !pair ? 0.f : a.scale ? a.scale[r.e] : 1.f;
+  for (int b0 = 0; b0 < r.all; b0 += 16) {
+    const int at = b0 + lr;
+    const bool mine = at < r.all, live = at < r.n;
+    const int64_t t = list[min(at, r.all - 1)];
+    // S: the waves take 32-channel steps in turn, four steps' loads at a time
+    const uint32_t xoff = live ? (uint32_t)(t * a.d * 2) : kOutOfRange;
+    f32x4 acc[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int64_t k = w * 32; k < a.d; k += 4 * SW * 32) {
+      u32x4 xv[4], av[4][NR];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t kk = k + u * (SW * 32) + q * 8;
+        const uint32_t cc = kk < a.d ? (uint32_t)kk * 2 : kOutOfRange;
+        xv[u] = buf_load16(xr, min(xoff + cc, kOutOfRange), 0);
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+          av[u][n] = buf_load16(ar, min((uint32_t)((n * 16 + lr) * a.d * 2) + cc, kOutOfRange), 0);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv[u]),
+                                                          __builtin_bit_cast(bf16x8, av[u][n]),
+                                                          acc[n], 0, 0, 0);
+    }
+    // lane l of a 16 x 16 product holds column l & 15 and rows 4 (l >> 4) + i
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[w][q * 4 + i][n * 16 + lr] = acc[n][i];
+    // base is on its way while the waves meet
+    const float* bp = a.base ? a.base + t * a.d_out + q * 4 : nullptr;
+    float* yp = a.Y + t * a.d_out + q * 4;
+    f32x4 y[ST * OT];
+#pragma unroll
+    for (int i = 0; i < ST * OT; ++i) {
+      y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int64_t col = o0 + i * 16 + q * 4;
+      if (!bp || !mine) continue;
+      if (a.vec) {
+        if (col < a.d_out) y[i] = *(const f32x4*)(bp + o0 + i * 16);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (col + x < a.d_out) y[i][x] = bp[o0 + i * 16 + x];
+      }
+    }
+    __syncthreads();
+    if (tid < NK * 128) {
+      const int sr = tid / (NK * 8), sc = tid % (NK * 8) * 4;
+      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+      // (columns past the rank: the zeros read for A_e times an infinite x)
+      if (sc < a.rank) {
+#pragma unroll
+        for (int ww = 0; ww < SW; ++ww) s += *(const f32x4*)&part[ww][sr][sc];
+      }
+      const float s8[8] = {s.x, s.y, s.z, s.w, 0.f, 0.f, 0.f, 0.f};
+      u32x4 pl[3];
+      split24<true>(s8, pl);
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+        reinterpret_cast<u32x2*>(&planes[sc / 32][x][sc % 32 / 8 * 16 + sr])[sc / 4 % 2] =
+            u32x2{pl[x].x, pl[x].y};
+    }
+    __syncthreads();
+    f32x4 d[ST * OT];
+#pragma unroll
+    for (int i = 0; i < ST * OT; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        const u32x4 pl = planes[k][x][l];
+#pragma unroll
+        for (int i = 0; i < ST * OT; ++i)
+          d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bv[i][k]),
+                                                        __builtin_bit_cast(bf16x8, pl), d[i], 0, 0, 0);
+      }
+    if (!mine) continue;
+#pragma unroll
+    for (int i = 0; i < ST * OT; ++i) {
+      const int64_t col = o0 + i * 16 + q * 4;
+      if (live) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) y[i][x] = fmaf(c, d[i][x], y[i][x]);
+      }
+      if (a.vec) {
+        if (col < a.d_out) *(f32x4*)(yp + o0 + i * 16) = y[i];
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (col + x < a.d_out) yp[o0 + i * 16 + x] = y[i][x];
+      }
+    }
+  }
+}
+
 // Y of prompts: workgroup (tile, its pairs, outputs).  The planes of up to 64 gathered rows' S go
 // to LDS, once for the workgroup's four waves, which take 16 * OT outputs at a
 // time.
@@ -485,6 +622,16 @@ __global__ __launch_bounds__(AW * 64) void k_ad_expand(AdaptersArgs a) {
 }
 
 }  // namespace
+
+hipError_t launch_ad_step(const AdaptersArgs& a, const Launch& L) {
+  const int64_t per = SW * ST * OT * 16, blocks = (a.d_out + per - 1) / per;
+  const dim3 grid(1, (unsigned)a.T, (unsigned)blocks), blk(SW * 64);
+  switch ((a.rank + 31) / 32) {
+    case 1: return ext_launch(k_ad_step<1>, grid, blk, 0, L, a);
+    case 2: return ext_launch(k_ad_step<2>, grid, blk, 0, L, a);
+    default: return hipErrorInvalidValue;
+  }
+}
 
 hipError_t launch_ad_shrink(const AdaptersArgs& a, int slots, const Launch& L) {
   const bool step = a.T <= kAdStepTokens;

@@ -54,8 +54,7 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs a) {
   const int64_t nchunk = (a.C + 511) / 512;
   const int64_t row = wid / nchunk;
   if (row >= a.T) return;  // uniform over the wave
-  const int64_t slot = a.slots[row];
-  if (slot < 0 || slot >= a.n_slots) return;
+  const int64_t slot = a.slots[row];  // (looked at once x is on its way)
   const int64_t c0 = (wid % nchunk) * 512 + l * 8;
   const bool live = c0 < a.C;  // C is a multiple of GS: whole groups
 
@@ -79,6 +78,7 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs a) {
       u[4] *= h1.x; u[5] *= h1.y; u[6] *= h1.z; u[7] *= h1.w;
     }
   }
+  if (slot < 0 || slot >= a.n_slots) return;  // uniform
   float mn = u[0], mx = u[0];
   int bad = 0;
 #pragma unroll
@@ -121,10 +121,18 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs a) {
 // One wave reads 512 channels of CR consecutive rows of one sequence, 8 a
 // lane.  Rows at or past the sequence's length, and rows whose page lies
 // outside the cache, are left as they were.
-constexpr int CR = 4;
-
-template <int CB, bool F8, bool OF32>
+//
+// NT: the result is written past the last-level cache.  Where it is far larger
+// than that cache, keeping it out gives the codes room (8 sequences of up to
+// 4096 rows of 8192 channels, 4-bit -> bf16: 125 -> 111 us, 4.4 TB/s, where a
+// plain copy reaches 4.8); where it fits, whoever reads it next finds it there
+// (2047 rows of 8192 float32: 18 us written through the cache, 30 past it).
+template <int CB, bool F8, bool OF32, int CR, bool NT>
 __global__ __launch_bounds__(256) void k_cache_read(CacheReadArgs a) {
+  auto store = [](auto v, auto* at) {
+    if constexpr (NT) __builtin_nontemporal_store(v, at);
+    else *at = v;
+  };
   const int l = threadIdx.x & 63;
   const int64_t nchunk = (a.C + 511) / 512;
   const int64_t wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -189,12 +197,12 @@ __global__ __launch_bounds__(256) void k_cache_read(CacheReadArgs a) {
     const int64_t o = (seq * a.T + t0 + i) * a.C + c0;
     if constexpr (OF32) {
       float* out = static_cast<float*>(a.out) + o;
-      *(f32x4*)out = f32x4{v[0], v[1], v[2], v[3]};
-      *(f32x4*)(out + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4*)out);
+      store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4*)(out + 4));
     } else {
-      *(u32x4*)(static_cast<bf16_t*>(a.out) + o) =
-          u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                pack_bf16(v[6], v[7])};
+      store(u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                  pack_bf16(v[6], v[7])},
+            (u32x4*)(static_cast<bf16_t*>(a.out) + o));
     }
   }
 }
@@ -225,12 +233,20 @@ hipError_t launch_cache_write(const CacheWriteArgs& a, int group, const Launch& 
 }
 
 hipError_t launch_cache_read(const CacheReadArgs& a, int cb, const Launch& L) {
-  const int64_t waves = (a.T + CR - 1) / CR * ((a.C + 511) / 512);
-  if (waves == 0 || a.n_seq == 0) return hipSuccess;
-  const dim3 grid((unsigned)((waves + 3) / 4), (unsigned)a.n_seq), blk(256);
-#define TTQ_CR(CBV, F8)                                                              \
-  return a.out_f32 ? ext_launch(k_cache_read<CBV, F8, true>, grid, blk, 0, L, a)     \
-                   : ext_launch(k_cache_read<CBV, F8, false>, grid, blk, 0, L, a);
+  const int64_t chunks = (a.C + 511) / 512;
+  if (a.T == 0 || a.n_seq == 0) return hipSuccess;
+  // more than the last-level cache holds (256 MiB), by the room for the rows;
+  // there a wave's four rows in flight also pay (133 us with two), while short
+  // reads want the most waves (33 rows of 1024: 3.5 us with four, 2.7 with one)
+  const bool nt = a.n_seq * a.T * a.C > (int64_t(256) << 20) / (a.out_f32 ? 4 : 2);
+  auto go = [&](auto kernel, int rows) {
+    return ext_launch(kernel, dim3((unsigned)(((a.T + rows - 1) / rows * chunks + 3) / 4),
+                                   (unsigned)a.n_seq), dim3(256), 0, L, a);
+  };
+#define TTQ_CR(CBV, F8)                                                                       \
+  if (a.out_f32)                                                                              \
+    return nt ? go(k_cache_read<CBV, F8, true, 4, true>, 4) : go(k_cache_read<CBV, F8, true, 1, false>, 1); \
+  return nt ? go(k_cache_read<CBV, F8, false, 4, true>, 4) : go(k_cache_read<CBV, F8, false, 1, false>, 1);
   if (a.qf == QF_FP8) {
     if (cb != 8) return hipErrorInvalidValue;
     TTQ_CR(8, true)

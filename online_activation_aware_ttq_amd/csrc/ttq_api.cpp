@@ -248,7 +248,7 @@ const char* kKernelNames[K_NUM_KINDS] = {
     "qgemv", "dequant", "qfused", "lowrank_zsum", "gemm_quant", "seg_copy",
     "pca_skinny", "pca_psum", "pca_chol", "pca_trsm", "pca_residual",
     "pca_complete", "stream_read", "cache_write", "cache_read",
-    "adapters_shrink", "adapters_expand", "moe_score", "moe_route", "moe_up", "moe_down", "moe_sum"};
+    "adapters_step", "adapters_shrink", "adapters_expand", "moe_score", "moe_route", "moe_up", "moe_down", "moe_sum"};
 
 hipEvent_t take_event() {
   if (!g_timing.pool.empty()) {
@@ -1181,11 +1181,14 @@ struct AdaptersPlan {
   int slots = 1;      // distinct pairs of a tile with workgroups of their own
   int nks = 1;        // channel ranges of the first product
   int64_t kc = 0;
+  bool one = false;   // both products in one launch
   size_t total = 0;
 };
 
 AdaptersPlan make_adapters_plan(const ttq_params* prm, int64_t n) {
   AdaptersPlan P;
+  P.one = ad_one_launch(prm->T, prm->d, prm->d_out, prm->rank);
+  if (P.one) return P;
   const bool step = prm->T <= kAdStepTokens;
   const int64_t tiles = step ? 1 : (prm->T + 63) / 64;
   // a decode step: a workgroup per row, those of a pair's first row work; tiles
@@ -1215,7 +1218,7 @@ int adapters_impl(const ttq_params* prm, int64_t n, const void* X,
       misaligned(Y, 4) || misaligned(workspace, 256))
     return TTQ_EALIGN;
   const AdaptersPlan P = make_adapters_plan(prm, n);
-  if (!workspace) return TTQ_ENULL;
+  if (P.total > 0 && !workspace) return TTQ_ENULL;
   if (workspace_bytes < P.total) return TTQ_EWORKSPACE;
   if (inject_hip_error()) return TTQ_EHIP;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -1228,6 +1231,8 @@ int adapters_impl(const ttq_params* prm, int64_t n, const void* X,
   a.T = T; a.n = n; a.d = prm->d; a.d_out = dout; a.rank = prm->rank;
   a.kc = P.kc; a.nks = P.nks;
   a.vec = dout % 4 == 0 && !misaligned(Y, 16) && !misaligned(base, 16);
+  if (P.one)
+    return run(K_AD_STEP, s, [&](const Launch& L) { return launch_ad_step(a, L); });
   if (n > 0) {
     st = run(K_AD_SHRINK, s, [&](const Launch& L) { return launch_ad_shrink(a, P.slots, L); });
     if (st != TTQ_OK) return st;

@@ -42,6 +42,7 @@ enum KernelKind {
   K_STREAM_READ,       // plain read of device memory (measurement ceiling)
   K_CACHE_WRITE,       // rows quantized into a cache
   K_CACHE_READ,        // rows of a cache read back
+  K_AD_STEP,           // adapters: both products of a small decode step
   K_AD_SHRINK,         // adapters: A_e x per row
   K_AD_EXPAND,         // adapters: base + c_e B_e (A_e x)
   K_MOE_SCORE,         // experts: scores
@@ -703,6 +704,16 @@ struct AdaptersArgs {
 // batches of up to this many rows are one tile (decode steps), longer ones go
 // in tiles of 64
 constexpr int64_t kAdStepTokens = 128;
+// Decode steps small enough for one launch, each workgroup (512 outputs) reading
+// all of its pair's A: at most 64 KiB, 16 MiB in all.  (One row of rank 8 on
+// 512 -> 512: 8.5 us a call, 10.9 in two launches; eight rows of rank 32 on
+// 4096 -> 4096, 256 KiB each: a kernel of 12.1 us, against 5.1 + 4.4 us.)
+inline bool ad_one_launch(int64_t T, int64_t d, int64_t d_out, int64_t rank) {
+  const int64_t bytes = rank * d * 2;
+  return T <= kAdStepTokens && rank <= 64 && bytes <= (64 << 10) &&
+         T * ((d_out + 511) / 512) * bytes <= (16 << 20);
+}
+hipError_t launch_ad_step(const AdaptersArgs& a, const Launch& L);
 // slots: distinct pairs of a tile that get workgroups of their own
 hipError_t launch_ad_shrink(const AdaptersArgs& a, int slots, const Launch& L);
 hipError_t launch_ad_expand(const AdaptersArgs& a, int slots, const Launch& L);

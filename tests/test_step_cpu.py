@@ -15,7 +15,7 @@ def lib():
 
 # ---------------------------------------------------------------- adapters
 def aprm(**kw):
-    base = dict(d=256, d_out=100, T=5, rank=16, bits=0, group=0, p=0.0, lam=0.0, alpha=0.0)
+    base = dict(d=256, d_out=100, T=200, rank=16, bits=0, group=0, p=0.0, lam=0.0, alpha=0.0)
     base.update(kw)
     return ttq.make_params(**base)
 
@@ -62,7 +62,9 @@ def test_adapters_workspace_of_every_size():
         for n in (0, 1, 1000):
             for d in (8, 512, 1 << 17):
                 need = ttq.ttq_adapters_workspace_bytes(aprm(T=T, d=d), n)
-                assert (need == 0) == (T == 0) and need <= 8 * T * 16 * 4
+                # none for nothing, nor for steps small enough for one launch
+                assert need <= 4 * T * 16 * 4
+                assert (need > 0) == (T > 128 or (T > 0 and d == 1 << 17))
 
 
 def test_adapters_nothing_to_do():
