@@ -166,8 +166,9 @@ __global__ __launch_bounds__(1024) void k_moe_route(MoeArgs a) {
 // pattern, is code * 2^-9 (0..7 are its subnormals, 8..15 its first binade),
 // so the E4M3 conversion with a scale of 2^9 expands two codes at once.  The
 // pairs come in the order of the bytes that hold the codes; see code_order.
-template <int CB, bool F8>
-__device__ __forceinline__ u32x4 codes_bf16(u32x2 raw) {
+template <int CB, int GS, bool F8>
+__device__ __forceinline__ u32x4 codes_bf16(const GroupCodes<CB, GS>& gc, int k) {
+  const u32x2 raw = CB == 2 ? u32x2{gc.w[k / 2], 0u} : step_codes<CB, GS>(gc, k);
   auto pair = [](unsigned w, bool hi, float sc) {
     return hi ? __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, sc, true))
               : __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, sc, false));
@@ -192,11 +193,12 @@ __device__ __forceinline__ u32x4 codes_bf16(u32x2 raw) {
     return u32x4{pair(lo, false, 512.f), pair(lo, true, 512.f), pair(hi, false, 512.f),
                  pair(hi, true, 512.f)};
   } else if constexpr (CB == 2) {
-    // codes 0 4 | 1 5 | 2 6 | 3 7 (the two bytes of the 16 bits)
-    const unsigned a = raw.x & 0x0303u, b = (raw.x >> 2) & 0x0303u;
-    const unsigned c = (raw.x >> 4) & 0x0303u, d = (raw.x >> 6) & 0x0303u;
-    return u32x4{pair(a, false, 512.f), pair(b, false, 512.f), pair(c, false, 512.f),
-                 pair(d, false, 512.f)};
+    // codes 0 4 | 1 5 | 2 6 | 3 7 (the two bytes of the step's 16 bits; two
+    // steps share a word, whose masks the compiler forms once)
+    const unsigned a = raw.x & 0x03030303u, b = (raw.x >> 2) & 0x03030303u;
+    const unsigned c = (raw.x >> 4) & 0x03030303u, d = (raw.x >> 6) & 0x03030303u;
+    const bool hi = k % 2;
+    return u32x4{pair(a, hi, 512.f), pair(b, hi, 512.f), pair(c, hi, 512.f), pair(d, hi, 512.f)};
   } else {
     unsigned p[4];
 #pragma unroll
@@ -271,14 +273,16 @@ __device__ __forceinline__ Rows expert_rows(const MoeArgs& a, int e, int64_t row
 
 // The scales and offsets of `rows` rows of one kind from row0 on, scale groups
 // [g0, g0 + ng), to LDS as sm[row][group] (an odd pitch: 16 rows of a read in
-// 16 banks): rows are contiguous in memory, so each is fetched once.
+// 16 banks): rows are contiguous in memory, so each is fetched once.  Groups
+// up to `full` (of a last slot that the rows do not fill) count nothing.
 __device__ __forceinline__ void stage_scales(float2* sm, int pitch, const float* s, const float* m,
                                              int64_t row0, int rows, int64_t nrow, int64_t Gs,
-                                             int64_t g0, int ng) {
-  for (int i = threadIdx.x; i < rows * ng; i += blockDim.x) {
-    const int r = i / ng, g = i % ng;
-    const int64_t at = (row0 + min((int64_t)r, nrow - 1)) * Gs + g0 + g;
-    sm[r * pitch + g] = float2{s[at], m[at]};
+                                             int64_t g0, int ng, int full) {
+  for (int i = threadIdx.x; i < rows * full; i += blockDim.x) {
+    const int r = i / full, g = i % full;
+    const int64_t at = (row0 + min((int64_t)r, nrow - 1)) * Gs + g0 + min(g, ng - 1);
+    const float2 v = {s[at], m[at]};
+    sm[r * pitch + g] = g < ng ? v : float2{0.f, 0.f};
   }
 }
 
@@ -376,7 +380,7 @@ __device__ __forceinline__ void use_group(const uint8_t* lds, int j, const u32x4
     for (int b = 0; b < NB; ++b) p[b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < GS / 32; ++k) {
-      const u32x4 cq = codes_bf16<CB, F8>(step_codes<CB, GS>(c, k));
+      const u32x4 cq = codes_bf16<CB, GS, F8>(c, k);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
         p[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[k][b]),
@@ -432,8 +436,7 @@ __device__ __forceinline__ void contract(const Rows& r, const bf16_t* const (&co
 #pragma unroll
         for (int i = 0; i < XG; ++i) planes(j + i);
       }
-      if (j == 0 || g < G)  // uniform
-        use_group<CB, F8, GS, RT, NB>(lds, j, x[j % XG], sm + ((g >> gdiv) - gs0), pitch, lr, q, acc);
+      use_group<CB, F8, GS, RT, NB>(lds, j, x[j % XG], sm + ((g >> gdiv) - gs0), pitch, lr, q, acc);
     }
   }
 }
@@ -525,6 +528,7 @@ __global__ __launch_bounds__(W * 64) void k_moe_proj(MoeArgs a) {
     for (int gs0 = 0; gs0 < Gs; gs0 += a.ngs) {
       const int ng = min(a.ngs, (int)Gs - gs0);
       const int g1 = min(G, (gs0 + ng) << gdiv);
+      const int full = ((g1 + SG - 1) / SG * SG >> gdiv) - gs0;
       contract<CB, F8, GS, RT, RB, NB>(
           rows, col, rb, (gs0 << gdiv) / SG + w % KS, (g1 + SG - 1) / SG, KS, g1, slot, sml, pitch,
           gs0, gdiv, l, acc, [&] {
@@ -533,7 +537,7 @@ __global__ __launch_bounds__(W * 64) void k_moe_proj(MoeArgs a) {
               for (int kind = 0; kind < (UP ? 2 : 1); ++kind)
                 stage_scales(sm + (b * RT + kind * RB) * 16 * pitch, pitch, ss, mm,
                              erow + kind * a.ff + min((int64_t)b * RB * 16, wn - 1), RB * 16,
-                             max((int64_t)1, wn - b * RB * 16), Gs, gs0, ng);
+                             max((int64_t)1, wn - b * RB * 16), Gs, gs0, ng, full);
             __syncthreads();
           });
     }
@@ -571,6 +575,193 @@ __global__ __launch_bounds__(W * 64) void k_moe_proj(MoeArgs a) {
   }
 }
 
+// The same for experts that many tokens chose, where the planes, not the codes,
+// are what the products read most of: they go through LDS, once for the four
+// waves of a workgroup, each of which has RT row blocks of its own and all
+// channels.  A step is XC channels of NB * 16 columns; the next step's planes,
+// and with a slot's first step the next slot's codes and scales, are in flight
+// while it is contracted.  (Planes from L2 by every wave: 256 + 115 us for 97
+// tokens over 16 2-bit experts of 4096 / 2816.)
+template <int CB, bool F8, int GS, int NB, bool UP>
+__global__ __launch_bounds__(256, 2) void k_moe_wide(MoeArgs a) {
+  constexpr int RT = 4, W = 4, RB = UP ? RT / 2 : RT, NKS = GS / 32;
+  constexpr int ORDER = order_of(CB, F8);
+  using S = Slot<CB, GS>;
+  constexpr int XC = 128, XG = XC / GS, XK = XC / 32;
+  constexpr int NC = S::SB * 8 / CB / XC;           // steps of a slot
+  constexpr int NX = (XK * NB + W - 1) / W;         // fragments of a step a wave brings
+  constexpr int SLOT = RT * 16 * S::SB, PITCH = S::SG | 1;
+  constexpr int WR = RB * 16 * W;                   // rows (of one kind) of the workgroup
+  constexpr int PR = UP ? 2 : 1;                    // row blocks of a turn of the epilogue
+  constexpr size_t WORK = W * SLOT + W * RT * 16 * PITCH * 8 + XK * NB * 1024;
+  constexpr size_t PROD = (size_t)W * PR * NB * 16 * 17 * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t dyn[WORK > PROD ? WORK : PROD];
+  __shared__ int16_t list[kMoeMaxT];
+  const int tid = threadIdx.x, l = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = l & 15, q = l >> 4;
+  const Mine mine = my_expert(a, list);
+  const int n = mine.n, e = mine.e;
+  if (n == 0) return;  // uniform
+
+  uint8_t* slot = dyn + w * SLOT;
+  float2* sm = reinterpret_cast<float2*>(dyn + W * SLOT);
+  u32x4* xl = reinterpret_cast<u32x4*>(dyn + W * SLOT + W * RT * 16 * PITCH * 8);
+  float(*red)[PR][NB][16][17] = reinterpret_cast<float(*)[PR][NB][16][17]>(dyn);
+
+  const int64_t N = UP ? a.ff : a.d, rb = UP ? a.gu_rb : a.dn_rb;
+  const int G = (int)((UP ? a.d : a.ff) / GS);
+  const int gdiv = a.gshift - __builtin_ctz((unsigned)GS);
+  const int64_t Gs = (UP ? a.d : a.ff) >> a.gshift;
+  const int64_t wrow0 = (int64_t)blockIdx.x * WR, row0 = wrow0 + w * (RB * 16);
+  const Rows rows = expert_rows<RB, UP>(a, e, row0);
+  const bf16_t* xp = UP ? a.Xp : a.H;
+  const int64_t K3 = 3 * (UP ? a.d : a.ff);
+  const int ns = (G + S::SG - 1) / S::SG;
+  // the row whose scales this thread stages
+  const int64_t mine_row = (int64_t)e * (UP ? 2 * a.ff : a.d) + (UP && l >= 32 ? a.ff : 0) +
+                           min(row0 + (UP ? l % 32 : l), N - 1);
+  const float* sp = (UP ? a.gu_s : a.dn_s) + mine_row * Gs;
+  const float* mp = (UP ? a.gu_m : a.dn_m) + mine_row * Gs;
+  const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+
+  constexpr int TP = NB * 16 / 3;
+  for (int t0 = blockIdx.z * TP; t0 < n; t0 += TP * gridDim.z) {
+    const int here = min(TP, n - t0);
+    // a wave brings fragments f = w, w + W, ..: step f / NB, columns f % NB
+    const bf16_t* src[NX];
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      const int f = w + i * W;
+      const int c0 = (f % NB) * 16 + lr;
+      const int c = c0 < 3 * here ? c0 : 0;  // columns past the last: never stored
+      src[i] = xp + (int64_t)list[t0 + c / 3] * K3 + (c % 3) * GS + (f / NB) % NKS * 32 + q * 8;
+    }
+    u32x4 xr[NX];
+    float2 sr[S::SG];
+    Stage<CB, GS, RT> st;
+    auto load_x = [&](int step) {
+#pragma unroll
+      for (int i = 0; i < NX; ++i) {
+        const int g = step * XG + (w + i * W) / NB / NKS;
+        xr[i] = *(const u32x4*)(src[i] + (int64_t)min(g, G - 1) * 3 * GS);
+      }
+    };
+    auto load_scales = [&](int sl) {
+#pragma unroll
+      for (int j = 0; j < S::SG; ++j) {
+        // (groups past the end count nothing: their codes are another row's)
+        const int g = min(sl * S::SG + j, G - 1) >> gdiv;
+        const float2 v = {sp[g], mp[g]};
+        sr[j] = sl * S::SG + j < G ? v : float2{0.f, 0.f};
+      }
+    };
+    f32x4 acc[RT][NB];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[r][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    load_codes_of<CB, GS, RT, RB>(st, rows, rb, 0, l);
+    load_scales(0);
+    load_x(0);
+    for (int s = 0; s < ns; ++s) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int step = s * NC + c;
+        if (c > 0 && step * XG >= G) break;  // uniform
+        __syncthreads();
+        if (c == 0) {
+          put_codes<CB, GS, RT>(st, slot, l);
+#pragma unroll
+          for (int j = 0; j < S::SG; ++j) sm[tid * PITCH + j] = sr[j];
+        }
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+          const int f = w + i * W;
+          if (f < XK * NB) xl[f * 64 + l] = xr[i];
+        }
+        __syncthreads();
+        load_x(step + 1);
+        if (c == 0) {
+          load_codes_of<CB, GS, RT, RB>(st, rows, rb, s + 1, l);
+          load_scales(s + 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < XG; ++j) {
+          const int sj = c * XG + j;  // the group's place in the slot
+          f32x4 sx[NB];
+          u32x4 x[NKS][NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            sx[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < NKS; ++k) {
+              x[k][b] = xl[((j * NKS + k) * NB + b) * 64 + l];
+              sx[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[k][b]),
+                                                             __builtin_bit_cast(bf16x8, ones), sx[b],
+                                                             0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const float2 sc = sm[(w * RT * 16 + r * 16 + lr) * PITCH + sj];
+            const GroupCodes<CB, GS> gc = get_codes<CB, GS>(slot, r, sj, lr, q);
+            u32x4 cq[NKS];
+#pragma unroll
+            for (int k = 0; k < NKS; ++k) cq[k] = codes_bf16<CB, GS, F8>(gc, k);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int k = 0; k < NKS; ++k)
+                p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[k][b]),
+                                                           __builtin_bit_cast(bf16x8, cq[k]), p, 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[r][b][i] = fmaf(sc.x, p[i], fmaf(sc.y, sx[b][i], acc[r][b][i]));
+            }
+          }
+        }
+      }
+    }
+    // lane l of a product holds row l & 15 and columns 4 (l >> 4) + i; PR row
+    // blocks of every wave at a time
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      __syncthreads();
+#pragma unroll
+      for (int pr = 0; pr < PR; ++pr)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) red[w][pr][b][q * 4 + i][lr] = acc[r + pr * RB][b][i];
+      __syncthreads();
+      // thread: a row of a wave, and every fourth token
+      const int wb = tid >> 4 & 3, ri = tid & 15;
+      const int64_t row = wrow0 + wb * (RB * 16) + r * 16 + ri;
+      if (row < N) {
+        const float dhi = UP ? a.dn_dhi[(int64_t)e * a.ff + row] : 0.f;
+        for (int j = tid >> 6; j < here; j += 4) {
+          auto value = [&](int pr) {
+            float v = 0.f;
+#pragma unroll
+            for (int pl = 0; pl < 3; ++pl) {
+              const int c = 3 * j + pl;
+              v += red[wb][pr][c >> 4][c & 15][ri];
+            }
+            return v;
+          };
+          const int64_t p = list[t0 + j];
+          if constexpr (UP) store_hidden<ORDER>(a, p, row, value(0), value(1), dhi);
+          else a.Yp[p * a.d + row] = a.w[p] * value(0);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
 // The down products and their weighted sum of ONE token: a workgroup owns 16
 // rows of all its k experts, the waves being experts by ranges of groups.
 template <int CB, bool F8, int GS, int W>
@@ -598,6 +789,7 @@ __global__ __launch_bounds__(W * 64) void k_moe_down_one(MoeArgs a) {
     for (int gs0 = 0; gs0 < Gs; gs0 += a.ngs) {
       const int ng = min(a.ngs, (int)Gs - gs0);
       const int g1 = min(G, (gs0 + ng) << gdiv);
+      const int full = ((g1 + SG - 1) / SG * SG >> gdiv) - gs0;
       // (waves with no expert of their own in this turn go along with the last)
       const int jj = min(j, a.k - 1);
       const Rows rows = expert_rows<1, false>(a, a.ids[jj], row0);
@@ -608,7 +800,7 @@ __global__ __launch_bounds__(W * 64) void k_moe_down_one(MoeArgs a) {
             if (j0 > 0 || gs0 > 0) __syncthreads();
             for (int b = 0; b < EP && j0 + b < a.k; ++b)
               stage_scales(sm + b * 16 * pitch, pitch, a.dn_s, a.dn_m,
-                           (int64_t)a.ids[j0 + b] * a.d + row0, 16, a.d - row0, Gs, gs0, ng);
+                           (int64_t)a.ids[j0 + b] * a.d + row0, 16, a.d - row0, Gs, gs0, ng, full);
             __syncthreads();
           });
     }
@@ -654,7 +846,7 @@ hipError_t launch_proj(const MoeArgs& a, const Launch& L) {
   using S = Slot<CB, GS>;
   MoeArgs b = a;
   auto lds = [&](int rows, int slots, size_t products) {
-    b.ngs = (int)std::min(Gs, (int64_t)kStage / (rows * 8) / S::SG * S::SG);
+    b.ngs = (int)(std::min(Gs + S::SG - 1, (int64_t)kStage / (rows * 8)) / S::SG * S::SG);
     b.pitch = b.ngs | 1;
     return (uint32_t)std::max((size_t)slots * 16 * S::SB + (size_t)rows * b.pitch * 8, products);
   };
@@ -672,7 +864,10 @@ hipError_t launch_proj(const MoeArgs& a, const Launch& L) {
   }
   // columns an expert can expect: 16 of them are 5 tokens
   if (a.T * a.k <= 5 * (int64_t)a.E) return go(k_moe_proj<CB, F8, GS, 4, 1, 4, 4, UP>, 4, 1, 4, 4);
-  return go(k_moe_proj<CB, F8, GS, 4, 3, 4, 2, UP>, 4, 3, 4, 2);
+  constexpr int NB = 3;
+  const int per = UP ? 128 : 256;
+  return ext_launch(k_moe_wide<CB, F8, GS, NB, UP>, dim3((unsigned)((N + per - 1) / per), (unsigned)slots, 2),
+                    dim3(256), 0, L, b);
 }
 
 template <bool UP>
