@@ -278,11 +278,23 @@ __device__ __forceinline__ Rows expert_rows(const MoeArgs& a, int e, int64_t row
 __device__ __forceinline__ void stage_scales(float2* sm, int pitch, const float* s, const float* m,
                                              int64_t row0, int rows, int64_t nrow, int64_t Gs,
                                              int64_t g0, int ng, int full) {
-  for (int i = threadIdx.x; i < rows * full; i += blockDim.x) {
-    const int r = i / full, g = i % full;
-    const int64_t at = (row0 + min((int64_t)r, nrow - 1)) * Gs + g0 + min(g, ng - 1);
-    const float2 v = {s[at], m[at]};
-    sm[r * pitch + g] = g < ng ? v : float2{0.f, 0.f};
+  const int sh = 32 - __builtin_clz(full - 1 | 1);  // lanes of a row: a power of two
+  // four elements' loads at a time (past the end: the last one again)
+  for (int i0 = threadIdx.x; i0 < rows << sh; i0 += 4 * blockDim.x) {
+    float2 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = min(i0 + u * (int)blockDim.x, (rows << sh) - 1);
+      const int r = i >> sh, g = i & ((1 << sh) - 1);
+      const int64_t at = (row0 + min((int64_t)r, nrow - 1)) * Gs + g0 + min(g, ng - 1);
+      v[u] = float2{s[at], m[at]};
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * (int)blockDim.x;
+      const int r = i >> sh, g = i & ((1 << sh) - 1);
+      if (r < rows && g < full) sm[r * pitch + g] = g < ng ? v[u] : float2{0.f, 0.f};
+    }
   }
 }
 
@@ -306,14 +318,15 @@ struct Stage {
 };
 template <int CB, int GS, int RT, int RB>
 __device__ __forceinline__ void load_codes_of(Stage<CB, GS, RT>& st, const Rows& r, int64_t rb,
-                                              int slot, int l) {
+                                              int slot, int end, int l) {
+  // (a slot at or past the end: nothing is read)
+  const uint32_t at = slot < end ? (uint32_t)(slot * Slot<CB, GS>::SB) : kOutOfRange;
   using S = Slot<CB, GS>;
   constexpr int PER = RB * 16 / S::RPI;  // loads of one kind of row
 #pragma unroll
   for (int i = 0; i < RT * 16 / S::RPI; ++i)
     st.c[i] = buf_load16(i < PER ? r.c0 : r.c1,
-                         (uint32_t)(((i % PER) * S::RPI + l / S::LPR) * rb + l % S::LPR * 16),
-                         (uint32_t)(slot * S::SB));
+                         (uint32_t)(((i % PER) * S::RPI + l / S::LPR) * rb + l % S::LPR * 16), at);
 }
 template <int CB, int GS, int RT>
 __device__ __forceinline__ void put_codes(const Stage<CB, GS, RT>& st, uint8_t* lds, int l) {
@@ -406,38 +419,40 @@ __device__ __forceinline__ void contract(const Rows& r, const bf16_t* const (&co
   using S = Slot<CB, GS>;
   constexpr int NKS = GS / 32;
   const int lr = l & 15, q = l >> 4;
+  // planes of XG groups at a time, those of a slot's first groups asked for
+  // before its codes are waited for
+  constexpr int XG = S::SG * NKS * NB <= 12 ? S::SG : S::SG * NKS * NB <= 24 ? S::SG / 2 : 1;
+  u32x4 x[XG][NKS][NB];
+  auto planes = [&](int slot, int j) {
+    const int gg = min(slot * S::SG + j, G - 1);  // (a group past the end is not used)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int k = 0; k < NKS; ++k)
+        x[j % XG][k][b] = *(const u32x4*)(col[b] + (int64_t)gg * 3 * GS + k * 32 + q * 8);
+  };
   Stage<CB, GS, RT> st;
-  load_codes_of<CB, GS, RT, RB>(st, r, rb, s0, l);
+  load_codes_of<CB, GS, RT, RB>(st, r, rb, s0, s1, l);
+#pragma unroll
+  for (int j = 0; j < XG; ++j) planes(s0, j);
   __builtin_amdgcn_sched_barrier(0);
   stage();
   for (int s = s0; s < s1; s += step) {
     put_codes<CB, GS, RT>(st, lds, l);
-    // the planes come from L2 and are asked for ahead of the next codes, so
-    // that they are not waited for behind them
-    constexpr int XG = S::SG * NKS * NB <= 12 ? S::SG : S::SG * NKS * NB <= 24 ? S::SG / 2 : 1;
-    u32x4 x[XG][NKS][NB];
-    auto planes = [&](int j) {
-      const int gg = min(s * S::SG + j, G - 1);  // (a group past the end is not used)
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int k = 0; k < NKS; ++k)
-          x[j % XG][k][b] = *(const u32x4*)(col[b] + (int64_t)gg * 3 * GS + k * 32 + q * 8);
-    };
-#pragma unroll
-    for (int j = 0; j < XG; ++j) planes(j);
-    __builtin_amdgcn_sched_barrier(0);
-    load_codes_of<CB, GS, RT, RB>(st, r, rb, s + step, l);
+    load_codes_of<CB, GS, RT, RB>(st, r, rb, s + step, s1, l);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < S::SG; ++j) {
-      const int g = s * S::SG + j;
       if (j > 0 && j % XG == 0) {
 #pragma unroll
-        for (int i = 0; i < XG; ++i) planes(j + i);
+        for (int i = 0; i < XG; ++i) planes(s, j + i);
       }
-      use_group<CB, F8, GS, RT, NB>(lds, j, x[j % XG], sm + ((g >> gdiv) - gs0), pitch, lr, q, acc);
+      use_group<CB, F8, GS, RT, NB>(lds, j, x[j % XG], sm + (((s * S::SG + j) >> gdiv) - gs0), pitch,
+                                    lr, q, acc);
     }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < XG; ++j) planes(s + step, j);
   }
 }
 
@@ -661,7 +676,7 @@ __global__ __launch_bounds__(256, 2) void k_moe_wide(MoeArgs a) {
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[r][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    load_codes_of<CB, GS, RT, RB>(st, rows, rb, 0, l);
+    load_codes_of<CB, GS, RT, RB>(st, rows, rb, 0, ns, l);
     load_scales(0);
     load_x(0);
     for (int s = 0; s < ns; ++s) {
@@ -683,7 +698,7 @@ __global__ __launch_bounds__(256, 2) void k_moe_wide(MoeArgs a) {
         __syncthreads();
         load_x(step + 1);
         if (c == 0) {
-          load_codes_of<CB, GS, RT, RB>(st, rows, rb, s + 1, l);
+          load_codes_of<CB, GS, RT, RB>(st, rows, rb, s + 1, ns, l);
           load_scales(s + 1);
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -830,7 +845,14 @@ __global__ __launch_bounds__(256) void k_moe_sum(MoeArgs a) {
   if (i >= a.T * a.d) return;
   const int64_t t = i / a.d, c = i % a.d;
   f32x4 y = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < a.k; ++j) y += *(const f32x4*)(a.Yp + (t * a.k + j) * a.d + c);
+  for (int j0 = 0; j0 < a.k; j0 += 8) {
+    f32x4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = *(const f32x4*)(a.Yp + (t * a.k + min(j0 + j, a.k - 1)) * a.d + c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < a.k) y += v[j];
+  }
   *(f32x4*)(a.Y + i) = y;
 }
 
