@@ -17,6 +17,7 @@
 // results are added at the end.  One token then costs one instruction per 32
 // channels and 16 rows, not three, and 5 tokens no more than one.
 #include <algorithm>
+#include <cmath>
 
 #include "codes.h"
 #include "ttq_internal.h"
@@ -305,32 +306,33 @@ __device__ __forceinline__ void stage_scales(float2* sm, int pitch, const float*
 // requests, and with those the kernel stayed at 3.4 TB/s whatever its tiles.)
 // In LDS the 16-byte pieces of row r are swapped by r / 2, which puts the 16
 // rows of a read on all banks.
-template <int CB, int GS>
+template <int CB, int GS, bool WIDE = false>
 struct Slot {
-  static constexpr int SB = CB == 1 ? 64 : 128;
+  // (experts of many tokens: half lines, for the sake of LDS; at least a group)
+  static constexpr int SB = CB == 1 || (WIDE && GS * CB <= 512) ? 64 : 128;
   static constexpr int SG = SB * 8 / CB / GS;   // groups
   static constexpr int LPR = SB / 16;           // lanes a row
   static constexpr int RPI = 64 / LPR;          // rows a load
 };
-template <int CB, int GS, int RT>
+template <int CB, int GS, int RT, bool WIDE = false>
 struct Stage {
-  u32x4 c[RT * 16 / Slot<CB, GS>::RPI];
+  u32x4 c[RT * 16 / Slot<CB, GS, WIDE>::RPI];
 };
-template <int CB, int GS, int RT, int RB>
-__device__ __forceinline__ void load_codes_of(Stage<CB, GS, RT>& st, const Rows& r, int64_t rb,
+template <int CB, int GS, int RT, int RB, bool WIDE = false>
+__device__ __forceinline__ void load_codes_of(Stage<CB, GS, RT, WIDE>& st, const Rows& r, int64_t rb,
                                               int slot, int end, int l) {
   // (a slot at or past the end: nothing is read)
-  const uint32_t at = slot < end ? (uint32_t)(slot * Slot<CB, GS>::SB) : kOutOfRange;
-  using S = Slot<CB, GS>;
+  const uint32_t at = slot < end ? (uint32_t)(slot * Slot<CB, GS, WIDE>::SB) : kOutOfRange;
+  using S = Slot<CB, GS, WIDE>;
   constexpr int PER = RB * 16 / S::RPI;  // loads of one kind of row
 #pragma unroll
   for (int i = 0; i < RT * 16 / S::RPI; ++i)
     st.c[i] = buf_load16(i < PER ? r.c0 : r.c1,
                          (uint32_t)(((i % PER) * S::RPI + l / S::LPR) * rb + l % S::LPR * 16), at);
 }
-template <int CB, int GS, int RT>
-__device__ __forceinline__ void put_codes(const Stage<CB, GS, RT>& st, uint8_t* lds, int l) {
-  using S = Slot<CB, GS>;
+template <int CB, int GS, int RT, bool WIDE = false>
+__device__ __forceinline__ void put_codes(const Stage<CB, GS, RT, WIDE>& st, uint8_t* lds, int l) {
+  using S = Slot<CB, GS, WIDE>;
 #pragma unroll
   for (int i = 0; i < RT * 16 / S::RPI; ++i) {
     const int row = i * S::RPI + l / S::LPR;
@@ -338,9 +340,9 @@ __device__ __forceinline__ void put_codes(const Stage<CB, GS, RT>& st, uint8_t* 
   }
 }
 // the lane's quarter of group j of a slot, row block r
-template <int CB, int GS>
+template <int CB, int GS, bool WIDE = false>
 __device__ __forceinline__ GroupCodes<CB, GS> get_codes(const uint8_t* lds, int r, int j, int lr, int q) {
-  using S = Slot<CB, GS>;
+  using S = Slot<CB, GS, WIDE>;
   constexpr int NB = GroupCodes<CB, GS>::NB;
   const int row = r * 16 + lr, at = j * (GS * CB / 8) + q * NB;
   const int swz = row >> 1 & (S::LPR - 1);
@@ -601,7 +603,7 @@ template <int CB, bool F8, int GS, int NB, bool UP>
 __global__ __launch_bounds__(256, 2) void k_moe_wide(MoeArgs a) {
   constexpr int RT = 4, W = 4, RB = UP ? RT / 2 : RT, NKS = GS / 32;
   constexpr int ORDER = order_of(CB, F8);
-  using S = Slot<CB, GS>;
+  using S = Slot<CB, GS, true>;
   constexpr int XC = 128, XG = XC / GS, XK = XC / 32;
   constexpr int NC = S::SB * 8 / CB / XC;           // steps of a slot
   constexpr int NX = (XK * NB + W - 1) / W;         // fragments of a step a wave brings
@@ -654,7 +656,7 @@ __global__ __launch_bounds__(256, 2) void k_moe_wide(MoeArgs a) {
     }
     u32x4 xr[NX];
     float2 sr[S::SG];
-    Stage<CB, GS, RT> st;
+    Stage<CB, GS, RT, true> st;
     auto load_x = [&](int step) {
 #pragma unroll
       for (int i = 0; i < NX; ++i) {
@@ -663,12 +665,26 @@ __global__ __launch_bounds__(256, 2) void k_moe_wide(MoeArgs a) {
       }
     };
     auto load_scales = [&](int sl) {
+      // (four at a time where they are all the row's own: every lane has a row
+      // of its own, and a load costs as many requests as it has lanes)
+      typedef __attribute__((ext_vector_type(4), aligned(4))) float f32x4u;
+      if (S::SG % 4 == 0 && gdiv == 0 && (int64_t)(sl + 1) * S::SG <= Gs) {
 #pragma unroll
-      for (int j = 0; j < S::SG; ++j) {
-        // (groups past the end count nothing: their codes are another row's)
-        const int g = min(sl * S::SG + j, G - 1) >> gdiv;
-        const float2 v = {sp[g], mp[g]};
-        sr[j] = sl * S::SG + j < G ? v : float2{0.f, 0.f};
+        for (int j = 0; j < S::SG; j += 4) {
+          const f32x4u sv = *(const f32x4u*)(sp + sl * S::SG + j);
+          const f32x4u mv = *(const f32x4u*)(mp + sl * S::SG + j);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (j + i < S::SG) sr[j + i] = float2{sv[i], mv[i]};
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < S::SG; ++j) {
+          // (groups past the end count nothing: their codes are another row's)
+          const int g = min(sl * S::SG + j, G - 1) >> gdiv;
+          const float2 v = {sp[g], mp[g]};
+          sr[j] = sl * S::SG + j < G ? v : float2{0.f, 0.f};
+        }
       }
     };
     f32x4 acc[RT][NB];
@@ -676,7 +692,7 @@ __global__ __launch_bounds__(256, 2) void k_moe_wide(MoeArgs a) {
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[r][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    load_codes_of<CB, GS, RT, RB>(st, rows, rb, 0, ns, l);
+    load_codes_of<CB, GS, RT, RB, true>(st, rows, rb, 0, ns, l);
     load_scales(0);
     load_x(0);
     for (int s = 0; s < ns; ++s) {
@@ -686,7 +702,7 @@ __global__ __launch_bounds__(256, 2) void k_moe_wide(MoeArgs a) {
         if (c > 0 && step * XG >= G) break;  // uniform
         __syncthreads();
         if (c == 0) {
-          put_codes<CB, GS, RT>(st, slot, l);
+          put_codes<CB, GS, RT, true>(st, slot, l);
 #pragma unroll
           for (int j = 0; j < S::SG; ++j) sm[tid * PITCH + j] = sr[j];
         }
@@ -698,7 +714,7 @@ __global__ __launch_bounds__(256, 2) void k_moe_wide(MoeArgs a) {
         __syncthreads();
         load_x(step + 1);
         if (c == 0) {
-          load_codes_of<CB, GS, RT, RB>(st, rows, rb, s + 1, ns, l);
+          load_codes_of<CB, GS, RT, RB, true>(st, rows, rb, s + 1, ns, l);
           load_scales(s + 1);
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -721,7 +737,7 @@ __global__ __launch_bounds__(256, 2) void k_moe_wide(MoeArgs a) {
 #pragma unroll
           for (int r = 0; r < RT; ++r) {
             const float2 sc = sm[(w * RT * 16 + r * 16 + lr) * PITCH + sj];
-            const GroupCodes<CB, GS> gc = get_codes<CB, GS>(slot, r, sj, lr, q);
+            const GroupCodes<CB, GS> gc = get_codes<CB, GS, true>(slot, r, sj, lr, q);
             u32x4 cq[NKS];
 #pragma unroll
             for (int k = 0; k < NKS; ++k) cq[k] = codes_bf16<CB, GS, F8>(gc, k);
@@ -884,11 +900,22 @@ hipError_t launch_proj(const MoeArgs& a, const Launch& L) {
     return ext_launch(k_moe_down_one<CB, F8, GS, W>, dim3((unsigned)((N + 15) / 16)),
                       dim3(W * 64), bytes, L, b);
   }
-  // columns an expert can expect: 16 of them are 5 tokens
-  if (a.T * a.k <= 5 * (int64_t)a.E) return go(k_moe_proj<CB, F8, GS, 4, 1, 4, 4, UP>, 4, 1, 4, 4);
+  // Few tokens an expert (5 are 16 columns): every pass over them reads the
+  // codes again, but its small workgroups fill the chip also where experts are
+  // few.  Measured, a whole call: 64 experts of 2048 / 1408, top 8, at a mean of 5
+  // tokens 160 us either way, of 8 218 us and 194 with shared planes; 8 experts
+  // of 4096 / 2816, top 2, at 6 tokens 94 and 135 us, at 10 116 and 139.
+  const int64_t wide = (N + (UP ? 127 : 255)) / (UP ? 128 : 256) * slots;
+  if (a.T * a.k <= (wide < 512 ? 10 : 5) * (int64_t)a.E)
+    return go(k_moe_proj<CB, F8, GS, 4, 1, 4, 4, UP>, 4, 1, 4, 4);
+  // many tokens an expert: passes of 16 tokens side by side, as many as a
+  // mean and three of its deviations need (more take turns)
   constexpr int NB = 3;
   const int per = UP ? 128 : 256;
-  return ext_launch(k_moe_wide<CB, F8, GS, NB, UP>, dim3((unsigned)((N + per - 1) / per), (unsigned)slots, 2),
+  const double mean = (double)a.T * a.k / a.E;
+  const unsigned passes = (unsigned)std::min((double)(a.T + 15) / 16, (mean + 3 * std::sqrt(mean) + 15) / 16);
+  return ext_launch(k_moe_wide<CB, F8, GS, NB, UP>,
+                    dim3((unsigned)((N + per - 1) / per), (unsigned)slots, std::max(1u, passes)),
                     dim3(256), 0, L, b);
 }
 
