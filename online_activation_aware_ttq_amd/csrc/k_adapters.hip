@@ -659,9 +659,9 @@ hipError_t launch_ad_expand(const AdaptersArgs& a, int slots, const Launch& L) {
   int64_t blocks = (a.d_out + per - 1) / per;
   if (tiles == 0 || blocks == 0) return hipSuccess;
   // several blocks of outputs a workgroup, while that leaves enough of them for
-  // the chip (prompts: two per compute unit; decode steps, of whose workgroups
+  // the chip (prompts: four per compute unit; decode steps, of whose workgroups
   // some have no pair, eight)
-  blocks = std::max<int64_t>(1, std::min(blocks, step ? 2048 / a.T : 512 / tiles));
+  blocks = std::max<int64_t>(1, std::min(blocks, step ? 2048 / a.T : 1024 / tiles));
   const dim3 grid((unsigned)tiles, (unsigned)slots, (unsigned)blocks), blk(AW * 64);
 #define TTQ_AD_EXPAND(NK)                                                 \
   return step ? ext_launch(k_ad_expand_step<NK>, grid, blk, 0, L, a)      \

@@ -308,8 +308,9 @@ __device__ __forceinline__ void stage_scales(float2* sm, int pitch, const float*
 // rows of a read on all banks.
 template <int CB, int GS, bool WIDE = false>
 struct Slot {
-  // (experts of many tokens: half lines, for the sake of LDS; at least a group)
-  static constexpr int SB = CB == 1 || (WIDE && GS * CB <= 512) ? 64 : 128;
+  // (experts of many tokens: half lines, for the sake of LDS, while they hold
+  // the 128 channels of a step)
+  static constexpr int SB = CB == 1 || (WIDE && CB <= 4) ? 64 : 128;
   static constexpr int SG = SB * 8 / CB / GS;   // groups
   static constexpr int LPR = SB / 16;           // lanes a row
   static constexpr int RPI = 64 / LPR;          // rows a load
@@ -606,6 +607,7 @@ __global__ __launch_bounds__(256, 2) void k_moe_wide(MoeArgs a) {
   using S = Slot<CB, GS, true>;
   constexpr int XC = 128, XG = XC / GS, XK = XC / 32;
   constexpr int NC = S::SB * 8 / CB / XC;           // steps of a slot
+  static_assert(NC >= 1 && NC * XG == S::SG, "a slot is whole steps");
   constexpr int NX = (XK * NB + W - 1) / W;         // fragments of a step a wave brings
   constexpr int SLOT = RT * 16 * S::SB, PITCH = S::SG | 1;
   constexpr int WR = RB * 16 * W;                   // rows (of one kind) of the workgroup

@@ -102,3 +102,27 @@ def test_binding_checks_tensors():
     with pytest.raises(ValueError, match="GPU tensor"):
         ttq.ttq_cache_write(X, torch.zeros(4, dtype=torch.int64),
                             torch.zeros(8, 128, dtype=torch.uint8), z, z, bits=4, group=128)
+
+
+@pytest.mark.parametrize("fmt,bits", [("asym", 1), ("asym", 4), ("asym", 8), ("sym", 3), ("intzp", 4),
+                                      ("fp8", 8)])
+def test_oracle_rows_are_within_half_a_step(fmt, bits):
+    """The cache's quantizer in the oracle: every value within half a step of
+    what it stands for (E4M3: half a unit of its binade), codes in range, and a
+    repeated call the same."""
+    import numpy as np
+    import oracle
+    rng = np.random.default_rng(bits)
+    x = (rng.standard_normal((7, 96)) * 10.0 ** rng.integers(-3, 3, (7, 1))).astype(np.float32)
+    x[3] = 0
+    dh = (0.5 + rng.random(96)).astype(np.float32)
+    q = oracle.cache_rows(x, dh, bits, 32, fmt)
+    u = (x * dh).astype(np.float64)
+    s = np.repeat(q["s"].astype(np.float64), 32, axis=1)
+    half = s / 2
+    if fmt == "fp8":  # 3 fraction bits, and subnormals below 2^-6
+        half = s * 2.0 ** (np.floor(np.log2(np.maximum(np.abs(u) / np.where(s > 0, s, 1), 2.0 ** -6))) - 4)
+    assert (np.abs(q["values"] - u) <= half * (1 + 1e-5) + 1e-30).all()
+    assert q["codes"].max() <= (0xFE if fmt == "fp8" else 2 ** bits - 1)
+    assert (q["values"][3] == 0).all()
+    assert (oracle.cache_rows(x, dh, bits, 32, fmt)["codes"] == q["codes"]).all()

@@ -47,6 +47,8 @@ SHAPES = [
     (16, 16, 8, 1032, 130), (17, 2, 64, 128, 1000), (33, 7, 128, 264, 36),
     (40, 1, 40, 4104, 260), (64, 100, 16, 256, 64), (300, 9, 48, 96, 129),
     (1100, 3, 16, 64, 40), (17000, 4, 8, 16, 8),
+    (128, 60, 24, 2048, 5001), (129, 2, 64, 72, 516), (200, 5, 128, 136, 70), (700, 3, 88, 40, 2600),
+    (96, 1, 72, 1000, 300),
 ]
 
 

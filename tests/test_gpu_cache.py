@@ -206,6 +206,31 @@ def test_rows_past_2_to_31_bytes():
     assert (err <= step * 0.5001 + 1e-6).all()
 
 
+@pytest.mark.parametrize("ot", ["bf16", "f32"])
+def test_results_larger_than_the_last_level_cache(ot):
+    """They are written past it by another kernel, which has to give the same."""
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    d, group, page, T = 4096, 128, 64, 18000
+    dt = torch.bfloat16 if ot == "bf16" else torch.float32
+    codes, s, m = _cache(640, d, 4, group)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    X = torch.randn(640, d, device="cuda", generator=g)
+    ttq.ttq_cache_write(X, torch.arange(640, device="cuda"), codes, s, m, bits=4, group=group)
+    pages = torch.randint(0, 10, (2, 282), device="cuda", generator=g).to(torch.int32)
+    lens = torch.tensor([301, 17998], dtype=torch.int32, device="cuda")
+    kw = dict(bits=4, group=group, page_tokens=page)
+    big = ttq.ttq_cache_read(codes, s, m, pages, lens,
+                             out=torch.full((2, T, d), 3.0, dtype=dt, device="cuda"), **kw)
+    assert big.numel() * big.element_size() > 256 << 20
+    small = ttq.ttq_cache_read(codes, s, m, torch.arange(10, dtype=torch.int32, device="cuda")[None],
+                               torch.tensor([640], dtype=torch.int32, device="cuda"), T=640, dtype=dt, **kw)
+    for i, n in enumerate((301, 17998)):
+        rows = (pages[i].long()[:, None] * page + torch.arange(page, device="cuda")).reshape(-1)[:n]
+        assert torch.equal(big[i, :n], small[0][rows])
+        assert (big[i, n:] == 3).all()
+
+
 def test_captured_and_on_another_stream():
     import torch
     import online_activation_aware_ttq_amd as ttq

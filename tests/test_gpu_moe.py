@@ -112,6 +112,16 @@ CASES = [
     (20, 9, 2, 96, 224, 8, 32, "fp8", False),
     (9, 6, 2, 512, 768, 8, 256, "intzp", True),
     (1, 100, 10, 256, 128, 2, 128, "sym", True),
+    # many tokens an expert: their planes go through LDS
+    (128, 1, 1, 384, 128, 4, 128, "asym", True),
+    (33, 1, 1, 96, 160, 8, 32, "asym", True),
+    (60, 2, 1, 96, 224, 8, 32, "fp8", True),
+    (50, 2, 2, 256, 384, 8, 128, "fp8", False),
+    (77, 3, 2, 128, 640, 1, 128, "asym", True),
+    (45, 2, 1, 512, 768, 3, 256, "sym", True),
+    (64, 2, 1, 768, 256, 8, 256, "intzp", True),
+    (90, 4, 2, 320, 64, 2, 64, "asym", True),
+    (128, 9, 8, 128, 288, 4, 32, "asym", True),
 ]
 
 
@@ -132,7 +142,8 @@ def test_values(T, E, k, d, ff, bits, group, fmt, renorm):
 
 
 @pytest.mark.parametrize("bits,group,T,E", [(4, 128, 1, 3), (4, 32, 20, 2), (2, 64, 5, 4), (1, 128, 2, 2),
-                                            (8, 64, 18, 2), (3, 256, 1, 2)])
+                                            (8, 64, 18, 2), (3, 256, 1, 2), (4, 128, 70, 1),
+                                            (2, 64, 70, 2), (8, 128, 64, 1), (1, 32, 48, 1)])
 def test_whole_numbers_are_exact(bits, group, T, E):
     d, ff = 256, 256
     rng = np.random.default_rng(bits * 10 + T)
