@@ -635,11 +635,17 @@ def _gpu(t, name):
     return dev
 
 
-def _step_workspace(dev, stream, need):
-    """The stream's kept buffer (see _workspace), but one of its own for a call
-    that is being captured: it then lives in the graph's memory, and no other
-    graph or stream has it."""
+def _step_workspace(dev, stream, need, given):
+    """The caller's workspace, or the stream's kept buffer (see _workspace), but
+    one of its own for a call that is being captured: it then lives in the
+    graph's memory, and no other graph or stream has it."""
     import torch
+    if given is not None:
+        if given.dtype is not torch.uint8:
+            raise TypeError(f"workspace must be a torch.Tensor of torch.uint8, got {given.dtype}")
+        if given.device != dev or not given.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {dev}, got {given.device}")
+        return given
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(need, dtype=torch.uint8, device=dev)
     buf = _SCRATCH.get((dev.index, stream))
@@ -688,8 +694,7 @@ def ttq_adapters(X, A, B, index, *, scale=None, base=None, Y=None,
     ptrs = _expect((X, A, B, scale, index, base, Y), want, dev)
     if stream is None:
         stream = _current_stream(dev)
-    if workspace is None:
-        workspace = _step_workspace(dev, stream, need)
+    workspace = _step_workspace(dev, stream, need, workspace)
     _enqueue("ttq_adapters", dev, load_library().ttq_adapters,
              ctypes.byref(prm), n, *ptrs, workspace.data_ptr(),
              workspace.numel(), stream)
@@ -754,8 +759,7 @@ def ttq_moe(X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv, dn_codes,
                     weights_out), want, dev)
     if stream is None:
         stream = _current_stream(dev)
-    if workspace is None:
-        workspace = _step_workspace(dev, stream, need)
+    workspace = _step_workspace(dev, stream, need, workspace)
     _enqueue("ttq_moe", dev, load_library().ttq_moe, ctypes.byref(prm), *ptrs,
              workspace.data_ptr(), workspace.numel(), stream)
     return Y

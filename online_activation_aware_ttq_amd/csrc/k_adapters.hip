@@ -11,7 +11,8 @@
 // exact), as partial sums over ranges of channels; k_ad_expand adds the
 // partials in range order and contracts with B_e.  S enters that second
 // product as three bf16 planes that sum to it exactly (split24), so the result
-// is as exact as float32 products would be, on the matrix cores.
+// is as exact as float32 products would be, on the matrix cores.  Small decode
+// steps do both in one launch (k_ad_step).
 //
 // Both work on tiles of consecutive tokens (128 of a decode batch, 64 of
 // prompts).  A tile's distinct pairs are found by ballots over its indices, and
@@ -19,7 +20,14 @@
 // instruction: every pair is read once per tile that uses it, whatever the
 // order of the requests and with no sorting pass, and a tile of one request's
 // prompt is one ordinary matrix product.
+//
+// Bound by memory: a decode step by the pairs it reads, prompts by X, base and
+// Y.  128 rows with 64 pairs of rank 64 on 4096 -> 11008: 13.3 us for 34 MB of
+// A, 30 us for 90 MB of B and 11 MB of base and Y.  4096 rows of eight prompts,
+// rank 64 on 4096 -> 4096: 15 us for 34 MB of X, 36 us for 134 MB of base and Y
+// (a plain copy of those: 26 us).
 #include <algorithm>
+#include <type_traits>
 
 #include "ttq_internal.h"
 
@@ -29,9 +37,18 @@ namespace {
 
 constexpr int AW = 4;  // waves per workgroup
 
+// Prompts: workgroups go to the eight dies in turn, each of which has its own L2,
+// and the tiles of one prompt share a pair, so a die gets tiles in a row (8 per).
+__device__ __forceinline__ int64_t prompt_tile() {
+  return (int64_t)(blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8;
+}
+
 // The distinct pairs of the tile at t0 (TC * 64 tokens) that a workgroup takes,
 // one after another, and the rows that name them.  A decode step (TC = 2): the
-// pair of row blockIdx.y, if no earlier row names it.  Prompts, whose tiles
+// pair of row blockIdx.y, counted from row `turn` on, if no earlier row names
+// it.  (Workgroups go to the eight dies in turn, in the order of their numbers:
+// with turn = blockIdx.z a pair's workgroups, of which few rows have any, are
+// spread over them whatever the number of rows.)  Prompts, whose tiles
 // have few: every gridDim.y-th distinct one.  The rows that name no pair go
 // with the first workgroup.  Uniform; every wave writes the same list of rows,
 // so none waits for another: list[0, n) name pair e, list[n, all) none.
@@ -41,8 +58,10 @@ struct TilePairs {
   uint64_t left[TC], none[TC];  // rows not yet taken, rows that name no pair
   int e, n, all;
 
-  __device__ __forceinline__ TilePairs(const AdaptersArgs& a, int64_t t0) {
+  __device__ __forceinline__ TilePairs(const AdaptersArgs& a, int64_t t0, int turn) {
     const int l = threadIdx.x & 63;
+    int j = blockIdx.y;
+    if (TC > 1) j = (j + turn) % (int)gridDim.y;
 #pragma unroll
     for (int c = 0; c < TC; ++c) {
       const int64_t t = t0 + c * 64 + l;
@@ -52,9 +71,8 @@ struct TilePairs {
       none[c] = __ballot(t < a.T && idx[c] < 0);
     }
     if (TC == 1) {
-      for (int i = 0; i < (int)blockIdx.y; ++i) skip();
-    } else {  // only the rows that name what row blockIdx.y does, if it is their first
-      const int j = blockIdx.y;
+      for (int i = 0; i < j; ++i) skip();
+    } else {  // only the rows that name what row j does, if it is their first
       uint64_t same[TC];
       const int pick = lane_index(j);
       int first = -1;
@@ -66,7 +84,7 @@ struct TilePairs {
 #pragma unroll
       for (int c = 0; c < TC; ++c) left[c] = pick >= 0 && first == j ? same[c] : 0;
     }
-    if (blockIdx.y != 0) {
+    if (j != 0) {
 #pragma unroll
       for (int c = 0; c < TC; ++c) none[c] = 0;
     }
@@ -123,14 +141,15 @@ struct TilePairs {
 // of A_e; NB: 16-token blocks of a pass over the range.
 template <int TC, int NR, int NB>
 __global__ __launch_bounds__(AW * 64) void k_ad_shrink(AdaptersArgs a) {
-  __shared__ f32x4 red[AW - 1][NR][64];
+  __shared__ __attribute__((aligned(16))) float red[AW][16][NR * 16 + 4];
   __shared__ uint8_t list[TC * 64];
   const int l = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int lr = l & 15, q = l >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * TC * 64;
+  const int64_t t0 = TC == 1 ? prompt_tile() * 64 : 0;
+  if (t0 >= a.T) return;
   const int64_t k0 = blockIdx.z * a.kc, k1 = min(a.d, k0 + a.kc);
-  TilePairs<TC> r(a, t0);
+  TilePairs<TC> r(a, t0, blockIdx.z);
   while (r.next(list, false)) {  // uniform over the workgroup
     const __amdgpu_buffer_rsrc_t ar =
         make_rsrc(a.A + (int64_t)r.e * a.rank * a.d, (uint32_t)(a.rank * a.d * 2));
@@ -192,25 +211,20 @@ __global__ __launch_bounds__(AW * 64) void k_ad_shrink(AdaptersArgs a) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         if (b0 + b * 16 >= r.n) break;  // uniform
-        if (w > 0) {
+        // lane l of a 16 x 16 product holds column l & 15 and rows 4 (l >> 4) + i
 #pragma unroll
-          for (int n = 0; n < NR; ++n) red[w - 1][n][l] = acc[b][n];
-        }
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) red[w][q * 4 + i][n * 16 + lr] = acc[b][n][i];
         __syncthreads();
-        if (w == 0) {
-          // lane l of a 16 x 16 product holds column l & 15 and rows 4 (l >> 4) + i
+        // a thread adds up, and stores, 4 columns of a row
+        for (int i = threadIdx.x; i < NR * 64; i += AW * 64) {
+          const int at = b0 + b * 16 + i / (NR * 4), col = i % (NR * 4) * 4;
+          if (at >= r.n || col >= a.rank) continue;
+          f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int n = 0; n < NR; ++n) {
-#pragma unroll
-            for (int ww = 0; ww < AW - 1; ++ww) acc[b][n] += red[ww][n][l];
-            const int col = n * 16 + lr;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = b0 + b * 16 + q * 4 + i;
-              if (col < a.rank && at < r.n)
-                a.S[((int64_t)blockIdx.z * a.T + t0 + list[at]) * a.rank + col] = acc[b][n][i];
-            }
-          }
+          for (int ww = 0; ww < AW; ++ww) v += *(const f32x4*)&red[ww][i / (NR * 4)][col];
+          *(f32x4*)(a.S + ((int64_t)blockIdx.z * a.T + t0 + list[at]) * a.rank + col) = v;
         }
         __syncthreads();
       }
@@ -238,6 +252,46 @@ __device__ __forceinline__ void sum_parts(const AdaptersArgs& a, const float* sp
   }
 }
 
+// Four outputs of a row of base, and of Y, by bounded buffers: what lies past the
+// rows or the outputs reads zeros and is not written, with no branch.  (A wait
+// after a branch is for every load in flight: with tests around the accesses the
+// loads that were sent ahead hid nothing, and 4096 rows of 4096 outputs took 47 us,
+// not 40.)  VEC: in one access.
+constexpr uint32_t kNoRow = 0x80000000u;  // past any 128 rows of outputs
+
+template <bool VEC>
+__device__ __forceinline__ f32x4 load_y(__amdgpu_buffer_rsrc_t r, uint32_t row, int64_t col, int64_t d_out) {
+  if constexpr (VEC) {
+    return __builtin_bit_cast(f32x4, buf_load16(r, col < d_out ? row + (uint32_t)col * 4 : kNoRow, 0));
+  } else {
+    f32x4 y;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      y[x] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          r, col + x < d_out ? row + (uint32_t)(col + x) * 4 : kNoRow, 0, 0));
+    return y;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_y(f32x4 y, __amdgpu_buffer_rsrc_t r, uint32_t row, int64_t col,
+                                        int64_t d_out) {
+  if constexpr (VEC) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), r,
+                                           col < d_out ? row + (uint32_t)col * 4 : kNoRow, 0, 0);
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(y[x]), r,
+                                            col + x < d_out ? row + (uint32_t)(col + x) * 4 : kNoRow, 0, 0);
+  }
+}
+// `rows` rows of base (none: zeros) or Y from row t0 on
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t y_rows(const AdaptersArgs& a, const float* y, int64_t t0,
+                                                         int64_t rows) {
+  const int64_t n = min(rows, a.T - t0);
+  return make_rsrc(y ? y + t0 * a.d_out : a.Y, y ? (uint32_t)(n * a.d_out * 4) : 0u);
+}
+
 // Y of a decode step: workgroup (pair, outputs).  Its waves share the planes of
 // 16 of the pair's rows and take 16 * OT outputs each at a time, B_e and base of
 // the next ones in flight while these multiply.  (One turn per workgroup spent
@@ -245,28 +299,27 @@ __device__ __forceinline__ void sum_parts(const AdaptersArgs& a, const float* sp
 // 64 on 4096 -> 11008.)  NK: 32-column steps of the rank.
 constexpr int OT = 2;
 
-template <int NK>
+template <int NK, bool VEC>
 __global__ __launch_bounds__(AW * 64, NK <= 2 ? 2 : 1) void k_ad_expand_step(AdaptersArgs a) {
   __shared__ u32x4 planes[NK][3][64];
   __shared__ uint8_t list[128];
   const int tid = threadIdx.x, l = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = l & 15, q = l >> 4;
-  TilePairs<2> r(a, 0);
+  TilePairs<2> r(a, 0, blockIdx.z);
   if (!r.next(list, true)) return;  // uniform over the workgroup
   const bool pair = r.e >= 0;
   const __amdgpu_buffer_rsrc_t br =
       make_rsrc(a.B + (int64_t)max(r.e, 0) * a.d_out * a.rank,
                 pair ? (uint32_t)(a.d_out * a.rank * 2) : 0u);
+  const __amdgpu_buffer_rsrc_t yin = y_rows(a, a.base, 0, 128), yout = y_rows(a, a.Y, 0, 128);
   const float c = !pair ? 0.f : a.scale ? a.scale[r.e] : 1.f;
   const int64_t o0 = ((int64_t)blockIdx.z * AW + w) * (OT * 16);
   const int64_t ostep = (int64_t)gridDim.z * AW * (OT * 16);
   for (int b0 = 0; b0 < r.all; b0 += 16) {
     const int at = b0 + lr;
-    const bool mine = at < r.all, live = at < r.n;
-    const int64_t t = list[min(at, r.all - 1)];
-    const float* bp = a.base ? a.base + t * a.d_out + q * 4 : nullptr;
-    float* yp = a.Y + t * a.d_out + q * 4;
+    const bool live = at < r.n;
+    const uint32_t yrow = at < r.all ? (uint32_t)(list[min(at, r.all - 1)] * a.d_out * 4) : kNoRow;
     struct Turn {
       u32x4 b[OT][NK];
       f32x4 y[OT];  // lane l holds token l & 15 and outputs 4 (l >> 4) + i of each 16
@@ -278,19 +331,10 @@ __global__ __launch_bounds__(AW * 64, NK <= 2 ? 2 : 1) void k_ad_expand_step(Ada
         for (int k = 0; k < NK; ++k) {
           const int64_t row = o + i * 16 + lr;
           const int col = k * 32 + q * 8;
-          u.b[i][k] = buf_load16(br, row < a.d_out && col < a.rank
+          u.b[i][k] = buf_load16(br, ((row < a.d_out) & (col < a.rank))
                                          ? (uint32_t)((row * a.rank + col) * 2) : kOutOfRange, 0);
         }
-        u.y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int64_t col = o + i * 16 + q * 4;
-        if (!bp || !mine) continue;
-        if (a.vec) {
-          if (col < a.d_out) u.y[i] = *(const f32x4*)(bp + o + i * 16);
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (col + x < a.d_out) u.y[i][x] = bp[o + i * 16 + x];
-        }
+        u.y[i] = load_y<VEC>(yin, yrow, o + i * 16 + q * 4, a.d_out);
       }
     };
     auto use = [&](Turn& u, int64_t o) {
@@ -308,21 +352,11 @@ __global__ __launch_bounds__(AW * 64, NK <= 2 ? 2 : 1) void k_ad_expand_step(Ada
                                                             __builtin_bit_cast(bf16x8, pl), acc[i],
                                                             0, 0, 0);
         }
-      if (!mine) return;
 #pragma unroll
       for (int i = 0; i < OT; ++i) {
-        const int64_t col = o + i * 16 + q * 4;
-        if (live) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) u.y[i][x] = fmaf(c, acc[i][x], u.y[i][x]);
-        }
-        if (a.vec) {
-          if (col < a.d_out) *(f32x4*)(yp + o + i * 16) = u.y[i];
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (col + x < a.d_out) yp[o + i * 16 + x] = u.y[i][x];
-        }
+        for (int x = 0; x < 4; ++x) u.y[i][x] = live ? fmaf(c, acc[i][x], u.y[i][x]) : u.y[i][x];
+        store_y<VEC>(u.y[i], yout, yrow, o + i * 16 + q * 4, a.d_out);
       }
     };
     Turn u0, u1;
@@ -334,11 +368,11 @@ __global__ __launch_bounds__(AW * 64, NK <= 2 ? 2 : 1) void k_ad_expand_step(Ada
       f32x4 s = {0.f, 0.f, 0.f, 0.f};
       if (b0 + sr < r.n && sc < a.rank) {
         const float* sp = a.S + (int64_t)list[b0 + sr] * a.rank + sc;
-        f32x4 v[4];
+        f32x4 v[8];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) v[p] = *(const f32x4*)(sp + (int64_t)min(p, a.nks - 1) * a.T * a.rank);
+        for (int p = 0; p < 8; ++p) v[p] = *(const f32x4*)(sp + (int64_t)min(p, a.nks - 1) * a.T * a.rank);
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
+        for (int p = 0; p < 8; ++p)
           if (p < a.nks) s += v[p];
       }
       const float s8[8] = {s.x, s.y, s.z, s.w, 0.f, 0.f, 0.f, 0.f};
@@ -350,11 +384,11 @@ __global__ __launch_bounds__(AW * 64, NK <= 2 ? 2 : 1) void k_ad_expand_step(Ada
             u32x2{pl[x].x, pl[x].y};
     }
     __syncthreads();
-    for (int64_t o = o0; o < a.d_out; o += 2 * ostep) {
-      load(u1, o + ostep);  // (past the outputs: nothing is read)
+    for (int64_t o = o0; o < a.d_out; o += 2 * ostep) {  // (past the outputs: nothing)
+      load(u1, o + ostep);
       use(u0, o);
       load(u0, o + 2 * ostep);
-      if (o + ostep < a.d_out) use(u1, o + ostep);
+      use(u1, o + ostep);
     }
   }
 }
@@ -375,7 +409,7 @@ __global__ __launch_bounds__(SW * 64) void k_ad_step(AdaptersArgs a) {
   const int tid = threadIdx.x, l = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = l & 15, q = l >> 4;
-  TilePairs<2> r(a, 0);
+  TilePairs<2> r(a, 0, 0);
   if (!r.next(list, true)) return;  // uniform over the workgroup
   const bool pair = r.e >= 0;
   const __amdgpu_buffer_rsrc_t br =
@@ -496,45 +530,91 @@ __global__ __launch_bounds__(SW * 64) void k_ad_step(AdaptersArgs a) {
   }
 }
 
-// Y of prompts: workgroup (tile, its pairs, outputs).  The planes of up to 64 gathered rows' S go
-// to LDS, once for the workgroup's four waves, which take 16 * OT outputs at a
-// time.
-template <int TC, int NK>
-__global__ __launch_bounds__(AW * 64) void k_ad_expand(AdaptersArgs a) {
+// Y of prompts: workgroup (tile, its pairs, outputs).  The planes of up to 64
+// gathered rows' S go to LDS, once for the workgroup's four waves, which take
+// 16 * OT outputs at a time against 16 rows after another.
+template <int NK, bool VEC>
+__global__ __launch_bounds__(AW * 64, NK <= 2 ? 2 : 1) void k_ad_expand(AdaptersArgs a) {
   // [block of 16 rows][step][plane][lane]: a wave's read is 1 KiB in a row
   __shared__ u32x4 planes[4][NK][3][64];
-  __shared__ uint8_t list[TC * 64];
+  __shared__ uint8_t list[64];
   const int tid = threadIdx.x, l = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = l & 15, q = l >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * TC * 64;
-  TilePairs<TC> r(a, t0);
+  const int64_t t0 = prompt_tile() * 64;
+  if (t0 >= a.T) return;
+  const __amdgpu_buffer_rsrc_t yin = y_rows(a, a.base, t0, 64), yout = y_rows(a, a.Y, t0, 64);
+  constexpr int64_t ostep = AW * (OT * 16);
+  // a range of outputs in a row, turn by turn
+  const int64_t range = ((a.d_out + ostep - 1) / ostep + gridDim.z - 1) / gridDim.z * ostep;
+  const int64_t o0 = blockIdx.z * range + w * (OT * 16), o1 = min(a.d_out, (blockIdx.z + 1) * range);
+  TilePairs<1> r(a, t0, 0);
   while (r.next(list, true)) {  // uniform over the workgroup
     const float c = r.e < 0 ? 0.f : a.scale ? a.scale[r.e] : 1.f;
     const __amdgpu_buffer_rsrc_t br =
         make_rsrc(a.B + (int64_t)max(r.e, 0) * a.d_out * a.rank,
                   r.e < 0 ? 0u : (uint32_t)(a.d_out * a.rank * 2));
-    // the first outputs' factors are asked for ahead of S
-    const int64_t ostep = (int64_t)gridDim.z * AW * (OT * 16);
-    int64_t o0 = ((int64_t)blockIdx.z * AW + w) * (OT * 16);
-    u32x4 bv[OT][NK];
-    auto load_b = [&](int64_t o) {
+    // NB blocks of 16 rows; the next outputs' factors and base are in flight
+    // while these are computed
+    auto turns = [&](auto blocks) {
+      constexpr int NB = decltype(blocks)::value;
+      uint32_t row[NB];
 #pragma unroll
-      for (int i = 0; i < OT; ++i)
+      for (int b = 0; b < NB; ++b) {
+        const int at = b * 16 + lr;
+        row[b] = at < r.all ? (uint32_t)(list[min(at, r.all - 1)] * a.d_out * 4) : kNoRow;
+      }
+      struct Turn {
+        u32x4 b[OT][NK];
+        f32x4 y[NB][OT];  // lane l holds token l & 15 and outputs 4 (l >> 4) + i of each 16
+      };
+      auto load = [&](Turn& u, int64_t o) {
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          const int64_t row = o + i * 16 + lr;
-          const int col = k * 32 + q * 8;
-          bv[i][k] = buf_load16(br, row < a.d_out && col < a.rank
-                                        ? (uint32_t)((row * a.rank + col) * 2) : kOutOfRange, 0);
+        for (int i = 0; i < OT; ++i) {
+#pragma unroll
+          for (int k = 0; k < NK; ++k) {
+            const int64_t br_row = o + i * 16 + lr;
+            const int col = k * 32 + q * 8;
+            u.b[i][k] = buf_load16(br, ((br_row < o1) & (col < a.rank))
+                                           ? (uint32_t)((br_row * a.rank + col) * 2) : kOutOfRange, 0);
+          }
         }
-    };
-    load_b(o0);
-    for (int b0 = 0; b0 < r.all; b0 += 64) {
-      // S of 64 rows: wave w takes rows b0 + 16 w ..
-      if (b0 > 0) __syncthreads();
-      if (b0 + w * 16 < r.all) {
-        const int at = b0 + w * 16 + lr;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < OT; ++i) u.y[b][i] = load_y<VEC>(yin, row[b], o + i * 16 + q * 4, o1);
+      };
+      auto use = [&](Turn& u, int64_t o) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const bool live = b * 16 + lr < r.n;
+          f32x4 acc[OT];
+#pragma unroll
+          for (int i = 0; i < OT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < NK; ++k)
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+              const u32x4 pl = planes[b][k][x][l];
+#pragma unroll
+              for (int i = 0; i < OT; ++i)
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, u.b[i][k]),
+                                                                __builtin_bit_cast(bf16x8, pl), acc[i],
+                                                                0, 0, 0);
+            }
+#pragma unroll
+          for (int i = 0; i < OT; ++i) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) u.y[b][i][x] = live ? fmaf(c, acc[i][x], u.y[b][i][x]) : u.y[b][i][x];
+            store_y<VEC>(u.y[b][i], yout, row[b], o + i * 16 + q * 4, o1);
+          }
+        }
+      };
+      Turn u0, u1;
+      load(u0, o0);
+      // S: wave w takes rows 16 w ..
+      if (w < NB) {
+        const int at = w * 16 + lr;
         const int64_t t = t0 + list[min(at, r.all - 1)];
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
@@ -550,73 +630,15 @@ __global__ __launch_bounds__(AW * 64) void k_ad_expand(AdaptersArgs a) {
         }
       }
       __syncthreads();
-      const int nb = min(4, (r.all - b0 + 15) / 16);
-      // lane l holds token l & 15 and outputs 4 (l >> 4) + i of each 16; the
-      // next block's part of base is in flight while one is computed
-      f32x4 y[OT], yn[OT];
-      auto load_y = [&](f32x4 (&v)[OT], int64_t o, int b) {
-        const int at = b0 + b * 16 + lr;
-        const float* bp = a.base + (t0 + list[min(at, r.all - 1)]) * a.d_out + o + q * 4;
-#pragma unroll
-        for (int i = 0; i < OT; ++i) {
-          v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-          const int64_t col = o + i * 16 + q * 4;
-          if (!a.base || at >= r.all) continue;
-          if (a.vec) {
-            if (col < a.d_out) v[i] = *(const f32x4*)(bp + i * 16);
-          } else {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (col + x < a.d_out) v[i][x] = bp[i * 16 + x];
-          }
-        }
-      };
-      if (o0 < a.d_out) load_y(y, o0, 0);
-      for (int64_t o = o0; o < a.d_out; o += ostep) {
-        for (int b = 0; b < nb; ++b) {
-          const int at = b0 + b * 16 + lr;
-          const bool mine = at < r.all, live = at < r.n;
-          float* yp = a.Y + (t0 + list[min(at, r.all - 1)]) * a.d_out + o + q * 4;
-          if (b + 1 < nb) load_y(yn, o, b + 1);
-          else if (o + ostep < a.d_out) load_y(yn, o + ostep, 0);
-          f32x4 acc[OT];
-#pragma unroll
-          for (int i = 0; i < OT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < NK; ++k) {
-            u32x4 pl[3];
-#pragma unroll
-            for (int x = 0; x < 3; ++x) pl[x] = planes[b][k][x][l];
-#pragma unroll
-            for (int i = 0; i < OT; ++i)
-#pragma unroll
-              for (int x = 0; x < 3; ++x)
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, bv[i][k]), __builtin_bit_cast(bf16x8, pl[x]), acc[i],
-                    0, 0, 0);
-          }
-#pragma unroll
-          for (int i = 0; i < OT; ++i) {
-            const int64_t col = o + i * 16 + q * 4;
-            if (live) {
-#pragma unroll
-              for (int x = 0; x < 4; ++x) y[i][x] = fmaf(c, acc[i][x], y[i][x]);
-            }
-            if (mine && a.vec) {
-              if (col < a.d_out) *(f32x4*)(yp + i * 16) = y[i];
-            } else if (mine) {
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (col + x < a.d_out) yp[i * 16 + x] = y[i][x];
-            }
-            y[i] = yn[i];
-          }
-        }
-        // the next outputs' factors, or the first ones again for the next rows
-        const bool more = o + ostep < a.d_out;
-        if (more || (b0 + 64 < r.all && ostep < a.d_out)) load_b(more ? o + ostep : o0);
+      for (int64_t o = o0; o < o1; o += 2 * ostep) {  // (past the outputs: nothing)
+        load(u1, o + ostep);
+        use(u0, o);
+        load(u0, o + 2 * ostep);
+        use(u1, o + ostep);
       }
-    }
+    };
+    if (r.all <= 16) turns(std::integral_constant<int, 1>{});
+    else turns(std::integral_constant<int, 4>{});
     __syncthreads();
   }
 }
@@ -637,7 +659,8 @@ hipError_t launch_ad_shrink(const AdaptersArgs& a, int slots, const Launch& L) {
   const bool step = a.T <= kAdStepTokens;
   const int64_t tiles = (a.T + (step ? 127 : 63)) / (step ? 128 : 64);
   if (tiles == 0 || a.n == 0) return hipSuccess;
-  const dim3 grid((unsigned)tiles, (unsigned)slots, (unsigned)a.nks), blk(AW * 64);
+  const dim3 grid(step ? 1u : (unsigned)((tiles + 7) / 8 * 8), (unsigned)slots, (unsigned)a.nks);
+  const dim3 blk(AW * 64);
 #define TTQ_AD_SHRINK(NR)                                                         \
   return step ? ext_launch(k_ad_shrink<2, NR, 1>, grid, blk, 0, L, a)             \
               : ext_launch(k_ad_shrink<1, NR, NR <= 4 ? 4 : 2>, grid, blk, 0, L, a);
@@ -659,13 +682,17 @@ hipError_t launch_ad_expand(const AdaptersArgs& a, int slots, const Launch& L) {
   int64_t blocks = (a.d_out + per - 1) / per;
   if (tiles == 0 || blocks == 0) return hipSuccess;
   // several blocks of outputs a workgroup, while that leaves enough of them for
-  // the chip (prompts: four per compute unit; decode steps, of whose workgroups
-  // some have no pair, eight)
-  blocks = std::max<int64_t>(1, std::min(blocks, step ? 2048 / a.T : 1024 / tiles));
-  const dim3 grid((unsigned)tiles, (unsigned)slots, (unsigned)blocks), blk(AW * 64);
-#define TTQ_AD_EXPAND(NK)                                                 \
-  return step ? ext_launch(k_ad_expand_step<NK>, grid, blk, 0, L, a)      \
-              : ext_launch(k_ad_expand<1, NK>, grid, blk, 0, L, a);
+  // the chip: two per compute unit for prompts (4096 rows: 36.5 us; one 37.9, four
+  // 40.4), eight for decode steps, where some find no pair
+  blocks = std::max<int64_t>(1, std::min(blocks, step ? 2048 / a.T : 512 / tiles));
+  const dim3 grid(step ? 1u : (unsigned)((tiles + 7) / 8 * 8), (unsigned)slots, (unsigned)blocks);
+  const dim3 blk(AW * 64);
+#define TTQ_AD_EXPAND(NK)                                                          \
+  if (step)                                                                        \
+    return a.vec ? ext_launch(k_ad_expand_step<NK, true>, grid, blk, 0, L, a)      \
+                 : ext_launch(k_ad_expand_step<NK, false>, grid, blk, 0, L, a);    \
+  return a.vec ? ext_launch(k_ad_expand<NK, true>, grid, blk, 0, L, a)             \
+               : ext_launch(k_ad_expand<NK, false>, grid, blk, 0, L, a);
   switch ((a.rank + 31) / 32) {
     case 1: TTQ_AD_EXPAND(1)
     case 2: TTQ_AD_EXPAND(2)

@@ -698,7 +698,7 @@ struct AdaptersArgs {
   float* S;               // [nks][T][rank] partial sums of A_e x
   int64_t T, n, d, d_out, rank;
   int64_t kc;             // channels per range, a multiple of 32
-  int nks;                // ranges, at most 4
+  int nks;                // ranges, at most 8 (decode steps) or 4
   int vec;                // 16-byte accesses to base and Y
 };
 // batches of up to this many rows are one tile (decode steps), longer ones go
@@ -707,7 +707,7 @@ constexpr int64_t kAdStepTokens = 128;
 // Decode steps small enough for one launch, each workgroup (512 outputs) reading
 // all of its pair's A: at most 64 KiB, 16 MiB in all.  (One row of rank 8 on
 // 512 -> 512: 8.5 us a call, 10.9 in two launches; eight rows of rank 32 on
-// 4096 -> 4096, 256 KiB each: a kernel of 12.1 us, against 5.1 + 4.4 us.)
+// 4096 -> 4096, 256 KiB each: a kernel of 12.1 us, against 4.2 + 4.4 us.)
 inline bool ad_one_launch(int64_t T, int64_t d, int64_t d_out, int64_t rank) {
   const int64_t bytes = rank * d * 2;
   return T <= kAdStepTokens && rank <= 64 && bytes <= (64 << 10) &&

@@ -165,6 +165,15 @@ def test_in_place_no_pairs_and_caller_workspace():
     z = ttq.ttq_adapters(bf(X), bf(A)[:0], bf(B)[:0], idx, base=Y)
     assert torch.equal(z, Y)
     assert ttq.ttq_adapters(bf(X)[:0], bf(A), bf(B), idx[:0]).shape == (0, 33)
+    with pytest.raises(ValueError, match="workspace"):
+        ttq.ttq_adapters(bf(X), bf(A), bf(B), idx, workspace=torch.empty(1 << 16, dtype=torch.uint8))
+    with pytest.raises(TypeError, match="workspace"):
+        ttq.ttq_adapters(bf(X), bf(A), bf(B), idx, workspace=torch.empty(1 << 16, device="cuda"))
+    big = torch.zeros(4, 8, 4096, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ttq.TTQError):  # too small for its partial sums
+        ttq.ttq_adapters(torch.zeros(200, 4096, dtype=torch.bfloat16, device="cuda"), big,
+                         big.transpose(1, 2).contiguous(), torch.zeros(200, dtype=torch.int32, device="cuda"),
+                         workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
 
 
 def test_pairs_past_2_to_31_elements():
