@@ -306,34 +306,36 @@ __device__ __forceinline__ void stage_scales(float2* sm, int pitch, const float*
 // requests, and with those the kernel stayed at 3.4 TB/s whatever its tiles.)
 // In LDS the 16-byte pieces of row r are swapped by r / 2, which puts the 16
 // rows of a read on all banks.
-template <int CB, int GS, bool WIDE = false>
+template <int CB, int GS, bool HALF>
 struct Slot {
-  // (experts of many tokens: half lines, for the sake of LDS, while they hold
-  // the 128 channels of a step)
-  static constexpr int SB = CB == 1 || (WIDE && CB <= 4) ? 64 : 128;
+  // HALF lines, while they hold 128 channels, take half the LDS, and more
+  // workgroups share a compute unit: 46 + 27 us for 16 tokens over 64 experts of
+  // 2048 / 1408, where whole lines took 53 + 33.  (The down product of one token,
+  // which a few workgroups do: 20.7 us with half lines, 17.9 with whole ones.)
+  static constexpr int SB = CB == 1 || (HALF && CB <= 4) ? 64 : 128;
   static constexpr int SG = SB * 8 / CB / GS;   // groups
   static constexpr int LPR = SB / 16;           // lanes a row
   static constexpr int RPI = 64 / LPR;          // rows a load
 };
-template <int CB, int GS, int RT, bool WIDE = false>
+template <int CB, int GS, int RT, bool HALF>
 struct Stage {
-  u32x4 c[RT * 16 / Slot<CB, GS, WIDE>::RPI];
+  u32x4 c[RT * 16 / Slot<CB, GS, HALF>::RPI];
 };
-template <int CB, int GS, int RT, int RB, bool WIDE = false>
-__device__ __forceinline__ void load_codes_of(Stage<CB, GS, RT, WIDE>& st, const Rows& r, int64_t rb,
+template <int CB, int GS, int RT, int RB, bool HALF>
+__device__ __forceinline__ void load_codes_of(Stage<CB, GS, RT, HALF>& st, const Rows& r, int64_t rb,
                                               int slot, int end, int l) {
   // (a slot at or past the end: nothing is read)
-  const uint32_t at = slot < end ? (uint32_t)(slot * Slot<CB, GS, WIDE>::SB) : kOutOfRange;
-  using S = Slot<CB, GS, WIDE>;
+  const uint32_t at = slot < end ? (uint32_t)(slot * Slot<CB, GS, HALF>::SB) : kOutOfRange;
+  using S = Slot<CB, GS, HALF>;
   constexpr int PER = RB * 16 / S::RPI;  // loads of one kind of row
 #pragma unroll
   for (int i = 0; i < RT * 16 / S::RPI; ++i)
     st.c[i] = buf_load16(i < PER ? r.c0 : r.c1,
                          (uint32_t)(((i % PER) * S::RPI + l / S::LPR) * rb + l % S::LPR * 16), at);
 }
-template <int CB, int GS, int RT, bool WIDE = false>
-__device__ __forceinline__ void put_codes(const Stage<CB, GS, RT, WIDE>& st, uint8_t* lds, int l) {
-  using S = Slot<CB, GS, WIDE>;
+template <int CB, int GS, int RT, bool HALF>
+__device__ __forceinline__ void put_codes(const Stage<CB, GS, RT, HALF>& st, uint8_t* lds, int l) {
+  using S = Slot<CB, GS, HALF>;
 #pragma unroll
   for (int i = 0; i < RT * 16 / S::RPI; ++i) {
     const int row = i * S::RPI + l / S::LPR;
@@ -341,9 +343,9 @@ __device__ __forceinline__ void put_codes(const Stage<CB, GS, RT, WIDE>& st, uin
   }
 }
 // the lane's quarter of group j of a slot, row block r
-template <int CB, int GS, bool WIDE = false>
+template <int CB, int GS, bool HALF>
 __device__ __forceinline__ GroupCodes<CB, GS> get_codes(const uint8_t* lds, int r, int j, int lr, int q) {
-  using S = Slot<CB, GS, WIDE>;
+  using S = Slot<CB, GS, HALF>;
   constexpr int NB = GroupCodes<CB, GS>::NB;
   const int row = r * 16 + lr, at = j * (GS * CB / 8) + q * NB;
   const int swz = row >> 1 & (S::LPR - 1);
@@ -373,7 +375,7 @@ __device__ __forceinline__ GroupCodes<CB, GS> get_codes(const uint8_t* lds, int 
 }
 
 // group j of a slot: RT row blocks against NB * 16 columns of planes x
-template <int CB, bool F8, int GS, int RT, int NB>
+template <int CB, bool F8, int GS, int RT, int NB, bool HALF>
 __device__ __forceinline__ void use_group(const uint8_t* lds, int j, const u32x4 (&x)[GS / 32][NB],
                                           const float2* sm, int pitch, int lr, int q,
                                           f32x4 (&acc)[RT][NB]) {
@@ -390,7 +392,7 @@ __device__ __forceinline__ void use_group(const uint8_t* lds, int j, const u32x4
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     const float2 sc = sm[r * 16 * pitch];
-    const GroupCodes<CB, GS> c = get_codes<CB, GS>(lds, r, j, lr, q);
+    const GroupCodes<CB, GS> c = get_codes<CB, GS, HALF>(lds, r, j, lr, q);
     f32x4 p[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) p[b] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -414,12 +416,12 @@ __device__ __forceinline__ void use_group(const uint8_t* lds, int j, const u32x4
 // flight while one is contracted; sm: the lane's row of the staged scales,
 // whose first group is gs0.  stage() puts them there while the first codes are
 // on their way.
-template <int CB, bool F8, int GS, int RT, int RB, int NB, class F>
+template <int CB, bool F8, int GS, int RT, int RB, int NB, bool HALF, class F>
 __device__ __forceinline__ void contract(const Rows& r, const bf16_t* const (&col)[NB], int64_t rb,
                                          int s0, int s1, int step, int G, uint8_t* lds,
                                          const float2* sm, int pitch, int gs0, int gdiv, int l,
                                          f32x4 (&acc)[RT][NB], F&& stage) {
-  using S = Slot<CB, GS>;
+  using S = Slot<CB, GS, HALF>;
   constexpr int NKS = GS / 32;
   const int lr = l & 15, q = l >> 4;
   // planes of XG groups at a time, those of a slot's first groups asked for
@@ -434,15 +436,15 @@ __device__ __forceinline__ void contract(const Rows& r, const bf16_t* const (&co
       for (int k = 0; k < NKS; ++k)
         x[j % XG][k][b] = *(const u32x4*)(col[b] + (int64_t)gg * 3 * GS + k * 32 + q * 8);
   };
-  Stage<CB, GS, RT> st;
-  load_codes_of<CB, GS, RT, RB>(st, r, rb, s0, s1, l);
+  Stage<CB, GS, RT, HALF> st;
+  load_codes_of<CB, GS, RT, RB, HALF>(st, r, rb, s0, s1, l);
 #pragma unroll
   for (int j = 0; j < XG; ++j) planes(s0, j);
   __builtin_amdgcn_sched_barrier(0);
   stage();
   for (int s = s0; s < s1; s += step) {
-    put_codes<CB, GS, RT>(st, lds, l);
-    load_codes_of<CB, GS, RT, RB>(st, r, rb, s + step, s1, l);
+    put_codes<CB, GS, RT, HALF>(st, lds, l);
+    load_codes_of<CB, GS, RT, RB, HALF>(st, r, rb, s + step, s1, l);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < S::SG; ++j) {
@@ -450,7 +452,7 @@ __device__ __forceinline__ void contract(const Rows& r, const bf16_t* const (&co
 #pragma unroll
         for (int i = 0; i < XG; ++i) planes(s, j + i);
       }
-      use_group<CB, F8, GS, RT, NB>(lds, j, x[j % XG], sm + (((s * S::SG + j) >> gdiv) - gs0), pitch,
+      use_group<CB, F8, GS, RT, NB, HALF>(lds, j, x[j % XG], sm + (((s * S::SG + j) >> gdiv) - gs0), pitch,
                                     lr, q, acc);
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -483,7 +485,7 @@ __device__ __forceinline__ void store_hidden(const MoeArgs& a, int64_t p, int64_
 // of rows.  UP: a block is RT/2 * 16 gate rows and the up rows beside them, and
 // the result goes to H; else RT * 16 down rows, and the weighted result to Yp.
 template <int CB, bool F8, int GS, int RT, int NB, int W, int KS, bool UP>
-__global__ __launch_bounds__(W * 64) void k_moe_proj(MoeArgs a) {
+__global__ __launch_bounds__(W * 64, 4) void k_moe_proj(MoeArgs a) {
   constexpr int RB = UP ? RT / 2 : RT;
   constexpr int ORDER = order_of(CB, F8);
   __shared__ int16_t list[kMoeMaxT];
@@ -514,7 +516,7 @@ __global__ __launch_bounds__(W * 64) void k_moe_proj(MoeArgs a) {
   // scale groups staged at a time; the lane's first row there: its row block's
   // rows (of both kinds) are 16 RT rows one after another
   const int pitch = a.pitch;
-  constexpr int SLOT = RT * 16 * Slot<CB, GS>::SB;
+  constexpr int SLOT = RT * 16 * Slot<CB, GS, true>::SB;
   uint8_t* slot = reinterpret_cast<uint8_t*>(dyn) + w * SLOT;
   float2* sm = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(dyn) + W * SLOT);
   const float2* sml = sm + ((w / KS) * RT * 16 + lr) * pitch;
@@ -542,12 +544,12 @@ __global__ __launch_bounds__(W * 64) void k_moe_proj(MoeArgs a) {
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int b = 0; b < NB; ++b) acc[r][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    constexpr int SG = Slot<CB, GS>::SG;
+    constexpr int SG = Slot<CB, GS, true>::SG;
     for (int gs0 = 0; gs0 < Gs; gs0 += a.ngs) {
       const int ng = min(a.ngs, (int)Gs - gs0);
       const int g1 = min(G, (gs0 + ng) << gdiv);
       const int full = ((g1 + SG - 1) / SG * SG >> gdiv) - gs0;
-      contract<CB, F8, GS, RT, RB, NB>(
+      contract<CB, F8, GS, RT, RB, NB, true>(
           rows, col, rb, (gs0 << gdiv) / SG + w % KS, (g1 + SG - 1) / SG, KS, g1, slot, sml, pitch,
           gs0, gdiv, l, acc, [&] {
             if (gs0 > 0) __syncthreads();
@@ -803,7 +805,7 @@ __global__ __launch_bounds__(W * 64) void k_moe_down_one(MoeArgs a) {
   extern __shared__ __attribute__((aligned(16))) float dyn[];
   const int l = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  constexpr int SG = Slot<CB, GS>::SG, SLOT = 16 * Slot<CB, GS>::SB;
+  constexpr int SG = Slot<CB, GS, false>::SG, SLOT = 16 * Slot<CB, GS, false>::SB;
   uint8_t* slot = reinterpret_cast<uint8_t*>(dyn) + w * SLOT;
   float2* sm = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(dyn) + W * SLOT);
   const int lr = l & 15, q = l >> 4;
@@ -827,7 +829,7 @@ __global__ __launch_bounds__(W * 64) void k_moe_down_one(MoeArgs a) {
       const int jj = min(j, a.k - 1);
       const Rows rows = expert_rows<1, false>(a, a.ids[jj], row0);
       const bf16_t* const col[1] = {a.H + (int64_t)jj * 3 * a.ff + (lr < 3 ? lr : 0) * GS};
-      contract<CB, F8, GS, 1, 1, 1>(
+      contract<CB, F8, GS, 1, 1, 1, false>(
           rows, col, a.dn_rb, (gs0 << gdiv) / SG + w % KS, live ? (g1 + SG - 1) / SG : 0, KS, g1, slot,
           sm + ((w / KS) % EP * 16 + lr) * pitch, pitch, gs0, gdiv, l, acc, [&] {
             if (j0 > 0 || gs0 > 0) __syncthreads();
@@ -883,32 +885,32 @@ hipError_t launch_proj(const MoeArgs& a, const Launch& L) {
   // of them at a time (an odd number of float2 a row, whole slots' groups); the
   // products later, in their place
   constexpr int kStage = 40 * 1024;
-  using S = Slot<CB, GS>;
   MoeArgs b = a;
-  auto lds = [&](int rows, int slots, size_t products) {
+  auto lds = [&](auto slot, int rows, int slots, size_t products) {
+    using S = decltype(slot);
     b.ngs = (int)(std::min(Gs + S::SG - 1, (int64_t)kStage / (rows * 8)) / S::SG * S::SG);
     b.pitch = b.ngs | 1;
     return (uint32_t)std::max((size_t)slots * 16 * S::SB + (size_t)rows * b.pitch * 8, products);
   };
   auto go = [&](auto kernel, int RT, int NB, int W, int KS) {
     const int rows = RT * 16 * (W / KS), per = UP ? rows / 2 : rows;
-    const uint32_t bytes = lds(rows, W * RT, (size_t)W * RT * NB * 16 * 17 * 4);
+    const uint32_t bytes = lds(Slot<CB, GS, true>{}, rows, W * RT, (size_t)W * RT * NB * 16 * 17 * 4);
     return ext_launch(kernel, dim3((unsigned)((N + per - 1) / per), (unsigned)slots), dim3(W * 64),
                       bytes, L, b);
   };
   if (!UP && a.T == 1) {
     constexpr int W = 8;
-    const uint32_t bytes = lds(16 * (W / std::max(1, W / a.k)), W, 0);
+    const uint32_t bytes = lds(Slot<CB, GS, false>{}, 16 * (W / std::max(1, W / a.k)), W, 0);
     return ext_launch(k_moe_down_one<CB, F8, GS, W>, dim3((unsigned)((N + 15) / 16)),
                       dim3(W * 64), bytes, L, b);
   }
   // Few tokens an expert (5 are 16 columns): every pass over them reads the
   // codes again, but its small workgroups fill the chip also where experts are
-  // few.  Measured, a whole call: 64 experts of 2048 / 1408, top 8, at a mean of 5
-  // tokens 160 us either way, of 8 218 us and 194 with shared planes; 8 experts
-  // of 4096 / 2816, top 2, at 6 tokens 94 and 135 us, at 10 116 and 139.
+  // few.  Measured, a whole call: 64 experts of 2048 / 1408, top 8, at a mean of 6
+  // tokens 152 us and 170 with shared planes, of 8 183 and 186, of 10 214 and 197;
+  // 8 experts of 4096 / 2816, top 2, at 10 tokens 116 and 140, at 16 153 and 142.
   const int64_t wide = (N + (UP ? 127 : 255)) / (UP ? 128 : 256) * slots;
-  if (a.T * a.k <= (wide < 512 ? 10 : 5) * (int64_t)a.E)
+  if (a.T * a.k <= (wide < 512 ? 13 : 8) * (int64_t)a.E)
     return go(k_moe_proj<CB, F8, GS, 4, 1, 4, 4, UP>, 4, 1, 4, 4);
   // many tokens an expert: passes of 16 tokens side by side, as many as a
   // mean and three of its deviations need (more take turns)

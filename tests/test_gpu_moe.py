@@ -122,6 +122,10 @@ CASES = [
     (64, 2, 1, 768, 256, 8, 256, "intzp", True),
     (90, 4, 2, 320, 64, 2, 64, "asym", True),
     (128, 9, 8, 128, 288, 4, 32, "asym", True),
+    # several passes over the codes
+    (24, 2, 1, 256, 192, 4, 64, "asym", True),
+    (13, 1, 1, 640, 96, 8, 32, "fp8", True),
+    (26, 4, 2, 512, 768, 2, 256, "sym", True),
 ]
 
 
