@@ -685,6 +685,10 @@ hipError_t launch_ad_expand(const AdaptersArgs& a, int slots, const Launch& L) {
   // the chip: two per compute unit for prompts (4096 rows: 36.5 us; one 37.9, four
   // 40.4), eight for decode steps, where some find no pair
   blocks = std::max<int64_t>(1, std::min(blocks, step ? 2048 / a.T : 512 / tiles));
+  // and workgroups of their own for a tile's further pairs, of which most find
+  // none, only where the others leave compute units idle (557 rows of four prompts,
+  // rank 24 on 3904 -> 3076: 20.0 us, 25.7 with four for every tile)
+  if (!step) slots = (int)std::max<int64_t>(1, std::min<int64_t>(slots, 256 / (tiles * blocks)));
   const dim3 grid(step ? 1u : (unsigned)((tiles + 7) / 8 * 8), (unsigned)slots, (unsigned)blocks);
   const dim3 blk(AW * 64);
 #define TTQ_AD_EXPAND(NK)                                                          \
