@@ -305,7 +305,7 @@ int ttq_qmatmul(const ttq_params* prm, const uint8_t* codes,
  *   base   optional [T][d_out] float32, e.g. what ttq_linear or ttq_qmatmul
  *          gave (0 without); may be Y itself, but not otherwise overlap it
  *   Y      [T][d_out] float32
- *   workspace of at least ttq_adapters_workspace_bytes
+ *   workspace of at least ttq_adapters_workspace_bytes (0 for small steps)
  * Both products accumulate in float32 and A_e x_t enters the second one with
  * all its 24 bits.  n_adapters = 0 copies base.  X, A and B are 16-byte
  * aligned, the rest as for ttq_linear; the same error rules. */

@@ -248,7 +248,8 @@ const char* kKernelNames[K_NUM_KINDS] = {
     "qgemv", "dequant", "qfused", "lowrank_zsum", "gemm_quant", "seg_copy",
     "pca_skinny", "pca_psum", "pca_chol", "pca_trsm", "pca_residual",
     "pca_complete", "stream_read", "cache_write", "cache_read",
-    "adapters_step", "adapters_shrink", "adapters_expand", "moe_score", "moe_route", "moe_up", "moe_down", "moe_sum"};
+    "adapters_step", "adapters_shrink", "adapters_expand", "moe_score",
+    "moe_route", "moe_up", "moe_down", "moe_sum"};
 
 hipEvent_t take_event() {
   if (!g_timing.pool.empty()) {
