@@ -591,7 +591,8 @@ def _plan(key, make):
 
 def _expect(tensors, want, dev):
     """Raise unless every tensor (None: absent) is as its (name, dtype, shape)
-    says, contiguous and on ``dev``; returns their addresses."""
+    says (shape None: part of the plan's key), contiguous and on ``dev``; returns
+    their addresses."""
     di = dev.index
     ptrs = []
     for t, (name, dtype, shape) in zip(tensors, want):
@@ -599,27 +600,37 @@ def _expect(tensors, want, dev):
             ptrs.append(None)
             continue
         try:
-            ok = (t.dtype is dtype and t.shape == shape and t.get_device() == di
-                  and t.is_contiguous())
+            ok = (t.dtype is dtype and (shape is None or t.shape == shape)
+                  and t.get_device() == di and t.is_contiguous())
         except AttributeError:
             ok = False
         if not ok:
-            _check(t, name, dtype, shape, dev)
+            _check(t, name, dtype, t.shape if shape is None else shape, dev)
         ptrs.append(t.data_ptr())
     return ptrs
 
 
-_several = None  # more than one device
+# Looked up once: torch, whether there are several devices, the entry points.
+_several = None
+_torch = None
+_lib_fn = {}
 
 
-def _enqueue(where, dev, fn, *args):
-    """Call a library entry point with the tensors' device current."""
-    global _several
+def _host():
+    global _torch, _several
     import torch
-    if _several is None:
-        _several = torch.cuda.device_count() > 1
-    if _several and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
+    _several = torch.cuda.device_count() > 1
+    _torch = torch
+    return torch
+
+
+def _enqueue(where, dev, *args):
+    """Call a library entry point with the tensors' device current."""
+    fn = _lib_fn.get(where)
+    if fn is None:
+        fn = _lib_fn[where] = getattr(load_library(), where)
+    if _several and dev.index != _torch.cuda.current_device():
+        with _torch.cuda.device(dev):
             st = fn(*args)
     else:
         st = fn(*args)
@@ -639,7 +650,7 @@ def _step_workspace(dev, stream, need, given):
     """The caller's workspace, or the stream's kept buffer (see _workspace), but
     one of its own for a call that is being captured: it then lives in the
     graph's memory, and no other graph or stream has it."""
-    import torch
+    torch = _torch
     if given is not None:
         if given.dtype is not torch.uint8:
             raise TypeError(f"workspace must be a torch.Tensor of torch.uint8, got {given.dtype}")
@@ -673,31 +684,33 @@ def ttq_adapters(X, A, B, index, *, scale=None, base=None, Y=None,
     pair).  ``base`` is what ttq_linear, ttq_linear_batched (flattened),
     ttq_linear_segmented or ttq_qmatmul gave for X; ``Y=base`` adds in place.
     """
-    import torch
-    T, d = X.shape
-    n, r, _ = A.shape
-    d_out = B.shape[1]
+    torch = _torch or _host()
+    xs, as_, bs = X.shape, A.shape, B.shape
     dev = _gpu(X, "X")
 
     def make():
+        (T, d), (n, r, _), d_out = xs, as_, bs[1]
         bf, f32 = torch.bfloat16, torch.float32
+        _check(A, "A", bf, (n, r, d), dev)
+        _check(B, "B", bf, (n, d_out, r), dev)
         prm = make_params(d=d, d_out=d_out, T=T, rank=r, bits=4, group=32, p=2.0,
                           lam=0.0, alpha=0.0)
-        return prm, max(256, ttq_adapters_workspace_bytes(prm, n)), (
-            ("X", bf, (T, d)), ("A", bf, (n, r, d)), ("B", bf, (n, d_out, r)),
+        return n, (T, d_out), ctypes.byref(prm), ttq_adapters_workspace_bytes(prm, n), (
+            ("X", bf, None), ("A", bf, None), ("B", bf, None),
             ("scale", f32, (n,)), ("index", torch.int32, (T,)),
             ("base", f32, (T, d_out)), ("Y", f32, (T, d_out)))
 
-    prm, need, want = _plan(("adapters", T, d, n, r, d_out), make)
+    n, ys, prm, need, want = _plan(("adapters", xs, as_, bs), make)
     if Y is None:
-        Y = torch.empty((T, d_out), dtype=torch.float32, device=dev)
+        Y = torch.empty(ys, dtype=torch.float32, device=dev)
     ptrs = _expect((X, A, B, scale, index, base, Y), want, dev)
     if stream is None:
         stream = _current_stream(dev)
-    workspace = _step_workspace(dev, stream, need, workspace)
-    _enqueue("ttq_adapters", dev, load_library().ttq_adapters,
-             ctypes.byref(prm), n, *ptrs, workspace.data_ptr(),
-             workspace.numel(), stream)
+    ws = size = 0
+    if need or workspace is not None:  # (small steps need none)
+        workspace = _step_workspace(dev, stream, need, workspace)
+        ws, size = workspace.data_ptr(), workspace.numel()
+    _enqueue("ttq_adapters", dev, prm, n, *ptrs, ws, size, stream)
     return Y
 
 
@@ -728,12 +741,12 @@ def ttq_moe(X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv, dn_codes,
     rows in dn_* [E, d, ...], dhalf_inv [E, d] and [E, ff]; router [E, d]
     bfloat16.  ``ids_out`` and ``weights_out`` [T, top_k] receive the chosen
     experts (int32, best first) and their weights (float32)."""
-    import torch
-    T, d = X.shape
-    E, ff = dn_dhalf_inv.shape
+    torch = _torch or _host()
+    xs, es = X.shape, dn_dhalf_inv.shape
     dev = _gpu(X, "X")
 
     def make():
+        (T, d), (E, ff) = xs, es
         prm = make_moe_params(T=T, d=d, ff=ff, experts=E, top_k=top_k, bits=bits,
                               group=group, renormalize=renormalize,
                               qformat=qformat)
@@ -741,27 +754,27 @@ def ttq_moe(X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv, dn_codes,
         bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
         rb, rf = (_row_bytes(c, bits, group) for c in (d, ff))
         gu, dn = (E, 2 * ff, d // group), (E, d, ff // group)
-        return prm, need, (
-            ("X", bf, (T, d)), ("router", bf, (E, d)),
+        return (T, d), ctypes.byref(prm), need, (
+            ("X", bf, None), ("router", bf, (E, d)),
             ("gu_codes", u8, (E, 2 * ff, rb)), ("gu_scales", f32, gu),
             ("gu_mins", f32, gu), ("gu_dhalf_inv", f32, (E, d)),
             ("dn_codes", u8, (E, d, rf)), ("dn_scales", f32, dn),
-            ("dn_mins", f32, dn), ("dn_dhalf_inv", f32, (E, ff)),
+            ("dn_mins", f32, dn), ("dn_dhalf_inv", f32, None),
             ("Y", f32, (T, d)), ("ids_out", torch.int32, (T, top_k)),
             ("weights_out", f32, (T, top_k)))
 
-    prm, need, want = _plan(("moe", T, d, ff, E, top_k, bits, group,
-                             bool(renormalize), qformat), make)
+    ys, prm, need, want = _plan(("moe", xs, es, top_k, bits, group,
+                                 bool(renormalize), qformat), make)
     if Y is None:
-        Y = torch.empty((T, d), dtype=torch.float32, device=dev)
+        Y = torch.empty(ys, dtype=torch.float32, device=dev)
     ptrs = _expect((X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv,
                     dn_codes, dn_scales, dn_mins, dn_dhalf_inv, Y, ids_out,
                     weights_out), want, dev)
     if stream is None:
         stream = _current_stream(dev)
     workspace = _step_workspace(dev, stream, need, workspace)
-    _enqueue("ttq_moe", dev, load_library().ttq_moe, ctypes.byref(prm), *ptrs,
-             workspace.data_ptr(), workspace.numel(), stream)
+    _enqueue("ttq_moe", dev, prm, *ptrs, workspace.data_ptr(), workspace.numel(),
+             stream)
     return Y
 
 
@@ -782,33 +795,34 @@ def ttq_cache_write(X, slots, codes, scales, mins, *, bits: int, group: int,
     d / group] float32), updated in place; with ``dhalf`` [d] the codes are
     those of x D^{1/2} (see include/ttq.h).
     """
-    import torch
-    T, d = X.shape
-    n_slots = codes.shape[0]
+    torch = _torch or _host()
+    xs, cs = X.shape, codes.shape
     dev = _gpu(codes, "codes")
     x_type = _elem_type(X, "X")
-    if X.device != dev:
+    if X.get_device() != dev.index:
         raise ValueError(f"X must be on {dev}, got {X.device}")
-    if d > 1 and X.stride(1) != 1:
+    ld, one = X.stride()
+    T, d = xs
+    if d > 1 and one != 1:
         raise ValueError("X must have contiguous rows")
-    ldx = X.stride(0) if T > 1 else d
+    ldx = ld if T > 1 else d
 
     def make():
-        f32 = torch.float32
+        f32, n_slots = torch.float32, cs[0]
         prm, rb = _cache_params(T, d, bits, group, qformat)
-        return prm, (
+        _check(codes, "codes", torch.uint8, (n_slots, rb), dev)
+        return n_slots, ctypes.byref(prm), (
             ("dhalf", f32, (d,)), ("slots", torch.int64, (T,)),
-            ("codes", torch.uint8, (n_slots, rb)),
+            ("codes", torch.uint8, None),
             ("scales", f32, (n_slots, d // group)),
             ("mins", f32, (n_slots, d // group)))
 
-    prm, want = _plan(("write", T, d, n_slots, bits, group, qformat), make)
+    n_slots, prm, want = _plan(("write", xs, cs, bits, group, qformat), make)
     ptrs = _expect((dhalf, slots, codes, scales, mins), want, dev)
     if stream is None:
         stream = _current_stream(dev)
-    _enqueue("ttq_cache_write", dev, load_library().ttq_cache_write,
-             ctypes.byref(prm), n_slots, x_type, X.data_ptr(), ldx, *ptrs,
-             stream)
+    _enqueue("ttq_cache_write", dev, prm, n_slots, x_type, X.data_ptr(), ldx,
+             *ptrs, stream)
 
 
 def ttq_cache_read(codes, scales, mins, pages, lens, *, bits: int, group: int,
@@ -822,37 +836,37 @@ def ttq_cache_read(codes, scales, mins, pages, lens, *, bits: int, group: int,
     for ``T`` rows of ``d`` channels is made (default: all pages, the channels
     of the stored groups; ``dtype`` bfloat16 by default).
     """
-    import torch
-    n_seq, max_pages = pages.shape
+    torch = _torch or _host()
+    ps, cs = pages.shape, codes.shape
+    dev = _gpu(codes, "codes")
     if out is None:
         d = scales.shape[1] * group if d is None else d
-        T = max_pages * page_tokens if T is None else T
-        out = torch.zeros((n_seq, T, d), dtype=dtype or torch.bfloat16,
-                          device=codes.device)
-    _, T, d = out.shape
-    n_slots = codes.shape[0]
-    dev = _gpu(codes, "codes")
+        T = ps[1] * page_tokens if T is None else T
+        out = torch.zeros((ps[0], T, d), dtype=dtype or torch.bfloat16, device=dev)
+    os_ = out.shape
     out_type = _elem_type(out, "out")
 
     def make():
+        (n_seq, max_pages), n_slots, (_, T, d) = ps, cs[0], os_
         f32, i32 = torch.float32, torch.int32
         prm, rb = _cache_params(T, d, bits, group, qformat)
-        return prm, (
-            ("pages", i32, (n_seq, max_pages)), ("lens", i32, (n_seq,)),
-            ("codes", torch.uint8, (n_slots, rb)),
+        _check(codes, "codes", torch.uint8, (n_slots, rb), dev)
+        _check(out, "out", (torch.bfloat16, f32)[out_type], (n_seq, T, d), dev)
+        return n_slots, n_seq, max_pages, ctypes.byref(prm), (
+            ("pages", i32, None), ("lens", i32, (n_seq,)),
+            ("codes", torch.uint8, None),
             ("scales", f32, (n_slots, d // group)),
             ("mins", f32, (n_slots, d // group)), ("dhalf_inv", f32, (d,)),
-            ("out", (torch.bfloat16, f32)[out_type], (n_seq, T, d)))
+            ("out", (torch.bfloat16, f32)[out_type], None))
 
-    prm, want = _plan(("read", T, d, n_slots, n_seq, max_pages, out_type, bits,
-                       group, qformat), make)
+    n_slots, n_seq, max_pages, prm, want = _plan(
+        ("read", ps, cs, os_, out_type, bits, group, qformat), make)
     *ptrs, po = _expect((pages, lens, codes, scales, mins, dhalf_inv, out), want,
                         dev)
     if stream is None:
         stream = _current_stream(dev)
-    _enqueue("ttq_cache_read", dev, load_library().ttq_cache_read,
-             ctypes.byref(prm), n_slots, n_seq, max_pages, page_tokens, *ptrs,
-             out_type, po, stream)
+    _enqueue("ttq_cache_read", dev, prm, n_slots, n_seq, max_pages, page_tokens,
+             *ptrs, out_type, po, stream)
     return out
 
 

@@ -100,9 +100,11 @@ __host__ __device__ constexpr int64_t plane_piece(int64_t c, int gs) {
   return g * 3 * gs + k * 32 + q * 8;
 }
 
-// One workgroup per token: the scores (its own, when few), every expert's rank
-// by counting those before it, the weights, and x' of the chosen ones as
-// planes.
+// The scores of a token (its own, when few), every expert's rank by counting
+// those before it, the weights, and x' of the chosen ones as planes.  Several
+// workgroups a token, each of which finds the chosen experts and writes a part of
+// the planes (16 tokens, 8 experts of 2048 channels each: 6.4 us with two, 7.9 with
+// one).
 template <int ORDER>
 __global__ __launch_bounds__(1024) void k_moe_route(MoeArgs a) {
   __shared__ double score[kMoeMaxE];
@@ -137,7 +139,7 @@ __global__ __launch_bounds__(1024) void k_moe_route(MoeArgs a) {
   __syncthreads();
   if (tid < a.E && rank[tid] < a.k) chosen[rank[tid]] = tid;
   __syncthreads();
-  if (tid < a.k) {
+  if (blockIdx.y == 0 && tid < a.k) {
     const int e = chosen[tid];
     const double top = score[chosen[0]];
     float sum = 0.f;
@@ -149,7 +151,7 @@ __global__ __launch_bounds__(1024) void k_moe_route(MoeArgs a) {
     a.w[t * a.k + tid] = expf((float)(score[e] - top)) / sum;
   }
   const int np = (int)(a.d / 8);
-  for (int i = tid; i < a.k * np; i += 1024) {
+  for (int i = blockIdx.y * 1024 + tid; i < a.k * np; i += gridDim.y * 1024) {
     const int j = i / np;
     const int64_t c = (int64_t)(i % np) * 8;
     const u32x4 xv = *(const u32x4*)(x + c);
@@ -959,7 +961,8 @@ hipError_t launch_moe_score(const MoeArgs& a, const Launch& L) {
   return ext_launch(k_moe_score, dim3((unsigned)((a.E + 3) / 4), (unsigned)a.T), dim3(256), 0, L, a);
 }
 hipError_t launch_moe_route(const MoeArgs& a, int cb, const Launch& L) {
-  const dim3 grid((unsigned)a.T), blk(1024);
+  const int64_t parts = std::min<int64_t>(256 / a.T, (a.k * (a.d / 8) + 1023) / 1024);
+  const dim3 grid((unsigned)a.T, (unsigned)std::max<int64_t>(1, parts)), blk(1024);
   switch (order_of(cb, a.qf == QF_FP8)) {
     case 1: return ext_launch(k_moe_route<1>, grid, blk, 0, L, a);
     case 2: return ext_launch(k_moe_route<2>, grid, blk, 0, L, a);
