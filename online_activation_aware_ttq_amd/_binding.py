@@ -564,7 +564,7 @@ TTQ_MOE_RENORMALIZE = 1
 
 
 def _elem_type(t, name) -> int:
-    import torch
+    torch = _torch or _host()
     dt = getattr(t, "dtype", None)
     if dt is torch.bfloat16:
         return TTQ_BF16

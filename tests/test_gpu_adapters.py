@@ -192,6 +192,25 @@ def test_pairs_past_2_to_31_elements():
     assert torch.equal(Y.double(), ref)
 
 
+@pytest.mark.parametrize("T", [128, 200])
+def test_tiles_of_2_to_31_bytes(T):
+    """Whole numbers, so exact: the first and last of 2^22 outputs of every row."""
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    g = torch.Generator(device="cuda").manual_seed(T)
+    do = 1 << 22
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g, device="cuda").to(torch.bfloat16)
+    X, A, B = ints(T, 64), ints(2, 8, 64), ints(2, do, 8)
+    idx = (torch.arange(T, device="cuda") % 3 - 1).to(torch.int32)
+    Y = ttq.ttq_adapters(X, A, B, idx)
+    for cols in (slice(0, 300), slice(do - 300, do)):
+        ref = torch.zeros(T, 300, dtype=torch.float64)
+        for e in (0, 1):
+            rows = (idx == e).cpu()
+            ref[rows] = X.double().cpu()[rows] @ A[e].double().cpu().T @ B[e, cols].double().cpu().T
+        assert torch.equal(Y[:, cols].double().cpu(), ref)
+
+
 def test_captured_graphs_do_not_share_a_workspace():
     import torch
     import online_activation_aware_ttq_amd as ttq
