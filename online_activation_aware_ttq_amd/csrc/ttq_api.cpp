@@ -1251,7 +1251,9 @@ struct MoePlan {
   size_t off_ids = 0, off_w = 0, off_score = 0, off_xp = 0, off_h = 0, off_yp = 0,
          total = 0;
 };
-// one workgroup per token takes up to this many router weights itself
+// the routing kernel takes up to this many router weights itself (8 experts of
+// 4096 channels, one token: 50.4 us a call, 54.4 with a launch of their own; 64 of
+// 2048, 16 tokens: 93.5 and 87.2)
 constexpr int64_t kMoeRouteElems = 65536;
 
 int validate_moe(const ttq_moe_params* prm, MoePlan* P) {
