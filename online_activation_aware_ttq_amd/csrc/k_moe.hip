@@ -892,24 +892,31 @@ hipError_t launch_proj(const MoeArgs& a, const Launch& L) {
   const int64_t Gs = (UP ? a.d : a.ff) >> a.gshift;
   // LDS: the waves' slots, and `rows` rows of staged scales, up to kStage bytes
   // of them at a time (an odd number of float2 a row, whole slots' groups); the
-  // products later, in their place
-  constexpr int kStage = 40 * 1024;
+  // products later, in their place.  More than 64 KiB of dynamic LDS would have to
+  // be allowed per kernel: 16 slots of 64 bytes a row leave 48 KiB for the scales,
+  // those of 8-bit codes, of 128, leave 32 (as a multiple of 4 slots' groups, in
+  // which the waves take turns, 24 of them: the sums keep their order).
+  constexpr int kStage = 40 * 1024, kStage8 = 24 * 1024;
+  constexpr uint32_t kMoeLds = 64 * 1024;
   MoeArgs b = a;
   auto lds = [&](auto slot, int rows, int slots, size_t products) {
     using S = decltype(slot);
-    b.ngs = (int)(std::min(Gs + S::SG - 1, (int64_t)kStage / (rows * 8)) / S::SG * S::SG);
+    const int64_t stage = CB == 8 && slots == 16 ? kStage8 : kStage;
+    b.ngs = (int)(std::min(Gs + S::SG - 1, stage / (rows * 8)) / S::SG * S::SG);
     b.pitch = b.ngs | 1;
     return (uint32_t)std::max((size_t)slots * 16 * S::SB + (size_t)rows * b.pitch * 8, products);
   };
   auto go = [&](auto kernel, int RT, int NB, int W, int KS) {
     const int rows = RT * 16 * (W / KS), per = UP ? rows / 2 : rows;
     const uint32_t bytes = lds(Slot<CB, GS, true>{}, rows, W * RT, (size_t)W * RT * NB * 16 * 17 * 4);
+    if (bytes > kMoeLds) return hipErrorInvalidValue;
     return ext_launch(kernel, dim3((unsigned)((N + per - 1) / per), (unsigned)slots), dim3(W * 64),
                       bytes, L, b);
   };
   if (!UP && a.T == 1) {
     constexpr int W = 8;
     const uint32_t bytes = lds(Slot<CB, GS, false>{}, 16 * (W / std::max(1, W / a.k)), W, 0);
+    if (bytes > kMoeLds) return hipErrorInvalidValue;
     return ext_launch(k_moe_down_one<CB, F8, GS, W>, dim3((unsigned)((N + 15) / 16)),
                       dim3(W * 64), bytes, L, b);
   }
