@@ -337,10 +337,13 @@ __device__ __forceinline__ void load_codes_of(Stage<CB, GS, RT, HALF>& st, const
   const uint32_t at = slot < end ? (uint32_t)(slot * Slot<CB, GS, HALF>::SB) : kOutOfRange;
   using S = Slot<CB, GS, HALF>;
   constexpr int PER = RB * 16 / S::RPI;  // loads of one kind of row
+  // Behind a row's end lie the next row's codes, and zeros are put in their place:
+  // the scales of those groups are 0, but 0 times an E4M3 NaN is not.
+  const uint32_t col = l % S::LPR * 16;
+  const uint32_t off = slot * S::SB + col < (uint32_t)rb ? l / S::LPR * (uint32_t)rb + col : kOutOfRange;
 #pragma unroll
   for (int i = 0; i < RT * 16 / S::RPI; ++i)
-    st.c[i] = buf_load16(i < PER ? r.c0 : r.c1,
-                         (uint32_t)(((i % PER) * S::RPI + l / S::LPR) * rb + l % S::LPR * 16), at);
+    st.c[i] = buf_load16(i < PER ? r.c0 : r.c1, off + (uint32_t)((i % PER) * S::RPI * rb), at);
 }
 template <int CB, int GS, int RT, bool HALF>
 __device__ __forceinline__ void put_codes(const Stage<CB, GS, RT, HALF>& st, uint8_t* lds, int l) {

@@ -1,0 +1,25 @@
+"""What is not finite, or overflows, in ttq_moe: where it may be seen."""
+import numpy as np
+import pytest
+
+from test_gpu_moe import _bf16, _reference, _run, _stored
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 2, 2), (1, 1, 1), (3, 2, 2), (40, 1, 1)])
+def test_a_row_of_nan_codes_stays_in_its_output(T, E, k):
+    """Rows of 96 channels end inside a slot of codes: the next row's codes lie
+    behind theirs.  A down row of NaN (E4M3 codes 0x7F) is its own output's alone."""
+    rng = np.random.default_rng(T)
+    d = ff = 96
+    X, Wr = _bf16(rng.standard_normal((T, d))), _bf16(rng.standard_normal((E, d)) * 0.1)
+    gu, dn = (_stored(rng, E, r, c, 8, 32, "fp8") for r, c in ((2 * ff, d), (d, ff)))
+    ref, tol, _, _ = _reference(X, Wr, gu, dn, k, 32)
+    for row in (1, 16, 63, 95):
+        codes = dn["packed"].copy()
+        codes[:, row] = 0x7F
+        y, _, _ = _run(X, Wr, gu, dict(dn, packed=codes), k, 8, 32, "fp8")
+        rest = np.arange(d) != row
+        assert np.isnan(y[:, row]).all()
+        assert (np.abs(y - ref)[:, rest] <= tol[:, rest]).all(), row
