@@ -69,8 +69,9 @@ __device__ __forceinline__ double score_part(const bf16_t* x, const bf16_t* r, i
       if (c + i * step >= d) break;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s0 += (double)(bf16lo(xv[i][j]) * bf16lo(rv[i][j]));
-        s1 += (double)(bf16hi(xv[i][j]) * bf16hi(rv[i][j]));
+        // (in float64: exact also where the product leaves float32's range)
+        s0 = fma((double)bf16lo(xv[i][j]), (double)bf16lo(rv[i][j]), s0);
+        s1 = fma((double)bf16hi(xv[i][j]), (double)bf16hi(rv[i][j]), s1);
       }
     }
   }

@@ -23,3 +23,24 @@ def test_a_row_of_nan_codes_stays_in_its_output(T, E, k):
         rest = np.arange(d) != row
         assert np.isnan(y[:, row]).all()
         assert (np.abs(y - ref)[:, rest] <= tol[:, rest]).all(), row
+
+
+@pytest.mark.parametrize("E,d", [(6, 128), (70, 1024)])
+@pytest.mark.parametrize("exp", [70, -80])
+def test_scores_whose_products_leave_float32(E, d, exp):
+    """Scores are float64: two bfloat16 values of 2^70 have a product of 2^140,
+    two of 2^-80 one of 2^-160.  (70 experts of 1024: the scores' own launch.)"""
+    rng = np.random.default_rng(E + exp + 100)
+    T, ff, k = 3, 64, 4
+    X, Wr = np.zeros((T, d)), np.zeros((E, d))
+    X[:, 5] = 2.0 ** exp
+    Wr[:, 5] = rng.permutation(E) * 2.0 ** exp * np.where(np.arange(E) % 3 == 0, -1, 1)
+    gu, dn = (_stored(rng, E, r, c, 4, 32, "asym") for r, c in ((2 * ff, d), (d, ff)))
+    gu["dhi"][:, 5] = 0                       # the channel is the router's alone
+    X[:, 7:] = rng.standard_normal((T, d - 7))
+    X = _bf16(X)
+    ref, tol, ids, w = _reference(X, Wr, gu, dn, k, 32)
+    y, gi, gw = _run(X, Wr, gu, dn, k, 4, 32, "asym")
+    np.testing.assert_array_equal(gi, ids)
+    assert np.abs(gw - w).max() <= 2.0 ** -20
+    assert np.isfinite(y).all() and (np.abs(y - ref) <= tol).all()
