@@ -307,7 +307,9 @@ int ttq_qmatmul(const ttq_params* prm, const uint8_t* codes,
  *   Y      [T][d_out] float32
  *   workspace of at least ttq_adapters_workspace_bytes (0 for small steps)
  * Both products accumulate in float32 and A_e x_t enters the second one with
- * all its 24 bits.  n_adapters = 0 copies base.  X, A and B are 16-byte
+ * all its 24 bits, as a sum of three parts.  An infinity in A_e x_t keeps its
+ * sign in the outputs; one in B_e makes its own output infinite or NaN (a part
+ * that is 0 times it).  n_adapters = 0 copies base.  X, A and B are 16-byte
  * aligned, the rest as for ttq_linear; the same error rules. */
 int ttq_adapters_workspace_bytes(const ttq_params* prm, int64_t n_adapters,
                                  size_t* bytes);
@@ -338,7 +340,10 @@ int ttq_adapters(const ttq_params* prm, int64_t n_adapters, const void* X,
  *   ids_out, weights_out   optional [T][top_k] int32 / float32, best first
  *   workspace of at least ttq_moe_workspace_bytes
  * The contractions accumulate in float32, with x D^{-1/2} and h D^{-1/2} in
- * all their 24 bits.  Larger T, experts or top_k are TTQ_EUNSUPPORTED.  X,
+ * all their 24 bits.  A token whose x D^{-1/2}, or whose h D^{-1/2} for one of
+ * its experts, holds an infinity or a NaN (h overflows float32 at 3.4e38) has a
+ * row of NaN; the other rows are as they would be without it.
+ * Larger T, experts or top_k are TTQ_EUNSUPPORTED.  X,
  * router, codes, dhalf_inv and Y are 16-byte aligned, the rest their type's;
  * the error rules of ttq_linear. */
 #define TTQ_MOE_RENORMALIZE 1u

@@ -44,3 +44,31 @@ def test_scores_whose_products_leave_float32(E, d, exp):
     np.testing.assert_array_equal(gi, ids)
     assert np.abs(gw - w).max() <= 2.0 ** -20
     assert np.isfinite(y).all() and (np.abs(y - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("T,E", [(1, 2), (4, 2), (40, 1)])
+@pytest.mark.parametrize("how", ["x", "hidden"])
+def test_what_overflows_makes_its_own_row_nan(T, E, how):
+    """An infinite x D^{-1/2}, or a product of gate and up past float32, is a row
+    of NaN; every other row has the bits that it has without it."""
+    rng = np.random.default_rng(T)
+    d, ff = 96, 160
+    X, Wr = _bf16(rng.standard_normal((T, d))), _bf16(rng.standard_normal((E, d)) * 0.1)
+    Wr[:, 9] = 0
+    X[:, 9] = 1
+    gu, dn = (_stored(rng, E, r, c, 8, 32, "asym") for r, c in ((2 * ff, d), (d, ff)))
+    ok, ids, w = _run(X, Wr, gu, dn, 1, 8, 32, "asym")
+    assert np.isfinite(ok).all()
+    bad = X.copy()
+    if how == "x":
+        gu["dhi"][:, 9] = 8                   # 2^126 times 8 is infinite, 1 times 8 is 8
+        ok, ids, w = _run(X, Wr, gu, dn, 1, 8, 32, "asym")
+        bad[T // 2, 9] = 2.0 ** 126
+    else:
+        bad[T // 2, 9] = 2.0 ** 80            # gate and up of 2^75 and more
+    y, gi, gw = _run(bad, Wr, gu, dn, 1, 8, 32, "asym")
+    rest = np.arange(T) != T // 2
+    np.testing.assert_array_equal(gi, ids)    # (the router does not see the channel)
+    np.testing.assert_array_equal(gw, w)
+    assert np.isnan(y[T // 2]).all()
+    np.testing.assert_array_equal(y[rest], ok[rest])
