@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -179,38 +180,76 @@ def _params(d, d_out, T, rank, bits, group, p, lam, alpha, flags, qformat):
     return prm, key
 
 
+# Looked up once: torch, and whether there are several devices.
+_several = None
+_torch = None
+
+
+def _host():
+    global _torch, _several
+    import torch
+    _several = torch.cuda.device_count() > 1
+    _torch = torch
+    return torch
+
+
 def _current_stream(dev) -> int:
     """Raw handle of torch's current stream on `dev` (the cheap accessor when
     this torch build has it)."""
-    import torch
+    torch = _torch or _host()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is not None:
         return raw(dev.index if dev.index is not None else torch.cuda.current_device())
     return torch.cuda.current_stream(dev).cuda_stream
 
 
-# Workspace for calls that bring none: one buffer per (device, stream), kept
-# between calls.  Calls on one stream run in order, so they can share it;
-# calls on different streams get different buffers.  When a buffer has to
-# grow, the stream is drained before the old one is released.
+# Workspace for calls that bring none: one buffer per (thread, device, stream),
+# kept between calls.  A thread's calls on one stream run in order, so they can
+# share it; the kernels of two threads' calls may alternate on a stream, and calls
+# on different streams run at once: those get different buffers.  A call that is
+# being captured gets one of its own, which lives in the graph's memory: no other
+# graph or call has it, and none is released under a graph.  (A capture that torch
+# does not know of, by hipStreamBeginCapture, has no such memory: it has to bring
+# its workspace.)  Buffers are taken as memory of the stream that uses them, where
+# what was released is used again only behind the kernels enqueued before.
 _NEED = {}
-_SCRATCH = {}
+
+
+class _Scratch(threading.local):
+    def __init__(self):
+        self.kept = {}
+
+
+_SCRATCH = _Scratch()
+
+
+def _is_current(dev, stream):
+    """Whether ``stream`` of ``dev`` is where torch allocates and enqueues now."""
+    return stream == _current_stream(dev) and not (
+        _several and dev.index != _torch.cuda.current_device())
+
+
+def _scratch(torch, dev, stream, need):
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    kept, key = _SCRATCH.kept, (dev.index, stream)
+    buf = kept.get(key)
+    if buf is None or buf.numel() < need:
+        buf = kept[key] = torch.empty(need, dtype=torch.uint8, device=dev)
+    return buf
 
 
 def _workspace(dev, stream, need_key, query):
-    import torch
+    torch = _torch or _host()
     need = _NEED.get(need_key) if need_key is not None else None
     if need is None:
         need = max(int(query()), 256)
         if need_key is not None:
             _NEED[need_key] = need
-    key = (dev.index, stream)
-    buf = _SCRATCH.get(key)
-    if buf is None or buf.numel() < need:
-        if buf is not None:
-            torch.cuda.synchronize(dev)
-        buf = _SCRATCH[key] = torch.empty(need, dtype=torch.uint8, device=dev)
-    return buf
+    if _is_current(dev, stream):
+        return _scratch(torch, dev, stream, need)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+        return _scratch(torch, dev, stream, need)
 
 
 def ttq_status_string(status: int) -> str:
@@ -610,18 +649,8 @@ def _expect(tensors, want, dev):
     return ptrs
 
 
-# Looked up once: torch, whether there are several devices, the entry points.
-_several = None
-_torch = None
+# Entry points, looked up once.
 _lib_fn = {}
-
-
-def _host():
-    global _torch, _several
-    import torch
-    _several = torch.cuda.device_count() > 1
-    _torch = torch
-    return torch
 
 
 def _enqueue(where, dev, *args):
@@ -647,21 +676,13 @@ def _gpu(t, name):
 
 
 def _step_workspace(dev, stream, need, given):
-    """The caller's workspace, or the stream's kept buffer (see _workspace), but
-    one of its own for a call that is being captured: it then lives in the
-    graph's memory, and no other graph or stream has it."""
-    torch = _torch
+    """The caller's workspace, or one of ``need`` bytes (see _workspace)."""
     if given is not None:
-        if given.dtype is not torch.uint8:
+        if given.dtype is not _torch.uint8:
             raise TypeError(f"workspace must be a torch.Tensor of torch.uint8, got {given.dtype}")
         if given.device != dev or not given.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {dev}, got {given.device}")
         return given
-    if torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    buf = _SCRATCH.get((dev.index, stream))
-    if buf is not None and buf.numel() >= need:
-        return buf
     return _workspace(dev, stream, None, lambda: need)
 
 
