@@ -252,6 +252,18 @@ def _workspace(dev, stream, need_key, query):
         return _scratch(torch, dev, stream, need)
 
 
+def _result(shape, dtype, dev, stream, make=None):
+    """Memory for a result of a call on ``stream`` (None: torch's current one),
+    taken, and with ``make`` (torch.zeros) filled, there: in the order of that
+    stream's work, and reused in it."""
+    torch = _torch or _host()
+    make = make or torch.empty
+    if stream is None or _is_current(dev, stream):
+        return make(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
+        return make(shape, dtype=dtype, device=dev)
+
+
 def ttq_status_string(status: int) -> str:
     return load_library().ttq_status_string(int(status)).decode()
 
@@ -320,7 +332,7 @@ def _call(batched: bool, W, X, B, A, *, p, lam, alpha, bits, group, Y,
     prm, key = _params(d, d_out, T, rank, bits, group, p, lam, alpha, flags,
                        qformat)
     if Y is None:
-        Y = torch.empty(lead + (T, d_out), dtype=torch.float32, device=dev)
+        Y = _result(lead + (T, d_out), torch.float32, dev, stream)
     _check(Y, "Y", torch.float32, lead + (T, d_out), dev)
     _check(codes_out, "codes_out", torch.uint8, lead + (d_out, d), dev)
     _check(scales_out, "scales_out", torch.float32, lead + (d_out, G), dev)
@@ -357,7 +369,9 @@ def ttq_linear(W, X, B=None, A=None, *, p: float, lam: float, alpha: float,
     """Y[T, d_out] = Q_D[W] X + B (A X) for one request (see include/ttq.h).
 
     W [d_out, d], X [T, d], B [d_out, r], A [r, d] are bfloat16 GPU tensors;
-    Y is float32.  Enqueued on ``stream`` (default: torch's current stream).
+    Y is float32.  Enqueued on ``stream`` (default: torch's current stream); the
+    results that this and the other calls make are memory of that stream, as if
+    made under ``torch.cuda.stream``.
     """
     return _call(False, W, X, B, A, p=p, lam=lam, alpha=alpha, bits=bits,
                  group=group, Y=Y, codes_out=codes_out, scales_out=scales_out,
@@ -436,7 +450,7 @@ def ttq_linear_segmented(W, X, B=None, A=None, *, seg_offsets, p: float,
                       group=group, p=p, lam=lam, alpha=alpha, flags=flags,
                       qformat=qformat)
     if Y is None:
-        Y = torch.empty((T, d_out), dtype=torch.float32, device=dev)
+        Y = _result((T, d_out), torch.float32, dev, stream)
     _check(Y, "Y", torch.float32, (T, d_out), dev)
     _check(codes_out, "codes_out", torch.uint8, (n, d_out, d), dev)
     _check(scales_out, "scales_out", torch.float32, (n, d_out, G), dev)
@@ -527,13 +541,13 @@ def ttq_quantize(W, X, *, p: float, lam: float, alpha: float, bits: int,
     _check(W, "W", torch.bfloat16, (d_out, d), dev)
     _check(X, "X", torch.bfloat16, (T, d), dev)
     if codes is None:
-        codes = torch.empty((d_out, rb), dtype=torch.uint8, device=dev)
+        codes = _result((d_out, rb), torch.uint8, dev, stream)
     if scales is None:
-        scales = torch.empty((d_out, G), dtype=torch.float32, device=dev)
+        scales = _result((d_out, G), torch.float32, dev, stream)
     if mins is None:
-        mins = torch.empty((d_out, G), dtype=torch.float32, device=dev)
+        mins = _result((d_out, G), torch.float32, dev, stream)
     if dhalf_inv is None:
-        dhalf_inv = torch.empty((d,), dtype=torch.float32, device=dev)
+        dhalf_inv = _result((d,), torch.float32, dev, stream)
     _check(codes, "codes", torch.uint8, (d_out, rb), dev)
     _check(scales, "scales", torch.float32, (d_out, G), dev)
     _check(mins, "mins", torch.float32, (d_out, G), dev)
@@ -581,7 +595,7 @@ def ttq_qmatmul(codes, scales, mins, dhalf_inv, X, B=None, A=None, *,
     _check(B, "B", torch.bfloat16, (d_out, rank), dev)
     _check(A, "A", torch.bfloat16, (rank, d), dev)
     if Y is None:
-        Y = torch.empty((T, d_out), dtype=torch.float32, device=dev)
+        Y = _result((T, d_out), torch.float32, dev, stream)
     _check(Y, "Y", torch.float32, (T, d_out), dev)
     if stream is None:
         stream = _current_stream(dev)
@@ -723,7 +737,7 @@ def ttq_adapters(X, A, B, index, *, scale=None, base=None, Y=None,
 
     n, ys, prm, need, want = _plan(("adapters", xs, as_, bs), make)
     if Y is None:
-        Y = torch.empty(ys, dtype=torch.float32, device=dev)
+        Y = _result(ys, torch.float32, dev, stream)
     ptrs = _expect((X, A, B, scale, index, base, Y), want, dev)
     if stream is None:
         stream = _current_stream(dev)
@@ -787,7 +801,7 @@ def ttq_moe(X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv, dn_codes,
     ys, prm, need, want = _plan(("moe", xs, es, top_k, bits, group,
                                  bool(renormalize), qformat), make)
     if Y is None:
-        Y = torch.empty(ys, dtype=torch.float32, device=dev)
+        Y = _result(ys, torch.float32, dev, stream)
     ptrs = _expect((X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv,
                     dn_codes, dn_scales, dn_mins, dn_dhalf_inv, Y, ids_out,
                     weights_out), want, dev)
@@ -863,7 +877,7 @@ def ttq_cache_read(codes, scales, mins, pages, lens, *, bits: int, group: int,
     if out is None:
         d = scales.shape[1] * group if d is None else d
         T = ps[1] * page_tokens if T is None else T
-        out = torch.zeros((ps[0], T, d), dtype=dtype or torch.bfloat16, device=dev)
+        out = _result((ps[0], T, d), dtype or torch.bfloat16, dev, stream, torch.zeros)
     os_ = out.shape
     out_type = _elem_type(out, "out")
 
@@ -921,10 +935,9 @@ def ttq_lowrank_pca(W, Omega, *, iters: int, X=None, p: float = 2.0,
         _check(X, "X", torch.bfloat16, (T, d), dev)
     prm = make_params(d=d, d_out=d_out, T=T, rank=r, bits=4, group=32, p=p,
                       lam=lam, alpha=alpha)
-    B = torch.empty((d_out, r), dtype=torch.bfloat16, device=dev)
-    A = torch.empty((r, d), dtype=torch.bfloat16, device=dev)
-    Wres = torch.empty((d_out, d), dtype=torch.bfloat16, device=dev) \
-        if want_residual else None
+    B = _result((d_out, r), torch.bfloat16, dev, stream)
+    A = _result((r, d), torch.bfloat16, dev, stream)
+    Wres = _result((d_out, d), torch.bfloat16, dev, stream) if want_residual else None
     if stream is None:
         stream = _current_stream(dev)
     if workspace is None:
@@ -949,7 +962,7 @@ def stream_read(src, sink=None, stream=None):
     nbytes = src.numel() * src.element_size()
     nblk = -(-nbytes // (128 * 1024))
     if sink is None:
-        sink = torch.empty(max(1, nblk), dtype=torch.int32, device=src.device)
+        sink = _result(max(1, nblk), torch.int32, src.device, stream)
     if stream is None:
         stream = _current_stream(src.device)
     st = load_library().ttq_stream_read(_ptr(src), nbytes, _ptr(sink), stream)

@@ -99,3 +99,34 @@ def test_captured_on_a_stream_given_as_argument():
         assert _same(eager, bigger)
         for a, b in zip(got, want):
             assert _same(a, b)
+
+
+def test_results_of_a_stream_given_as_argument():
+    """While torch's current stream is busy: what the call makes, zeros behind the
+    lengths among it, is in the order of the call's stream."""
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    d, n = 1024, 64
+    codes = torch.zeros(n, d // 2, dtype=torch.uint8, device="cuda")
+    s, m = torch.zeros(n, d // 128, device="cuda"), torch.zeros(n, d // 128, device="cuda")
+    X = torch.randn(n, d, device="cuda")
+    kw = dict(bits=4, group=128)
+    ttq.ttq_cache_write(X, torch.arange(n, device="cuda"), codes, s, m, **kw)
+    pages = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([50], dtype=torch.int32, device="cuda")
+    read = lambda **k: ttq.ttq_cache_read(codes, s, m, pages, lens, page_tokens=16, **kw, **k)
+    run = _layer(7)
+    want, layer = read(), run()
+    a = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for _ in range(8):
+            a = a @ a * 1e-2                  # some milliseconds of the current stream
+        got, rows = read(stream=side.cuda_stream), run(stream=side.cuda_stream)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            got, rows = got.clone(), [r.clone() for r in rows]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and _same(rows, layer)
+        assert (got[0, 50:] == 0).all() and (got[0, :50] != 0).any(1).all()

@@ -103,3 +103,56 @@ def test_memory_is_taken_on_the_stream_that_uses_it(streams, step):
     for stream in (5, 11):
         assert streams.taken[get(stream, 3000, step).data_ptr()] == stream
     assert streams.now == 5
+
+
+class Fake:
+    """What the entry points ask of a GPU tensor."""
+
+    def __init__(self, shape, dtype):
+        self.shape = torch.Size([shape] if isinstance(shape, int) else shape)
+        self.dtype, self.device = dtype, torch.device("cuda", 0)
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x7f0000000000
+
+    def numel(self):
+        return self.shape.numel()
+
+
+@pytest.mark.parametrize("stream", [None, 5, 9])
+def test_results_are_made_on_the_stream_of_the_call(streams, monkeypatch, stream):
+    """In the order of its work: the zeros behind a cache read's lengths above all,
+    which another stream would write at any time, over the rows that were read."""
+    import online_activation_aware_ttq_amd as ttq
+    made = []
+
+    def make(shape, dtype=None, device=None):
+        made.append(streams.now)
+        return Fake(shape, dtype)
+
+    monkeypatch.setattr(torch, "empty", make)
+    monkeypatch.setattr(torch, "zeros", make)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(_binding, "_enqueue", lambda *a: None)
+    monkeypatch.setenv("TTQ_INJECT_HIP_ERROR", "1")  # for those that call the library directly
+    bf, f32, u8, i32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+    X, codes, s = Fake((3, 64), bf), Fake((8, 32), u8), Fake((8, 2), f32)
+    kw = dict(bits=4, group=32, stream=stream)
+    ttq.ttq_cache_read(codes, s, s, Fake((1, 2), i32), Fake((1,), i32), page_tokens=4, **kw)
+    ttq.ttq_adapters(X, Fake((2, 8, 64), bf), Fake((2, 16, 8), bf), Fake((3,), i32), stream=stream)
+    ttq.ttq_moe(X, Fake((2, 64), bf), Fake((2, 128, 32), u8), Fake((2, 128, 2), f32),
+                Fake((2, 128, 2), f32), Fake((2, 64), f32), Fake((2, 64, 32), u8), Fake((2, 64, 2), f32),
+                Fake((2, 64, 2), f32), Fake((2, 64), f32), top_k=1, **kw)
+    with pytest.raises(ttq.TTQError):
+        ttq.ttq_qmatmul(codes, s, s, Fake((64,), f32), X, **kw)
+    with pytest.raises(ttq.TTQError):
+        ttq.ttq_quantize(Fake((8, 64), bf), X, p=2.0, lam=0.0, alpha=0.5, **kw)
+    with pytest.raises(ttq.TTQError):
+        ttq.ttq_linear(Fake((8, 64), bf), X, p=2.0, lam=0.0, alpha=0.5, **kw)
+    assert len(made) >= 8 and set(made) == {stream or 5}
