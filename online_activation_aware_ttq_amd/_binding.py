@@ -180,26 +180,27 @@ def _params(d, d_out, T, rank, bits, group, p, lam, alpha, flags, qformat):
     return prm, key
 
 
-# Looked up once: torch, and whether there are several devices.
-_several = None
+# Looked up once: torch, its cheap accessor of the current stream's raw handle
+# (where this torch build has it), and whether there are several devices.
 _torch = None
+_raw_stream = None
+_several = None
 
 
 def _host():
-    global _torch, _several
+    global _torch, _raw_stream, _several
     import torch
     _several = torch.cuda.device_count() > 1
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _torch = torch
     return torch
 
 
 def _current_stream(dev) -> int:
-    """Raw handle of torch's current stream on `dev` (the cheap accessor when
-    this torch build has it)."""
+    """Raw handle of torch's current stream on `dev`."""
     torch = _torch or _host()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:
-        return raw(dev.index if dev.index is not None else torch.cuda.current_device())
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
 
 
@@ -697,6 +698,8 @@ def _step_workspace(dev, stream, need, given):
         if given.device != dev or not given.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {dev}, got {given.device}")
         return given
+    if _is_current(dev, stream):
+        return _scratch(_torch, dev, stream, need)
     return _workspace(dev, stream, None, lambda: need)
 
 
