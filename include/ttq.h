@@ -372,14 +372,18 @@ int ttq_moe(const ttq_moe_params* prm, const void* X, const void* router,
  * the K and V rows of a decoder ("Test-time quantization: quantising on the
  * fly with no calibration dataset", lo0 blog: KV-cache scales derived on the
  * fly by the same logic).  A cache has n_slots rows of d channels (all heads
- * of a token, K and V side by side or in two caches), each stored as a weight
+ * of a token, K and V side by side or in two caches), each laid out as a weight
  * row of ttq_quantize is: `bits` wide codes packed in ttq_packed_row_bytes,
  * and float32 scales and mins per group:
  *   codes [n_slots][row_bytes], scales, mins [n_slots][d/group].
  * Formats and the float32 code decision are those of TTQ_QF_*, except that a
  * scale is the group's range times the float32 nearest to 1/N (1/Z for
- * TTQ_QF_SYM, 1/448 for TTQ_QF_FP8) instead of the range divided by it (at
- * most one unit in the last place away).
+ * TTQ_QF_SYM, 1/448 for TTQ_QF_FP8) instead of the range divided by it.  So a
+ * row's bits are not those that ttq_quantize gives it: scales are up to three
+ * half units in the last place apart, and a value half way between two levels
+ * may get the other one (0.01 to 0.14 % of the levels of normal bfloat16 rows,
+ * which are often half way, next to none with dhalf); either is within half a
+ * step of it.
  * With dhalf, the D^{1/2} of each channel (e.g. dhalf_out of ttq_quantize for
  * the prompt's queries), the codes are those of x D^{1/2}; reading with
  * dhalf_inv = 1 / dhalf undoes it.

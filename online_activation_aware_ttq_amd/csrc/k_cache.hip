@@ -4,7 +4,7 @@
 // the same logic applied to the cache).
 //
 // A cache row holds all C channels of a token (every head of K and V) and is
-// stored as ttq_quantize stores a weight row: CB-bit containers, a scale and
+// laid out as ttq_quantize lays out a weight row: CB-bit containers, a scale and
 // an offset per group of GS channels.  With D^{1/2} given (e.g. of the
 // prompt's queries) the codes are those of u = x D^{1/2} and the row reads
 // back as u_hat D^{-1/2}.
@@ -44,11 +44,12 @@ __device__ __forceinline__ float qrange(float mn, float mx) {
 // adjacent lanes.  The code decision is that of the weight quantizer
 // (qgroup_si / qlevels8: float32, no fused operations) except that the scale
 // is the range times a.rN, the float32 nearest to 1/N (1/Z, 1/448), instead of
-// the range divided by N: at most one unit in the last place away, and no
-// division in the chain of every row.  A group that holds a value that is not
-// finite, or whose range overflows, gets a NaN scale and offset, and so reads
-// back as NaN; a scale below float32's normal range (whose reciprocal may
-// overflow) counts as 0.
+// the range divided by N: the bits of the same steps in elementary torch
+// operations on the GPU, which divide by a number so.  It is no matter of speed
+// (2047 float32 rows of 8192 channels: 18.4 us, 18.7 with the quotient).  A group
+// that holds a value that is not finite, or whose range overflows, gets a NaN
+// scale and offset, and so reads back as NaN; a scale below float32's normal range
+// (whose reciprocal may overflow) counts as 0.
 template <int GS, int QF>
 __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs a) {
   constexpr int LPG = GS / 8;
