@@ -240,14 +240,16 @@ def _scratch(torch, dev, stream, need):
     return buf
 
 
-def _workspace(dev, stream, need_key, query):
+def _workspace(dev, stream, need_key, query, here=False):
+    """A workspace of query() bytes, remembered by need_key (None: not); ``here``:
+    the caller has just got ``stream`` as torch's current one."""
     torch = _torch or _host()
     need = _NEED.get(need_key) if need_key is not None else None
     if need is None:
         need = max(int(query()), 256)
         if need_key is not None:
             _NEED[need_key] = need
-    if _is_current(dev, stream):
+    if (here and not _several) or _is_current(dev, stream):
         return _scratch(torch, dev, stream, need)
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)):
         return _scratch(torch, dev, stream, need)
@@ -311,7 +313,7 @@ def _check(t, name, dtype, shape, device):
 def _call(batched: bool, W, X, B, A, *, p, lam, alpha, bits, group, Y,
           codes_out, scales_out, mins_out, dhalf_out, workspace, stream,
           flags, qformat, noalloc=False):
-    import torch
+    torch = _torch or _host()
     lib = load_library()
     if batched:
         R, T, d = X.shape
@@ -339,7 +341,8 @@ def _call(batched: bool, W, X, B, A, *, p, lam, alpha, bits, group, Y,
     _check(scales_out, "scales_out", torch.float32, lead + (d_out, G), dev)
     _check(mins_out, "mins_out", torch.float32, lead + (d_out, G), dev)
     _check(dhalf_out, "dhalf_out", torch.float32, lead + (d,), dev)
-    if stream is None:
+    here = stream is None
+    if here:
         stream = _current_stream(dev)
     if noalloc:
         args = [_ptr(W), _ptr(X), _ptr(B), _ptr(A), _ptr(Y), _ptr(codes_out),
@@ -350,7 +353,7 @@ def _call(batched: bool, W, X, B, A, *, p, lam, alpha, bits, group, Y,
         return Y
     if workspace is None:  # (a given workspace is checked by the library)
         workspace = _workspace(dev, stream, ("linear", key, R),
-                               lambda: ttq_workspace_bytes(prm, R))
+                               lambda: ttq_workspace_bytes(prm, R), here)
     args = [_ptr(W), _ptr(X), _ptr(B), _ptr(A), _ptr(Y), _ptr(codes_out),
             _ptr(scales_out), _ptr(mins_out), _ptr(dhalf_out),
             _ptr(workspace), workspace.numel(), stream]
@@ -432,7 +435,7 @@ def ttq_linear_segmented(W, X, B=None, A=None, *, seg_offsets, p: float,
                          flags: int = 0, qformat="asym"):
     """Requests of different lengths packed in X [T, d]: request i owns rows
     seg_offsets[i] .. seg_offsets[i+1]-1 and has its own statistics."""
-    import torch
+    torch = _torch or _host()
     T, d = X.shape
     d_out = W.shape[0]
     rank = 0 if A is None else A.shape[0]
@@ -528,7 +531,7 @@ def ttq_quantize(W, X, *, p: float, lam: float, alpha: float, bits: int,
     Returns (codes [d_out, row_bytes] uint8, scales [d_out, G] float32,
     mins [d_out, G] float32, dhalf_inv [d] float32).
     """
-    import torch
+    torch = _torch or _host()
     lib = load_library()
     T, d = X.shape
     d_out = W.shape[0]
@@ -574,7 +577,7 @@ def ttq_qmatmul(codes, scales, mins, dhalf_inv, X, B=None, A=None, *,
     """Y[T, d_out] = X ((min + s q) D^{-1/2})^T + (X A^T) B^T from the codes
     stored by ttq_quantize (see include/ttq.h; ``qformat`` as given to it:
     E4M3 codes decode as FP8 values)."""
-    import torch
+    torch = _torch or _host()
     lib = load_library()
     T, d = X.shape
     d_out = codes.shape[0]
@@ -598,11 +601,12 @@ def ttq_qmatmul(codes, scales, mins, dhalf_inv, X, B=None, A=None, *,
     if Y is None:
         Y = _result((T, d_out), torch.float32, dev, stream)
     _check(Y, "Y", torch.float32, (T, d_out), dev)
-    if stream is None:
+    here = stream is None
+    if here:
         stream = _current_stream(dev)
     if workspace is None:  # (a given workspace is checked by the library)
         workspace = _workspace(dev, stream, ("qmatmul", key),
-                               lambda: ttq_qmatmul_workspace_bytes(prm))
+                               lambda: ttq_qmatmul_workspace_bytes(prm), here)
     st = lib.ttq_qmatmul(ctypes.byref(prm), _ptr(codes), _ptr(scales),
                          _ptr(mins), _ptr(dhalf_inv), _ptr(X), _ptr(B), _ptr(A),
                          _ptr(Y), _ptr(workspace), workspace.numel(), stream)
@@ -690,7 +694,7 @@ def _gpu(t, name):
     return dev
 
 
-def _step_workspace(dev, stream, need, given):
+def _step_workspace(dev, stream, need, given, here=False):
     """The caller's workspace, or one of ``need`` bytes (see _workspace)."""
     if given is not None:
         if given.dtype is not _torch.uint8:
@@ -698,7 +702,7 @@ def _step_workspace(dev, stream, need, given):
         if given.device != dev or not given.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {dev}, got {given.device}")
         return given
-    if _is_current(dev, stream):
+    if here and not _several:
         return _scratch(_torch, dev, stream, need)
     return _workspace(dev, stream, None, lambda: need)
 
@@ -742,11 +746,12 @@ def ttq_adapters(X, A, B, index, *, scale=None, base=None, Y=None,
     if Y is None:
         Y = _result(ys, torch.float32, dev, stream)
     ptrs = _expect((X, A, B, scale, index, base, Y), want, dev)
-    if stream is None:
+    here = stream is None
+    if here:
         stream = _current_stream(dev)
     ws = size = 0
     if need or workspace is not None:  # (small steps need none)
-        workspace = _step_workspace(dev, stream, need, workspace)
+        workspace = _step_workspace(dev, stream, need, workspace, here)
         ws, size = workspace.data_ptr(), workspace.numel()
     _enqueue("ttq_adapters", dev, prm, n, *ptrs, ws, size, stream)
     return Y
@@ -808,9 +813,10 @@ def ttq_moe(X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv, dn_codes,
     ptrs = _expect((X, router, gu_codes, gu_scales, gu_mins, gu_dhalf_inv,
                     dn_codes, dn_scales, dn_mins, dn_dhalf_inv, Y, ids_out,
                     weights_out), want, dev)
-    if stream is None:
+    here = stream is None
+    if here:
         stream = _current_stream(dev)
-    workspace = _step_workspace(dev, stream, need, workspace)
+    workspace = _step_workspace(dev, stream, need, workspace, here)
     _enqueue("ttq_moe", dev, prm, *ptrs, workspace.data_ptr(), workspace.numel(),
              stream)
     return Y
@@ -925,7 +931,7 @@ def ttq_lowrank_pca(W, Omega, *, iters: int, X=None, p: float = 2.0,
     A [r, d], Wres [d_out, d] or None), bf16 GPU tensors.  ``Omega`` is the
     float32 [d, r] Gaussian test matrix; with ``X`` ([T, d] bf16) the
     principal subspace is that of W D^{1/2}."""
-    import torch
+    torch = _torch or _host()
     d_out, d = W.shape
     r = Omega.shape[1]
     T = 0 if X is None else X.shape[0]
@@ -959,7 +965,7 @@ def stream_read(src, sink=None, stream=None):
     """Plain read of a device tensor's bytes (the ceiling of a one-pass
     kernel over W; see ttq_stream_read).  Returns the per-workgroup XOR
     words (uint32 stored in an int32 tensor)."""
-    import torch
+    torch = _torch or _host()
     if not src.is_cuda or not src.is_contiguous():
         raise ValueError("stream_read: src must be a contiguous device tensor")
     nbytes = src.numel() * src.element_size()
