@@ -306,6 +306,10 @@ int ttq_qmatmul(const ttq_params* prm, const uint8_t* codes,
  *          gave (0 without); may be Y itself, but not otherwise overlap it
  *   Y      [T][d_out] float32
  *   workspace of at least ttq_adapters_workspace_bytes (0 for small steps)
+ * Up to 128 rows (decode steps) may name as many pairs as they are; more are
+ * taken as prompts, with runs of rows of one pair.  Any order is right, but more
+ * than 128 rows of mixed pairs are several times faster in calls of 128 rows
+ * each (256 rows with 100 pairs: 72 us in two calls, 473 us in one).
  * Both products accumulate in float32 and A_e x_t enters the second one with
  * all its 24 bits, as a sum of three parts.  An infinity in A_e x_t keeps its
  * sign in the outputs; one in B_e makes its own output infinite or NaN (a part

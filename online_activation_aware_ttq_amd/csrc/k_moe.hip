@@ -21,8 +21,10 @@
 // experts of 4096 / 11008, 4 bits in groups of 128: 25 us for 101 MB of gate and
 // up, 18 us for 51 MB of down (4.1 and 2.8 TB/s; codes alone stream in 18 and
 // 11).  16 tokens, 8 of 64 experts of 2048 / 1408: 47 us for 184 MB, 27 for 92.
-// Bound by vector instructions beside the matrix ones where they are many: 97
-// tokens, 4 of 16 2-bit experts of 4096 / 2816: 177 and 85 us.
+// Where they are many, bound by waiting: 97 tokens, 4 of 16 2-bit experts of 4096
+// / 2816, take 177 and 85 us, with the vector units busy 35 and 27 % of it, the
+// matrix ones 20 and 15 %, and 1.3 and 1.1 waves a SIMD, which wait (barriers,
+// loads) two fifths of their time.
 #include <algorithm>
 #include <cmath>
 

@@ -704,7 +704,9 @@ struct AdaptersArgs {
 // batches of up to this many rows are one tile (decode steps), longer ones go
 // in tiles of 64, whose pairs take turns (128 rows with 64 pairs of rank 64 on
 // 4096 -> 11008: 43 us, 404 in tiles; 128 rows of one pair of rank 32 on 4096 ->
-// 4096: 33 and 28)
+// 4096: 33 and 28).  A longer batch that is no prompts, each row with a pair of its
+// own, is therefore better made in calls of this many rows: 256 rows with 100 pairs
+// of rank 64 on 4096 -> 11008: 72 us in two calls, 473 in one.
 constexpr int64_t kAdStepTokens = 128;
 // Decode steps small enough for one launch, each workgroup (512 outputs) reading
 // all of its pair's A: at most 64 KiB, 16 MiB in all.  (One row of rank 8 on
