@@ -130,3 +130,17 @@ def test_results_of_a_stream_given_as_argument():
         torch.cuda.synchronize()
         assert torch.equal(got, want) and _same(rows, layer)
         assert (got[0, 50:] == 0).all() and (got[0, :50] != 0).any(1).all()
+
+
+def test_the_default_stream_given_as_argument():
+    """From within another stream: handle 0, and a handle of torch's own streams."""
+    import torch
+    run = _layer(8)
+    want = run()
+    torch.cuda.synchronize()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for handle in (0, other.cuda_stream, side.cuda_stream):
+            got = run(stream=handle)
+            torch.cuda.synchronize()
+            assert _same(got, want), handle
