@@ -899,9 +899,9 @@ hipError_t launch_proj(const MoeArgs& a, const Launch& L) {
   // LDS: the waves' slots, and `rows` rows of staged scales, up to kStage bytes
   // of them at a time (an odd number of float2 a row, whole slots' groups); the
   // products later, in their place.  More than 64 KiB of dynamic LDS would have to
-  // be allowed per kernel: 16 slots of 64 bytes a row leave 48 KiB for the scales,
-  // those of 8-bit codes, of 128, leave 32 (as a multiple of 4 slots' groups, in
-  // which the waves take turns, 24 of them: the sums keep their order).
+  // be allowed per kernel.  16 slots of 64-byte rows leave 48 KiB for the scales;
+  // those of 8-bit codes, of 128-byte rows, leave 32, of which 24 are used: 48
+  // groups, which are whole turns of the 4 waves, so the sums keep their order.
   constexpr int kStage = 40 * 1024, kStage8 = 24 * 1024;
   constexpr uint32_t kMoeLds = 64 * 1024;
   MoeArgs b = a;
