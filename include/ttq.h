@@ -430,6 +430,138 @@ int ttq_cache_read(const ttq_params* prm, int64_t n_slots, int64_t n_seq,
                    const float* dhalf_inv, int32_t out_type, void* out,
                    void* stream);
 
+/* ---- attention over such a cache -----------------------------------------
+ * The rest of what a decoder does with its cache in a step: where the step's
+ * rows go (ttq_cache_extend), its heads' norms and rotation with K and V
+ * quantized into their rows in the same pass (ttq_cache_rope), and attention
+ * over the stored codes (ttq_cache_attention).  ttq_heads says where the heads
+ * lie:
+ *   d, bits, group, qformat   the cache's, as for ttq_cache_write
+ *   n_slots    its rows
+ *   heads, kv_heads, head_dim  query heads (a multiple of the K/V heads: query
+ *              head h reads K/V head h / (heads / kv_heads)) and their channels:
+ *              64, 128 or 256
+ *   k_first, v_first   channels of a row at which the K and the V heads begin,
+ *              multiples of group.  K and V may lie side by side in one cache
+ *              (the same pointers, two ranges that do not overlap) or in two
+ *              caches of this format (two sets of pointers).
+ * kv_heads * head_dim is a multiple of group. */
+typedef struct ttq_heads {
+  int64_t d;
+  int64_t n_slots;
+  int64_t k_first;
+  int64_t v_first;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t bits;
+  int32_t group;
+  uint32_t qformat;
+} ttq_heads;
+
+/* Page tables and slot maps of a step, from its request lengths, on the device.
+ * A cache of n_pages pages of page_tokens rows (a power of two up to 4096); a
+ * table pages [n_seq][max_pages] of the pages that each sequence holds, and a
+ * stack of free ones: free_pages [n_pages], the first *free_count are free.
+ *   lens   [n_seq] rows that each sequence holds (its first
+ *          ceil(lens / page_tokens) table entries are in use)
+ *   added  [n_seq] rows that this step adds to it; negative: it has ended.
+ * The step's rows are packed in the order of the sequences into T rows.
+ *   lens_out   [n_seq] lens + added; 0 for an ended sequence
+ *   offsets    [n_seq + 1] the first row of each sequence (at most T)
+ *   positions  [T] the position of each row in its sequence (0 behind the last)
+ *   slots      [T] its cache row, as ttq_cache_write takes it (-1 behind the last)
+ * Pages of ended sequences go onto the stack first, in order (what would pass
+ * n_pages is dropped).  New pages are taken from its top, in the order of the
+ * sequences; pages, free_pages (above *free_count) are updated, and
+ * free_count_out is what is left.
+ * A sequence that would pass max_pages, whose rows would pass row T, or for which
+ * no pages are left (nor for any behind it that needs some) is refused: it gets
+ * no page, its slots are -1, and its length becomes -1 - lens, which
+ * ttq_cache_read and ttq_cache_attention take as empty, and a later
+ * ttq_cache_extend as lens, so that it may try again.
+ * lens_out may be lens and free_count_out free_count; no other two may overlap.
+ * Alignment: the types'.  n_seq up to 65535; error rules as for ttq_linear. */
+int ttq_cache_extend(int64_t n_seq, int64_t T, int64_t max_pages,
+                     int64_t n_pages, int32_t page_tokens, const int32_t* lens,
+                     const int32_t* added, int32_t* pages, int32_t* free_pages,
+                     const int32_t* free_count, int32_t* lens_out,
+                     int32_t* free_count_out, int32_t* offsets,
+                     int32_t* positions, int64_t* slots, void* stream);
+
+/* Norms and rotation of T rows' query and key heads, with K and V quantized into
+ * the cache rows slots [T] in the same pass:
+ *   y = (x r) w,  r = 1 / sqrt(mean(x^2) + eps)    per head, with q_weight or
+ *                 k_weight [head_dim] float32; y = x without (NULL)
+ *   (a, b) -> (a c - b s, b c + a s),  c, s = cos, sin(positions[t] inv_freq[i])
+ * for the pairs i < rot_dim / 2 of a head: channels (i, i + rot_dim / 2), or
+ * (2i, 2i + 1) with TTQ_ROPE_INTERLEAVED; channels from rot_dim on stay.
+ *   Q [T] rows of heads * head_dim, K and V [T] rows of kv_heads * head_dim
+ *             values of x_type, ldq, ldk, ldv elements apart (column ranges of
+ *             one projection's result are fine); 16-byte aligned, as is every row
+ *   inv_freq  [rot_dim / 2] float32; rot_dim a multiple of 16 up to head_dim, or
+ *             0: no rotation (inv_freq and positions may be NULL)
+ *   Q_out     [T][heads][head_dim] bf16
+ *   slots, k_*, v_*   as for ttq_cache_write, K and V of a row at k_first and
+ *             v_first; k_dhalf, v_dhalf optional [d] (the one of the row)
+ * The angle is the product in float64, its cosine and sine and r are rounded to
+ * float32 from float64; the products and sums above are float32, each rounded, none
+ * fused.  So the stored codes, scales and offsets are those that ttq_cache_write
+ * gives for the float32 rows.  Q = NULL (heads = 0): only K and V.
+ * Alignment: pointers 16 bytes (slots 8, positions, scales and mins 4). */
+#define TTQ_ROPE_INTERLEAVED 1u
+int ttq_cache_rope(const ttq_heads* hd, int64_t T, int32_t x_type,
+                   const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                   const void* V, int64_t ldv, const float* q_weight,
+                   const float* k_weight, double eps, const float* inv_freq,
+                   int32_t rot_dim, uint32_t flags, const int32_t* positions,
+                   void* Q_out, const int64_t* slots, const float* k_dhalf,
+                   const float* v_dhalf, uint8_t* k_codes, float* k_scales,
+                   float* k_mins, uint8_t* v_codes, float* v_scales,
+                   float* v_mins, void* stream);
+
+/* Causal attention of T rows over the cached K and V of their sequences:
+ *   out[t][h] = sum_j p_j v_j,  p = softmax_j(scale q . k_j)
+ * over the keys j of row t's sequence with j <= pos and, with window > 0,
+ * j > pos - window.  Row r of a sequence's n rows has pos = lens - n + r: its own
+ * K and V are in the cache already.  k_j and v_j are the stored values
+ * (m + s q) D^{-1/2}.
+ *   Q        [T] rows of heads * head_dim bf16, ldq elements apart, 16-byte
+ *            aligned, as is every row
+ *   offsets  [n_seq + 1] int32: sequence i has rows offsets[i] .. offsets[i+1]-1
+ *            (as ttq_cache_extend gives them); NULL: one row each, T = n_seq.
+ *            Rows of no sequence are left as they were.
+ *   pages, lens, max_pages, page_tokens   as for ttq_cache_read
+ *   max_len  an upper bound of lens that the caller knows (work is divided by
+ *            it; keys behind it are not seen), 0: what the pages hold
+ *   k_dhalf_inv, v_dhalf_inv   optional [d] float32
+ *   out      [T][heads][head_dim] bf16
+ *   workspace of at least ttq_cache_attention_workspace_bytes
+ * A row that sees no key (an empty or negative length, or every page outside the
+ * cache: such keys are not seen) is 0.  Nothing of a key that a row does not see
+ * enters it, an infinity or NaN neither; of one that it sees, K's makes the head's
+ * row NaN, V's the channels of its group (at least).
+ * Products are those of exact codes with q D^{-1/2} and p in 11 bits (fp16, scaled
+ * by powers of two); V's scales and offsets enter in 11 bits too.  Scores, sums
+ * and the softmax are float32.
+ * bits 3 to 8 (others: TTQ_EUNSUPPORTED, as are n_slots from 2^31 on).
+ * heads * T up to 2^31 - 1. */
+int ttq_cache_attention_workspace_bytes(const ttq_heads* hd, int64_t T,
+                                        int64_t n_seq, int64_t max_pages,
+                                        int32_t page_tokens, int64_t max_len,
+                                        size_t* bytes);
+int ttq_cache_attention(const ttq_heads* hd, int64_t T, int64_t n_seq,
+                        int64_t max_pages, int32_t page_tokens, int64_t max_len,
+                        int64_t window, double scale, const void* Q,
+                        int64_t ldq, const int32_t* offsets,
+                        const int32_t* pages, const int32_t* lens,
+                        const uint8_t* k_codes, const float* k_scales,
+                        const float* k_mins, const uint8_t* v_codes,
+                        const float* v_scales, const float* v_mins,
+                        const float* k_dhalf_inv, const float* v_dhalf_inv,
+                        void* out, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
 /* Human-readable text of a status code (static storage). */
 const char* ttq_status_string(int status);
 

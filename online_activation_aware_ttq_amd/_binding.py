@@ -68,6 +68,16 @@ EXPORTS = {
     "ttq_cache_read": (_c.c_int, [_vp, _c.c_int64, _c.c_int64, _c.c_int64,
                                   _c.c_int32, _vp, _vp, _vp, _vp, _vp, _vp,
                                   _c.c_int32, _vp, _vp]),
+    "ttq_cache_extend": (_c.c_int, [_c.c_int64] * 4 + [_c.c_int32] + [_vp] * 11),
+    "ttq_cache_rope": (_c.c_int, [_vp, _c.c_int64, _c.c_int32]
+                       + [_vp, _c.c_int64] * 3 + [_vp, _vp, _c.c_double, _vp, _c.c_int32,
+                                                  _c.c_uint32] + [_vp] * 12),
+    "ttq_cache_attention_workspace_bytes": (
+        _c.c_int, [_vp, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int64,
+                   _c.POINTER(_c.c_size_t)]),
+    "ttq_cache_attention": (_c.c_int, [_vp, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32,
+                                       _c.c_int64, _c.c_int64, _c.c_double, _vp, _c.c_int64]
+                            + [_vp] * 13 + [_c.c_size_t, _vp]),
     "ttq_status_string": (_c.c_char_p, [_c.c_int]),
     "ttq_last_hip_error": (_c.c_int, []),
     "ttq_stream_read": (_c.c_int, [_vp, _c.c_int64, _vp, _vp]),
@@ -107,6 +117,21 @@ class ttq_moe_params(ctypes.Structure):
         ("bits", ctypes.c_int32),
         ("group", ctypes.c_int32),
         ("flags", ctypes.c_uint32),
+        ("qformat", ctypes.c_uint32),
+    ]
+
+
+class ttq_heads(ctypes.Structure):
+    _fields_ = [
+        ("d", ctypes.c_int64),
+        ("n_slots", ctypes.c_int64),
+        ("k_first", ctypes.c_int64),
+        ("v_first", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("bits", ctypes.c_int32),
+        ("group", ctypes.c_int32),
         ("qformat", ctypes.c_uint32),
     ]
 
@@ -911,6 +936,234 @@ def ttq_cache_read(codes, scales, mins, pages, lens, *, bits: int, group: int,
         stream = _current_stream(dev)
     _enqueue("ttq_cache_read", dev, prm, n_slots, n_seq, max_pages, page_tokens,
              *ptrs, out_type, po, stream)
+    return out
+
+
+# ------------------------------------------------- attention over a cache
+TTQ_ROPE_INTERLEAVED = 1
+
+
+def ttq_cache_extend(lens, added, pages, free_pages, free_count, *, page_tokens: int,
+                     T=None, lens_out=None, free_count_out=None, offsets=None,
+                     positions=None, slots=None, stream=None):
+    """Page tables and slot maps of a step from its request lengths, on the device
+    (see include/ttq.h).
+
+    Sequence i holds ``lens[i]`` rows and gets ``added[i]`` more (negative: it has
+    ended, and its pages are given back).  ``pages`` [n_seq, max_pages] and the
+    stack ``free_pages`` [n_pages] (its first ``free_count`` [1] are free) are
+    updated; all are int32.  The step's rows are packed into ``T`` rows (default: of
+    ``positions`` or ``slots``).  Returns (lens_out [n_seq], free_count_out [1],
+    offsets [n_seq + 1], positions [T] int32, slots [T] int64); lens_out may be
+    ``lens`` and free_count_out ``free_count``.  A sequence without room is refused:
+    its slots are -1 and its length is -1 - lens until a later call takes it.
+    """
+    torch = _torch or _host()
+    dev = _gpu(pages, "pages")
+    ps, fs = pages.shape, free_pages.shape
+    if T is None:
+        rows = positions if positions is not None else slots
+        if rows is None:
+            raise ValueError("T is needed where neither positions nor slots are given")
+        T = rows.shape[0]
+
+    def make():
+        (n_seq, max_pages), (n_pages,) = ps, fs
+        i32 = torch.int32
+        return (n_seq, T, max_pages, n_pages), (
+            ("lens", i32, (n_seq,)), ("added", i32, (n_seq,)), ("pages", i32, None),
+            ("free_pages", i32, None), ("free_count", i32, (1,)), ("lens_out", i32, (n_seq,)),
+            ("free_count_out", i32, (1,)), ("offsets", i32, (n_seq + 1,)),
+            ("positions", i32, (T,)), ("slots", torch.int64, (T,)))
+
+    sizes, want = _plan(("extend", ps, fs, T), make)
+    if lens_out is None:
+        lens_out = _result((sizes[0],), torch.int32, dev, stream)
+    if free_count_out is None:
+        free_count_out = _result((1,), torch.int32, dev, stream)
+    if offsets is None:
+        offsets = _result((sizes[0] + 1,), torch.int32, dev, stream)
+    if positions is None:
+        positions = _result((T,), torch.int32, dev, stream)
+    if slots is None:
+        slots = _result((T,), torch.int64, dev, stream)
+    ptrs = _expect((lens, added, pages, free_pages, free_count, lens_out, free_count_out,
+                    offsets, positions, slots), want, dev)
+    if stream is None:
+        stream = _current_stream(dev)
+    _enqueue("ttq_cache_extend", dev, *sizes, page_tokens, *ptrs, stream)
+    return lens_out, free_count_out, offsets, positions, slots
+
+
+def _rows(t, name, dev, dtype, width):
+    """(address, distance of the rows) of ``t`` [T, width] or [T, heads, head_dim],
+    whose rows are contiguous but may lie apart."""
+    torch = _torch
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be a torch.Tensor of {dtype}, got {t.dtype}")
+    if t.get_device() != dev.index or t.device.type != "cuda":
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dim() == 3:
+        T, n, d = t.shape
+        ld, sn, one = t.stride()
+        ok = n * d == width and (one == 1 or d == 1) and (n == 1 or sn == d)
+    else:
+        T, d = t.shape
+        ld, one = t.stride()
+        ok = d == width and (one == 1 or d == 1)
+    if not ok:
+        raise ValueError(f"{name} must have contiguous rows of {width} values, got shape "
+                         f"{tuple(t.shape)} and strides {t.stride()}")
+    return t.data_ptr(), (ld if T > 1 else width)
+
+
+def _head_plan(torch, dev, cs, vs, heads, kv_heads, head_dim, k_first, v_first, bits, group,
+               qformat):
+    """ttq_heads of a cache of ``cs`` codes (``vs``: V's own), and what its tensors
+    have to be."""
+    n_slots, rb = cs
+    d = rb * 8 // container_bits(bits)
+    width = kv_heads * head_dim
+    if v_first is None:
+        v_first = k_first + width if vs is None else 0
+    if vs is not None and vs != cs:
+        raise ValueError(f"v_cache must have the shape of the cache, got {tuple(vs)} and {tuple(cs)}")
+    hd = ttq_heads(d, n_slots, k_first, v_first, heads, kv_heads, head_dim, bits, group,
+                   qformat_code(qformat))
+    sm = (n_slots, d // group)
+    f32 = torch.float32
+    cache = lambda n: ((n + "codes", torch.uint8, None), (n + "scales", f32, sm), (n + "mins", f32, sm))
+    return hd, d, cache("k_") + cache("v_")
+
+
+def ttq_cache_rope(Q, K, V, positions, slots, codes, scales, mins, *, head_dim: int,
+                   bits: int, group: int, inv_freq=None, interleaved: bool = False,
+                   q_weight=None, k_weight=None, eps: float = 1e-6, v_cache=None,
+                   k_first: int = 0, v_first=None, dhalf=None, v_dhalf=None, out=None,
+                   qformat="asym", stream=None):
+    """Norms (with ``q_weight``, ``k_weight`` [head_dim] float32) and rotation by
+    ``positions`` [T] int32 (with ``inv_freq`` [rot_dim / 2] float32) of the query and
+    key heads; K and V are quantized into the cache rows ``slots`` [T] (int64) as
+    ttq_cache_write does (see include/ttq.h).
+
+    Q [T, heads * head_dim], K and V [T, kv_heads * head_dim] (or [T, heads,
+    head_dim]) are all bfloat16 or all float32; rows may lie apart.  The cache holds
+    K at channel ``k_first`` and V at ``v_first`` (default: behind K) of its rows;
+    with ``v_cache`` (codes, scales, mins) V is in a cache of its own (default: from
+    channel 0).  ``dhalf`` [d] goes with the rows of K (and V, unless ``v_dhalf`` is
+    given for a cache of its own).  Returns the queries [T, heads, head_dim]
+    bfloat16 (``out``); Q None: only K and V.
+    """
+    torch = _torch or _host()
+    dev = _gpu(codes, "codes")
+    cs = codes.shape
+    vs = None if v_cache is None else v_cache[0].shape
+    T = K.shape[0]
+    kw, qw = K.numel() // T if T else K.shape[1:].numel(), 0
+    if Q is not None:
+        qw = Q.numel() // T if T else Q.shape[1:].numel()
+    x_type = _elem_type(K, "K")
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+
+    def make():
+        if head_dim < 1 or qw % head_dim or kw % head_dim:
+            raise ValueError(f"rows of {qw} and {kw} values are no whole heads of {head_dim}")
+        hd, d, cache = _head_plan(torch, dev, cs, vs, qw // head_dim, kw // head_dim, head_dim,
+                                  k_first, v_first, bits, group, qformat)
+        f32 = torch.float32
+        head = ("q_weight", f32, (head_dim,)), ("k_weight", f32, (head_dim,))
+        return ctypes.byref(hd), hd, (T, qw // head_dim, head_dim), head + (
+            ("inv_freq", f32, None), ("positions", torch.int32, (T,)),
+            ("out", torch.bfloat16, (T, qw // head_dim, head_dim)),
+            ("slots", torch.int64, (T,)), ("dhalf", f32, (d,)), ("v_dhalf", f32, (d,))) + cache
+
+    ref, _, os_, want = _plan(("rope", cs, vs, T, qw, kw, head_dim, k_first, v_first, bits,
+                               group, qformat), make)
+    xd = K.dtype
+    kp, ldk = _rows(K, "K", dev, xd, kw)
+    vp, ldv = _rows(V, "V", dev, xd, kw)
+    if V.shape[0] != T or (Q is not None and Q.shape[0] != T):
+        raise ValueError("Q, K and V must have as many rows")
+    qp, ldq = (None, 0) if Q is None else _rows(Q, "Q", dev, xd, qw)
+    if out is None and Q is not None:
+        out = _result(os_, torch.bfloat16, dev, stream)
+    if v_cache is None:
+        v_cache = (codes, scales, mins)
+    if v_dhalf is None:
+        v_dhalf = dhalf
+    wq, wk, fr, ps, op, sl, dk, dv, *cp = _expect(
+        (q_weight, k_weight, inv_freq, positions, out, slots, dhalf, v_dhalf, codes, scales,
+         mins, *v_cache), want, dev)
+    if stream is None:
+        stream = _current_stream(dev)
+    _enqueue("ttq_cache_rope", dev, ref, T, x_type, qp, ldq, kp, ldk, vp, ldv, wq, wk, eps, fr,
+             rot, TTQ_ROPE_INTERLEAVED if interleaved else 0, ps, op, sl, dk, dv, *cp, stream)
+    return out
+
+
+def ttq_cache_attention_workspace_bytes(hd: ttq_heads, T: int, n_seq: int, max_pages: int,
+                                        page_tokens: int, max_len: int = 0) -> int:
+    out = ctypes.c_size_t(0)
+    st = load_library().ttq_cache_attention_workspace_bytes(
+        ctypes.byref(hd), int(T), int(n_seq), int(max_pages), int(page_tokens), int(max_len),
+        ctypes.byref(out))
+    if st != TTQ_OK:
+        raise TTQError(st, "ttq_cache_attention_workspace_bytes")
+    return int(out.value)
+
+
+def ttq_cache_attention(Q, pages, lens, codes, scales, mins, *, kv_heads: int, bits: int,
+                        group: int, page_tokens: int, offsets=None, scale=None,
+                        window: int = 0, max_len: int = 0, v_cache=None, k_first: int = 0,
+                        v_first=None, dhalf_inv=None, v_dhalf_inv=None, out=None,
+                        workspace=None, qformat="asym", stream=None):
+    """Causal attention of the rows Q [T, heads, head_dim] (bfloat16, rows may lie
+    apart) over the cached keys and values of their sequences (see include/ttq.h).
+
+    ``pages`` [n_seq, max_pages] and ``lens`` [n_seq] (int32) as for ttq_cache_read;
+    the lengths count this step's rows, whose K and V are in the cache.  Sequence i
+    has rows ``offsets[i]`` .. ``offsets[i + 1] - 1`` (int32 [n_seq + 1]; without, one
+    row each).  ``scale`` is 1 / sqrt(head_dim) by default; with ``window`` > 0 a row
+    sees that many keys, itself the last.  Where K and V lie, and their D^{-1/2}
+    (``dhalf_inv``, ``v_dhalf_inv``), as for ttq_cache_rope.  Returns ``out`` [T,
+    heads, head_dim] bfloat16 (made here it is zero where no sequence has a row).
+    """
+    torch = _torch or _host()
+    dev = _gpu(Q, "Q")
+    qs, ps, cs = Q.shape, pages.shape, codes.shape
+    vs = None if v_cache is None else v_cache[0].shape
+
+    def make():
+        (T, heads, head_dim), (n_seq, max_pages) = qs, ps
+        hd, d, cache = _head_plan(torch, dev, cs, vs, heads, kv_heads, head_dim, k_first, v_first,
+                                  bits, group, qformat)
+        need = ttq_cache_attention_workspace_bytes(hd, T, n_seq, max_pages, page_tokens, max_len)
+        f32, i32 = torch.float32, torch.int32
+        return (ctypes.byref(hd), T, n_seq, max_pages, page_tokens, max_len), need, hd, (
+            ("offsets", i32, (n_seq + 1,)), ("pages", i32, None), ("lens", i32, (n_seq,)),
+            *cache, ("dhalf_inv", f32, (d,)), ("v_dhalf_inv", f32, (d,)),
+            ("out", torch.bfloat16, (T, heads, head_dim)))
+
+    args, need, _, want = _plan(("attention", qs, ps, cs, vs, kv_heads, k_first, v_first, bits,
+                                 group, qformat, page_tokens, max_len), make)
+    qp, ldq = _rows(Q, "Q", dev, torch.bfloat16, qs[1] * qs[2])
+    if out is None:
+        out = _result(qs, torch.bfloat16, dev, stream, torch.empty if offsets is None else torch.zeros)
+    if v_cache is None:
+        v_cache = (codes, scales, mins)
+    if v_dhalf_inv is None:
+        v_dhalf_inv = dhalf_inv
+    *ptrs, op = _expect((offsets, pages, lens, codes, scales, mins, *v_cache, dhalf_inv,
+                         v_dhalf_inv, out), want, dev)
+    here = stream is None
+    if here:
+        stream = _current_stream(dev)
+    ws = size = 0
+    if need or workspace is not None:
+        workspace = _step_workspace(dev, stream, need, workspace, here)
+        ws, size = workspace.data_ptr(), workspace.numel()
+    _enqueue("ttq_cache_attention", dev, *args, window, qs[2] ** -0.5 if scale is None else scale,
+             qp, ldq, *ptrs, op, ws, size, stream)
     return out
 
 

@@ -38,6 +38,9 @@ SOURCES = [
     "k_pca.hip",
     "k_stream.hip",
     "k_cache.hip",
+    "k_pages.hip",
+    "k_rope.hip",
+    "k_attention.hip",
     "k_adapters.hip",
     "k_moe.hip",
     "ttq_api.cpp",

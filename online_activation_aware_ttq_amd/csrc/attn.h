@@ -1,0 +1,97 @@
+// Pieces shared by the attention kernels: stored codes as fp16 operands of the
+// matrix cores, and where a block of query rows and its keys lie.
+//
+// A stored code is an exact fp16 value as it stands: an integer code c of up to 10
+// bits is the pattern of the subnormal c 2^-24, which the matrix cores multiply
+// exactly; so a mask leaves two operands of a register's halves, with no
+// conversion, and a nibble taken in place counts 16-fold, which the other operand
+// or the result makes up for.  E4M3 codes become fp16 by gfx950's conversion, two
+// an instruction.
+#pragma once
+
+#include "ttq_internal.h"
+
+namespace ttq {
+
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+
+// what a code's operand is to be multiplied with to be the code: 2^kUnit
+template <bool F8>
+constexpr int kUnit = F8 ? 0 : 24;
+
+__device__ __forceinline__ unsigned e4m3_pair(unsigned w, bool hi) {
+  return __builtin_bit_cast(unsigned, hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true)
+                                         : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false));
+}
+
+// Eight codes of one row (CB bytes, low bits first) as an operand.  4 bits: slots
+// (2i, 2i + 1) are codes (i, i + 4), 16-fold where i is odd (slot_code,
+// slot_shift); 8 bits: in order.
+template <int CB, bool F8>
+__device__ __forceinline__ f16x8 codes8(unsigned w0, unsigned w1) {
+  u32x4 r;
+  if constexpr (F8) {
+    r = u32x4{e4m3_pair(w0, false), e4m3_pair(w0, true), e4m3_pair(w1, false), e4m3_pair(w1, true)};
+  } else if constexpr (CB == 8) {
+    r = u32x4{__builtin_amdgcn_perm(0u, w0, 0x0c010c00u), __builtin_amdgcn_perm(0u, w0, 0x0c030c02u),
+              __builtin_amdgcn_perm(0u, w1, 0x0c010c00u), __builtin_amdgcn_perm(0u, w1, 0x0c030c02u)};
+  } else {
+    const unsigned h = w0 >> 8;
+    r = u32x4{w0 & 0x000f000fu, w0 & 0x00f000f0u, h & 0x000f000fu, h & 0x00f000f0u};
+  }
+  return __builtin_bit_cast(f16x8, r);
+}
+template <int CB>
+__device__ __forceinline__ constexpr int slot_code(int slot) {
+  return CB == 4 ? slot / 2 + 4 * (slot & 1) : slot;
+}
+template <int CB>
+__device__ __forceinline__ constexpr int slot_shift(int slot) {
+  return CB == 4 && (slot / 2) & 1 ? 4 : 0;
+}
+
+// The rows of a sequence, and which keys they may see.  A query row r of a K/V
+// head is (token r / G, head r % G) of its sequence.
+struct SeqRows {
+  int64_t first;   // row of its first token
+  int rows;        // tokens * G
+  int64_t shift;   // position of token j: shift + j
+  int64_t len;     // keys that the pages hold
+};
+
+// The block b of SZ query rows of a K/V head: its sequence and first row.  Sequence
+// i's blocks begin at offsets[i] G / SZ + i, which leaves each enough, so no table
+// of them is needed; a block past its sequence's last has no rows (false).
+template <int SZ>
+__device__ __forceinline__ bool find_block(const AttnArgs& a, int64_t b, int64_t& seq, SeqRows& s,
+                                           int64_t& r0) {
+  int64_t begin;
+  if (a.offsets) {
+    auto off = [&](int64_t i) { return min(max((int64_t)a.offsets[i], (int64_t)0), a.T); };
+    int64_t lo = 0, hi = a.n_seq;
+    while (hi - lo > 1) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (off(mid) * a.G / SZ + mid <= b) lo = mid;
+      else hi = mid;
+    }
+    seq = lo;
+    s.first = off(lo);
+    const int64_t n = off(lo + 1) - s.first;
+    s.rows = (int)(max(n, (int64_t)0) * a.G);
+    begin = s.first * a.G / SZ + lo;
+  } else {
+    const int64_t per = (a.G + SZ - 1) / SZ;
+    seq = b / per;
+    s.first = seq;
+    s.rows = a.G;
+    begin = seq * per;
+  }
+  r0 = (b - begin) * SZ;
+  if (r0 < 0 || r0 >= s.rows) return false;
+  const int64_t n = max(a.lens[seq], 0);
+  s.shift = n - s.rows / a.G;
+  s.len = min(min(n, a.max_len), a.max_pages << a.pshift);
+  return true;
+}
+
+}  // namespace ttq

@@ -14,45 +14,15 @@
 // in groups of 128 is 2 C bytes out for 0.56 C in).  8 sequences of up to 4096
 // rows of 8192 channels read back: 111 us, 4.4 TB/s; 2047 float32 rows of as many
 // channels written in 2 bits: 18 us, 3.9 TB/s.
-#include "ttq_internal.h"
+#include "cache_row.h"
 
 namespace ttq {
 
 namespace {
 
-// min and max over the LPG consecutive lanes of a group, and whether any of
-// them saw a value that is not finite
-template <int LPG>
-__device__ __forceinline__ void group_range(float& mn, float& mx, int& bad) {
-#pragma unroll
-  for (int off = 1; off < LPG; off <<= 1) {
-    mn = fminf(mn, __shfl_xor(mn, off));
-    mx = fmaxf(mx, __shfl_xor(mx, off));
-    bad |= __shfl_xor(bad, off);
-  }
-}
-
-// what the scale of a format is a fixed part of
-template <int QF>
-__device__ __forceinline__ float qrange(float mn, float mx) {
-  if constexpr (QF == QF_ASYM) return mx - mn;
-  else if constexpr (QF == QF_INTZP) return fmaxf(mx, 0.f) - fminf(mn, 0.f);
-  else return fmaxf(-mn, mx);
-}
-
-// One wave quantizes 512 channels of one row, 8 a lane: a group is GS / 8
-// adjacent lanes.  The code decision is that of the weight quantizer
-// (qgroup_si / qlevels8: float32, no fused operations) except that the scale
-// is the range times a.rN, the float32 nearest to 1/N (1/Z, 1/448), instead of
-// the range divided by N: the bits of the same steps in elementary torch
-// operations on the GPU, which divide by a number so.  It is no matter of speed
-// (2047 float32 rows of 8192 channels: 18.4 us, 18.7 with the quotient).  A group
-// that holds a value that is not finite, or whose range overflows, gets a NaN
-// scale and offset, and so reads back as NaN; a scale below float32's normal range
-// (whose reciprocal may overflow) counts as 0.
+// One wave quantizes 512 channels of one row, 8 a lane (cache_row.h).
 template <int GS, int QF>
 __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs a) {
-  constexpr int LPG = GS / 8;
   const int l = threadIdx.x & 63;
   const int64_t wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int64_t nchunk = (a.C + 511) / 512;
@@ -83,43 +53,7 @@ __global__ __launch_bounds__(256) void k_cache_write(CacheWriteArgs a) {
     }
   }
   if (slot < 0 || slot >= a.n_slots) return;  // uniform
-  float mn = u[0], mx = u[0];
-  int bad = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    mn = fminf(mn, u[j]);
-    mx = fmaxf(mx, u[j]);
-    bad |= !(__builtin_fabsf(u[j]) <= 3.402823466e38f);
-  }
-  group_range<LPG>(mn, mx, bad);
-  float s = qrange<QF>(mn, mx) * a.rN;
-  bad |= !(s <= 3.402823466e38f);
-  if (s < 1.17549435e-38f) s = 0.f;
-  QGroup g = qgroup_si<QF>(mn, s, s > 0.f ? 1.0f / s : 0.f, a.Nf);
-  if (bad) g.s = g.off = __builtin_nanf("");
-  float L[8];
-  qlevels8<QF>(g, u, L);
-  if (!live) return;
-  unsigned q[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) q[j] = bad ? 0u : qcode<QF>(g, L[j]);
-  uint8_t* dst = a.codes + slot * a.row_bytes + c0 * a.cb / 8;
-  if (a.cb == 8) {
-    *(u32x2*)dst = u32x2{q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24),
-                         q[4] | (q[5] << 8) | (q[6] << 16) | (q[7] << 24)};
-  } else {
-    unsigned c = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c |= q[j] << (j * a.cb);
-    if (a.cb == 4) *(unsigned*)dst = c;
-    else if (a.cb == 2) *(uint16_t*)dst = (uint16_t)c;
-    else *dst = (uint8_t)c;
-  }
-  if (l % LPG == 0) {
-    const int64_t o = slot * (a.C / GS) + c0 / GS;
-    a.s[o] = g.s;
-    a.m[o] = g.off;
-  }
+  quantize8<GS, QF>(u, live, slot, c0, a.C, a.row_bytes, a.Nf, a.rN, a.cb, a.codes, a.s, a.m);
 }
 
 // One wave reads 512 channels of CR consecutive rows of one sequence, 8 a

@@ -249,7 +249,8 @@ const char* kKernelNames[K_NUM_KINDS] = {
     "pca_skinny", "pca_psum", "pca_chol", "pca_trsm", "pca_residual",
     "pca_complete", "stream_read", "cache_write", "cache_read",
     "adapters_step", "adapters_shrink", "adapters_expand", "moe_score",
-    "moe_route", "moe_up", "moe_down", "moe_sum"};
+    "moe_route", "moe_up", "moe_down", "moe_sum", "cache_extend",
+    "cache_extend_rows", "cache_rope", "attention_split", "attention_join"};
 
 hipEvent_t take_event() {
   if (!g_timing.pool.empty()) {
@@ -1370,6 +1371,15 @@ int validate_cache(const ttq_params* prm, int64_t n_slots, ttq_params* q,
   return TTQ_OK;
 }
 
+// what the quantizer of rows needs to know of its format
+void set_code_constants(const ttq_params& q, float* Nf, float* rN, int* cb, int* qf) {
+  *Nf = (float)((1 << q.bits) - 1);
+  *rN = 1.0f / (q.qformat == TTQ_QF_FP8 ? 448.0f
+                : q.qformat == TTQ_QF_SYM ? (float)((1 << (q.bits - 1)) - 1) : *Nf);
+  *cb = container_bits(q.bits);
+  *qf = (int)q.qformat;
+}
+
 int cache_write_impl(const ttq_params* prm, int64_t n_slots, int32_t x_type,
                      const void* X, int64_t ldx, const float* dhalf,
                      const int64_t* slots, uint8_t* codes, float* scales,
@@ -1391,11 +1401,7 @@ int cache_write_impl(const ttq_params* prm, int64_t n_slots, int32_t x_type,
   a.X = X; a.ldx = ldx; a.x_f32 = x_type == TTQ_F32; a.dh = dhalf;
   a.slots = slots; a.codes = codes; a.s = scales; a.m = mins;
   a.T = q.T; a.C = q.d; a.n_slots = n_slots; a.row_bytes = rb;
-  a.Nf = (float)((1 << q.bits) - 1);
-  a.rN = 1.0f / (q.qformat == TTQ_QF_FP8 ? 448.0f
-                 : q.qformat == TTQ_QF_SYM ? (float)((1 << (q.bits - 1)) - 1) : a.Nf);
-  a.cb = container_bits(q.bits);
-  a.qf = (int)q.qformat;
+  set_code_constants(q, &a.Nf, &a.rN, &a.cb, &a.qf);
   return run(K_CACHE_WRITE, static_cast<hipStream_t>(stream),
              [&](const Launch& L) { return launch_cache_write(a, q.group, L); });
 }
@@ -1434,6 +1440,227 @@ int cache_read_impl(const ttq_params* prm, int64_t n_slots, int64_t n_seq,
   a.qf = (int)q.qformat;
   return run(K_CACHE_READ, static_cast<hipStream_t>(stream),
              [&](const Launch& L) { return launch_cache_read(a, container_bits(q.bits), L); });
+}
+
+// ------------------------------------------- attention over such a cache
+// (k_pages.hip, k_rope.hip, k_attention.hip)
+int validate_page_tokens(int32_t page_tokens) {
+  if (page_tokens < 1) return TTQ_EINVAL;
+  if (page_tokens > 4096 || (page_tokens & (page_tokens - 1)) != 0) return TTQ_EUNSUPPORTED;
+  return TTQ_OK;
+}
+
+int cache_extend_impl(int64_t n_seq, int64_t T, int64_t max_pages, int64_t n_pages,
+                      int32_t page_tokens, const int32_t* lens, const int32_t* added,
+                      int32_t* pages, int32_t* free_pages, const int32_t* free_count,
+                      int32_t* lens_out, int32_t* free_count_out, int32_t* offsets,
+                      int32_t* positions, int64_t* slots, void* stream) {
+  if (n_seq < 0 || n_seq > kMaxSeq || T < 0 || T > kMaxT) return TTQ_EINVAL;
+  if (max_pages < 0 || max_pages > kMaxT) return TTQ_EINVAL;
+  if (n_pages < 0 || n_pages > INT32_MAX - 1) return TTQ_EINVAL;
+  const int st = validate_page_tokens(page_tokens);
+  if (st != TTQ_OK) return st;
+  if (!free_count || !free_count_out || !offsets) return TTQ_ENULL;
+  if (n_seq > 0 && (!lens || !added || !lens_out)) return TTQ_ENULL;
+  if (n_seq > 0 && max_pages > 0 && !pages) return TTQ_ENULL;
+  if (n_pages > 0 && !free_pages) return TTQ_ENULL;
+  if (T > 0 && (!positions || !slots)) return TTQ_ENULL;
+  if (misaligned(lens, 4) || misaligned(added, 4) || misaligned(pages, 4) ||
+      misaligned(free_pages, 4) || misaligned(free_count, 4) || misaligned(lens_out, 4) ||
+      misaligned(free_count_out, 4) || misaligned(offsets, 4) || misaligned(positions, 4) ||
+      misaligned(slots, 8))
+    return TTQ_EALIGN;
+  if (inject_hip_error()) return TTQ_EHIP;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  ExtendArgs a{};
+  a.lens = lens; a.added = added; a.pages = pages; a.free_pages = free_pages;
+  a.free_count = free_count; a.lens_out = lens_out; a.free_count_out = free_count_out;
+  a.offsets = offsets; a.positions = positions; a.slots = slots;
+  a.n_seq = n_seq; a.T = T; a.max_pages = max_pages; a.n_pages = n_pages;
+  a.pshift = __builtin_ctz((unsigned)page_tokens);
+  const bool apart = extend_rows_apart(a);
+  a.rows_here = !apart;
+  const int st1 = run(K_EXTEND, s, [&](const Launch& L) { return launch_extend(a, L); });
+  if (st1 != TTQ_OK || !apart) return st1;
+  return run(K_EXTEND_ROWS, s, [&](const Launch& L) { return launch_extend_rows(a, L); });
+}
+
+// The cache's format and where its heads lie.
+int validate_heads(const ttq_heads* h, ttq_params* f, int64_t* rb) {
+  if (!h) return TTQ_ENULL;
+  ttq_params p{};
+  p.d = h->d; p.d_out = 1; p.bits = h->bits; p.group = h->group; p.p = 2.0;
+  p.qformat = h->qformat;
+  const int st = validate_cache(&p, h->n_slots, f, rb);
+  if (st != TTQ_OK) return st;
+  if (h->kv_heads < 1 || h->kv_heads > 65535 || h->heads < 0 || h->heads > 65535 ||
+      h->heads % h->kv_heads != 0 || h->head_dim < 1)
+    return TTQ_EINVAL;
+  if (h->head_dim != 64 && h->head_dim != 128 && h->head_dim != 256) return TTQ_EUNSUPPORTED;
+  const int64_t width = (int64_t)h->kv_heads * h->head_dim;
+  if (width > h->d || width % h->group != 0) return TTQ_EINVAL;
+  if (h->k_first < 0 || h->k_first > h->d - width || h->v_first < 0 ||
+      h->v_first > h->d - width)
+    return TTQ_EINVAL;
+  if (h->k_first % h->group != 0 || h->v_first % h->group != 0) return TTQ_EINVAL;
+  return TTQ_OK;
+}
+
+int cache_rope_impl(const ttq_heads* h, int64_t T, int32_t x_type, const void* Q, int64_t ldq,
+                    const void* K, int64_t ldk, const void* V, int64_t ldv,
+                    const float* q_weight, const float* k_weight, double eps,
+                    const float* inv_freq, int32_t rot_dim, uint32_t flags,
+                    const int32_t* positions, void* Q_out, const int64_t* slots,
+                    const float* k_dhalf, const float* v_dhalf, uint8_t* k_codes,
+                    float* k_scales, float* k_mins, uint8_t* v_codes, float* v_scales,
+                    float* v_mins, void* stream) {
+  ttq_params f;
+  int64_t rb = 0;
+  const int st = validate_heads(h, &f, &rb);
+  if (st != TTQ_OK) return st;
+  if (T < 0 || T > kMaxT) return TTQ_EINVAL;
+  if (x_type != TTQ_BF16 && x_type != TTQ_F32) return TTQ_EINVAL;
+  if (flags & ~TTQ_ROPE_INTERLEAVED) return TTQ_EINVAL;
+  if (!(eps >= 0.0) || !std::isfinite(eps)) return TTQ_EINVAL;
+  if (rot_dim < 0 || rot_dim > h->head_dim) return TTQ_EINVAL;
+  if (rot_dim % 16 != 0) return rot_dim % 2 ? TTQ_EINVAL : TTQ_EUNSUPPORTED;
+  const int64_t qw = (int64_t)h->heads * h->head_dim, kw = (int64_t)h->kv_heads * h->head_dim;
+  if (T > 0 && ((qw > 0 && (ldq < qw || ldq > kMaxElems)) || ldk < kw || ldk > kMaxElems ||
+                ldv < kw || ldv > kMaxElems))
+    return TTQ_EINVAL;
+  const bool same = k_codes == v_codes;
+  if (same && k_codes && h->k_first < h->v_first + kw && h->v_first < h->k_first + kw)
+    return TTQ_EINVAL;  // K and V of one cache on the same channels
+  if (T == 0) return TTQ_OK;
+  if ((qw > 0 && (!Q || !Q_out)) || !K || !V || !slots) return TTQ_ENULL;
+  if (rot_dim > 0 && (!inv_freq || !positions)) return TTQ_ENULL;
+  if (h->n_slots > 0 &&
+      (!k_codes || !k_scales || !k_mins || !v_codes || !v_scales || !v_mins))
+    return TTQ_ENULL;
+  const int64_t el = x_type == TTQ_F32 ? 4 : 8;
+  if (misaligned(Q, 16) || misaligned(K, 16) || misaligned(V, 16) ||
+      misaligned(q_weight, 16) || misaligned(k_weight, 16) || misaligned(inv_freq, 16) ||
+      misaligned(positions, 4) || misaligned(Q_out, 16) || misaligned(slots, 8) ||
+      misaligned(k_dhalf, 16) || misaligned(v_dhalf, 16) || misaligned(k_codes, 16) ||
+      misaligned(v_codes, 16) || misaligned(k_scales, 4) || misaligned(k_mins, 4) ||
+      misaligned(v_scales, 4) || misaligned(v_mins, 4) || (qw > 0 && ldq % el != 0) ||
+      ldk % el != 0 || ldv % el != 0)
+    return TTQ_EALIGN;
+  if (inject_hip_error()) return TTQ_EHIP;
+  RopeArgs a{};
+  a.Q = Q; a.K = K; a.V = V; a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;
+  a.x_f32 = x_type == TTQ_F32;
+  a.wq = q_weight; a.wk = k_weight; a.eps = eps; a.inv_hd = 1.0 / h->head_dim;
+  a.inv_freq = inv_freq; a.positions = positions;
+  a.head_dim = h->head_dim; a.rot_dim = rot_dim; a.inter = (flags & TTQ_ROPE_INTERLEAVED) != 0;
+  a.q_width = (int)qw; a.kv_width = (int)kw;
+  a.Q_out = static_cast<bf16_t*>(Q_out);
+  a.slots = slots; a.k_dh = k_dhalf; a.v_dh = v_dhalf;
+  a.k_codes = k_codes; a.v_codes = v_codes;
+  a.k_s = k_scales; a.k_m = k_mins; a.v_s = v_scales; a.v_m = v_mins;
+  a.k_first = h->k_first; a.v_first = h->v_first;
+  a.T = T; a.C = h->d; a.n_slots = h->n_slots; a.row_bytes = rb;
+  set_code_constants(f, &a.Nf, &a.rN, &a.cb, &a.qf);
+  return run(K_CACHE_ROPE, static_cast<hipStream_t>(stream),
+             [&](const Launch& L) { return launch_cache_rope(a, f.group, L); });
+}
+
+struct AttnPlan {
+  int64_t tiles = 0, max_len = 0;
+  int nsplit = 1;
+  size_t off_ml = 0, total = 0;
+};
+// waves that fill the chip (256 compute units, 8 waves each), and keys below which
+// a range is not divided further
+constexpr int64_t kAttnWaves = 2048, kAttnMinKeys = 64;
+
+int plan_attention(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t max_pages,
+                   int32_t page_tokens, int64_t max_len, bool packed, AttnPlan* P) {
+  ttq_params f;
+  int64_t rb = 0;
+  int st = validate_heads(h, &f, &rb);
+  if (st != TTQ_OK) return st;
+  if (h->heads < 1) return TTQ_EINVAL;
+  if (T < 0 || T > kMaxT || n_seq < 0 || n_seq > kMaxSeq) return TTQ_EINVAL;
+  if (max_pages < 0 || max_pages > kMaxT || max_len < 0) return TTQ_EINVAL;
+  if (!packed && T != n_seq) return TTQ_EINVAL;
+  st = validate_page_tokens(page_tokens);
+  if (st != TTQ_OK) return st;
+  if (T * h->heads > INT32_MAX) return TTQ_EINVAL;
+  const int cb = container_bits(f.bits);
+  if (cb != 4 && cb != 8) return TTQ_EUNSUPPORTED;
+  if (h->n_slots > INT32_MAX) return TTQ_EUNSUPPORTED;
+  const int64_t room = max_pages * page_tokens;
+  P->max_len = max_len > 0 ? std::min(max_len, room) : room;
+  const int64_t G = h->heads / h->kv_heads;
+  P->tiles = packed ? T * G / 16 + n_seq : n_seq * ((G + 15) / 16);
+  const int64_t units = std::max<int64_t>(1, P->tiles * h->kv_heads);
+  P->nsplit = (int)std::clamp<int64_t>(
+      kAttnWaves / units, 1, std::max<int64_t>(1, P->max_len / kAttnMinKeys));
+  if (P->nsplit > 1) {
+    const size_t rows = (size_t)T * h->heads * P->nsplit;
+    P->off_ml = align_up(rows * h->head_dim * sizeof(float), 256);
+    P->total = P->off_ml + align_up(rows * 2 * sizeof(float), 256);
+  }
+  return TTQ_OK;
+}
+
+int cache_attention_impl(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t max_pages,
+                         int32_t page_tokens, int64_t max_len, int64_t window, double scale,
+                         const void* Q, int64_t ldq, const int32_t* offsets,
+                         const int32_t* pages, const int32_t* lens, const uint8_t* k_codes,
+                         const float* k_scales, const float* k_mins, const uint8_t* v_codes,
+                         const float* v_scales, const float* v_mins,
+                         const float* k_dhalf_inv, const float* v_dhalf_inv, void* out,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  AttnPlan P;
+  int st = plan_attention(h, T, n_seq, max_pages, page_tokens, max_len, offsets != nullptr, &P);
+  if (st != TTQ_OK) return st;
+  if (window < 0 || !std::isfinite(scale)) return TTQ_EINVAL;
+  const int64_t qw = (int64_t)h->heads * h->head_dim;
+  if (T > 0 && (ldq < qw || ldq > kMaxElems)) return TTQ_EINVAL;
+  if (T == 0 || n_seq == 0) return TTQ_OK;
+  if (!Q || !lens || !out) return TTQ_ENULL;
+  if (max_pages > 0 && !pages) return TTQ_ENULL;
+  if (h->n_slots > 0 &&
+      (!k_codes || !k_scales || !k_mins || !v_codes || !v_scales || !v_mins))
+    return TTQ_ENULL;
+  if (misaligned(Q, 16) || misaligned(offsets, 4) || misaligned(pages, 4) ||
+      misaligned(lens, 4) || misaligned(k_codes, 16) || misaligned(v_codes, 16) ||
+      misaligned(k_scales, 4) || misaligned(k_mins, 4) || misaligned(v_scales, 4) ||
+      misaligned(v_mins, 4) || misaligned(k_dhalf_inv, 16) || misaligned(v_dhalf_inv, 16) ||
+      misaligned(out, 16) || misaligned(workspace, 256) || ldq % 8 != 0)
+    return TTQ_EALIGN;
+  if (P.total > 0 && !workspace) return TTQ_ENULL;
+  if (workspace_bytes < P.total) return TTQ_EWORKSPACE;
+  if (inject_hip_error()) return TTQ_EHIP;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  ttq_params f;
+  int64_t rb = 0;
+  (void)validate_heads(h, &f, &rb);
+  AttnArgs a{};
+  a.Q = static_cast<const bf16_t*>(Q); a.ldq = ldq;
+  a.offsets = offsets; a.pages = pages; a.lens = lens;
+  a.kc = k_codes; a.vc = v_codes; a.ks = k_scales; a.km = k_mins; a.vs = v_scales;
+  a.vm = v_mins; a.kdhi = k_dhalf_inv; a.vdhi = v_dhalf_inv;
+  a.out = static_cast<bf16_t*>(out);
+  a.part = static_cast<float*>(workspace);
+  a.ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + P.off_ml);
+  a.T = T; a.n_seq = n_seq; a.max_pages = max_pages;
+  a.max_len = h->n_slots > 0 ? P.max_len : 0;  // (no row: no key)
+  a.window = std::min<int64_t>(window, kMaxElems); a.row_bytes = rb; a.groups = h->d / h->group;
+  a.k_first = h->k_first; a.v_first = h->v_first; a.n_slots = (int)h->n_slots;
+  a.H = h->heads; a.KV = h->kv_heads; a.G = h->heads / h->kv_heads;
+  a.pshift = __builtin_ctz((unsigned)page_tokens);
+  a.gshift = __builtin_ctz((unsigned)h->group);
+  a.scale2 = (float)(scale * 1.4426950408889634);
+  a.nsplit = P.nsplit; a.tiles = P.tiles;
+  const int cb = container_bits(f.bits);
+  st = run(K_ATTN_SPLIT, s, [&](const Launch& L) {
+    return launch_attn_split(a, h->head_dim, cb, (int)f.qformat, f.group, L);
+  });
+  if (st != TTQ_OK || P.nsplit == 1) return st;
+  return run(K_ATTN_JOIN, s, [&](const Launch& L) { return launch_attn_join(a, h->head_dim, L); });
 }
 
 // ------------------------------------------- allocation-free entry point
@@ -1657,6 +1884,57 @@ int ttq_cache_read(const ttq_params* prm, int64_t n_slots, int64_t n_seq,
   return cache_read_impl(prm, n_slots, n_seq, max_pages, page_tokens, pages,
                          lens, codes, scales, mins, dhalf_inv, out_type, out,
                          stream);
+}
+
+int ttq_cache_extend(int64_t n_seq, int64_t T, int64_t max_pages, int64_t n_pages,
+                     int32_t page_tokens, const int32_t* lens, const int32_t* added,
+                     int32_t* pages, int32_t* free_pages, const int32_t* free_count,
+                     int32_t* lens_out, int32_t* free_count_out, int32_t* offsets,
+                     int32_t* positions, int64_t* slots, void* stream) {
+  return cache_extend_impl(n_seq, T, max_pages, n_pages, page_tokens, lens, added, pages,
+                           free_pages, free_count, lens_out, free_count_out, offsets,
+                           positions, slots, stream);
+}
+
+int ttq_cache_rope(const ttq_heads* hd, int64_t T, int32_t x_type, const void* Q, int64_t ldq,
+                   const void* K, int64_t ldk, const void* V, int64_t ldv,
+                   const float* q_weight, const float* k_weight, double eps,
+                   const float* inv_freq, int32_t rot_dim, uint32_t flags,
+                   const int32_t* positions, void* Q_out, const int64_t* slots,
+                   const float* k_dhalf, const float* v_dhalf, uint8_t* k_codes,
+                   float* k_scales, float* k_mins, uint8_t* v_codes, float* v_scales,
+                   float* v_mins, void* stream) {
+  return cache_rope_impl(hd, T, x_type, Q, ldq, K, ldk, V, ldv, q_weight, k_weight, eps,
+                         inv_freq, rot_dim, flags, positions, Q_out, slots, k_dhalf, v_dhalf,
+                         k_codes, k_scales, k_mins, v_codes, v_scales, v_mins, stream);
+}
+
+int ttq_cache_attention_workspace_bytes(const ttq_heads* hd, int64_t T, int64_t n_seq,
+                                        int64_t max_pages, int32_t page_tokens,
+                                        int64_t max_len, size_t* bytes) {
+  if (!bytes) return TTQ_ENULL;
+  // packed rows or one each: the larger of the two
+  AttnPlan P, one;
+  const int st = plan_attention(hd, T, n_seq, max_pages, page_tokens, max_len, true, &P);
+  if (st != TTQ_OK) return st;
+  if (T == n_seq)
+    (void)plan_attention(hd, T, n_seq, max_pages, page_tokens, max_len, false, &one);
+  *bytes = std::max(P.total, one.total);
+  return TTQ_OK;
+}
+
+int ttq_cache_attention(const ttq_heads* hd, int64_t T, int64_t n_seq, int64_t max_pages,
+                        int32_t page_tokens, int64_t max_len, int64_t window, double scale,
+                        const void* Q, int64_t ldq, const int32_t* offsets,
+                        const int32_t* pages, const int32_t* lens, const uint8_t* k_codes,
+                        const float* k_scales, const float* k_mins, const uint8_t* v_codes,
+                        const float* v_scales, const float* v_mins,
+                        const float* k_dhalf_inv, const float* v_dhalf_inv, void* out,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  return cache_attention_impl(hd, T, n_seq, max_pages, page_tokens, max_len, window, scale, Q,
+                              ldq, offsets, pages, lens, k_codes, k_scales, k_mins, v_codes,
+                              v_scales, v_mins, k_dhalf_inv, v_dhalf_inv, out, workspace,
+                              workspace_bytes, stream);
 }
 
 const char* ttq_status_string(int status) {

@@ -50,6 +50,11 @@ enum KernelKind {
   K_MOE_UP,            // experts: gate and up products, silu(g) u
   K_MOE_DOWN,          // experts: down products
   K_MOE_SUM,           // experts: weighted sum of a row's experts
+  K_EXTEND,            // page tables and slot maps of a step
+  K_EXTEND_ROWS,       // positions and slots of a large step's rows
+  K_CACHE_ROPE,        // heads normed and rotated, K and V into the cache
+  K_ATTN_SPLIT,        // attention over a cache: ranges of keys
+  K_ATTN_JOIN,         // attention: the ranges of a row joined
   K_NUM_KINDS
 };
 
@@ -786,6 +791,72 @@ struct CacheReadArgs {
   int qf;                 // QF_FP8: E4M3 codes; any other format: integer codes
 };
 hipError_t launch_cache_read(const CacheReadArgs& a, int cb, const Launch& L);
+
+struct ExtendArgs {
+  const int32_t* lens;        // [n_seq]
+  const int32_t* added;       // [n_seq], negative: ended
+  int32_t* pages;             // [n_seq][max_pages]
+  int32_t* free_pages;        // [n_pages]
+  const int32_t* free_count;
+  int32_t* lens_out;          // [n_seq], may be lens
+  int32_t* free_count_out;    // may be free_count
+  int32_t* offsets;           // [n_seq + 1]
+  int32_t* positions;         // [T]
+  int64_t* slots;             // [T]
+  int64_t n_seq, T, max_pages, n_pages;
+  int pshift;                 // log2 of the rows per page
+  int rows_here;              // positions and slots by the same launch
+};
+bool extend_rows_apart(const ExtendArgs& a);
+hipError_t launch_extend(const ExtendArgs& a, const Launch& L);
+hipError_t launch_extend_rows(const ExtendArgs& a, const Launch& L);
+
+struct RopeArgs {
+  const void *Q, *K, *V;      // [T] rows, bf16 or float32
+  int64_t ldq, ldk, ldv;
+  int x_f32;
+  const float *wq, *wk;       // optional [head_dim]
+  double eps, inv_hd;
+  const float* inv_freq;      // [rot_dim / 2]
+  const int32_t* positions;   // [T]
+  int head_dim, rot_dim, inter;
+  int q_width, kv_width;      // channels of a row's Q, and of its K or V
+  bf16_t* Q_out;              // [T][q_width]
+  const int64_t* slots;       // [T]
+  const float *k_dh, *v_dh;   // optional [C]
+  uint8_t *k_codes, *v_codes;
+  float *k_s, *k_m, *v_s, *v_m;
+  int64_t k_first, v_first;
+  int64_t T, C, n_slots, row_bytes;
+  float Nf, rN;               // as in CacheWriteArgs
+  int cb, qf;
+  int parts;                  // waves of a row (set by the launcher)
+};
+hipError_t launch_cache_rope(RopeArgs a, int group, const Launch& L);
+
+struct AttnArgs {
+  const bf16_t* Q;            // [T] rows of H * head_dim
+  int64_t ldq;
+  const int32_t* offsets;     // optional [n_seq + 1]
+  const int32_t* pages;       // [n_seq][max_pages]
+  const int32_t* lens;        // [n_seq]
+  const uint8_t *kc, *vc;
+  const float *ks, *km, *vs, *vm;
+  const float *kdhi, *vdhi;   // optional [C]
+  bf16_t* out;                // [T][H][head_dim]
+  float* part;                // [T][H][nsplit][head_dim] of ranges of keys
+  float* ml;                  // [T][H][nsplit][2]: their maximum and sum
+  int64_t T, n_seq, max_pages, max_len, window, row_bytes, groups, k_first, v_first;
+  int n_slots;
+  int H, KV, G;               // query heads, K/V heads, their quotient
+  int pshift, gshift;
+  float scale2;               // scale * log2(e)
+  int nsplit;                 // ranges of keys
+  int64_t tiles;              // blocks of 16 query rows of a K/V head
+};
+hipError_t launch_attn_split(const AttnArgs& a, int head_dim, int cb, int qf, int group,
+                             const Launch& L);
+hipError_t launch_attn_join(const AttnArgs& a, int head_dim, const Launch& L);
 
 // Plain streaming read (measurement ceiling of the one-token projection):
 // one workgroup per kStreamReadBlockBytes, one XOR per workgroup to sink.

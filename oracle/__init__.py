@@ -6,3 +6,4 @@ shares no code with it.
 """
 from .ttq_oracle import *  # noqa: F401,F403
 from .ttq_oracle import overhead_ratio  # noqa: F401
+from .attention_oracle import *  # noqa: F401,F403
