@@ -41,6 +41,7 @@ SOURCES = [
     "k_pages.hip",
     "k_rope.hip",
     "k_attention.hip",
+    "k_attn_tile.hip",
     "k_adapters.hip",
     "k_moe.hip",
     "ttq_api.cpp",

@@ -61,40 +61,6 @@ __device__ __forceinline__ void load_words(Words<NB>& d, const uint8_t* p) {
   }
 }
 
-// Operand pairs (key a, key b) of a lane's channels: a and b hold NC of them
-template <int CB, bool F8, int NC>
-__device__ __forceinline__ void pairs(const unsigned* a, const unsigned* b, unsigned* out) {
-  if constexpr (F8) {
-#pragma unroll
-    for (int i = 0; i < NC / 4; ++i) {
-      const unsigned lo = __builtin_amdgcn_perm(b[i], a[i], 0x05010400u);
-      const unsigned hi = __builtin_amdgcn_perm(b[i], a[i], 0x07030602u);
-      out[4 * i] = e4m3_pair(lo, false);
-      out[4 * i + 1] = e4m3_pair(lo, true);
-      out[4 * i + 2] = e4m3_pair(hi, false);
-      out[4 * i + 3] = e4m3_pair(hi, true);
-    }
-  } else if constexpr (CB == 8) {
-#pragma unroll
-    for (int i = 0; i < NC / 4; ++i) {
-      out[4 * i] = __builtin_amdgcn_perm(b[i], a[i], 0x0c040c00u);
-      out[4 * i + 1] = __builtin_amdgcn_perm(b[i], a[i], 0x0c050c01u);
-      out[4 * i + 2] = __builtin_amdgcn_perm(b[i], a[i], 0x0c060c02u);
-      out[4 * i + 3] = __builtin_amdgcn_perm(b[i], a[i], 0x0c070c03u);
-    }
-  } else {  // channel i is 16-fold where i is odd
-#pragma unroll
-    for (int i = 0; i < NC / 4; ++i) {
-      const unsigned x = __builtin_amdgcn_perm(b[i / 2], a[i / 2], i % 2 ? 0x07060302u : 0x05040100u);
-      const unsigned h = x >> 8;
-      out[4 * i] = x & 0x000f000fu;
-      out[4 * i + 1] = x & 0x00f000f0u;
-      out[4 * i + 2] = h & 0x000f000fu;
-      out[4 * i + 3] = h & 0x00f000f0u;
-    }
-  }
-}
-
 __device__ __forceinline__ unsigned mul_pair(unsigned a, unsigned b) {
   return __builtin_bit_cast(unsigned, __builtin_bit_cast(f16x2, a) * __builtin_bit_cast(f16x2, b));
 }
@@ -350,7 +316,7 @@ __global__ __launch_bounds__(256) void k_attn_split(AttnArgs a) {
     const u32x4 sv = *(const u32x4*)&sm_v[w][0][n * NC / GSE][c * 8];
     unsigned vp[4][NC];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) pairs<CB, F8, NC>(b.v[2 * j].w, b.v[2 * j + 1].w, vp[j]);
+    for (int j = 0; j < 4; ++j) key_pairs<CB, F8, NC>(b.v[2 * j].w, b.v[2 * j + 1].w, vp[j]);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const u32x4 v = {mul_pair(vp[0][i], sv.x), mul_pair(vp[1][i], sv.y), mul_pair(vp[2][i], sv.z),

@@ -250,7 +250,7 @@ const char* kKernelNames[K_NUM_KINDS] = {
     "pca_complete", "stream_read", "cache_write", "cache_read",
     "adapters_step", "adapters_shrink", "adapters_expand", "moe_score",
     "moe_route", "moe_up", "moe_down", "moe_sum", "cache_extend",
-    "cache_extend_rows", "cache_rope", "attention_split", "attention_join"};
+    "cache_extend_rows", "cache_rope", "attention_split", "attention_tile", "attention_join"};
 
 hipEvent_t take_event() {
   if (!g_timing.pool.empty()) {
@@ -1568,11 +1568,15 @@ int cache_rope_impl(const ttq_heads* h, int64_t T, int32_t x_type, const void* Q
 struct AttnPlan {
   int64_t tiles = 0, max_len = 0;
   int nsplit = 1;
+  bool tile = false;  // blocks of 256 rows that share decoded tiles, else of 16
   size_t off_ml = 0, total = 0;
 };
 // waves that fill the chip (256 compute units, 8 waves each), and keys below which
 // a range is not divided further
 constexpr int64_t kAttnWaves = 2048, kAttnMinKeys = 64;
+// the same for the workgroups of decoded tiles, and the rows a sequence and K/V head
+// from which they are used
+constexpr int64_t kAttnTileGroups = 512, kAttnTileMinKeys = 512, kAttnTileRows = 64;
 
 int plan_attention(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t max_pages,
                    int32_t page_tokens, int64_t max_len, bool packed, AttnPlan* P) {
@@ -1593,10 +1597,13 @@ int plan_attention(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t max_pag
   const int64_t room = max_pages * page_tokens;
   P->max_len = max_len > 0 ? std::min(max_len, room) : room;
   const int64_t G = h->heads / h->kv_heads;
-  P->tiles = packed ? T * G / 16 + n_seq : n_seq * ((G + 15) / 16);
+  P->tile = T * G >= kAttnTileRows * n_seq;
+  const int64_t rows_block = P->tile ? 256 : 16;
+  P->tiles = packed ? T * G / rows_block + n_seq : n_seq * ((G + rows_block - 1) / rows_block);
   const int64_t units = std::max<int64_t>(1, P->tiles * h->kv_heads);
   P->nsplit = (int)std::clamp<int64_t>(
-      kAttnWaves / units, 1, std::max<int64_t>(1, P->max_len / kAttnMinKeys));
+      (P->tile ? kAttnTileGroups : kAttnWaves) / units, 1,
+      std::max<int64_t>(1, P->max_len / (P->tile ? kAttnTileMinKeys : kAttnMinKeys)));
   if (P->nsplit > 1) {
     const size_t rows = (size_t)T * h->heads * P->nsplit;
     P->off_ml = align_up(rows * h->head_dim * sizeof(float), 256);
@@ -1656,7 +1663,9 @@ int cache_attention_impl(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t m
   a.scale2 = (float)(scale * 1.4426950408889634);
   a.nsplit = P.nsplit; a.tiles = P.tiles;
   const int cb = container_bits(f.bits);
-  st = run(K_ATTN_SPLIT, s, [&](const Launch& L) {
+  st = P.tile ? run(K_ATTN_TILE, s, [&](const Launch& L) {
+    return launch_attn_tile(a, h->head_dim, cb, (int)f.qformat, L);
+  }) : run(K_ATTN_SPLIT, s, [&](const Launch& L) {
     return launch_attn_split(a, h->head_dim, cb, (int)f.qformat, f.group, L);
   });
   if (st != TTQ_OK || P.nsplit == 1) return st;

@@ -54,6 +54,7 @@ enum KernelKind {
   K_EXTEND_ROWS,       // positions and slots of a large step's rows
   K_CACHE_ROPE,        // heads normed and rotated, K and V into the cache
   K_ATTN_SPLIT,        // attention over a cache: ranges of keys
+  K_ATTN_TILE,         // attention over a cache: decoded tiles of keys
   K_ATTN_JOIN,         // attention: the ranges of a row joined
   K_NUM_KINDS
 };
@@ -852,10 +853,11 @@ struct AttnArgs {
   int pshift, gshift;
   float scale2;               // scale * log2(e)
   int nsplit;                 // ranges of keys
-  int64_t tiles;              // blocks of 16 query rows of a K/V head
+  int64_t tiles;              // blocks of query rows of a K/V head
 };
 hipError_t launch_attn_split(const AttnArgs& a, int head_dim, int cb, int qf, int group,
                              const Launch& L);
+hipError_t launch_attn_tile(const AttnArgs& a, int head_dim, int cb, int qf, const Launch& L);
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, const Launch& L);
 
 // Plain streaming read (measurement ceiling of the one-token projection):
