@@ -50,38 +50,29 @@ __device__ __forceinline__ constexpr int slot_shift(int slot) {
   return CB == 4 && (slot / 2) & 1 ? 4 : 0;
 }
 
-// NC channels of two keys a and b as pairs (a, b), one a channel; 4 bits: 16-fold
-// where the channel is odd
-template <int CB, bool F8, int NC>
-__device__ __forceinline__ void key_pairs(const unsigned* a, const unsigned* b, unsigned* out) {
+// Channels 4 i .. 4 i + 3 of two keys a and b as pairs (a, b), one a channel; 4 bits:
+// 16-fold where the channel is odd
+template <int CB, bool F8>
+__device__ __forceinline__ void key_pairs(const unsigned* a, const unsigned* b, int i, unsigned (&out)[4]) {
   if constexpr (F8) {
-#pragma unroll
-    for (int i = 0; i < NC / 4; ++i) {
-      const unsigned lo = __builtin_amdgcn_perm(b[i], a[i], 0x05010400u);
-      const unsigned hi = __builtin_amdgcn_perm(b[i], a[i], 0x07030602u);
-      out[4 * i] = e4m3_pair(lo, false);
-      out[4 * i + 1] = e4m3_pair(lo, true);
-      out[4 * i + 2] = e4m3_pair(hi, false);
-      out[4 * i + 3] = e4m3_pair(hi, true);
-    }
+    const unsigned lo = __builtin_amdgcn_perm(b[i], a[i], 0x05010400u);
+    const unsigned hi = __builtin_amdgcn_perm(b[i], a[i], 0x07030602u);
+    out[0] = e4m3_pair(lo, false);
+    out[1] = e4m3_pair(lo, true);
+    out[2] = e4m3_pair(hi, false);
+    out[3] = e4m3_pair(hi, true);
   } else if constexpr (CB == 8) {
-#pragma unroll
-    for (int i = 0; i < NC / 4; ++i) {
-      out[4 * i] = __builtin_amdgcn_perm(b[i], a[i], 0x0c040c00u);
-      out[4 * i + 1] = __builtin_amdgcn_perm(b[i], a[i], 0x0c050c01u);
-      out[4 * i + 2] = __builtin_amdgcn_perm(b[i], a[i], 0x0c060c02u);
-      out[4 * i + 3] = __builtin_amdgcn_perm(b[i], a[i], 0x0c070c03u);
-    }
+    out[0] = __builtin_amdgcn_perm(b[i], a[i], 0x0c040c00u);
+    out[1] = __builtin_amdgcn_perm(b[i], a[i], 0x0c050c01u);
+    out[2] = __builtin_amdgcn_perm(b[i], a[i], 0x0c060c02u);
+    out[3] = __builtin_amdgcn_perm(b[i], a[i], 0x0c070c03u);
   } else {
-#pragma unroll
-    for (int i = 0; i < NC / 4; ++i) {
-      const unsigned x = __builtin_amdgcn_perm(b[i / 2], a[i / 2], i % 2 ? 0x07060302u : 0x05040100u);
-      const unsigned h = x >> 8;
-      out[4 * i] = x & 0x000f000fu;
-      out[4 * i + 1] = x & 0x00f000f0u;
-      out[4 * i + 2] = h & 0x000f000fu;
-      out[4 * i + 3] = h & 0x00f000f0u;
-    }
+    const unsigned x = __builtin_amdgcn_perm(b[i / 2], a[i / 2], i % 2 ? 0x07060302u : 0x05040100u);
+    const unsigned h = x >> 8;
+    out[0] = x & 0x000f000fu;
+    out[1] = x & 0x00f000f0u;
+    out[2] = h & 0x000f000fu;
+    out[3] = h & 0x00f000f0u;
   }
 }
 

@@ -58,7 +58,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   __shared__ unsigned sm_bad[2][KT];  // of a key: groups of V that are NaN; kOut
   __shared__ int sm_flag[3], sm_y[2];
 
-  const int tid = threadIdx.x, l = tid & 63, w = tid >> 6;
+  const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = l & 31, hf = l >> 5;
   const int h = (int)(blockIdx.x % a.KV);
   const int64_t bs = blockIdx.x / a.KV;
@@ -223,14 +223,15 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
       if (s[j] > kSMax || __builtin_fabsf(m[j]) > 30000.f) f |= 1;
     }
     const unsigned s1 = both(s[0], s[1]), s16 = both(s[0] * 0.0625f, s[1] * 0.0625f), mm = both(m[0], m[1]);
-    unsigned p[8];
-    key_pairs<CB, F8, 8>(x.v[0], x.v[1], p);
+    unsigned p[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) key_pairs<CB, F8>(x.v[0], x.v[1], i, p[i]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int ch = vch + i;
       const int sw = KT >= 64 ? (ch ^ (ch >> 3)) & 7 : ((ch >> 2) ^ (ch >> 3)) & 3;
       *(unsigned*)&sm_v[b][ch * KT + (((vkey >> 3) ^ sw) << 3) + (vkey & 7)] =
-          fma2(p[i], !F8 && CB == 4 && (i & 1) ? s16 : s1, mm);
+          fma2(p[i / 4][i % 4], !F8 && CB == 4 && (i & 1) ? s16 : s1, mm);
     }
     if (f) atomicOr(&sm_flag[slot], f);
   };

@@ -1576,7 +1576,7 @@ struct AttnPlan {
 constexpr int64_t kAttnWaves = 2048, kAttnMinKeys = 64;
 // the same for the workgroups of decoded tiles, and the rows a sequence and K/V head
 // from which they are used
-constexpr int64_t kAttnTileGroups = 512, kAttnTileMinKeys = 512, kAttnTileRows = 64;
+constexpr int64_t kAttnTileGroups = 256, kAttnTileMinKeys = 512, kAttnTileRows = 64;
 
 int plan_attention(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t max_pages,
                    int32_t page_tokens, int64_t max_len, bool packed, AttnPlan* P) {
@@ -1603,7 +1603,7 @@ int plan_attention(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t max_pag
   const int64_t units = std::max<int64_t>(1, P->tiles * h->kv_heads);
   P->nsplit = (int)std::clamp<int64_t>(
       (P->tile ? kAttnTileGroups : kAttnWaves) / units, 1,
-      std::max<int64_t>(1, P->max_len / (P->tile ? kAttnTileMinKeys : kAttnMinKeys)));
+      std::clamp<int64_t>(P->max_len / (P->tile ? kAttnTileMinKeys : kAttnMinKeys), 1, kAttnMaxSplit));
   if (P->nsplit > 1) {
     const size_t rows = (size_t)T * h->heads * P->nsplit;
     P->off_ml = align_up(rows * h->head_dim * sizeof(float), 256);
@@ -1661,6 +1661,8 @@ int cache_attention_impl(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t m
   a.pshift = __builtin_ctz((unsigned)page_tokens);
   a.gshift = __builtin_ctz((unsigned)h->group);
   a.scale2 = (float)(scale * 1.4426950408889634);
+  a.octets = page_tokens >= 8 && h->n_slots % 8 == 0 &&
+             h->n_slots * std::max<int64_t>(rb, 4 * a.groups) <= int64_t(1) << 32;
   a.nsplit = P.nsplit; a.tiles = P.tiles;
   const int cb = container_bits(f.bits);
   st = P.tile ? run(K_ATTN_TILE, s, [&](const Launch& L) {

@@ -852,9 +852,11 @@ struct AttnArgs {
   int H, KV, G;               // query heads, K/V heads, their quotient
   int pshift, gshift;
   float scale2;               // scale * log2(e)
+  int octets;                 // 8 rows of a page are adjacent, offsets fit 32 bits
   int nsplit;                 // ranges of keys
   int64_t tiles;              // blocks of query rows of a K/V head
 };
+constexpr int kAttnMaxSplit = 256;  // ranges of keys at most
 hipError_t launch_attn_split(const AttnArgs& a, int head_dim, int cb, int qf, int group,
                              const Launch& L);
 hipError_t launch_attn_tile(const AttnArgs& a, int head_dim, int cb, int qf, const Launch& L);
