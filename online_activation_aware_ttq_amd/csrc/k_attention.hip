@@ -39,18 +39,17 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// NB bytes at p, aligned to the smaller of NB and 16
 template <int NB>
 struct Words {
   unsigned w[NB >= 4 ? NB / 4 : 1];
 };
 template <int NB>
-__device__ __forceinline__ void load_words(Words<NB>& d, const uint8_t* p) {
+__device__ __forceinline__ void read_words(Words<NB>& d, const uint8_t* p) {
   if constexpr (NB >= 16) {
-#pragma unroll
-    for (int i = 0; i < NB / 16; ++i) {
-      const u32x4 v = *(const u32x4*)(p + 16 * i);
-      d.w[4 * i] = v.x; d.w[4 * i + 1] = v.y; d.w[4 * i + 2] = v.z; d.w[4 * i + 3] = v.w;
-    }
+    static_assert(NB == 16);
+    const u32x4 v = *(const u32x4*)p;
+    d.w[0] = v.x; d.w[1] = v.y; d.w[2] = v.z; d.w[3] = v.w;
   } else if constexpr (NB == 8) {
     const u32x2 v = *(const u32x2*)p;
     d.w[0] = v.x; d.w[1] = v.y;
@@ -60,24 +59,21 @@ __device__ __forceinline__ void load_words(Words<NB>& d, const uint8_t* p) {
     d.w[0] = *(const uint16_t*)p;
   }
 }
-// the same at byte lane + uniform of a buffer: no address arithmetic a lane
-template <int NB>
-__device__ __forceinline__ void load_words(Words<NB>& d, __amdgpu_buffer_rsrc_t r, unsigned lane,
-                                           unsigned uniform) {
-  if constexpr (NB >= 16) {
-#pragma unroll
-    for (int i = 0; i < NB / 16; ++i) {
-      const u32x4 v = buf_load16(r, lane + 16 * i, uniform);
-      d.w[4 * i] = v.x; d.w[4 * i + 1] = v.y; d.w[4 * i + 2] = v.z; d.w[4 * i + 3] = v.w;
-    }
-  } else if constexpr (NB == 8) {
-    const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, lane, uniform, 0);
-    d.w[0] = v[0]; d.w[1] = v[1];
-  } else if constexpr (NB == 4) {
-    d.w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, lane, uniform, 0);
-  } else {
-    d.w[0] = __builtin_amdgcn_raw_buffer_load_b16(r, lane, uniform, 0);
-  }
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+
+// 16 or 4 bytes a lane from each lane's address into LDS, lane after lane
+__device__ __forceinline__ void load_lds16(const void* p, void* lds) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
+                                   (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(const void* p, void* lds) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
+                                   (__attribute__((address_space(3))) void*)lds, 4, 0, 0);
 }
 
 __device__ __forceinline__ unsigned mul_pair(unsigned a, unsigned b) {
@@ -85,10 +81,25 @@ __device__ __forceinline__ unsigned mul_pair(unsigned a, unsigned b) {
 }
 
 // HD channels a head; GSE = min(group, HD) of them a group; CB-bit codes
-template <int HD, int GSE, int CB, bool F8, bool OCT>
-__global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_attn_split(AttnArgs a) {
-  constexpr int NG = HD / GSE;           // groups of a head
+template <int HD, int GSE, int CB, bool F8>
+struct SplitShape {
+  static constexpr int NG = HD / GSE;           // groups of a head
+  static constexpr int HB = HD * CB / 8;        // bytes of a head
+  static constexpr int NW = HB == 256 ? 2 : 4;  // waves
+  static constexpr int NS = HB <= 64 ? 3 : 2;   // buffers
+  static constexpr int CODES = 32 * NW * HB;    // bytes of K's (or V's) codes of a step
+  static constexpr int SCALES = 128 * NW * NG;  // of one of its four arrays of scales
+  static constexpr int STEP = 2 * CODES + 4 * SCALES;
+  static constexpr int NPAGE = 1024;            // entries of the page table at hand
+  static constexpr int LDS = NS * STEP + 4 * NPAGE;
+};
+
+template <int HD, int GSE, int CB, bool F8>
+__global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1 : 2) void k_attn_split(AttnArgs a) {
+  using Sh = SplitShape<HD, GSE, CB, F8>;
+  constexpr int NG = Sh::NG, HB = Sh::HB, NS = Sh::NS, NW = Sh::NW;
   constexpr int KB = GSE * CB / 32;      // bytes of a lane's quarter of a group of K
+  constexpr int KP = KB > 16 ? KB / 16 : 1, KW = KB > 16 ? 16 : KB;  // in pieces
   constexpr int NC = HD / 16;            // channels of V of a lane
   constexpr int VB = NC * CB / 8;
   constexpr int U = kUnit<F8>;
@@ -101,23 +112,26 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_
   constexpr int MU = F8 ? 0 : kP ? 20 : 10;  // V's offsets: 2^MU of O's unit
   constexpr int kMid = F8 ? 0 : 1 << (CB - 1);
   constexpr float kLazy = 8.f;
-  __shared__ __align__(16) unsigned sm_row[4][32];
-  __shared__ __align__(16) float sm_k[4][2][NG][32];
-  __shared__ __align__(16) _Float16 sm_s[4][NG][32], sm_m[4][F8 ? 1 : 2 * NG][32];
+  __shared__ __align__(16) float sm_k[NW][2][NG][32];
+  __shared__ __align__(16) _Float16 sm_s[NW][NG][32], sm_m[NW][F8 ? 1 : 2 * NG][32];
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  int* sm_page = (int*)(smem + NS * Sh::STEP);
 
-  const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = l & 15, c = l >> 4;
-  // units: (block of rows, range of keys, K/V head), the heads of a range in
-  // neighbouring waves: they read the same rows of the cache
-  const int64_t unit = (int64_t)blockIdx.x * 4 + w;
-  const int h = (int)(unit % a.KV);
-  const int64_t bs = unit / a.KV;
-  const int split = (int)(bs % a.nsplit);
-  const int64_t block = bs / a.nsplit;
-  if (block >= a.tiles) return;  // uniform over the wave, as all that follows
+  // a workgroup: a block of rows, a range of keys, HW neighbouring K/V heads; wave w
+  // takes head w % HW and 32 of a step's 32 * NW / HW keys
+  const int lh = a.hw_shift, HW = 1 << lh, lg = (NW == 4 ? 2 : 1) - lh;
+  const int hgroups = a.KV >> lh, ranges = a.nsplit >> lg;
+  const int h0 = (int)(blockIdx.x % hgroups) << lh;
+  const int64_t bs = blockIdx.x / hgroups;
+  const int range = (int)(bs % ranges);
+  const int64_t block = bs / ranges;
+  const int hh = w & (HW - 1), sub = w >> lh;
+  const int h = h0 + hh, split = (range << lg) + sub;
   int64_t seq, r0;
   SeqRows sr;
-  if (!find_block<16>(a, block, seq, sr, r0)) return;
+  if (!find_block<16>(a, block, seq, sr, r0)) return;  // uniform over the workgroup
 
   // this lane's row
   const int r = (int)min(r0 + n, (int64_t)sr.rows - 1);
@@ -127,8 +141,9 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_
   const int64_t pos_hi = sr.shift + (int)min(r0 + 15, (int64_t)sr.rows - 1) / a.G;
   int64_t lo = a.window > 0 ? max(pos_lo - a.window + 1, (int64_t)0) & ~int64_t(31) : 0;
   const int64_t hi = min(sr.len, pos_hi + 1);
-  const int64_t per = ((hi - lo + a.nsplit - 1) / a.nsplit + 31) & ~int64_t(31);
-  lo += per * split;
+  const int step = 32 << lg;  // keys of a step
+  const int64_t per = ((hi - lo + ranges - 1) / ranges + step - 1) / step * step;
+  lo += per * range;
   const int64_t end = min(lo + per, hi);
   const int64_t orow = ((sr.first + tok) * a.H + head) * a.nsplit + split;
 
@@ -191,70 +206,76 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_
   int Y = -200;
   unsigned nan_groups = 0;
 
-  // The keys in hand, 32 from k0 on; the next ones are asked for as each part has
-  // been used.
-  Words<KB> kw[2][NG];
-  Words<VB> vw[8];
-  float sc[NG], of[NG];   // scales and offsets of key l % 32: K's, or (l >= 32) V's
-  bool seen;              // that key is in the range and in the cache
-
+  // LDS of a step: rows of HW heads' codes, K's then V's, key r of 32 in place (r & 7)
+  // * 4 + r / 8, its 16-byte pieces p in slots p ^ fold(r): the reads below find all
+  // banks; then the scales and offsets of K and V, as they lie in the cache.
+  const int RB = HB << lh, pieces = RB / 16, lrb = __builtin_ctz((unsigned)RB);
+  auto fold = [&](int r) { return ((r & 3) | (((r >> 3) >> lg) << 2)) & (pieces - 1); };
   const int32_t* table = a.pages + seq * a.max_pages;
-  const int64_t pmask = (int64_t(1) << a.pshift) - 1;
-  auto page_of = [&](int64_t k0) {
-    const int64_t key = k0 + (l & 31);
-    return key < end ? table[key >> a.pshift] : -1;
+  const int pmask = (1 << a.pshift) - 1, max_page = (a.n_slots - 1) >> a.pshift;
+  int64_t e0 = 0;  // the first key of the first page at hand
+  // page of a key (-1 behind the last one), and its cache row; where it has none,
+  // row 0, which is there to be read
+  auto page_of = [&](int64_t key) {
+    const int page = sm_page[min((unsigned)(int)(key - e0) >> a.pshift, (unsigned)Sh::NPAGE - 1)];
+    return key < end ? page : -1;
   };
-  const uint8_t* kbase = a.kc + (a.k_first + h * HD) * CB / 8;
-  const uint8_t* vbase = a.vc + (a.v_first + h * HD) * CB / 8;
-  const int64_t go = ((l < 32 ? a.k_first : a.v_first) + h * HD) >> a.gshift;
-  const float* sp = (l < 32 ? a.ks : a.vs) + go;
-  const float* mp = (l < 32 ? a.km : a.vm) + go;
-  const unsigned rb = (unsigned)a.row_bytes;
-  // (up to 2^32 - 1 bytes from a head's first channel on: rows of 32-bit offsets)
-  const int64_t room = std::min<int64_t>(a.n_slots * a.row_bytes, 0xffffffff);
-  const auto kbuf = make_rsrc(kbase, (uint32_t)(room - (kbase - a.kc)));
-  const auto vbuf = make_rsrc(vbase, (uint32_t)(room - (vbase - a.vc)));
-
-  unsigned row;                 // of this lane's key of the next block
-  unsigned ko = 0, vo = 0;      // OCT: where this lane's parts of it begin
-  auto locate = [&](int64_t k0, int page) {
-    const int64_t at = ((int64_t)page << a.pshift) + ((k0 + (l & 31)) & pmask);
-    seen = page >= 0 && at < a.n_slots;
-    row = seen ? (unsigned)at : 0u;  // (row 0 is there to be read)
-    wave_sync();
-    sm_row[w][l & 31] = OCT ? row * rb : row;
-    wave_sync();
-    if constexpr (OCT) {
-      ko = sm_row[w][(n >> 2) * 8] + (n & 3) * rb + c * KB;
-      vo = sm_row[w][c * 8] + n * VB;
+  auto row_of = [&](int64_t key, int page, bool& in) {
+    const unsigned row = ((unsigned)page << a.pshift) + ((int)(key - e0) & pmask);
+    in = (unsigned)page <= (unsigned)max_page && row < (unsigned)a.n_slots;
+    return in ? row : 0u;
+  };
+  const uint8_t* kbase = a.kc + (a.k_first + h0 * HD) * CB / 8;
+  const uint8_t* vbase = a.vc + (a.v_first + h0 * HD) * CB / 8;
+  // this wave's part of a step: 1 KiB of codes an instruction, and 4 / NW of the
+  // arrays of scales, 64 values an instruction
+  constexpr int NQ = HB / 32, PER = 2 * NQ + 2 * NG, NA = 4 / NW;
+  const int lsg = lh + __builtin_ctz((unsigned)NG);  // log2 of a key's scales
+  const int hg = l & ((1 << lsg) - 1);
+  const float* sbase[NA];
+#pragma unroll
+  for (int j = 0; j < NA; ++j) {
+    const int x = w * NA + j;
+    const int64_t first = x < 2 ? a.k_first : a.v_first;
+    sbase[j] = (x == 0 ? a.ks : x == 1 ? a.km : x == 2 ? a.vs : a.vm) +
+               ((first + (h0 + hg / NG) * HD) >> a.gshift) + hg % NG;
+  }
+  auto issue = [&](int64_t k0, int buf) {
+    uint8_t* to = smem + buf * Sh::STEP;
+    constexpr int NI = NW * NG / 2;
+    int pq[NQ], ps[NI];
+    auto code_key = [&](int i, int& piece) {
+      const int at = (w * NQ + i) * 1024 + l * 16, p = at >> lrb;
+      const int r = ((p & 31) >> 2) | ((p & 3) << 3);
+      piece = ((at >> 4) & (pieces - 1)) ^ fold(r);
+      return k0 + (p & ~31) + r;
+    };
+    auto scale_key = [&](int i) { return k0 + ((i * 64 + l) >> lsg); };
+    int piece;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) pq[i] = page_of(code_key(i, piece));
+#pragma unroll
+    for (int i = 0; i < NI; ++i) ps[i] = page_of(scale_key(i));
+    bool in;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int64_t key = code_key(i, piece);
+      const uint64_t off = (uint64_t)row_of(key, pq[i], in) * (unsigned)a.row_bytes + piece * 16;
+      load_lds16(kbase + off, to + (w * NQ + i) * 1024);
+      load_lds16(vbase + off, to + Sh::CODES + (w * NQ + i) * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint64_t off = (uint64_t)row_of(scale_key(i), ps[i], in) * (unsigned)a.groups;
+#pragma unroll
+      for (int j = 0; j < NA; ++j)
+        load_lds4(sbase[j] + off, to + 2 * Sh::CODES + (w * NA + j) * Sh::SCALES + i * 256);
     }
   };
-  auto fetch_k = [&] {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if constexpr (OCT) {  // eight rows one after another, 32-bit offsets
-#pragma unroll
-        for (int g = 0; g < NG; ++g) load_words<KB>(kw[t][g], kbuf, ko + g * (GSE * CB / 8), t * 4 * rb);
-      } else {
-        const uint8_t* p = kbase + (int64_t)sm_row[w][(n >> 2) * 8 + t * 4 + (n & 3)] * a.row_bytes + c * KB;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) load_words<KB>(kw[t][g], p + g * (GSE * CB / 8));
-      }
-    }
-    const int64_t so = (int64_t)row * a.groups;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      sc[g] = sp[so + g];
-      of[g] = mp[so + g];
-    }
-  };
-  auto fetch_v = [&] {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if constexpr (OCT) load_words<VB>(vw[j], vbuf, vo, j * rb);
-      else load_words<VB>(vw[j], vbase + (int64_t)sm_row[w][c * 8 + j] * a.row_bytes + n * VB);
-    }
-  };
+  // where this lane's operands lie in a step
+  const int kat = ((sub * 32 + (n & 3) * 4 + (n >> 2)) << lrb), kf = fold((n >> 2) * 8 + (n & 3));
+  const int vat = ((sub * 32 + c) << lrb), vf = fold(c * 8);
+  const int sat = ((sub * 32 + (l & 31)) << lsg) + hh * NG;
 
   auto rescale = [&](float f) {
 #pragma unroll
@@ -262,15 +283,37 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_
     om *= f;
   };
 
-  int page = -1;
-  if (lo < end) {
-    locate(lo, page_of(lo));
-    page = page_of(lo + 32);
-    fetch_k();
-    fetch_v();
-  }
-  for (int64_t k0 = lo; k0 < end; k0 += 32) {
-    const bool now = seen;
+  const int64_t epoch = ((int64_t)(Sh::NPAGE - 1) << a.pshift) / step * step;
+  for (int64_t from = lo; from < end; from += epoch) {
+  const int64_t to = min(from + epoch, end);
+  __syncthreads();  // the pages and buffers before have been read
+  e0 = from >> a.pshift << a.pshift;
+  for (int i = tid; i <= (int)((to - 1 - e0) >> a.pshift); i += 64 * NW) sm_page[i] = table[(e0 >> a.pshift) + i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i)
+    if (from + i * step < to) issue(from + i * step, i);
+  int buf = 0;
+  for (int64_t k1 = from; k1 < to; k1 += step, buf = buf + 1 == NS ? 0 : buf + 1) {
+    // this step's part of each wave is there, then all of it; the buffer that is
+    // filled next has been read
+    if (NS == 3 && k1 + step < to) wait_vm<PER>();
+    else wait_vm<0>();
+    lds_barrier();
+    if (k1 + (NS - 1) * step < to) issue(k1 + (NS - 1) * step, buf == 0 ? NS - 1 : buf - 1);
+    const uint8_t* codes = smem + buf * Sh::STEP;
+    const int64_t k0 = k1 + sub * 32;
+    bool now;
+    (void)row_of(k0 + (l & 31), page_of(k0 + (l & 31)), now);
+    float sc[NG], of[NG];  // scales and offsets of key l % 32: K's, or (l >= 32) V's
+    {
+      const float* p = (const float*)(codes + 2 * Sh::CODES + (l < 32 ? 0 : 2 * Sh::SCALES)) + sat;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        sc[g] = p[g];
+        of[g] = p[Sh::SCALES / 4 + g];
+      }
+    }
     // scales to where the lanes that need them find them
     bool grow = false, bad = false;
 #pragma unroll
@@ -290,7 +333,10 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) top = max(top, __shfl_xor(top, off));
       const int y = max(Y, top + 1 - kSBits);
-      rescale(ldexpf(1.f, Y - y));
+      const float f = ldexpf(1.f, Y - y);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) o[i] *= f;
+      if (c < 2) om *= f;  // the offsets' rows, not the sum's
       Y = y;
     }
     const bool any_bad = __ballot(l >= 32 && bad) != 0;
@@ -322,11 +368,6 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_
       }
     }
     const unsigned seen_keys = (unsigned)__ballot(now && l < 32);
-    const bool more = k0 + 32 < end;
-    if (more) {
-      locate(k0 + 32, page);
-      page = page_of(k0 + 64);
-    }
     wave_sync();
 
     float t[8];
@@ -335,10 +376,19 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        unsigned kx[KB / 4];
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+          const int off = hh * HB + g * (GSE * CB / 8) + c * KB + i * 16;
+          Words<KW> x;
+          read_words<KW>(x, codes + kat + (16 * half << lrb) + (((off >> 4) ^ kf) << 4) + (off & 15));
+#pragma unroll
+          for (int j = 0; j < KW / 4; ++j) kx[4 * i + j] = x.w[j];
+        }
 #pragma unroll
         for (int s = 0; s < GSE / 32; ++s) {
-          const unsigned* kx = kw[half][g].w;
-          const f16x8 k = CB == 8 ? codes8<CB, F8>(kx[2 * s], kx[2 * s + 1]) : codes8<CB, F8>(kx[s], 0u);
+          const f16x8 k = CB == 8 ? codes8<CB, F8>(kx[CB == 8 ? 2 * s : 0], kx[CB == 8 ? 2 * s + 1 : 0])
+                                  : codes8<CB, F8>(kx[s], 0u);
           acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[g * (GSE / 32) + s], acc, 0, 0, 0);
         }
         const f32x4 s4 = *(const f32x4*)&sm_k[w][0][g][c * 8 + half * 4];
@@ -352,7 +402,6 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_
         }
       }
     }
-    if (more) fetch_k();
     // where not all rows see all keys: bit j of mask, this lane's row sees its key j
     unsigned mask = 0xffu;
     if (seen_keys != 0xffffffffu || k0 + 31 > pos_lo || (a.window > 0 && k0 <= pos_hi - a.window)) {
@@ -386,6 +435,13 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_
     }
     // V's operands, their scales (of this lane's channels: one group) in p or in V
     const u32x4 sv = *(const u32x4*)&sm_s[w][n * NC / GSE][c * 8];
+    Words<VB> vw[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int off = hh * HB + n * VB;
+      read_words<VB>(vw[j], codes + Sh::CODES + vat + (4 * j << lrb) +
+                                (((off >> 4) ^ vf ^ (j & 3 & (pieces - 1))) << 4) + (off & 15));
+    }
     f16x8 ps = p;
     if constexpr (kP) ps = p * __builtin_bit_cast(f16x8, sv);
 #pragma unroll
@@ -401,7 +457,6 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_
         o[4 * i + k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, v), ps, o[4 * i + k], 0, 0, 0);
       }
     }
-    if (more) fetch_v();
     // rows 0 .. NG - 1 of this product: V's offsets; 15: ones
     u32x4 mv = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
     if (n < 15) mv = u32x4{0u, 0u, 0u, 0u};
@@ -412,6 +467,7 @@ __global__ __launch_bounds__(256, HD == 256 ? 1 : HD / GSE <= 2 ? 3 : 2) void k_
       if (n < NG) ml = *(const u32x4*)&sm_m[w][NG + n][c * 8];
       om = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, ml), p, om, 0, 0, 0);
     }
+  }
   }
 
   // rows of O^T are channels c HD/4 + i NC + j of this lane's row
@@ -516,22 +572,32 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 }  // namespace
 
+namespace {
+
+template <int HD, int GSE, int CB, bool F8>
+hipError_t go_split(const AttnArgs& a, const Launch& L) {
+  constexpr int lds = SplitShape<HD, GSE, CB, F8>::LDS;
+  static hipError_t attr = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(k_attn_split<HD, GSE, CB, F8>),
+      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (attr != hipSuccess) return attr;
+  using Sh = SplitShape<HD, GSE, CB, F8>;
+  const int lg = (Sh::NW == 4 ? 2 : 1) - a.hw_shift;
+  const int64_t groups = a.tiles * (a.nsplit >> lg) * (a.KV >> a.hw_shift);
+  return ext_launch(k_attn_split<HD, GSE, CB, F8>, dim3((unsigned)groups), dim3(64 * Sh::NW), lds,
+                    L, a);
+}
+
+}  // namespace
+
 hipError_t launch_attn_split(const AttnArgs& a, int head_dim, int cb, int qf, int group,
                              const Launch& L) {
-  const int64_t units = a.tiles * a.nsplit * a.KV;
-  const dim3 grid((unsigned)((units + 3) / 4)), blk(256);
   const int gse = std::min(group, head_dim);
-  auto go = [&](auto octets, auto rows) {
-    return ext_launch(a.octets ? octets : rows, grid, blk, 0, L, a);
-  };
-#define TTQ_AS(HDV, GSV)                                                      \
-  if (head_dim == HDV && gse == GSV) {                                        \
-    if (qf == QF_FP8) return go(k_attn_split<HDV, GSV, 8, true, true>,        \
-                                k_attn_split<HDV, GSV, 8, true, false>);      \
-    if (cb == 8) return go(k_attn_split<HDV, GSV, 8, false, true>,            \
-                           k_attn_split<HDV, GSV, 8, false, false>);          \
-    return go(k_attn_split<HDV, GSV, 4, false, true>,                         \
-              k_attn_split<HDV, GSV, 4, false, false>);                       \
+#define TTQ_AS(HDV, GSV)                                              \
+  if (head_dim == HDV && gse == GSV) {                                \
+    if (qf == QF_FP8) return go_split<HDV, GSV, 8, true>(a, L);       \
+    if (cb == 8) return go_split<HDV, GSV, 8, false>(a, L);           \
+    return go_split<HDV, GSV, 4, false>(a, L);                        \
   }
   TTQ_AS(64, 32)
   TTQ_AS(64, 64)

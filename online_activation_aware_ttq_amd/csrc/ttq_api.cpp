@@ -1568,12 +1568,13 @@ int cache_rope_impl(const ttq_heads* h, int64_t T, int32_t x_type, const void* Q
 struct AttnPlan {
   int64_t tiles = 0, max_len = 0;
   int nsplit = 1;
+  int hw_shift = 2;
   bool tile = false;  // blocks of 256 rows that share decoded tiles, else of 16
   size_t off_ml = 0, total = 0;
 };
-// waves that fill the chip (256 compute units, 8 waves each), and keys below which
-// a range is not divided further
-constexpr int64_t kAttnWaves = 2048, kAttnMinKeys = 64;
+// workgroups that fill the chip (two a compute unit), and keys below which a wave's
+// range is not divided further
+constexpr int64_t kAttnGroups = 512, kAttnMinKeys = 64;
 // the same for the workgroups of decoded tiles, and the rows a sequence and K/V head
 // from which they are used
 constexpr int64_t kAttnTileGroups = 256, kAttnTileMinKeys = 512, kAttnTileRows = 64;
@@ -1600,10 +1601,21 @@ int plan_attention(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t max_pag
   P->tile = T * G >= kAttnTileRows * n_seq;
   const int64_t rows_block = P->tile ? 256 : 16;
   P->tiles = packed ? T * G / rows_block + n_seq : n_seq * ((G + rows_block - 1) / rows_block);
-  const int64_t units = std::max<int64_t>(1, P->tiles * h->kv_heads);
-  P->nsplit = (int)std::clamp<int64_t>(
-      (P->tile ? kAttnTileGroups : kAttnWaves) / units, 1,
-      std::clamp<int64_t>(P->max_len / (P->tile ? kAttnTileMinKeys : kAttnMinKeys), 1, kAttnMaxSplit));
+  if (P->tile) {
+    P->nsplit = (int)std::clamp<int64_t>(kAttnTileGroups / std::max<int64_t>(1, P->tiles * h->kv_heads), 1,
+                                         std::clamp<int64_t>(P->max_len / kAttnTileMinKeys, 1, kAttnMaxSplit));
+  } else {
+    // a workgroup's waves: up to 4 (2 for 256-byte heads) neighbouring heads, or as
+    // many parts of each step of its keys, which are ranges of their own
+    const int lw = h->head_dim * cb == 2048 ? 1 : 2;
+    P->hw_shift = std::min(lw, __builtin_ctz((unsigned)h->kv_heads));
+    const int parts = 1 << (lw - P->hw_shift);
+    const int64_t groups = std::max<int64_t>(1, P->tiles * (h->kv_heads >> P->hw_shift));
+    const int64_t ranges = std::clamp<int64_t>(
+        kAttnGroups / groups, 1,
+        std::clamp<int64_t>(P->max_len / (kAttnMinKeys * parts), 1, kAttnMaxSplit / parts));
+    P->nsplit = (int)ranges * parts;
+  }
   if (P->nsplit > 1) {
     const size_t rows = (size_t)T * h->heads * P->nsplit;
     P->off_ml = align_up(rows * h->head_dim * sizeof(float), 256);
@@ -1661,8 +1673,7 @@ int cache_attention_impl(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t m
   a.pshift = __builtin_ctz((unsigned)page_tokens);
   a.gshift = __builtin_ctz((unsigned)h->group);
   a.scale2 = (float)(scale * 1.4426950408889634);
-  a.octets = page_tokens >= 8 && h->n_slots % 8 == 0 &&
-             h->n_slots * std::max<int64_t>(rb, 4 * a.groups) <= int64_t(1) << 32;
+  a.hw_shift = P.hw_shift;
   a.nsplit = P.nsplit; a.tiles = P.tiles;
   const int cb = container_bits(f.bits);
   st = P.tile ? run(K_ATTN_TILE, s, [&](const Launch& L) {

@@ -852,7 +852,7 @@ struct AttnArgs {
   int H, KV, G;               // query heads, K/V heads, their quotient
   int pshift, gshift;
   float scale2;               // scale * log2(e)
-  int octets;                 // 8 rows of a page are adjacent, offsets fit 32 bits
+  int hw_shift;               // log2 of the K/V heads that a workgroup takes
   int nsplit;                 // ranges of keys
   int64_t tiles;              // blocks of query rows of a K/V head
 };
