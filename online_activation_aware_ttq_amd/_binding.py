@@ -995,26 +995,32 @@ def ttq_cache_extend(lens, added, pages, free_pages, free_count, *, page_tokens:
     return lens_out, free_count_out, offsets, positions, slots
 
 
-def _rows(t, name, dev, dtype, width):
-    """(address, distance of the rows) of ``t`` [T, width] or [T, heads, head_dim],
-    whose rows are contiguous but may lie apart."""
-    torch = _torch
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be a torch.Tensor of {dtype}, got {t.dtype}")
-    if t.get_device() != dev.index or t.device.type != "cuda":
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dim() == 3:
-        T, n, d = t.shape
-        ld, sn, one = t.stride()
+def _row_step(shape, stride, name, width):
+    """Distance of the rows of a [T, width] or [T, heads, head_dim] tensor, whose rows
+    are contiguous but may lie apart."""
+    if len(shape) == 3:
+        T, n, d = shape
+        ld, sn, one = stride
         ok = n * d == width and (one == 1 or d == 1) and (n == 1 or sn == d)
-    else:
-        T, d = t.shape
-        ld, one = t.stride()
+    elif len(shape) == 2:
+        T, d = shape
+        ld, one = stride
         ok = d == width and (one == 1 or d == 1)
+    else:
+        ok = False
     if not ok:
         raise ValueError(f"{name} must have contiguous rows of {width} values, got shape "
-                         f"{tuple(t.shape)} and strides {t.stride()}")
-    return t.data_ptr(), (ld if T > 1 else width)
+                         f"{tuple(shape)} and strides {stride}")
+    return ld if T > 1 else width
+
+
+def _row_ptr(t, name, dev, dtype):
+    """Address of ``t``, whose shape and strides the plan's key holds."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be a torch.Tensor of {dtype}, got {t.dtype}")
+    if t.get_device() != dev.index:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    return t.data_ptr()
 
 
 def _head_plan(torch, dev, cs, vs, heads, kv_heads, head_dim, k_first, v_first, bits, group,
@@ -1058,35 +1064,38 @@ def ttq_cache_rope(Q, K, V, positions, slots, codes, scales, mins, *, head_dim: 
     dev = _gpu(codes, "codes")
     cs = codes.shape
     vs = None if v_cache is None else v_cache[0].shape
-    T = K.shape[0]
-    kw, qw = K.numel() // T if T else K.shape[1:].numel(), 0
+    xd, ks = K.dtype, K.shape
+    qs = qst = None
     if Q is not None:
-        qw = Q.numel() // T if T else Q.shape[1:].numel()
-    x_type = _elem_type(K, "K")
-    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+        qs, qst = Q.shape, Q.stride()
 
     def make():
+        T = ks[0]
+        kw, qw = ks[1:].numel(), 0 if qs is None else qs[1:].numel()
         if head_dim < 1 or qw % head_dim or kw % head_dim:
             raise ValueError(f"rows of {qw} and {kw} values are no whole heads of {head_dim}")
+        if V.shape[0] != T or (qs is not None and qs[0] != T):
+            raise ValueError("Q, K and V must have as many rows")
         hd, d, cache = _head_plan(torch, dev, cs, vs, qw // head_dim, kw // head_dim, head_dim,
                                   k_first, v_first, bits, group, qformat)
-        f32 = torch.float32
-        head = ("q_weight", f32, (head_dim,)), ("k_weight", f32, (head_dim,))
-        return ctypes.byref(hd), hd, (T, qw // head_dim, head_dim), head + (
+        f32, os_ = torch.float32, (T, qw // head_dim, head_dim)
+        lds = (0 if qs is None else _row_step(qs, qst, "Q", qw), _row_step(ks, K.stride(), "K", kw),
+               _row_step(V.shape, V.stride(), "V", kw))
+        return ctypes.byref(hd), hd, T, _elem_type(K, "K"), lds, os_, (
+            ("q_weight", f32, (head_dim,)), ("k_weight", f32, (head_dim,)),
             ("inv_freq", f32, None), ("positions", torch.int32, (T,)),
-            ("out", torch.bfloat16, (T, qw // head_dim, head_dim)),
-            ("slots", torch.int64, (T,)), ("dhalf", f32, (d,)), ("v_dhalf", f32, (d,))) + cache
+            ("out", torch.bfloat16, os_), ("slots", torch.int64, (T,)),
+            ("dhalf", f32, (d,)), ("v_dhalf", f32, (d,))) + cache
 
-    ref, _, os_, want = _plan(("rope", cs, vs, T, qw, kw, head_dim, k_first, v_first, bits,
-                               group, qformat), make)
-    xd = K.dtype
-    kp, ldk = _rows(K, "K", dev, xd, kw)
-    vp, ldv = _rows(V, "V", dev, xd, kw)
-    if V.shape[0] != T or (Q is not None and Q.shape[0] != T):
-        raise ValueError("Q, K and V must have as many rows")
-    qp, ldq = (None, 0) if Q is None else _rows(Q, "Q", dev, xd, qw)
-    if out is None and Q is not None:
-        out = _result(os_, torch.bfloat16, dev, stream)
+    ref, _, T, x_type, (ldq, ldk, ldv), os_, want = _plan(
+        ("rope", cs, vs, xd, qs, qst, ks, K.stride(), V.shape, V.stride(), head_dim, k_first,
+         v_first, bits, group, qformat), make)
+    kp, vp = _row_ptr(K, "K", dev, xd), _row_ptr(V, "V", dev, xd)
+    qp = None
+    if Q is not None:
+        qp = _row_ptr(Q, "Q", dev, xd)
+        if out is None:
+            out = _result(os_, torch.bfloat16, dev, stream)
     if v_cache is None:
         v_cache = (codes, scales, mins)
     if v_dhalf is None:
@@ -1097,7 +1106,8 @@ def ttq_cache_rope(Q, K, V, positions, slots, codes, scales, mins, *, head_dim: 
     if stream is None:
         stream = _current_stream(dev)
     _enqueue("ttq_cache_rope", dev, ref, T, x_type, qp, ldq, kp, ldk, vp, ldv, wq, wk, eps, fr,
-             rot, TTQ_ROPE_INTERLEAVED if interleaved else 0, ps, op, sl, dk, dv, *cp, stream)
+             0 if inv_freq is None else 2 * inv_freq.shape[0],
+             TTQ_ROPE_INTERLEAVED if interleaved else 0, ps, op, sl, dk, dv, *cp, stream)
     return out
 
 
@@ -1130,7 +1140,7 @@ def ttq_cache_attention(Q, pages, lens, codes, scales, mins, *, kv_heads: int, b
     """
     torch = _torch or _host()
     dev = _gpu(Q, "Q")
-    qs, ps, cs = Q.shape, pages.shape, codes.shape
+    qs, qst, ps, cs = Q.shape, Q.stride(), pages.shape, codes.shape
     vs = None if v_cache is None else v_cache[0].shape
 
     def make():
@@ -1139,14 +1149,15 @@ def ttq_cache_attention(Q, pages, lens, codes, scales, mins, *, kv_heads: int, b
                                   bits, group, qformat)
         need = ttq_cache_attention_workspace_bytes(hd, T, n_seq, max_pages, page_tokens, max_len)
         f32, i32 = torch.float32, torch.int32
-        return (ctypes.byref(hd), T, n_seq, max_pages, page_tokens, max_len), need, hd, (
+        ldq = _row_step(qs, qst, "Q", heads * head_dim)
+        return (ctypes.byref(hd), T, n_seq, max_pages, page_tokens, max_len), need, ldq, hd, (
             ("offsets", i32, (n_seq + 1,)), ("pages", i32, None), ("lens", i32, (n_seq,)),
             *cache, ("dhalf_inv", f32, (d,)), ("v_dhalf_inv", f32, (d,)),
             ("out", torch.bfloat16, (T, heads, head_dim)))
 
-    args, need, _, want = _plan(("attention", qs, ps, cs, vs, kv_heads, k_first, v_first, bits,
-                                 group, qformat, page_tokens, max_len), make)
-    qp, ldq = _rows(Q, "Q", dev, torch.bfloat16, qs[1] * qs[2])
+    args, need, ldq, _, want = _plan(("attention", qs, qst, ps, cs, vs, kv_heads, k_first, v_first,
+                                      bits, group, qformat, page_tokens, max_len), make)
+    qp = _row_ptr(Q, "Q", dev, torch.bfloat16)
     if out is None:
         out = _result(qs, torch.bfloat16, dev, stream, torch.empty if offsets is None else torch.zeros)
     if v_cache is None:

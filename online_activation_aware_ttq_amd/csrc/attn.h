@@ -93,7 +93,7 @@ __device__ __forceinline__ bool find_block(const AttnArgs& a, int64_t b, int64_t
                                            int64_t& r0) {
   int64_t begin;
   if (a.offsets) {
-    auto off = [&](int64_t i) { return min(max((int64_t)a.offsets[i], (int64_t)0), a.T); };
+    auto off = [&](int64_t i) __attribute__((always_inline)) { return min(max((int64_t)a.offsets[i], (int64_t)0), a.T); };
     int64_t lo = 0, hi = a.n_seq;
     while (hi - lo > 1) {
       const int64_t mid = (lo + hi) >> 1;

@@ -76,8 +76,37 @@ __device__ __forceinline__ void load_lds4(const void* p, void* lds) {
                                    (__attribute__((address_space(3))) void*)lds, 4, 0, 0);
 }
 
+// the maximum over lanes l % 16, l % 16 + 16, .. (NaN, if any is)
+__device__ __forceinline__ float max_rows(float x) {
+  unsigned u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  x = __builtin_elementwise_maximum(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  u = __float_as_uint(x);
+  const auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_elementwise_maximum(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
 __device__ __forceinline__ unsigned mul_pair(unsigned a, unsigned b) {
   return __builtin_bit_cast(unsigned, __builtin_bit_cast(f16x2, a) * __builtin_bit_cast(f16x2, b));
+}
+
+// A block of 16 query rows and the keys that any of them sees
+struct Item {
+  int64_t seq, r0, lo, hi, pos_lo, pos_hi;
+  SeqRows sr;
+};
+// its steps (a block without keys has one, which writes its rows; 0: no rows)
+__device__ __forceinline__ int64_t find_item(const AttnArgs& a, int64_t b, int step, Item& x) {
+  if (!find_block<16>(a, b, x.seq, x.sr, x.r0)) return 0;
+  x.pos_lo = x.sr.shift + (int)x.r0 / a.G;
+  x.pos_hi = x.sr.shift + (int)min(x.r0 + 15, (int64_t)x.sr.rows - 1) / a.G;
+  x.lo = a.window > 0 ? max(x.pos_lo - a.window + 1, (int64_t)0) & ~int64_t(31) : 0;
+  x.hi = min(x.sr.len, x.pos_hi + 1);
+  return max((x.hi - x.lo + step - 1) / step, (int64_t)1);
+}
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const unsigned lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
 // HD channels a head; GSE = min(group, HD) of them a group; CB-bit codes
@@ -86,18 +115,21 @@ struct SplitShape {
   static constexpr int NG = HD / GSE;           // groups of a head
   static constexpr int HB = HD * CB / 8;        // bytes of a head
   static constexpr int NW = HB == 256 ? 2 : 4;  // waves
-  static constexpr int NS = HB <= 64 ? 3 : 2;   // buffers
-  static constexpr int CODES = 32 * NW * HB;    // bytes of K's (or V's) codes of a step
-  static constexpr int SCALES = 128 * NW * NG;  // of one of its four arrays of scales
+  static constexpr int NB = HB <= 64 && NG == 1 ? 2 : 1;  // 32 keys of a wave's step
+  static constexpr int KS = 32 * NB;            // its keys
+  static constexpr int NS = NB * HB <= 64 ? 3 : 2;  // buffers
+  static constexpr int CODES = KS * NW * HB;    // bytes of K's (or V's) codes of a step
+  static constexpr int SCALES = 4 * KS * NW * NG;  // of one of its four arrays of scales
   static constexpr int STEP = 2 * CODES + 4 * SCALES;
   static constexpr int NPAGE = 1024;            // entries of the page table at hand
   static constexpr int LDS = NS * STEP + 4 * NPAGE;
 };
 
-template <int HD, int GSE, int CB, bool F8>
+// LH: log2 of the K/V heads of a workgroup, or -1 where it is not known here
+template <int HD, int GSE, int CB, bool F8, int LH>
 __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1 : 2) void k_attn_split(AttnArgs a) {
   using Sh = SplitShape<HD, GSE, CB, F8>;
-  constexpr int NG = Sh::NG, HB = Sh::HB, NS = Sh::NS, NW = Sh::NW;
+  constexpr int NG = Sh::NG, HB = Sh::HB, NS = Sh::NS, NW = Sh::NW, NB = Sh::NB, KS = Sh::KS;
   constexpr int KB = GSE * CB / 32;      // bytes of a lane's quarter of a group of K
   constexpr int KP = KB > 16 ? KB / 16 : 1, KW = KB > 16 ? 16 : KB;  // in pieces
   constexpr int NC = HD / 16;            // channels of V of a lane
@@ -112,71 +144,123 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
   constexpr int MU = F8 ? 0 : kP ? 20 : 10;  // V's offsets: 2^MU of O's unit
   constexpr int kMid = F8 ? 0 : 1 << (CB - 1);
   constexpr float kLazy = 8.f;
-  __shared__ __align__(16) float sm_k[NW][2][NG][32];
-  __shared__ __align__(16) _Float16 sm_s[NW][NG][32], sm_m[NW][F8 ? 1 : 2 * NG][32];
+  __shared__ __align__(16) float sm_k[NW][2][NG][KS];
+  __shared__ __align__(16) _Float16 sm_s[NW][NG][KS], sm_m[NW][F8 ? 1 : 2 * NG][KS];
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   int* sm_page = (int*)(smem + NS * Sh::STEP);
 
   const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = l & 15, c = l >> 4;
-  // a workgroup: a block of rows, a range of keys, HW neighbouring K/V heads; wave w
-  // takes head w % HW and 32 of a step's 32 * NW / HW keys
-  const int lh = a.hw_shift, HW = 1 << lh, lg = (NW == 4 ? 2 : 1) - lh;
-  const int hgroups = a.KV >> lh, ranges = a.nsplit >> lg;
-  const int h0 = (int)(blockIdx.x % hgroups) << lh;
-  const int64_t bs = blockIdx.x / hgroups;
-  const int range = (int)(bs % ranges);
-  const int64_t block = bs / ranges;
-  const int hh = w & (HW - 1), sub = w >> lh;
-  const int h = h0 + hh, split = (range << lg) + sub;
-  int64_t seq, r0;
-  SeqRows sr;
-  if (!find_block<16>(a, block, seq, sr, r0)) return;  // uniform over the workgroup
+  // A workgroup takes HW neighbouring K/V heads; wave w head w % HW and KS of a step's
+  // KS * NW / HW keys.  The steps of all blocks, one block after another, are divided
+  // evenly over the workgroups of a head group (a.parts of them), so a range may end
+  // in one block and go on in the next; or (a.parts = 0) each takes a block.
+  const int lh = LH < 0 ? a.hw_shift : LH, HW = 1 << lh, lg = (NW == 4 ? 2 : 1) - lh;
+  const int hgroups = a.KV >> lh, step = KS << lg;
+  // Workgroup b runs on die b % 8: the head groups of a part go to one die, whose L2
+  // then reads the lines that their scales share once (a part's scales of four heads
+  // are 16 bytes of a line).
+  const int64_t count = a.parts > 0 ? a.parts : a.tiles, even = (count & ~int64_t(7)) * hgroups;
+  const int64_t in_die = blockIdx.x / 8, rest = blockIdx.x - even;
+  const int64_t part = blockIdx.x < even ? in_die / hgroups * 8 + blockIdx.x % 8 : (count & ~int64_t(7)) + rest / hgroups;
+  const int h0 = (int)(blockIdx.x < even ? in_die % hgroups : rest % hgroups) << lh;
+  const int hh = w & (HW - 1), sub = w >> lh, h = h0 + hh;
+  int64_t block, left, skip;  // the first block, the steps to do, those of it to leave out
+  if (a.parts > 0) {
+    __shared__ int64_t sm_sum[NW], sm_skip;
+    __shared__ int sm_first;
+    int64_t* pre = (int64_t*)smem;  // where the steps of each block begin
+    const int each = (int)((a.tiles + 64 * NW - 1) / (64 * NW)), b0 = tid * each;
+    int64_t mine = 0;
+    for (int i = b0; i < min((int64_t)(b0 + each), a.tiles); ++i) {
+      Item x;
+      mine += pre[i + 1] = find_item(a, i, step, x);
+    }
+    int64_t run = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t o = __shfl_up((long long)run, off);
+      if (l >= off) run += o;
+    }
+    if (l == 63) sm_sum[w] = run;
+    __syncthreads();
+    int64_t total = 0;
+    run -= mine;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      run += i < w ? sm_sum[i] : 0;
+      total += sm_sum[i];
+    }
+    total = uniform64(total);
+    const int64_t per = (total + a.parts - 1) / a.parts, begin = part * per;
+    if (tid == 0 && blockIdx.x == 0) a.pre[0] = 0;
+    for (int i = b0; i < min((int64_t)(b0 + each), a.tiles); ++i) {
+      const int64_t next = run + pre[i + 1];
+      if (run <= begin && begin < next) {
+        sm_first = i;
+        sm_skip = begin - run;
+      }
+      if (blockIdx.x == 0) a.pre[i + 1] = next;
+      run = next;
+    }
+    __syncthreads();
+    if (begin >= total) return;  // uniform over the workgroup
+    block = __builtin_amdgcn_readfirstlane(sm_first);
+    skip = uniform64(sm_skip);
+    left = min(per, total - begin);
+  } else {
+    block = part;
+    skip = 0;
+    left = int64_t(1) << 40;
+    if (block >= a.tiles) return;
+  }
 
+  for (; left > 0 && block < a.tiles; ++block) {
+  Item it;
+  const int64_t steps = find_item(a, block, step, it);
+  if (steps == 0) continue;
+  const int64_t todo = min(steps - skip, left);
+  const bool all = todo == steps && lg == 0;  // the block's keys are all this wave's
+  const int64_t lo = it.lo + skip * step, hi = it.hi;
+  const int64_t end = min(lo + todo * step, hi);
+  left = a.parts > 0 ? left - todo : 0;
+  skip = 0;
+  const SeqRows& sr = it.sr;
+  const int64_t seq = it.seq, r0 = it.r0, pos_lo = it.pos_lo, pos_hi = it.pos_hi;
   // this lane's row
   const int r = (int)min(r0 + n, (int64_t)sr.rows - 1);
   const int tok = r / a.G, head = h * a.G + r % a.G;
   const int64_t pos = sr.shift + tok;
-  const int64_t pos_lo = sr.shift + (int)r0 / a.G;
-  const int64_t pos_hi = sr.shift + (int)min(r0 + 15, (int64_t)sr.rows - 1) / a.G;
-  int64_t lo = a.window > 0 ? max(pos_lo - a.window + 1, (int64_t)0) & ~int64_t(31) : 0;
-  const int64_t hi = min(sr.len, pos_hi + 1);
-  const int step = 32 << lg;  // keys of a step
-  const int64_t per = ((hi - lo + ranges - 1) / ranges + step - 1) / step * step;
-  lo += per * range;
-  const int64_t end = min(lo + per, hi);
-  const int64_t orow = ((sr.first + tok) * a.H + head) * a.nsplit + split;
 
-  // q' of this lane's channels, by group and step, and its sums
+  // q' of this lane's channels, by group and step, and its sums: the values are asked
+  // for here and used once the first codes are
   f16x8 q[HD / 32];
   float qs[NG], qm;
+  u32x4 xq[HD / 32];
+  f32x4 dq[HD / 16];
+  auto q_channel = [&](int i) __attribute__((always_inline)) { return i / (GSE / 32) * GSE + c * (GSE / 4) + i % (GSE / 32) * 8; };
   {
     const bf16_t* src = a.Q + (sr.first + tok) * a.ldq + head * HD;
+#pragma unroll
+    for (int i = 0; i < HD / 32; ++i) xq[i] = *(const u32x4*)(src + q_channel(i));
+#pragma unroll
+    for (int i = 0; i < HD / 16; ++i) dq[i] = f32x4{1.f, 1.f, 1.f, 1.f};
+    if (a.kdhi) {
+      const float* d = a.kdhi + a.k_first + h * HD;
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i) dq[i] = *(const f32x4*)(d + q_channel(i / 2) + i % 2 * 4);
+    }
+  }
+  auto make_q = [&]() __attribute__((always_inline)) {
     const float sign = a.scale2 == 0.f ? 0.f : a.scale2 < 0.f ? -1.f : 1.f;
     float qf[HD / 4], top = 0.f;
 #pragma unroll
-    for (int i = 0; i < HD / 32; ++i) {
-      const int ch = i / (GSE / 32) * GSE + c * (GSE / 4) + i % (GSE / 32) * 8;
-      const u32x4 x = *(const u32x4*)(src + ch);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        qf[8 * i + 2 * j] = bf16lo(x[j]) * sign;
-        qf[8 * i + 2 * j + 1] = bf16hi(x[j]) * sign;
-      }
-      if (a.kdhi) {
-        const float* d = a.kdhi + a.k_first + h * HD + ch;
-        const f32x4 d0 = *(const f32x4*)d, d1 = *(const f32x4*)(d + 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          qf[8 * i + j] *= d0[j];
-          qf[8 * i + 4 + j] *= d1[j];
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(qf[8 * i + j]));
+    for (int i = 0; i < HD / 4; ++i) {
+      const unsigned x = xq[i / 8][i % 8 / 2];
+      qf[i] = (i % 2 ? bf16hi(x) : bf16lo(x)) * sign * dq[i / 4][i % 4];
+      top = fmaxf(top, __builtin_fabsf(qf[i]));
     }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = max_rows(top);
     const int e = (top > 0.f ? min(ilogbf(top), 127) : 0) - 10;
 #pragma unroll
     for (int g = 0; g < NG; ++g) qs[g] = 0.f;
@@ -197,7 +281,7 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
       qs[g] = ldexpf(qs[g], -U);
     }
     qm = sign == 0.f ? 1.f : fmaxf(ldexpf(__builtin_fabsf(a.scale2), e + U), 1.17549435e-38f);
-  }
+  };
 
   f32x4 o[NC], om = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -210,17 +294,17 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
   // * 4 + r / 8, its 16-byte pieces p in slots p ^ fold(r): the reads below find all
   // banks; then the scales and offsets of K and V, as they lie in the cache.
   const int RB = HB << lh, pieces = RB / 16, lrb = __builtin_ctz((unsigned)RB);
-  auto fold = [&](int r) { return ((r & 3) | (((r >> 3) >> lg) << 2)) & (pieces - 1); };
+  auto fold = [&](int r) __attribute__((always_inline)) { return ((r & 3) | (((r >> 3) >> lg) << 2)) & (pieces - 1); };
   const int32_t* table = a.pages + seq * a.max_pages;
   const int pmask = (1 << a.pshift) - 1, max_page = (a.n_slots - 1) >> a.pshift;
   int64_t e0 = 0;  // the first key of the first page at hand
   // page of a key (-1 behind the last one), and its cache row; where it has none,
   // row 0, which is there to be read
-  auto page_of = [&](int64_t key) {
+  auto page_of = [&](int64_t key) __attribute__((always_inline)) {
     const int page = sm_page[min((unsigned)(int)(key - e0) >> a.pshift, (unsigned)Sh::NPAGE - 1)];
     return key < end ? page : -1;
   };
-  auto row_of = [&](int64_t key, int page, bool& in) {
+  auto row_of = [&](int64_t key, int page, bool& in) __attribute__((always_inline)) {
     const unsigned row = ((unsigned)page << a.pshift) + ((int)(key - e0) & pmask);
     in = (unsigned)page <= (unsigned)max_page && row < (unsigned)a.n_slots;
     return in ? row : 0u;
@@ -228,10 +312,14 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
   const uint8_t* kbase = a.kc + (a.k_first + h0 * HD) * CB / 8;
   const uint8_t* vbase = a.vc + (a.v_first + h0 * HD) * CB / 8;
   // this wave's part of a step: 1 KiB of codes an instruction, and 4 / NW of the
-  // arrays of scales, 64 values an instruction
-  constexpr int NQ = HB / 32, PER = 2 * NQ + 2 * NG, NA = 4 / NW;
+  // arrays of scales, 64 values an instruction or, where a key's values are whole 16
+  // bytes (a.wide), four times as many: a load of 4 bytes a lane takes the address
+  // units as long (context 131071, groups of 64: 72 us without, 44 with)
+  constexpr int NQ = KS * HB / 1024, NI = KS * NW * NG / 64, NA = 4 / NW;
+  constexpr int PER = 2 * NQ + NA * NI, NIW = (NI + 3) / 4, PERW = 2 * NQ + NA * NIW;
   const int lsg = lh + __builtin_ctz((unsigned)NG);  // log2 of a key's scales
-  const int hg = l & ((1 << lsg) - 1);
+  const bool wide = NI % 4 == 0 && a.wide;
+  const int lw = wide ? 2 : 0, hg = (l << lw) & ((1 << lsg) - 1);
   const float* sbase[NA];
 #pragma unroll
   for (int j = 0; j < NA; ++j) {
@@ -240,22 +328,21 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
     sbase[j] = (x == 0 ? a.ks : x == 1 ? a.km : x == 2 ? a.vs : a.vm) +
                ((first + (h0 + hg / NG) * HD) >> a.gshift) + hg % NG;
   }
-  auto issue = [&](int64_t k0, int buf) {
+  auto issue = [&](int64_t k0, int buf) __attribute__((always_inline)) {
     uint8_t* to = smem + buf * Sh::STEP;
-    constexpr int NI = NW * NG / 2;
     int pq[NQ], ps[NI];
-    auto code_key = [&](int i, int& piece) {
+    auto code_key = [&](int i, int& piece) __attribute__((always_inline)) {
       const int at = (w * NQ + i) * 1024 + l * 16, p = at >> lrb;
       const int r = ((p & 31) >> 2) | ((p & 3) << 3);
       piece = ((at >> 4) & (pieces - 1)) ^ fold(r);
       return k0 + (p & ~31) + r;
     };
-    auto scale_key = [&](int i) { return k0 + ((i * 64 + l) >> lsg); };
+    auto scale_key = [&](int i) __attribute__((always_inline)) { return k0 + (((i * 64 + l) << lw) >> lsg); };
     int piece;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) pq[i] = page_of(code_key(i, piece));
 #pragma unroll
-    for (int i = 0; i < NI; ++i) ps[i] = page_of(scale_key(i));
+    for (int i = 0; i < NIW; ++i) ps[i] = page_of(scale_key(i));
     bool in;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
@@ -264,72 +351,98 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
       load_lds16(kbase + off, to + (w * NQ + i) * 1024);
       load_lds16(vbase + off, to + Sh::CODES + (w * NQ + i) * 1024);
     }
+    uint8_t* sto = to + 2 * Sh::CODES + w * NA * Sh::SCALES;
+    if (wide) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const uint64_t off = (uint64_t)row_of(scale_key(i), ps[i], in) * (unsigned)a.groups;
+      for (int i = 0; i < NIW; ++i) {
+        const uint64_t off = (uint64_t)row_of(scale_key(i), ps[i], in) * (unsigned)a.groups;
 #pragma unroll
-      for (int j = 0; j < NA; ++j)
-        load_lds4(sbase[j] + off, to + 2 * Sh::CODES + (w * NA + j) * Sh::SCALES + i * 256);
+        for (int j = 0; j < NA; ++j) load_lds16(sbase[j] + off, sto + j * Sh::SCALES + i * 1024);
+      }
+    } else {
+#pragma unroll
+      for (int i = NIW; i < NI; ++i) ps[i] = page_of(scale_key(i));
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const uint64_t off = (uint64_t)row_of(scale_key(i), ps[i], in) * (unsigned)a.groups;
+#pragma unroll
+        for (int j = 0; j < NA; ++j) load_lds4(sbase[j] + off, sto + j * Sh::SCALES + i * 256);
+      }
     }
   };
   // where this lane's operands lie in a step
-  const int kat = ((sub * 32 + (n & 3) * 4 + (n >> 2)) << lrb), kf = fold((n >> 2) * 8 + (n & 3));
-  const int vat = ((sub * 32 + c) << lrb), vf = fold(c * 8);
-  const int sat = ((sub * 32 + (l & 31)) << lsg) + hh * NG;
+  const int kat = ((sub * KS + (n & 3) * 4 + (n >> 2)) << lrb), kf = fold((n >> 2) * 8 + (n & 3));
+  const int vat = ((sub * KS + c) << lrb), vf = fold(c * 8);
+  const int kl = l & (KS - 1), sat = ((sub * KS + kl) << lsg) + hh * NG;
 
-  auto rescale = [&](float f) {
+  auto rescale = [&](float f) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) o[i] *= f;
     om *= f;
   };
 
+  // The pages of as many keys as the table takes, and the first steps of them
   const int64_t epoch = ((int64_t)(Sh::NPAGE - 1) << a.pshift) / step * step;
+  auto open = [&](int64_t from) __attribute__((always_inline)) {
+    const int64_t to = min(from + epoch, end);
+    __syncthreads();  // the pages and buffers before have been read
+    e0 = from >> a.pshift << a.pshift;
+    for (int i = tid; i <= (int)((to - 1 - e0) >> a.pshift); i += 64 * NW) sm_page[i] = table[(e0 >> a.pshift) + i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i)
+      if (from + i * step < to) issue(from + i * step, i);
+  };
+  if (lo < end) {
+    open(lo);
+    make_q();
+  }
   for (int64_t from = lo; from < end; from += epoch) {
   const int64_t to = min(from + epoch, end);
-  __syncthreads();  // the pages and buffers before have been read
-  e0 = from >> a.pshift << a.pshift;
-  for (int i = tid; i <= (int)((to - 1 - e0) >> a.pshift); i += 64 * NW) sm_page[i] = table[(e0 >> a.pshift) + i];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < NS - 1; ++i)
-    if (from + i * step < to) issue(from + i * step, i);
+  if (from > lo) open(from);
   int buf = 0;
   for (int64_t k1 = from; k1 < to; k1 += step, buf = buf + 1 == NS ? 0 : buf + 1) {
     // this step's part of each wave is there, then all of it; the buffer that is
     // filled next has been read
-    if (NS == 3 && k1 + step < to) wait_vm<PER>();
-    else wait_vm<0>();
+    if (NS == 2 || k1 + step >= to) wait_vm<0>();
+    else if (wide) wait_vm<PERW>();
+    else wait_vm<PER>();
     lds_barrier();
     if (k1 + (NS - 1) * step < to) issue(k1 + (NS - 1) * step, buf == 0 ? NS - 1 : buf - 1);
     const uint8_t* codes = smem + buf * Sh::STEP;
-    const int64_t k0 = k1 + sub * 32;
-    bool now;
-    (void)row_of(k0 + (l & 31), page_of(k0 + (l & 31)), now);
-    float sc[NG], of[NG];  // scales and offsets of key l % 32: K's, or (l >= 32) V's
+    const int64_t k0 = k1 + sub * KS;
+    // scales and offsets of key kl, to where the lanes that need them find them
+    bool now, grow = false, bad = false;
+    (void)row_of(k0 + kl, page_of(k0 + kl), now);
+    float vs[NG], vm[NG];
     {
-      const float* p = (const float*)(codes + 2 * Sh::CODES + (l < 32 ? 0 : 2 * Sh::SCALES)) + sat;
+      const float* p = (const float*)(codes + 2 * Sh::CODES) + sat;
+      float ks[NG], km[NG];
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        sc[g] = p[g];
-        of[g] = p[Sh::SCALES / 4 + g];
+        ks[g] = p[g];
+        if (!F8) km[g] = p[Sh::SCALES / 4 + g];
+        vs[g] = p[2 * (Sh::SCALES / 4) + g];
+        vm[g] = p[3 * (Sh::SCALES / 4) + g];
+      }
+      wave_sync();
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        sm_k[w][0][g][kl] = now ? ks[g] : 0.f;
+        if (!F8) sm_k[w][1][g][kl] = now ? km[g] : 0.f;
+        if (!now) vs[g] = vm[g] = 0.f;
+        grow |= ldexpf(vs[g], -Y) > kSMax || (!F8 && ldexpf(__builtin_fabsf(vm[g]), MU - U - Y) > 30000.f);
+        bad |= vs[g] != vs[g] || vm[g] != vm[g];
       }
     }
-    // scales to where the lanes that need them find them
-    bool grow = false, bad = false;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      if (!now) sc[g] = of[g] = 0.f;
-      grow |= ldexpf(sc[g], -Y) > kSMax || (!F8 && ldexpf(__builtin_fabsf(of[g]), MU - U - Y) > 30000.f);
-      bad |= sc[g] != sc[g] || of[g] != of[g];
-    }
-    if (__ballot(l >= 32 && grow)) {
+    const uint64_t seen = __ballot(now);
+    if (__ballot(grow)) {
       int top = -1000;
-      if (l >= 32)
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          if (sc[g] > 0.f) top = max(top, ilogbf(sc[g]));
-          if (of[g] != 0.f && of[g] == of[g]) top = max(top, ilogbf(of[g]) + MU - U + kSBits - 13);
-        }
+      for (int g = 0; g < NG; ++g) {
+        if (vs[g] > 0.f) top = max(top, ilogbf(vs[g]));
+        if (vm[g] != 0.f && vm[g] == vm[g]) top = max(top, ilogbf(vm[g]) + MU - U + kSBits - 13);
+      }
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) top = max(top, __shfl_xor(top, off));
       const int y = max(Y, top + 1 - kSBits);
@@ -339,133 +452,139 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
       if (c < 2) om *= f;  // the offsets' rows, not the sum's
       Y = y;
     }
-    const bool any_bad = __ballot(l >= 32 && bad) != 0;
-    unsigned bad_keys[NG];
+    const bool any_bad = __ballot(bad) != 0;
+    uint64_t bad_keys[NG];
     if (any_bad) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
-        bad_keys[g] = (unsigned)(__ballot(l >= 32 && (sc[g] != sc[g] || of[g] != of[g])) >> 32);
+      for (int g = 0; g < NG; ++g) bad_keys[g] = __ballot(vs[g] != vs[g] || vm[g] != vm[g]);
     }
-    wave_sync();
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      if (l < 32) {
-        sm_k[w][0][g][l] = sc[g];
-        if (!F8) sm_k[w][1][g][l] = of[g];
-      } else {
-        // the scale in 11 bits; what it is off is made up for in the middle of the
-        // codes by the offset, which is a sum of two fp16 values
-        const bool x = sc[g] != sc[g] || of[g] != of[g];
-        const float sv = x ? 0.f : ldexpf(sc[g], -Y);
-        const _Float16 s16 = (_Float16)sv;
-        sm_s[w][g][l - 32] = s16;
-        if constexpr (!F8) {
-          const float mv = x ? 0.f : fmaf(sv - (float)s16, ldexpf((float)kMid, MU - U), ldexpf(of[g], MU - U - Y));
-          const _Float16 m16 = (_Float16)mv;
-          sm_m[w][g][l - 32] = m16;
-          sm_m[w][NG + g][l - 32] = (_Float16)(mv - (float)m16);
-        }
+      // V's scale in 11 bits; what it is off is made up for in the middle of the codes
+      // by the offset, which is a sum of two fp16 values
+      const bool x = vs[g] != vs[g] || vm[g] != vm[g];
+      const float sv = x ? 0.f : ldexpf(vs[g], -Y);
+      const _Float16 s16 = (_Float16)sv;
+      sm_s[w][g][kl] = s16;
+      if constexpr (!F8) {
+        const float mv = x ? 0.f : fmaf(sv - (float)s16, ldexpf((float)kMid, MU - U), ldexpf(vm[g], MU - U - Y));
+        const _Float16 m16 = (_Float16)mv;
+        sm_m[w][g][kl] = m16;
+        sm_m[w][NG + g][kl] = (_Float16)(mv - (float)m16);
       }
     }
-    const unsigned seen_keys = (unsigned)__ballot(now && l < 32);
     wave_sync();
 
-    float t[8];
+    float t[NB][8];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        unsigned kx[KB / 4];
+      for (int u = 0; u < NB; ++u) {
 #pragma unroll
-        for (int i = 0; i < KP; ++i) {
-          const int off = hh * HB + g * (GSE * CB / 8) + c * KB + i * 16;
-          Words<KW> x;
-          read_words<KW>(x, codes + kat + (16 * half << lrb) + (((off >> 4) ^ kf) << 4) + (off & 15));
+        for (int half = 0; half < 2; ++half) {
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+          unsigned kx[KB / 4];
 #pragma unroll
-          for (int j = 0; j < KW / 4; ++j) kx[4 * i + j] = x.w[j];
-        }
+          for (int i = 0; i < KP; ++i) {
+            const int off = hh * HB + g * (GSE * CB / 8) + c * KB + i * 16;
+            Words<KW> x;
+            read_words<KW>(x, codes + kat + (32 * u + 16 * half << lrb) + (((off >> 4) ^ kf) << 4) + (off & 15));
 #pragma unroll
-        for (int s = 0; s < GSE / 32; ++s) {
-          const f16x8 k = CB == 8 ? codes8<CB, F8>(kx[CB == 8 ? 2 * s : 0], kx[CB == 8 ? 2 * s + 1 : 0])
-                                  : codes8<CB, F8>(kx[s], 0u);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[g * (GSE / 32) + s], acc, 0, 0, 0);
-        }
-        const f32x4 s4 = *(const f32x4*)&sm_k[w][0][g][c * 8 + half * 4];
+            for (int j = 0; j < KW / 4; ++j) kx[4 * i + j] = x.w[j];
+          }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          t[half * 4 + i] = g == 0 ? s4[i] * acc[i] : fmaf(s4[i], acc[i], t[half * 4 + i]);
-        if constexpr (!F8) {
-          const f32x4 m4 = *(const f32x4*)&sm_k[w][1][g][c * 8 + half * 4];
+          for (int s = 0; s < GSE / 32; ++s) {
+            const f16x8 k = CB == 8 ? codes8<CB, F8>(kx[CB == 8 ? 2 * s : 0], kx[CB == 8 ? 2 * s + 1 : 0])
+                                    : codes8<CB, F8>(kx[s], 0u);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[g * (GSE / 32) + s], acc, 0, 0, 0);
+          }
+          const f32x4 s4 = *(const f32x4*)&sm_k[w][0][g][u * 32 + c * 8 + half * 4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) t[half * 4 + i] = fmaf(m4[i], qs[g], t[half * 4 + i]);
+          for (int i = 0; i < 4; ++i)
+            t[u][half * 4 + i] = g == 0 ? s4[i] * acc[i] : fmaf(s4[i], acc[i], t[u][half * 4 + i]);
+          if constexpr (!F8) {
+            const f32x4 m4 = *(const f32x4*)&sm_k[w][1][g][u * 32 + c * 8 + half * 4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[u][half * 4 + i] = fmaf(m4[i], qs[g], t[u][half * 4 + i]);
+          }
         }
       }
     }
     // where not all rows see all keys: bit j of mask, this lane's row sees its key j
-    unsigned mask = 0xffu;
-    if (seen_keys != 0xffffffffu || k0 + 31 > pos_lo || (a.window > 0 && k0 <= pos_hi - a.window)) {
+    unsigned mask[NB];
+#pragma unroll
+    for (int u = 0; u < NB; ++u) mask[u] = 0xffu;
+    if (seen != ~uint64_t(0) || k0 + KS - 1 > pos_lo || (a.window > 0 && k0 <= pos_hi - a.window)) {
       const int top = (int)max(min(pos - k0, (int64_t)64), (int64_t)-1);
       const int bottom = a.window > 0 ? (int)max(min(pos - a.window - k0, (int64_t)64), (int64_t)-1) : -1;
-      mask = (seen_keys >> (c * 8)) & 0xffu;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int key = c * 8 + i;
-        if (key > top || key <= bottom) mask &= ~(1u << i);
-        if (!((mask >> i) & 1)) t[i] = -kInf;
+      for (int u = 0; u < NB; ++u) {
+        mask[u] = (unsigned)(seen >> (u * 32 + c * 8)) & 0xffu;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int key = u * 32 + c * 8 + i;
+          if (key > top || key <= bottom) mask[u] &= ~(1u << i);
+          if (!((mask[u] >> i) & 1)) t[u][i] = -kInf;
+        }
       }
     }
     auto mx2 = [](float x, float y) { return __builtin_elementwise_maximum(x, y); };
-    float mx = mx2(mx2(mx2(t[0], t[1]), mx2(t[2], t[3])), mx2(mx2(t[4], t[5]), mx2(t[6], t[7])));
-    mx = mx2(mx, __shfl_xor(mx, 16));
-    mx = mx2(mx, __shfl_xor(mx, 32)) * qm;
+    float mx = t[0][0];
+#pragma unroll
+    for (int i = 1; i < 8 * NB; ++i) mx = mx2(mx, t[i / 8][i % 8]);
+    mx = max_rows(mx) * qm;
     if (__ballot(mx > mrun + kLazy)) {
       const float mnew = fmaxf(mrun, mx);
       rescale(mrun == -kInf ? 0.f : __builtin_amdgcn_exp2f(mrun - mnew));
       mrun = mnew;
     }
     const float base = mrun == -kInf ? 0.f : -mrun;
-    f16x8 p;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = (_Float16)__builtin_amdgcn_exp2f(fmaf(t[i], qm, base));
     if (any_bad) {  // a scale of V that is NaN: its group, in the rows that see it
 #pragma unroll
       for (int g = 0; g < NG; ++g)
-        if (mask & (bad_keys[g] >> (c * 8)) & 0xffu) nan_groups |= 1u << g;
+#pragma unroll
+        for (int u = 0; u < NB; ++u)
+          if (mask[u] & (unsigned)(bad_keys[g] >> (u * 32 + c * 8)) & 0xffu) nan_groups |= 1u << g;
     }
-    // V's operands, their scales (of this lane's channels: one group) in p or in V
-    const u32x4 sv = *(const u32x4*)&sm_s[w][n * NC / GSE][c * 8];
-    Words<VB> vw[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int off = hh * HB + n * VB;
-      read_words<VB>(vw[j], codes + Sh::CODES + vat + (4 * j << lrb) +
-                                (((off >> 4) ^ vf ^ (j & 3 & (pieces - 1))) << 4) + (off & 15));
-    }
-    f16x8 ps = p;
-    if constexpr (kP) ps = p * __builtin_bit_cast(f16x8, sv);
+    for (int u = 0; u < NB; ++u) {
+      f16x8 p;
 #pragma unroll
-    for (int i = 0; i < NC / 4; ++i) {
-      unsigned vp[4][4];
+      for (int i = 0; i < 8; ++i) p[i] = (_Float16)__builtin_amdgcn_exp2f(fmaf(t[u][i], qm, base));
+      // V's operands, their scales (of this lane's channels: one group) in p or in V
+      const u32x4 sv = *(const u32x4*)&sm_s[w][n * NC / GSE][u * 32 + c * 8];
+      Words<VB> vw[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) key_pairs<CB, F8>(vw[2 * j].w, vw[2 * j + 1].w, i, vp[j]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const u32x4 v = kP ? u32x4{vp[0][k], vp[1][k], vp[2][k], vp[3][k]}
-                           : u32x4{mul_pair(vp[0][k], sv.x), mul_pair(vp[1][k], sv.y),
-                                   mul_pair(vp[2][k], sv.z), mul_pair(vp[3][k], sv.w)};
-        o[4 * i + k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, v), ps, o[4 * i + k], 0, 0, 0);
+      for (int j = 0; j < 8; ++j) {
+        const int off = hh * HB + n * VB;
+        read_words<VB>(vw[j], codes + Sh::CODES + vat + (32 * u + 4 * j << lrb) +
+                                  (((off >> 4) ^ vf ^ (j & 3 & (pieces - 1))) << 4) + (off & 15));
       }
-    }
-    // rows 0 .. NG - 1 of this product: V's offsets; 15: ones
-    u32x4 mv = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
-    if (n < 15) mv = u32x4{0u, 0u, 0u, 0u};
-    if (!F8 && n < NG) mv = *(const u32x4*)&sm_m[w][n][c * 8];
-    om = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, mv), p, om, 0, 0, 0);
-    if constexpr (!F8) {
-      u32x4 ml = {0u, 0u, 0u, 0u};
-      if (n < NG) ml = *(const u32x4*)&sm_m[w][NG + n][c * 8];
-      om = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, ml), p, om, 0, 0, 0);
+      f16x8 ps = p;
+      if constexpr (kP) ps = p * __builtin_bit_cast(f16x8, sv);
+#pragma unroll
+      for (int i = 0; i < NC / 4; ++i) {
+        unsigned vp[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) key_pairs<CB, F8>(vw[2 * j].w, vw[2 * j + 1].w, i, vp[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const u32x4 v = kP ? u32x4{vp[0][k], vp[1][k], vp[2][k], vp[3][k]}
+                             : u32x4{mul_pair(vp[0][k], sv.x), mul_pair(vp[1][k], sv.y),
+                                     mul_pair(vp[2][k], sv.z), mul_pair(vp[3][k], sv.w)};
+          o[4 * i + k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, v), ps, o[4 * i + k], 0, 0, 0);
+        }
+      }
+      // rows 0 .. NG - 1 of this product: V's offsets; 15: ones
+      u32x4 mv = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+      if (n < 15) mv = u32x4{0u, 0u, 0u, 0u};
+      if (!F8 && n < NG) mv = *(const u32x4*)&sm_m[w][n][u * 32 + c * 8];
+      om = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, mv), p, om, 0, 0, 0);
+      if constexpr (!F8) {
+        u32x4 ml = {0u, 0u, 0u, 0u};
+        if (n < NG) ml = *(const u32x4*)&sm_m[w][NG + n][u * 32 + c * 8];
+        om = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, ml), p, om, 0, 0, 0);
+      }
     }
   }
   }
@@ -481,12 +600,27 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
     off[g] = __shfl(om[g & 3], (g >> 2) * 16 + n);
     if ((nan_groups >> g) & 1) off[g] = __builtin_nanf("");
   }
-  if (r0 + n >= sr.rows) return;  // (no shuffles below)
-  if (a.nsplit > 1 && c == 0) {
-    a.ml[2 * orow] = mrun;
-    a.ml[2 * orow + 1] = sum;
+  if (r0 + n >= sr.rows) continue;  // (no shuffles below)
+  // a block that several waves share: row n of slot (part + block, sub), which no
+  // other has, since a workgroup goes from block to block and from part to part
+  const int64_t slot = ((a.parts > 0 ? part : 0) + block << lg) + sub;
+  const int64_t orow = ((int64_t)h * a.slots + slot) * a.slot_rows + n;
+  const bool any = sum > 0.f || sum != sum;
+  if (!all) {
+    if (c == 0) {
+      a.ml[2 * orow] = mrun;
+      a.ml[2 * orow + 1] = sum;
+    }
+    if (!any) continue;
   }
-  if (a.nsplit > 1 && !(sum > 0.f || sum != sum)) return;
+  f32x4 dv[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) dv[i] = f32x4{1.f, 1.f, 1.f, 1.f};
+  if (a.vdhi) {
+    const float* d = a.vdhi + a.v_first + h * HD + c * (HD / 4);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) dv[i] = *(const f32x4*)(d + 4 * i);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float x[NC];
@@ -497,10 +631,9 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const float v = o[j][i] * (CB == 4 && (j & 1) ? 0.0625f : 1.f);
-      x[j] = ldexpf((v + ldexpf(f, -MU)) * inv, Y + U);
-      if (a.vdhi) x[j] *= a.vdhi[a.v_first + h * HD + ch + j];
+      x[j] = ldexpf((v + ldexpf(f, -MU)) * inv, Y + U) * dv[(i * NC + j) / 4][j % 4];
     }
-    if (a.nsplit > 1) {
+    if (!all) {
       float* dst = a.part + orow * HD + ch;
 #pragma unroll
       for (int j = 0; j < NC; j += 4) *(f32x4*)(dst + j) = f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]};
@@ -510,49 +643,85 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
       for (int j = 0; j < NC; j += 4) *(u32x2*)(dst + j) = u32x2{pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3])};
     }
   }
+  }
 }
 
-// One workgroup joins the ranges of a row: out = sum_s w_s l_s o_s / sum_s w_s l_s,
-// w_s = exp(m_s - max m), o_s the mean of range s.  The weights first, all at once;
-// then HD / 4 lanes a range, 1024 / HD ranges side by side.
-template <int HD>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int LN = HD / 4, SB = 256 / LN;
-  __shared__ float sm_w[kAttnMaxSplit], sm_red[8];
+// One workgroup joins the parts of a row: out = sum_s w_s l_s o_s / sum_s w_s l_s,
+// w_s = exp(m_s - max m), o_s the mean of part s.  The weights first, all at once;
+// then HD / 4 lanes a part, NT / (HD / 4) parts side by side.
+template <int HD, int NT>
+__global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a) {
+  constexpr int LN = HD / 4, SB = NT / LN;
+  __shared__ float sm_w[kAttnMaxParts], sm_red[2][NT / 64];
   __shared__ __align__(16) float sm[SB][HD];
   const int tid = threadIdx.x, l = tid & 63, w = tid >> 6;
   const int64_t row = blockIdx.x, t = row / a.H;
   if (a.offsets && (t >= a.offsets[a.n_seq] || t < a.offsets[0])) return;  // uniform
-  const float* ml = a.ml + row * a.nsplit * 2;
-  float m = -__builtin_inff(), sum = 0.f;
-  static_assert(kAttnMaxSplit <= 256);
-  if (tid < a.nsplit) {
-    m = ml[2 * tid];
-    sum = ml[2 * tid + 1];
+  // its parts: rows base + s stride
+  int64_t base = row * a.nsplit, stride = 1;
+  int count = a.nsplit;
+  if (a.slots > 0) {
+    const int h = (int)(row % a.H) / a.G, g = (int)(row % a.H) % a.G;
+    int64_t tile, n;
+    if (a.offsets) {
+      int64_t lo = 0, hi = a.n_seq;
+      while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (a.offsets[mid] <= t) lo = mid;
+        else hi = mid;
+      }
+      const int64_t first = max(a.offsets[lo], 0), r = (t - first) * a.G + g;
+      tile = first * a.G / 16 + lo + r / 16;
+      n = r % 16;
+    } else {
+      tile = t * ((a.G + 15) / 16) + g / 16;
+      n = g % 16;
+    }
+    if (tile >= a.tiles) return;
+    int64_t from = 0, to = 0;
+    if (a.parts > 0) {
+      const int64_t per = (a.pre[a.tiles] + a.parts - 1) / a.parts;
+      if (a.pre[tile + 1] == a.pre[tile]) return;
+      from = a.pre[tile] / per;
+      to = (a.pre[tile + 1] - 1) / per;
+    }
+    if (from == to && a.lg == 0) return;  // one wave had all of it and wrote it
+    base = ((int64_t)h * a.slots + ((from + tile) << a.lg)) * a.slot_rows + n;
+    stride = a.slot_rows;
+    count = (int)((to - from + 1) << a.lg);
   }
-  float mx = m;
+  const float* ml = a.ml + base * 2;
+  float mx = -__builtin_inff();
+  for (int s = tid; s < count; s += NT) mx = fmaxf(mx, ml[2 * s * stride]);
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) mx = fmaxf(mx, __shfl_xor(mx, off));
-  if (l == 0) sm_red[w] = mx;
+  if (l == 0) sm_red[0][w] = mx;
   __syncthreads();
-  mx = fmaxf(fmaxf(sm_red[0], sm_red[1]), fmaxf(sm_red[2], sm_red[3]));
-  // (a range without keys has no sum and has written no row)
-  const float f = sum > 0.f || sum != sum ? __builtin_amdgcn_exp2f(m - mx) * sum : 0.f;
-  sm_w[tid] = f;
-  float total = f;
+#pragma unroll
+  for (int i = 0; i < NT / 64; ++i) mx = fmaxf(mx, sm_red[0][i]);
+  float total = 0.f;
+  for (int s = tid; s < count; s += NT) {
+    // (a part without keys has no sum and has written no row)
+    const float sum = ml[2 * s * stride + 1];
+    const float f = sum > 0.f || sum != sum ? __builtin_amdgcn_exp2f(ml[2 * s * stride] - mx) * sum : 0.f;
+    sm_w[s] = f;
+    total += f;
+  }
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) total += __shfl_xor(total, off);
-  if (l == 0) sm_red[4 + w] = total;
+  if (l == 0) sm_red[1][w] = total;
   __syncthreads();
-  total = sm_red[4] + sm_red[5] + sm_red[6] + sm_red[7];
+  total = 0.f;
+#pragma unroll
+  for (int i = 0; i < NT / 64; ++i) total += sm_red[1][i];
   const int c = tid % LN * 4, s0 = tid / LN;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  const float* p = a.part + row * a.nsplit * HD + c;
+  const float* p = a.part + base * HD + c;
 #pragma unroll 4
-  for (int s = s0; s < a.nsplit; s += SB) {
+  for (int s = s0; s < count; s += SB) {
     const float g = sm_w[s];
     if (g == 0.f) continue;
-    const f32x4 v = *(const f32x4*)(p + (int64_t)s * HD);
+    const f32x4 v = *(const f32x4*)(p + s * stride * HD);
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = fmaf(g, v[j], acc[j]);
   }
@@ -574,18 +743,23 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 namespace {
 
+template <int HD, int GSE, int CB, bool F8, int LH>
+hipError_t go_split(const AttnArgs& a, const Launch& L) {
+  using Sh = SplitShape<HD, GSE, CB, F8>;
+  static hipError_t attr = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(k_attn_split<HD, GSE, CB, F8, LH>),
+      hipFuncAttributeMaxDynamicSharedMemorySize, Sh::LDS);
+  if (attr != hipSuccess) return attr;
+  const int64_t groups = (a.parts > 0 ? a.parts : a.tiles) * (a.KV >> a.hw_shift);
+  return ext_launch(k_attn_split<HD, GSE, CB, F8, LH>, dim3((unsigned)groups), dim3(64 * Sh::NW),
+                    Sh::LDS, L, a);
+}
+
 template <int HD, int GSE, int CB, bool F8>
 hipError_t go_split(const AttnArgs& a, const Launch& L) {
-  constexpr int lds = SplitShape<HD, GSE, CB, F8>::LDS;
-  static hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(k_attn_split<HD, GSE, CB, F8>),
-      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (attr != hipSuccess) return attr;
-  using Sh = SplitShape<HD, GSE, CB, F8>;
-  const int lg = (Sh::NW == 4 ? 2 : 1) - a.hw_shift;
-  const int64_t groups = a.tiles * (a.nsplit >> lg) * (a.KV >> a.hw_shift);
-  return ext_launch(k_attn_split<HD, GSE, CB, F8>, dim3((unsigned)groups), dim3(64 * Sh::NW), lds,
-                    L, a);
+  // (as many heads as waves: offsets in LDS are constants)
+  constexpr int LW = SplitShape<HD, GSE, CB, F8>::NW == 4 ? 2 : 1;
+  return a.hw_shift == LW ? go_split<HD, GSE, CB, F8, LW>(a, L) : go_split<HD, GSE, CB, F8, -1>(a, L);
 }
 
 }  // namespace
@@ -613,10 +787,18 @@ hipError_t launch_attn_split(const AttnArgs& a, int head_dim, int cb, int qf, in
 }
 
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, const Launch& L) {
-  const dim3 grid((unsigned)(a.T * a.H)), blk(256);
-  if (head_dim == 64) return ext_launch(k_attn_join<64>, grid, blk, 0, L, a);
-  if (head_dim == 128) return ext_launch(k_attn_join<128>, grid, blk, 0, L, a);
-  return ext_launch(k_attn_join<256>, grid, blk, 0, L, a);
+  const dim3 grid((unsigned)(a.T * a.H));
+  // many parts of few rows: more of them side by side
+  const bool wide = a.parts > 64 && a.T * a.H <= 1024;
+#define TTQ_AJ(HDV)                                                                     \
+  if (head_dim == HDV)                                                                  \
+    return wide ? ext_launch(k_attn_join<HDV, 1024>, grid, dim3(1024), 0, L, a)         \
+                : ext_launch(k_attn_join<HDV, 256>, grid, dim3(256), 0, L, a);
+  TTQ_AJ(64)
+  TTQ_AJ(128)
+  TTQ_AJ(256)
+#undef TTQ_AJ
+  return hipErrorInvalidValue;
 }
 
 }  // namespace ttq

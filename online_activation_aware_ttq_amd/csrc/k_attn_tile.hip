@@ -92,7 +92,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     const bf16_t* src = a.Q + (sr.first + tok) * a.ldq + head * HD;
     const float sign = a.scale2 == 0.f ? 0.f : a.scale2 < 0.f ? -1.f : 1.f;
     float top = 0.f;
-    auto load = [&](int i, float (&v)[8]) {
+    auto load = [&](int i, float (&v)[8]) __attribute__((always_inline)) {
       const int ch = i * 16 + hf * 8;
       const u32x4 x = *(const u32x4*)(src + ch);
 #pragma unroll
@@ -154,16 +154,16 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   const int32_t* table = a.pages + seq * a.max_pages;
   const int64_t pmask = (int64_t(1) << a.pshift) - 1;
   const int64_t kc = a.k_first + h * HD + kch, vc = a.v_first + h * HD + vch;
-  auto page_of = [&](int64_t key) { return key < end ? table[key >> a.pshift] : -1; };
-  auto pages_of = [&](int64_t k0) {
+  auto page_of = [&](int64_t key) __attribute__((always_inline)) { return key < end ? table[key >> a.pshift] : -1; };
+  auto pages_of = [&](int64_t k0) __attribute__((always_inline)) {
     return Pages{page_of(k0 + kkey), {page_of(k0 + vkey), page_of(k0 + vkey + 1)}};
   };
-  auto row_of = [&](int page, int64_t key, bool& in) {
+  auto row_of = [&](int page, int64_t key, bool& in) __attribute__((always_inline)) {
     const int64_t at = ((int64_t)page << a.pshift) + (key & pmask);
     in = page >= 0 && at < a.n_slots;
     return in ? at : 0;  // (row 0 is there to be read)
   };
-  auto fetch = [&](Raw& x, const Pages& p, int64_t k0) {
+  auto fetch = [&](Raw& x, const Pages& p, int64_t k0) __attribute__((always_inline)) {
     {
       const int64_t row = row_of(p.k, k0 + kkey, x.kin);
       const uint8_t* c = a.kc + row * a.row_bytes + kc * CB / 8;
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
 
   // Decodes it into buffer b with YK and YV as they are; flags: 1 where they are too
   // small (what is then written is not used), 2 where mark() is needed.
-  auto decode = [&](Raw& x, int b, int64_t k0, int slot) {
+  auto decode = [&](Raw& x, int b, int64_t k0, int slot) __attribute__((always_inline)) {
     int f = 0;
     {
       if (!x.kin) x.ks = x.km = 0.f;
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   };
 
   // which keys of buffer b are in no page, and which groups of V are NaN
-  auto mark = [&](const Raw& x, int b) {
+  auto mark = [&](const Raw& x, int b) __attribute__((always_inline)) {
     if (tid < KT) sm_bad[b][tid] = 0;
     __syncthreads();
 #pragma unroll
@@ -250,10 +250,10 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   };
 
   // YK and YV for the tile that x is a part of, and O in the new units
-  auto raise = [&](const Raw& x) {
+  auto raise = [&](const Raw& x) __attribute__((always_inline)) {
     if (tid < 2) sm_y[tid] = -1000;
     __syncthreads();
-    auto exponent = [&](float s, float m) {
+    auto exponent = [&](float s, float m) __attribute__((always_inline)) {
       int e = -1000;
       if (s > 0.f) e = ilogbf(s);
       if (m != 0.f && m == m) e = max(e, ilogbf(m) - U);
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     YV = y;
   };
 
-  auto compute = [&](int b, int64_t k0, bool marked) {
+  auto compute = [&](int b, int64_t k0, bool marked) __attribute__((always_inline)) {
     f32x16 s[NKT];
 #pragma unroll
     for (int t = 0; t < NKT; ++t) {
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
       }
     }
     // value j of block t is that of key k0 + key_of(t, j)
-    auto key_of = [&](int t, int j) { return t * 32 + (j >> 3) * 16 + hf * 8 + (j & 7); };
+    auto key_of = [&](int t, int j) __attribute__((always_inline)) { return t * 32 + (j >> 3) * 16 + hf * 8 + (j & 7); };
     if (marked || k0 + KT - 1 > pos_lo || k0 + KT > end || (a.window > 0 && k0 <= pos_hi - a.window)) {
       const int top = (int)min(min(pos, end - 1) - k0, (int64_t)KT);
       const int bottom = a.window > 0 ? (int)max(min(pos - a.window - k0, (int64_t)KT), (int64_t)-1) : -1;
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     // tile t is decoded into buffer t % 2 with flags t % 3, which are cleared a tile
     // before: whoever reads them has done so two barriers ago
     int t = 0;
-    auto settle = [&](int64_t k0) {
+    auto settle = [&](int64_t k0) __attribute__((always_inline)) {
       if (tid == 0) sm_flag[(t + 1) % 3] = 0;
       decode(x, t & 1, k0, t % 3);
       __syncthreads();

@@ -72,7 +72,7 @@ __global__ __launch_bounds__(NT) void k_extend(ExtendArgs a) {
   const int64_t pmask = (int64_t(1) << a.pshift) - 1;
   const int64_t c0 = min((int64_t)max(*a.free_count, 0), a.n_pages);
   auto length = [](int n) { return n < 0 ? -1 - n : n; };
-  auto held_of = [&](int n) { return min((n + pmask) >> a.pshift, a.max_pages); };
+  auto held_of = [&](int n) __attribute__((always_inline)) { return min((n + pmask) >> a.pshift, a.max_pages); };
 
   // the pages of sequences that have ended, onto the stack
   int64_t released = 0;

@@ -1567,17 +1567,21 @@ int cache_rope_impl(const ttq_heads* h, int64_t T, int32_t x_type, const void* Q
 
 struct AttnPlan {
   int64_t tiles = 0, max_len = 0;
-  int nsplit = 1;
-  int hw_shift = 2;
   bool tile = false;  // blocks of 256 rows that share decoded tiles, else of 16
-  size_t off_ml = 0, total = 0;
+  int nsplit = 1;     // (tile) ranges of keys
+  int hw_shift = 2, lg = 0;
+  int64_t parts = 0, slots = 0, slot_rows = 0;
+  bool join = false;
+  size_t off_ml = 0, off_pre = 0, total = 0;
 };
-// workgroups that fill the chip (two a compute unit), and keys below which a wave's
-// range is not divided further
-constexpr int64_t kAttnGroups = 512, kAttnMinKeys = 64;
-// the same for the workgroups of decoded tiles, and the rows a sequence and K/V head
-// from which they are used
-constexpr int64_t kAttnTileGroups = 256, kAttnTileMinKeys = 512, kAttnTileRows = 64;
+// Rows of a sequence and K/V head from which tiles are decoded for 256 of them, and
+// the workgroups (a compute unit holds one) up to which their keys are divided, down
+// to so many keys.
+constexpr int64_t kAttnTileRows = 64, kAttnTileGroups = 256, kAttnTileMinKeys = 512;
+// Workgroups of the other kernel that fill the chip (two a compute unit).  From four
+// times as many blocks on each has its own workgroup, and what is longer than others
+// is made up for by the order in which they run.
+constexpr int64_t kAttnGroups = 512;
 
 int plan_attention(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t max_pages,
                    int32_t page_tokens, int64_t max_len, bool packed, AttnPlan* P) {
@@ -1601,25 +1605,35 @@ int plan_attention(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t max_pag
   P->tile = T * G >= kAttnTileRows * n_seq;
   const int64_t rows_block = P->tile ? 256 : 16;
   P->tiles = packed ? T * G / rows_block + n_seq : n_seq * ((G + rows_block - 1) / rows_block);
+  size_t rows = 0;
   if (P->tile) {
     P->nsplit = (int)std::clamp<int64_t>(kAttnTileGroups / std::max<int64_t>(1, P->tiles * h->kv_heads), 1,
-                                         std::clamp<int64_t>(P->max_len / kAttnTileMinKeys, 1, kAttnMaxSplit));
+                                         std::max<int64_t>(1, P->max_len / kAttnTileMinKeys));
+    P->join = P->nsplit > 1;
+    if (P->join) rows = (size_t)T * h->heads * P->nsplit;
   } else {
     // a workgroup's waves: up to 4 (2 for 256-byte heads) neighbouring heads, or as
-    // many parts of each step of its keys, which are ranges of their own
+    // many shares of each step of its keys
     const int lw = h->head_dim * cb == 2048 ? 1 : 2;
     P->hw_shift = std::min(lw, __builtin_ctz((unsigned)h->kv_heads));
-    const int parts = 1 << (lw - P->hw_shift);
-    const int64_t groups = std::max<int64_t>(1, P->tiles * (h->kv_heads >> P->hw_shift));
-    const int64_t ranges = std::clamp<int64_t>(
-        kAttnGroups / groups, 1,
-        std::clamp<int64_t>(P->max_len / (kAttnMinKeys * parts), 1, kAttnMaxSplit / parts));
-    P->nsplit = (int)ranges * parts;
+    P->lg = lw - P->hw_shift;
+    const int64_t hgroups = h->kv_heads >> P->hw_shift;
+    const int lk = 5 + P->lg;  // log2 of a step's keys, at least
+    const int64_t steps = (P->max_len + (int64_t(1) << lk) - 1) >> lk;
+    const int64_t most = std::max<int64_t>(1, kAttnGroups / hgroups);
+    if (P->tiles * hgroups < 4 * kAttnGroups && steps > 1)
+      P->parts = std::min(most, P->tiles * steps);
+    P->join = P->lg > 0 || P->parts > 0;
+    if (P->join) {
+      P->slots = (P->parts + P->tiles) << P->lg;
+      P->slot_rows = packed ? 16 : std::min<int64_t>(16, G);
+      rows = (size_t)h->kv_heads * P->slots * P->slot_rows;
+    }
   }
-  if (P->nsplit > 1) {
-    const size_t rows = (size_t)T * h->heads * P->nsplit;
+  if (P->join && rows > 0) {
     P->off_ml = align_up(rows * h->head_dim * sizeof(float), 256);
-    P->total = P->off_ml + align_up(rows * 2 * sizeof(float), 256);
+    P->off_pre = P->off_ml + align_up(rows * 2 * sizeof(float), 256);
+    P->total = P->off_pre + align_up((P->parts > 0 ? P->tiles + 1 : 0) * sizeof(int64_t), 256);
   }
   return TTQ_OK;
 }
@@ -1673,7 +1687,17 @@ int cache_attention_impl(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t m
   a.pshift = __builtin_ctz((unsigned)page_tokens);
   a.gshift = __builtin_ctz((unsigned)h->group);
   a.scale2 = (float)(scale * 1.4426950408889634);
-  a.hw_shift = P.hw_shift;
+  a.pre = reinterpret_cast<int64_t*>(static_cast<char*>(workspace) + P.off_pre);
+  a.hw_shift = P.hw_shift; a.lg = P.lg; a.parts = P.parts;
+  {
+    // a key's scales of the heads of a workgroup: whole 16 bytes, and adjacent
+    const int64_t values = ((int64_t)h->head_dim << P.hw_shift) / h->group;
+    a.wide = h->group <= h->head_dim && values % 4 == 0 && a.groups % 4 == 0 &&
+             (h->k_first / h->group) % 4 == 0 && (h->v_first / h->group) % 4 == 0 &&
+             !misaligned(k_scales, 16) && !misaligned(k_mins, 16) &&
+             !misaligned(v_scales, 16) && !misaligned(v_mins, 16);
+  }
+  a.slots = P.slots; a.slot_rows = P.slot_rows;
   a.nsplit = P.nsplit; a.tiles = P.tiles;
   const int cb = container_bits(f.bits);
   st = P.tile ? run(K_ATTN_TILE, s, [&](const Launch& L) {
@@ -1681,7 +1705,7 @@ int cache_attention_impl(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t m
   }) : run(K_ATTN_SPLIT, s, [&](const Launch& L) {
     return launch_attn_split(a, h->head_dim, cb, (int)f.qformat, f.group, L);
   });
-  if (st != TTQ_OK || P.nsplit == 1) return st;
+  if (st != TTQ_OK || !P.join) return st;
   return run(K_ATTN_JOIN, s, [&](const Launch& L) { return launch_attn_join(a, h->head_dim, L); });
 }
 

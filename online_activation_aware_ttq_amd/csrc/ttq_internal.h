@@ -845,18 +845,24 @@ struct AttnArgs {
   const float *ks, *km, *vs, *vm;
   const float *kdhi, *vdhi;   // optional [C]
   bf16_t* out;                // [T][H][head_dim]
-  float* part;                // [T][H][nsplit][head_dim] of ranges of keys
-  float* ml;                  // [T][H][nsplit][2]: their maximum and sum
+  float* part;                // [..][head_dim] of parts of a row's keys: [T][H][nsplit]
+                              // (tiles), or [KV][slots][slot_rows] (ranges)
+  float* ml;                  // [..][2]: their maximum and sum
+  int64_t* pre;               // [tiles + 1] where the steps of each block begin
   int64_t T, n_seq, max_pages, max_len, window, row_bytes, groups, k_first, v_first;
   int n_slots;
   int H, KV, G;               // query heads, K/V heads, their quotient
   int pshift, gshift;
   float scale2;               // scale * log2(e)
   int hw_shift;               // log2 of the K/V heads that a workgroup takes
-  int nsplit;                 // ranges of keys
+  int lg;                     // log2 of the waves that share a head
+  int wide;                   // a workgroup's scales of a key are whole 16 bytes
+  int64_t parts;              // workgroups of a head group that share all steps, or 0
+  int64_t slots, slot_rows;   // of a K/V head (slots 0: tiles)
+  int nsplit;                 // tiles: ranges of keys
   int64_t tiles;              // blocks of query rows of a K/V head
 };
-constexpr int kAttnMaxSplit = 256;  // ranges of keys at most
+constexpr int kAttnMaxParts = 2048;  // parts of a row's keys at most
 hipError_t launch_attn_split(const AttnArgs& a, int head_dim, int cb, int qf, int group,
                              const Launch& L);
 hipError_t launch_attn_tile(const AttnArgs& a, int head_dim, int cb, int qf, const Launch& L);

@@ -154,9 +154,9 @@ def test_attention_workspace():
     assert few > 0
     assert attention(h, T=2, max_pages=64, ws_bytes=few - 1) == ttq.TTQ_EWORKSPACE
     assert attention(h, T=2, max_pages=64, ws=None) == ttq.TTQ_ENULL
-    # a shorter bound on the lengths needs less, one key nothing
+    # a shorter bound on the lengths needs less; one key of four heads, a wave's each, nothing
     assert need(h, 2, 2, max_pages=64, max_len=256) < few
-    assert need(h, 2, 2, max_pages=64, max_len=1) == 0
+    assert need(heads(d=1024, v_first=512, kv_heads=4), 2, 2, max_pages=64, max_len=1) == 0
     # many rows fill the chip by themselves
     assert need(h, 1 << 20, 2, max_pages=64) == 0
     for T, n in ((0, 0), (1, 1), (65535, 65535), (1 << 20, 1), (7, 0)):
