@@ -24,6 +24,11 @@ __device__ __forceinline__ unsigned e4m3_pair(unsigned w, bool hi) {
                                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false));
 }
 
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const unsigned lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // Eight codes of one row (CB bytes, low bits first) as an operand.  4 bits: slots
 // (2i, 2i + 1) are codes (i, i + 4), 16-fold where i is odd (slot_code,
 // slot_shift); 8 bits: in order.

@@ -104,11 +104,6 @@ __device__ __forceinline__ int64_t find_item(const AttnArgs& a, int64_t b, int s
   x.hi = min(x.sr.len, x.pos_hi + 1);
   return max((x.hi - x.lo + step - 1) / step, (int64_t)1);
 }
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-  const unsigned lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
-  return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
 // HD channels a head; GSE = min(group, HD) of them a group; CB-bit codes
 template <int HD, int GSE, int CB, bool F8>
 struct SplitShape {
@@ -739,9 +734,33 @@ __global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a) {
   }
 }
 
-}  // namespace
-
-namespace {
+// The same where all rows have the same few parts beside each other: 4 channels a thread
+template <int HD>
+__global__ __launch_bounds__(256) void k_attn_merge(AttnArgs a) {
+  constexpr int LN = HD / 4;
+  const int64_t row = (int64_t)blockIdx.x * (256 / LN) + threadIdx.x / LN, t = row / a.H;
+  const int c = threadIdx.x % LN * 4;
+  if (row >= a.T * a.H) return;
+  if (a.offsets && (t >= a.offsets[a.n_seq] || t < a.offsets[0])) return;
+  const float* ml = a.ml + row * a.nsplit * 2;
+  const float* p = a.part + row * a.nsplit * HD + c;
+  float mx = -__builtin_inff();
+  for (int s = 0; s < a.nsplit; ++s) mx = fmaxf(mx, ml[2 * s]);
+  float total = 0.f;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < a.nsplit; ++s) {
+    const float sum = ml[2 * s + 1];
+    const float f = sum > 0.f || sum != sum ? __builtin_amdgcn_exp2f(ml[2 * s] - mx) * sum : 0.f;
+    if (f == 0.f) continue;  // (a part without keys has written no row)
+    total += f;
+    const f32x4 v = *(const f32x4*)(p + s * HD);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = fmaf(f, v[j], acc[j]);
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  *(u32x2*)(a.out + row * HD + c) = u32x2{pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv)};
+}
 
 template <int HD, int GSE, int CB, bool F8, int LH>
 hipError_t go_split(const AttnArgs& a, const Launch& L) {
@@ -787,13 +806,19 @@ hipError_t launch_attn_split(const AttnArgs& a, int head_dim, int cb, int qf, in
 }
 
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, const Launch& L) {
-  const dim3 grid((unsigned)(a.T * a.H));
-  // many parts of few rows: more of them side by side
-  const bool wide = a.parts > 64 && a.T * a.H <= 1024;
-#define TTQ_AJ(HDV)                                                                     \
-  if (head_dim == HDV)                                                                  \
-    return wide ? ext_launch(k_attn_join<HDV, 1024>, grid, dim3(1024), 0, L, a)         \
-                : ext_launch(k_attn_join<HDV, 256>, grid, dim3(256), 0, L, a);
+  const int64_t rows = a.T * a.H;
+  const dim3 grid((unsigned)rows);
+  const bool merge = a.slots == 0 && a.nsplit <= 16;
+  // many parts of a row: more of them side by side
+  const bool wide = a.parts > 64 * a.tiles;
+#define TTQ_AJ(HDV)                                                                        \
+  if (head_dim == HDV) {                                                                   \
+    if (merge)                                                                             \
+      return ext_launch(k_attn_merge<HDV>, dim3((unsigned)((rows * HDV + 1023) / 1024)),   \
+                        dim3(256), 0, L, a);                                               \
+    return wide ? ext_launch(k_attn_join<HDV, 1024>, grid, dim3(1024), 0, L, a)            \
+                : ext_launch(k_attn_join<HDV, 256>, grid, dim3(256), 0, L, a);             \
+  }
   TTQ_AJ(64)
   TTQ_AJ(128)
   TTQ_AJ(256)

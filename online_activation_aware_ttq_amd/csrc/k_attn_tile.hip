@@ -40,6 +40,90 @@ __device__ __forceinline__ unsigned both(float a, float b) {
   return u2(f16x2{(_Float16)a, (_Float16)b});
 }
 
+// Of 16 lanes that read 4 values each, 4 lanes a row, lane i is given column i of the
+// four rows
+typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
+typedef __attribute__((ext_vector_type(4))) short i16x4;
+__device__ __forceinline__ f16x4 read_columns(const _Float16* p) {
+  return __builtin_bit_cast(f16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) i16x4*)p));
+}
+
+// A value in a register of its own, so that a load can go to the one it was in: without
+// it the compiler copies what a step loads at that step's end, and waits for it there
+template <typename T>
+__device__ __forceinline__ void copy_reg(T& to, T from) {
+  asm("v_mov_b32 %0, %1" : "=&v"(to) : "v"(from));
+}
+
+// LDS is as all waves left it; global loads stay in flight
+__device__ __forceinline__ void step_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Sums of x over lanes 0 .. l
+__device__ __forceinline__ int lane_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);   // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast 15, 31
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+  return x;
+}
+
+// find_block with the blocks in another order, those of the most keys first (to within
+// 256 keys): the last workgroups to begin are then short, where prompts of 2047 and
+// 900 tokens in the order of the batch leave a fifth of the time to a few.  For up to
+// 64 sequences, one a lane; more have enough blocks for any order.
+__device__ __forceinline__ bool find_long_block(const AttnArgs& a, int64_t b, int64_t& seq, SeqRows& s,
+                                                int64_t& r0) {
+  const int l = threadIdx.x & 63;
+  int64_t first = 0, rows = 0, shift = 0, len = 0;
+  if (l < a.n_seq) {
+    first = min(max((int64_t)a.offsets[l], (int64_t)0), a.T);
+    rows = max(min(max((int64_t)a.offsets[l + 1], (int64_t)0), a.T) - first, (int64_t)0) * a.G;
+    len = max(a.lens[l], 0);
+    shift = len - rows / a.G;
+  }
+  const int blocks = (int)((rows + 255) >> 8);
+  // blocks of this lane's sequence that see more than x 256 keys: its last ones
+  auto count = [&](int x) __attribute__((always_inline)) {
+    if (x == 0) return blocks;
+    if (len <= (int64_t)x << 8) return 0;
+    const int64_t from = max((((int64_t)x << 8) - shift) * a.G, (int64_t)0) >> 8;
+    return max(blocks - (int)min(from, (int64_t)blocks - 1), 0);
+  };
+  auto total = [&](int x) __attribute__((always_inline)) {
+    return __builtin_amdgcn_readlane(lane_scan(count(x)), 63);
+  };
+  if (b >= total(0)) return false;
+  const int top = 31 - __builtin_clz((unsigned)max((int)(a.max_len >> 8), 1));
+  int x = 0;  // the largest that more than b blocks exceed
+  for (int i = top; i >= 0; --i)
+    if (total(x | 1 << i) > b) x |= 1 << i;
+  const bool last = x + 1 >> (top + 1);
+  const int above = last ? 0 : count(x + 1), n = count(x) - above;
+  const int rest = (int)b - __builtin_amdgcn_readlane(lane_scan(above), 63);
+  const int scan = lane_scan(n);
+  const int from = __builtin_ctzll(__ballot(scan > rest));
+  auto of = [&](int64_t v) __attribute__((always_inline)) {
+    const unsigned lo = __builtin_amdgcn_readlane((int)v, from), hi = __builtin_amdgcn_readlane((int)(v >> 32), from);
+    return (int64_t)((uint64_t)hi << 32 | lo);
+  };
+  seq = from;
+  s.first = of(first);
+  s.rows = (int)of(rows);
+  s.shift = of(shift);
+  s.len = min(min(of(len), a.max_len), a.max_pages << a.pshift);
+  r0 = (of(blocks - count(x)) + rest - of(scan - n)) << 8;
+  return true;
+}
+
 template <int HD, int CB, bool F8>
 __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   constexpr int KT = 8192 / HD;      // keys of a tile
@@ -47,49 +131,66 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   constexpr int NCT = HD / 32;       // blocks of 32 channels
   constexpr int KS = HD / 16;        // steps of 16 channels
   constexpr int PS = KT / 16;        // steps of 16 keys
+  constexpr int KP = HD / 16;        // threads that decode a key
   constexpr int U = kUnit<F8>;
   constexpr float kInf = __builtin_inff();
   constexpr float kSMax = F8 ? 100.f : 50000.f;  // (k_attention.hip)
   constexpr int kSBits = F8 ? 4 : 12;
   constexpr float kLazy = 8.f;
+  // LDS rows are of 16-byte pieces, K's in the order piece ^ key % 8.  Of V, 16 lanes
+  // read 32 bytes of 4 keys, the next 16 the 32 bytes beside them: in eight parts of the
+  // banks, and the first four in four of half of the banks.
+  auto v_flip = [](int key) { return (key & 3) << 1 | (HD == 64 ? 0 : (key & 1) << 3); };
   constexpr unsigned kOut = 1u << 31;  // the key is in no page of the cache
   __shared__ __align__(16) _Float16 sm_k[2][KT * HD];
-  __shared__ __align__(16) _Float16 sm_v[2][HD * KT];
-  __shared__ unsigned sm_bad[2][KT];  // of a key: groups of V that are NaN; kOut
-  __shared__ int sm_flag[3], sm_y[2];
+  __shared__ __align__(16) _Float16 sm_v[2][KT * HD];
+  __shared__ unsigned sm_bad[3][KT];  // of a key: groups of V that are NaN; kOut
+  __shared__ int4 sm_ctl[3];          // exponents that K and V ask for; a key is bad
 
   const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = l & 31, hf = l >> 5;
   const int h = (int)(blockIdx.x % a.KV);
   const int64_t bs = blockIdx.x / a.KV;
   const int split = (int)(bs % a.nsplit);
-  const int64_t block = a.tiles - 1 - bs / a.nsplit;  // long rows of a prompt first
+  const int64_t block = bs / a.nsplit;
   int64_t seq, r0;
   SeqRows sr;
-  if (!find_block<256>(a, block, seq, sr, r0)) return;  // uniform over the workgroup
+  if (!(a.offsets && a.n_seq <= 64 ? find_long_block(a, block, seq, sr, r0)
+                                   : find_block<256>(a, a.tiles - 1 - block, seq, sr, r0)))
+    return;  // uniform over the workgroup
 
-  // keys of the workgroup, and of this wave
+  seq = uniform64(seq);
+  r0 = uniform64(r0);
+  sr.first = uniform64(sr.first);
+  sr.shift = uniform64(sr.shift);
+  sr.len = uniform64(sr.len);
+  sr.rows = __builtin_amdgcn_readfirstlane(sr.rows);
+
+  // keys of the workgroup, and of this wave; key numbers are from lo on
   const int64_t last = sr.rows - 1;
   const int64_t wg_lo = sr.shift + r0 / a.G, wg_hi = sr.shift + min(r0 + 255, last) / a.G;
   int64_t lo = a.window > 0 ? max(wg_lo - a.window + 1, (int64_t)0) / KT * KT : 0;
   const int64_t hi = min(sr.len, wg_hi + 1);
   const int64_t per = ((hi - lo + a.nsplit - 1) / a.nsplit + KT - 1) / KT * KT;
   lo += per * split;
-  const int64_t end = min(lo + per, hi);
+  auto rel = [&](int64_t key) { return (int)min(max(key - lo, (int64_t)INT32_MIN), (int64_t)INT32_MAX); };
+  const int end = rel(min(lo + per, hi));
   const int64_t w0 = r0 + 32 * w;  // this wave's first row
-  const bool wave_live = w0 <= last;
   const int64_t pos_lo = sr.shift + min(w0, last) / a.G;
   const int64_t pos_hi = sr.shift + min(w0 + 31, last) / a.G;
-  const int r = (int)min(w0 + n, last);
-  const int tok = r / a.G, head = h * a.G + r % a.G;
-  const int64_t pos = sr.shift + tok;
-  const int64_t orow = ((sr.first + tok) * a.H + head) * a.nsplit + split;
+  // the keys that all of its rows see
+  const int full_hi = min(rel(pos_lo), end - 1);
+  const int full_lo = a.window > 0 ? rel(pos_hi - a.window + 1) : 0;
+  int r = (int)min(w0 + n, last);
+  const int64_t pos = sr.shift + r / a.G;
+  const int top_key = min(rel(pos), end - 1);
+  const int low_key = a.window > 0 ? rel(pos - a.window + 1) : 0;
+  const bf16_t* src = a.Q + (sr.first + r / a.G) * a.ldq + (h * a.G + r % a.G) * HD;
 
   // q' in fp16, its largest value in [2^10, 2^11); the sign of the scale goes with it
   f16x8 q[KS];
   float qm;
   {
-    const bf16_t* src = a.Q + (sr.first + tok) * a.ldq + head * HD;
     const float sign = a.scale2 == 0.f ? 0.f : a.scale2 < 0.f ? -1.f : 1.f;
     float top = 0.f;
     auto load = [&](int i, float (&v)[8]) __attribute__((always_inline)) {
@@ -135,183 +236,238 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
   float mrun = -kInf, sum = 0.f;
-  int YK = -200, YV = -200;
   unsigned nan_groups = 0;
 
-  // what this thread decodes of a tile: 16 channels of a key of K, 8 of two keys of V
-  constexpr int KP = HD / 16, VP = HD / 8;
+  // what this thread decodes of a tile: 16 channels of a key of K, and of V
   const int kkey = tid / KP, kch = tid % KP * 16;
-  const int vkey = tid / VP * 2, vch = tid % VP * 8;
   const int kpos = (kkey & ~31) + ((kkey >> 4) & 1) * 16 + ((kkey >> 2) & 1) * 8 + ((kkey >> 3) & 1) * 4 + (kkey & 3);
-  struct Raw {
-    unsigned k[CB / 2], v[2][CB / 4];
-    float ks, km, vs[2], vm[2];
-    bool kin, vin[2];
-  };
-  struct Pages {
-    int k, v[2];
-  };
   const int32_t* table = a.pages + seq * a.max_pages;
   const int64_t pmask = (int64_t(1) << a.pshift) - 1;
-  const int64_t kc = a.k_first + h * HD + kch, vc = a.v_first + h * HD + vch;
-  auto page_of = [&](int64_t key) __attribute__((always_inline)) { return key < end ? table[key >> a.pshift] : -1; };
-  auto pages_of = [&](int64_t k0) __attribute__((always_inline)) {
-    return Pages{page_of(k0 + kkey), {page_of(k0 + vkey), page_of(k0 + vkey + 1)}};
+  const int64_t kc = a.k_first + h * HD + kch, vc = a.v_first + h * HD + kch;
+  const int64_t kg = kc >> a.gshift, vg = vc >> a.gshift;
+  const unsigned nan_bit = 1u << (int)(vg - ((a.v_first + h * HD) >> a.gshift));
+  struct Codes {
+    unsigned k[CB / 2], v[CB / 2];
   };
-  auto row_of = [&](int page, int64_t key, bool& in) __attribute__((always_inline)) {
-    const int64_t at = ((int64_t)page << a.pshift) + (key & pmask);
-    in = page >= 0 && at < a.n_slots;
-    return in ? at : 0;  // (row 0 is there to be read)
+  struct Scales {
+    float ks, km, vs, vm;
   };
-  auto fetch = [&](Raw& x, const Pages& p, int64_t k0) __attribute__((always_inline)) {
-    {
-      const int64_t row = row_of(p.k, k0 + kkey, x.kin);
-      const uint8_t* c = a.kc + row * a.row_bytes + kc * CB / 8;
-      if constexpr (CB == 8) {
-        const u32x4 v = *(const u32x4*)c;
-        x.k[0] = v.x; x.k[1] = v.y; x.k[2] = v.z; x.k[3] = v.w;
-      } else {
-        const u32x2 v = *(const u32x2*)c;
-        x.k[0] = v.x; x.k[1] = v.y;
-      }
-      x.ks = a.ks[row * a.groups + (kc >> a.gshift)];
-      x.km = a.km[row * a.groups + (kc >> a.gshift)];
-    }
+  auto page_at = [&](int t) __attribute__((always_inline)) {
+    return table[(lo + min(t * KT + kkey, end - 1)) >> a.pshift];
+  };
+  auto row_at = [&](int t, int page) __attribute__((always_inline)) {
+    const int key = t * KT + kkey;
+    const int64_t at = ((int64_t)page << a.pshift) + ((lo + key) & pmask);
+    return (page >= 0) & (at < a.n_slots) & (key < end) ? (int)at : -1;
+  };
+  auto row_times = [](int row, int64_t by) { return (uint64_t)(unsigned)max(row, 0) * (unsigned)by; };
+  // (a key in no page reads row 0, which is there to be read, and counts nothing)
+  auto codes_of = [&](int rk, int rv) __attribute__((always_inline)) {
+    Codes x;
+    const uint8_t* ck = a.kc + row_times(rk, a.row_bytes) + kc * CB / 8;
+    const uint8_t* cv = a.vc + row_times(rv, a.row_bytes) + vc * CB / 8;
+    if constexpr (CB == 8) {
+      const u32x4 k = *(const u32x4*)ck, v = *(const u32x4*)cv;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t row = row_of(p.v[j], k0 + vkey + j, x.vin[j]);
-      const uint8_t* c = a.vc + row * a.row_bytes + vc * CB / 8;
-      if constexpr (CB == 8) {
-        const u32x2 v = *(const u32x2*)c;
-        x.v[j][0] = v.x; x.v[j][1] = v.y;
-      } else {
-        x.v[j][0] = *(const unsigned*)c;
+      for (int i = 0; i < 4; ++i) {
+        x.k[i] = k[i];
+        x.v[i] = v[i];
       }
-      x.vs[j] = a.vs[row * a.groups + (vc >> a.gshift)];
-      x.vm[j] = a.vm[row * a.groups + (vc >> a.gshift)];
+    } else {
+      const u32x2 k = *(const u32x2*)ck, v = *(const u32x2*)cv;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x.k[i] = k[i];
+        x.v[i] = v[i];
+      }
     }
+    return x;
+  };
+  auto scales_of = [&](int rk, int rv) __attribute__((always_inline)) {
+    const uint64_t k = row_times(rk, a.groups) + kg, v = row_times(rv, a.groups) + vg;
+    return Scales{a.ks[k], a.km[k], a.vs[v], a.vm[v]};
   };
   auto nan = [](float s, float m) { return s != s || m != m; };
-
-  // Decodes it into buffer b with YK and YV as they are; flags: 1 where they are too
-  // small (what is then written is not used), 2 where mark() is needed.
-  auto decode = [&](Raw& x, int b, int64_t k0, int slot) __attribute__((always_inline)) {
-    int f = 0;
-    {
-      if (!x.kin) x.ks = x.km = 0.f;
-      const float s = ldexpf(x.ks, -YK), m = ldexpf(x.km, -YK - U);
-      if (s > kSMax || __builtin_fabsf(m) > 30000.f) f |= 1;
-      const unsigned s1 = both(s, s), s16 = both(s * 0.0625f, s * 0.0625f), mm = both(m, m);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const f16x8 c = CB == 8 ? codes8<CB, F8>(x.k[CB == 8 ? 2 * u : 0], x.k[CB == 8 ? 2 * u + 1 : 0])
-                                : codes8<CB, F8>(x.k[u], 0u);
-        u32x4 v = __builtin_bit_cast(u32x4, c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = fma2(v[i], !F8 && slot_shift<CB>(2 * i) ? s16 : s1, mm);
-        *(u32x4*)&sm_k[b][kpos * HD + (((kch >> 3) + u) ^ (kpos & 7)) * 8] = v;
-      }
-    }
-    float s[2], m[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const bool bad = nan(x.vs[j], x.vm[j]);
-      const bool none = !x.vin[j] || bad;
-      if (x.vin[j] ? bad : k0 + vkey + j < end) f |= 2;
-      s[j] = none ? 0.f : ldexpf(x.vs[j], -YV);
-      m[j] = none ? 0.f : ldexpf(x.vm[j], -YV - U);
-      if (s[j] > kSMax || __builtin_fabsf(m[j]) > 30000.f) f |= 1;
-    }
-    const unsigned s1 = both(s[0], s[1]), s16 = both(s[0] * 0.0625f, s[1] * 0.0625f), mm = both(m[0], m[1]);
-    unsigned p[2][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) key_pairs<CB, F8>(x.v[0], x.v[1], i, p[i]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ch = vch + i;
-      const int sw = KT >= 64 ? (ch ^ (ch >> 3)) & 7 : ((ch >> 2) ^ (ch >> 3)) & 3;
-      *(unsigned*)&sm_v[b][ch * KT + (((vkey >> 3) ^ sw) << 3) + (vkey & 7)] =
-          fma2(p[i / 4][i % 4], !F8 && CB == 4 && (i & 1) ? s16 : s1, mm);
-    }
-    if (f) atomicOr(&sm_flag[slot], f);
-  };
-
-  // which keys of buffer b are in no page, and which groups of V are NaN
-  auto mark = [&](const Raw& x, int b) __attribute__((always_inline)) {
-    if (tid < KT) sm_bad[b][tid] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int g = (int)((vc >> a.gshift) - ((a.v_first + h * HD) >> a.gshift));
-      const unsigned bits = !x.vin[j] ? kOut : nan(x.vs[j], x.vm[j]) ? 1u << g : 0u;
-      if (bits) atomicOr(&sm_bad[b][vkey + j], bits);
-    }
-    __syncthreads();
-  };
-
-  // YK and YV for the tile that x is a part of, and O in the new units
-  auto raise = [&](const Raw& x) __attribute__((always_inline)) {
-    if (tid < 2) sm_y[tid] = -1000;
-    __syncthreads();
-    auto exponent = [&](float s, float m) __attribute__((always_inline)) {
-      int e = -1000;
-      if (s > 0.f) e = ilogbf(s);
-      if (m != 0.f && m == m) e = max(e, ilogbf(m) - U);
-      return e;
-    };
-    atomicMax(&sm_y[0], exponent(x.ks, x.km));
+  auto exponent = [](float s, float m) __attribute__((always_inline)) {
     int e = -1000;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (x.vin[j] && !nan(x.vs[j], x.vm[j])) e = max(e, exponent(x.vs[j], x.vm[j]));
-    atomicMax(&sm_y[1], e);
-    __syncthreads();
-    YK = max(YK, sm_y[0] + 1 - kSBits);
-    const int y = max(YV, sm_y[1] + 1 - kSBits);
-    const float f = ldexpf(1.f, YV - y);
-#pragma unroll
-    for (int i = 0; i < NCT; ++i) o[i] *= f;
-    YV = y;
+    if (s > 0.f) e = ilogbf(s);
+    if (m != 0.f && m == m) e = max(e, ilogbf(m) - U);
+    return e;
   };
 
-  auto compute = [&](int b, int64_t k0, bool marked) __attribute__((always_inline)) {
-    f32x16 s[NKT];
-#pragma unroll
-    for (int t = 0; t < NKT; ++t) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[t][j] = 0.f;
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        const f16x8 k = *(const f16x8*)&sm_k[b][(t * 32 + n) * HD + ((2 * i + hf) ^ (n & 7)) * 8];
-        s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[i], s[t], 0, 0, 0);
+  const int late = w >> 2;  // 0: the waves that are ahead, 1: half a step behind
+  Codes x;           // of pair d
+  Scales xs, next;   // of pairs d and d + 1
+  int r1, r2, r3;    // rows of this thread's key in tiles d + 1, d + 2, d + 3
+  int page;          // and its page in tile d + 4
+  int YK = -200, YV = -200, YK_old = -200, YO = -200;
+  bool bad_keys = false;  // tile d has keys of sm_bad
+  int4 ctl;
+
+  // The scales xs of pair d, K's of row rk and V's of row rv.  Rare: keys in no page,
+  // NaN, exponents that are too small.
+  auto check = [&](int d, int rk, int rv) __attribute__((always_inline)) {
+    const bool bad = nan(xs.vs, xs.vm);
+    const bool k_big = ldexpf(xs.ks, -YK) > kSMax || ldexpf(__builtin_fabsf(xs.km), -YK - U) > 30000.f;
+    const bool v_big = ldexpf(xs.vs, -YV) > kSMax || ldexpf(__builtin_fabsf(xs.vm), -YV - U) > 30000.f;
+    if (__ballot((rk | rv) < 0 || bad || k_big || v_big) == 0) return;
+    const int slot = (d + 3) % 3;
+    if (rk < 0) xs.ks = xs.km = 0.f;
+    else if (k_big) atomicMax(&sm_ctl[slot].x, exponent(xs.ks, xs.km));
+    if (rv < 0 || bad) {
+      if (d >= 0 && d * KT + kkey < end) {
+        atomicOr(&sm_bad[slot][kkey], rv < 0 ? kOut : nan_bit);
+        sm_ctl[slot].z = 1;
       }
+      xs.vs = xs.vm = 0.f;
+    } else if (v_big) {
+      atomicMax(&sm_ctl[slot].y, exponent(xs.vs, xs.vm));
     }
-    // value j of block t is that of key k0 + key_of(t, j)
-    auto key_of = [&](int t, int j) __attribute__((always_inline)) { return t * 32 + (j >> 3) * 16 + hf * 8 + (j & 7); };
-    if (marked || k0 + KT - 1 > pos_lo || k0 + KT > end || (a.window > 0 && k0 <= pos_hi - a.window)) {
-      const int top = (int)min(min(pos, end - 1) - k0, (int64_t)KT);
-      const int bottom = a.window > 0 ? (int)max(min(pos - a.window - k0, (int64_t)KT), (int64_t)-1) : -1;
+  };
+  // Pair d into LDS, and on with what later ones need, in kPieces of code.  The
+  // exponents of a pair are those that all its threads agreed on in its check, a
+  // barrier ago.
+  // (half of the threads begin with the other 8 channels, for the other banks)
+  const bool v_odd = tid >> 2 & 1, k_odd = HD > 64 && v_odd;
+  constexpr int kPieces = 10;
+  struct Factors {
+    unsigned s1, s16, m;
+  } fk, fv;
+  auto factors = [&](float s, float m, int y) __attribute__((always_inline)) {
+    const float a = ldexpf(s, -y), b = ldexpf(m, -y - U);
+    return Factors{both(a, a), both(a * 0.0625f, a * 0.0625f), both(b, b)};
+  };
+  auto decode = [&](const unsigned (&code)[CB / 2], int u, const Factors& x, _Float16* dst, int flip, bool odd) __attribute__((always_inline)) {
+    unsigned w[2];
 #pragma unroll
-      for (int t = 0; t < NKT; ++t)
+    for (int i = 0; i < CB / 4; ++i) {
+      const unsigned c0 = code[u * CB / 4 + i], c1 = code[(1 - u) * CB / 4 + i];
+      w[i] = odd ? c1 : c0;
+    }
+    if (CB == 4) w[1] = 0u;
+    // (E4M3 has NaN, and a row that is not this cache's may hold it)
+    if (F8 && x.s1 == 0u) w[0] = w[1] = 0u;
+    const f16x8 c = codes8<CB, F8>(w[0], w[1]);
+    u32x4 v = __builtin_bit_cast(u32x4, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fma2(v[i], !F8 && slot_shift<CB>(2 * i) ? x.s16 : x.s1, x.m);
+    *(u32x4*)&dst[(((kch >> 3) + (odd ? 1 - u : u)) ^ flip) * 8] = v;
+  };
+  auto stage = [&](int d, int piece) __attribute__((always_inline)) {
+    if (piece == 0) {
+      YK_old = YK;
+      YK = max(YK, __builtin_amdgcn_readfirstlane(ctl.x) + 1 - kSBits);
+      YV = max(YV, __builtin_amdgcn_readfirstlane(ctl.y) + 1 - kSBits);
+      bad_keys = __builtin_amdgcn_readfirstlane(ctl.z) != 0;
+      fk = factors(xs.ks, xs.km, YK);
+    }
+    if (piece == 1) decode(x.k, 0, fk, &sm_k[(d + 1) & 1][kpos * HD], kpos & 7, k_odd);
+    if (piece == 2) decode(x.k, 1, fk, &sm_k[(d + 1) & 1][kpos * HD], kpos & 7, k_odd);
+    if (piece == 3) fv = factors(xs.vs, xs.vm, YV);
+    if (piece == 4) decode(x.v, 0, fv, &sm_v[d & 1][kkey * HD], v_flip(kkey), v_odd);
+    if (piece == 5) decode(x.v, 1, fv, &sm_v[d & 1][kkey * HD], v_flip(kkey), v_odd);
+    if (piece == 6) x = codes_of(r2, r1);
+    if (piece == 7) {
+      copy_reg(xs.ks, next.ks);
+      copy_reg(xs.km, next.km);
+      copy_reg(xs.vs, next.vs);
+      copy_reg(xs.vm, next.vm);
+      check(d + 1, r2, r1);
+    }
+    if (piece == 8) {
+      next = scales_of(r3, r2);
+      int pg;
+      copy_reg(pg, page);
+      r1 = r2;
+      r2 = r3;
+      r3 = row_at(d + 4, pg);
+    }
+    if (piece == 9) page = page_at(d + 5);
+  };
+
+  f32x16 s[NKT];
+  f16x8 p[PS];
+#pragma unroll
+  for (int i = 0; i < PS; ++i) p[i] = f16x8{};
+  // value j of block t of s is that of key k0 + key_of(t, j)
+  auto key_of = [&](int t, int j) __attribute__((always_inline)) { return t * 32 + (j >> 3) * 16 + hf * 8 + (j & 7); };
+  // The products of p with the V of tile t - 1, then, but for the last, those of K of
+  // tile t with q', and pair t staged between them; operands are read LEAD products
+  // ahead.  The order is written out, since the compiler's puts each read before its
+  // product and the staging after all.
+  auto products = [&](int t, auto score) __attribute__((always_inline)) {
+    constexpr int NW = NCT * PS, N = NW + (score ? NKT * KS : 0);
+    constexpr int LEAD = 4, NA = HD == 64 ? 2 : 4;
+    const int y = YV;
+    if (y != YO) {  // O in the units of this V
+      const float f = ldexpf(1.f, YO - y);
+#pragma unroll
+      for (int i = 0; i < NCT; ++i) o[i] *= f;
+      YO = y;
+    }
+    const _Float16 *vrow[NA], *krow[4];
+    // 16 lanes read 4 keys of 16 channels, and each is given a channel of the 4
+    const int key = hf * 8 + ((l & 15) >> 2), ch = (l & 16) + (l & 3) * 4;
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      vrow[i] = &sm_v[(t + 1) & 1][key * HD + ((i * 4 + (ch >> 3)) ^ v_flip(key)) * 8 + (ch & 4)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) krow[i] = &sm_k[t & 1][n * HD + ((2 * i + hf) ^ (n & 7)) * 8];
+    auto operand = [&](int at) __attribute__((always_inline)) {
+      if (at < NW) {
+        const int c = at % NCT, i = at / NCT;
+        const _Float16* from = vrow[c % NA] + c / NA * NA * 32 + i * 16 * HD;
+        return __builtin_shufflevector(read_columns(from), read_columns(from + 4 * HD), 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+      const int b = (at - NW) % NKT, i = (at - NW) / NKT;
+      return *(const f16x8*)&krow[i & 3][b * 32 * HD + (i >> 2) * 64];
+    };
+    if (score) ctl = sm_ctl[t % 3];
+    f16x8 f[LEAD];
+#pragma unroll
+    for (int i = 0; i < LEAD; ++i) f[i] = operand(i);
+#pragma unroll
+    for (int at = 0; at < N; ++at) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (at < NW) {
+        f32x16& x = o[at % NCT];
+        x = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[at % LEAD], p[at / NCT], x, 0, 0, 0);
+      } else {
+        const int i = (at - NW) / NKT;
+        f32x16& x = s[(at - NW) % NKT];
+        x = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[at % LEAD], q[i], i ? x : f32x16{}, 0, 0, 0);
+      }
+      if (at + LEAD < N) f[at % LEAD] = operand(at + LEAD);
+      if (score && at >= 4 && at % 2 == 0 && at / 2 - 2 < kPieces) stage(t, at / 2 - 2);
+    }
+  };
+  auto softmax = [&](int t, float f, bool marked) __attribute__((always_inline)) {
+    const int k0 = t * KT;
+    if (marked || k0 + KT - 1 > full_hi || k0 < full_lo) {
+      const int top = min(top_key - k0, KT), bottom = max(low_key - k0, 0);
+#pragma unroll
+      for (int i = 0; i < NKT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const int key = key_of(t, j);
-          bool seen = key <= top && key > bottom;
+          const int key = key_of(i, j);
+          bool seen = key <= top && key >= bottom;
           if (marked && seen) {
-            const unsigned bad = sm_bad[b][key];
+            const unsigned bad = sm_bad[t % 3][key];
             if (bad & kOut) seen = false;
             else nan_groups |= bad;
           }
-          if (!seen) s[t][j] = -kInf;
+          if (!seen) s[i][j] = -kInf;
         }
     }
     float mx = -kInf;
 #pragma unroll
-    for (int t = 0; t < NKT; ++t)
+    for (int i = 0; i < NKT; ++i)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[t][j]);
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float f = ldexpf(qm, YK), top = mx * f;
+      for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[i][j]);
+    const unsigned ux = __float_as_uint(mx);
+    const auto halves = __builtin_amdgcn_permlane32_swap(ux, ux, false, false);
+    mx = __builtin_elementwise_maximum(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
+    const float top = mx * f;
     if (__ballot(top > mrun + kLazy)) {
       const float mnew = fmaxf(mrun, top);
       const float g = mrun == -kInf ? 0.f : __builtin_amdgcn_exp2f(mrun - mnew);
@@ -321,7 +477,6 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
       mrun = mnew;
     }
     const float base = mrun == -kInf ? 0.f : mrun;
-    f16x8 p[PS];
 #pragma unroll
     for (int i = 0; i < PS; ++i) {
       u32x4 v;
@@ -335,58 +490,50 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
       }
       p[i] = __builtin_bit_cast(f16x8, v);
     }
-#pragma unroll
-    for (int t = 0; t < NCT; ++t) {
-      const int ch = t * 32 + n;
-      const int sw = KT >= 64 ? (ch ^ (ch >> 3)) & 7 : ((ch >> 2) ^ (ch >> 3)) & 3;
-#pragma unroll
-      for (int i = 0; i < PS; ++i) {
-        const f16x8 v = *(const f16x8*)&sm_v[b][ch * KT + (((2 * i + hf) ^ sw) << 3)];
-        o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[i], o[t], 0, 0, 0);
-      }
-    }
   };
 
-  if (lo < end) {  // uniform over the workgroup
-    if (tid < 3) sm_flag[tid] = 0;
-    Raw x;
-    fetch(x, pages_of(lo), lo);
-    Pages next = pages_of(lo + KT);
+  if (end > 0) {  // uniform over the workgroup
+    const int nt = (end + KT - 1) / KT;
+    if (tid < 3) sm_ctl[tid] = int4{-1000, -1000, 0, 0};
+    for (int i = tid; i < 3 * KT; i += 512) (&sm_bad[0][0])[i] = 0;
+    r1 = row_at(0, page_at(0));
+    r2 = row_at(1, page_at(1));
+    r3 = row_at(2, page_at(2));
+    page = page_at(3);
+    x = codes_of(r1, -1);
+    xs = scales_of(r1, -1);
+    next = scales_of(r2, r1);
     __syncthreads();
-    // tile t is decoded into buffer t % 2 with flags t % 3, which are cleared a tile
-    // before: whoever reads them has done so two barriers ago
-    int t = 0;
-    auto settle = [&](int64_t k0) __attribute__((always_inline)) {
-      if (tid == 0) sm_flag[(t + 1) % 3] = 0;
-      decode(x, t & 1, k0, t % 3);
-      __syncthreads();
-      const int f = sm_flag[t % 3];
-      if (f & 1) {
-        raise(x);
-        decode(x, t & 1, k0, t % 3);
-        __syncthreads();
+    check(-1, r1, -1);
+    __syncthreads();
+    ctl = sm_ctl[2];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) stage(-1, i);
+    __syncthreads();
+    // A step of a wave is the products, a barrier, the softmax of tile t, a barrier;
+    // the late waves do the one while the others do the other.
+    if (late) step_barrier();
+    for (int t = 0; t < nt; ++t) {
+      __builtin_amdgcn_s_setprio(1);
+      products(t, std::true_type{});  // (V of tile -1: zeros)
+      __builtin_amdgcn_s_setprio(0);
+      if (late && tid - 256 < KT) {   // of pair t - 1, whose slot pair t + 2 takes
+        sm_bad[(t + 2) % 3][tid - 256] = 0;
+        if (tid == 256) sm_ctl[(t + 2) % 3] = int4{-1000, -1000, 0, 0};
       }
-      if (f & 2) mark(x, t & 1);
-      return (f & 2) != 0;
-    };
-    bool marked = settle(lo);
-    for (int64_t k0 = lo;; k0 += KT) {
-      const bool more = k0 + KT < end;
-      if (more) {
-        fetch(x, next, k0 + KT);
-        next = pages_of(k0 + 2 * KT);
-      }
-      if (wave_live && k0 <= pos_hi && (a.window <= 0 || k0 + KT - 1 > pos_lo - a.window))
-        compute(t & 1, k0, marked);
-      if (!more) break;
-      ++t;
-      marked = settle(k0 + KT);
+      step_barrier();
+      softmax(t, ldexpf(qm, YK_old), bad_keys);
+      step_barrier();
     }
+    products(nt, std::false_type{});
+    if (!late) step_barrier();
   }
 
   sum += __shfl_xor(sum, 32);
   nan_groups |= __shfl_xor(nan_groups, 32);
   if (w0 + n > last) return;
+  asm("" : "+v"(r));  // (not kept in other forms through the loop)
+  const int64_t row = (sr.first + r / a.G) * a.H + h * a.G + r % a.G, orow = row * a.nsplit + split;
   const bool any = sum > 0.f || sum != sum;
   const float inv = any ? 1.f / sum : 0.f;
   if (a.nsplit > 1) {
@@ -405,12 +552,17 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
       const bool bad = (nan_groups >> (((at + ch) >> a.gshift) - (at >> a.gshift))) & 1;
       f32x4 x;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = bad ? __builtin_nanf("") : ldexpf(o[t][4 * i + j] * inv, YV + U);
+      for (int j = 0; j < 4; ++j) x[j] = ldexpf(o[t][4 * i + j] * inv, YO + U);
+      if constexpr (CB == 4) {  // from slots to codes (slot_code)
+        const float y0 = __shfl_xor(hf ? x[0] : x[1], 32), y1 = __shfl_xor(hf ? x[2] : x[3], 32);
+        x = hf ? f32x4{y0, y1, x[1], x[3]} : f32x4{x[0], x[2], y0, y1};
+      }
+      if (bad) x = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
       if (a.vdhi) x *= *(const f32x4*)(a.vdhi + at + ch);
       if (a.nsplit > 1)
         *(f32x4*)(a.part + orow * HD + ch) = x;
       else
-        *(u32x2*)(a.out + ((sr.first + tok) * a.H + head) * HD + ch) =
+        *(u32x2*)(a.out + row * HD + ch) =
             u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
     }
 }
