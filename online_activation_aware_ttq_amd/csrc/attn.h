@@ -96,7 +96,7 @@ struct SeqRows {
 template <int SZ>
 __device__ __forceinline__ bool find_block(const AttnArgs& a, int64_t b, int64_t& seq, SeqRows& s,
                                            int64_t& r0) {
-  int64_t begin;
+  int64_t begin, tokens = 1;
   if (a.offsets) {
     auto off = [&](int64_t i) __attribute__((always_inline)) { return min(max((int64_t)a.offsets[i], (int64_t)0), a.T); };
     int64_t lo = 0, hi = a.n_seq;
@@ -107,8 +107,8 @@ __device__ __forceinline__ bool find_block(const AttnArgs& a, int64_t b, int64_t
     }
     seq = lo;
     s.first = off(lo);
-    const int64_t n = off(lo + 1) - s.first;
-    s.rows = (int)(max(n, (int64_t)0) * a.G);
+    tokens = max(off(lo + 1) - s.first, (int64_t)0);
+    s.rows = (int)(tokens * a.G);
     begin = s.first * a.G / SZ + lo;
   } else {
     const int64_t per = (a.G + SZ - 1) / SZ;
@@ -120,7 +120,7 @@ __device__ __forceinline__ bool find_block(const AttnArgs& a, int64_t b, int64_t
   r0 = (b - begin) * SZ;
   if (r0 < 0 || r0 >= s.rows) return false;
   const int64_t n = max(a.lens[seq], 0);
-  s.shift = n - s.rows / a.G;
+  s.shift = n - tokens;
   s.len = min(min(n, a.max_len), a.max_pages << a.pshift);
   return true;
 }

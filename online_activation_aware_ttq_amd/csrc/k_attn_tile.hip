@@ -76,6 +76,16 @@ __device__ __forceinline__ int lane_scan(int x) {
   return x;
 }
 
+// Lane 63 is given the largest
+__device__ __forceinline__ int lane_max(int x) {
+  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x111, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x112, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x114, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x118, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x142, 0xa, 0xf, false));
+  return max(x, __builtin_amdgcn_update_dpp(x, x, 0x143, 0xc, 0xf, false));
+}
+
 // find_block with the blocks in another order, those of the most keys first (to within
 // 256 keys): the last workgroups to begin are then short, where prompts of 2047 and
 // 900 tokens in the order of the batch leave a fifth of the time to a few.  For up to
@@ -86,9 +96,10 @@ __device__ __forceinline__ bool find_long_block(const AttnArgs& a, int64_t b, in
   int64_t first = 0, rows = 0, shift = 0, len = 0;
   if (l < a.n_seq) {
     first = min(max((int64_t)a.offsets[l], (int64_t)0), a.T);
-    rows = max(min(max((int64_t)a.offsets[l + 1], (int64_t)0), a.T) - first, (int64_t)0) * a.G;
+    const int64_t tokens = max(min(max((int64_t)a.offsets[l + 1], (int64_t)0), a.T) - first, (int64_t)0);
     len = max(a.lens[l], 0);
-    shift = len - rows / a.G;
+    rows = tokens * a.G;
+    shift = len - tokens;
   }
   const int blocks = (int)((rows + 255) >> 8);
   // blocks of this lane's sequence that see more than x 256 keys: its last ones
@@ -150,9 +161,9 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = l & 31, hf = l >> 5;
   const int h = (int)(blockIdx.x % a.KV);
-  const int64_t bs = blockIdx.x / a.KV;
-  const int split = (int)(bs % a.nsplit);
-  const int64_t block = bs / a.nsplit;
+  const unsigned bs = blockIdx.x / a.KV, nsplit = (unsigned)a.nsplit;
+  const int split = (int)(bs % nsplit);
+  const int64_t block = bs / nsplit;
   int64_t seq, r0;
   SeqRows sr;
   if (!(a.offsets && a.n_seq <= 64 ? find_long_block(a, block, seq, sr, r0)
@@ -167,69 +178,29 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   sr.rows = __builtin_amdgcn_readfirstlane(sr.rows);
 
   // keys of the workgroup, and of this wave; key numbers are from lo on
-  const int64_t last = sr.rows - 1;
-  const int64_t wg_lo = sr.shift + r0 / a.G, wg_hi = sr.shift + min(r0 + 255, last) / a.G;
+  // (32-bit divisions: all rows of a call are fewer than 2^31)
+  const unsigned first = (unsigned)r0, last = (unsigned)sr.rows - 1, G = (unsigned)a.G;
+  const int64_t wg_lo = sr.shift + first / G, wg_hi = sr.shift + min(first + 255, last) / G;
   int64_t lo = a.window > 0 ? max(wg_lo - a.window + 1, (int64_t)0) / KT * KT : 0;
   const int64_t hi = min(sr.len, wg_hi + 1);
-  const int64_t per = ((hi - lo + a.nsplit - 1) / a.nsplit + KT - 1) / KT * KT;
+  const int64_t tiles = max(hi - lo + KT - 1, (int64_t)0) / KT;  // (< 2^31)
+  const int64_t per = (int64_t)(((unsigned)tiles + nsplit - 1) / nsplit) * KT;
   lo += per * split;
   auto rel = [&](int64_t key) { return (int)min(max(key - lo, (int64_t)INT32_MIN), (int64_t)INT32_MAX); };
   const int end = rel(min(lo + per, hi));
-  const int64_t w0 = r0 + 32 * w;  // this wave's first row
-  const int64_t pos_lo = sr.shift + min(w0, last) / a.G;
-  const int64_t pos_hi = sr.shift + min(w0 + 31, last) / a.G;
+  const unsigned w0 = first + 32 * w;  // this wave's first row
+  const int64_t pos_lo = sr.shift + min(w0, last) / G;
+  const int64_t pos_hi = sr.shift + min(w0 + 31, last) / G;
   // the keys that all of its rows see
   const int full_hi = min(rel(pos_lo), end - 1);
   const int full_lo = a.window > 0 ? rel(pos_hi - a.window + 1) : 0;
-  int r = (int)min(w0 + n, last);
-  const int64_t pos = sr.shift + r / a.G;
+  unsigned r = min(w0 + n, last);
+  const int64_t pos = sr.shift + r / G;
   const int top_key = min(rel(pos), end - 1);
   const int low_key = a.window > 0 ? rel(pos - a.window + 1) : 0;
-  const bf16_t* src = a.Q + (sr.first + r / a.G) * a.ldq + (h * a.G + r % a.G) * HD;
+  const bf16_t* src = hf * 8 + a.Q + (sr.first + r / G) * a.ldq + (h * G + r % G) * HD;
 
-  // q' in fp16, its largest value in [2^10, 2^11); the sign of the scale goes with it
-  f16x8 q[KS];
-  float qm;
-  {
-    const float sign = a.scale2 == 0.f ? 0.f : a.scale2 < 0.f ? -1.f : 1.f;
-    float top = 0.f;
-    auto load = [&](int i, float (&v)[8]) __attribute__((always_inline)) {
-      const int ch = i * 16 + hf * 8;
-      const u32x4 x = *(const u32x4*)(src + ch);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = bf16lo(x[j]) * sign;
-        v[2 * j + 1] = bf16hi(x[j]) * sign;
-      }
-      if (a.kdhi) {
-        const float* d = a.kdhi + a.k_first + h * HD + ch;
-        const f32x4 d0 = *(const f32x4*)d, d1 = *(const f32x4*)(d + 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] *= d0[j];
-          v[4 + j] *= d1[j];
-        }
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      float v[8];
-      load(i, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(v[j]));
-    }
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const int e = (top > 0.f ? min(ilogbf(top), 127) : 0) - 10;
-#pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      float v[8];
-      load(i, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[i][j] = (_Float16)ldexpf(v[slot_code<CB>(j)], -e);
-    }
-    qm = sign == 0.f ? 1.f : fmaxf(ldexpf(__builtin_fabsf(a.scale2), e + U), 1.17549435e-38f);
-  }
-
+  u32x4 qraw[KS];
   f32x16 o[NCT];
 #pragma unroll
   for (int i = 0; i < NCT; ++i)
@@ -313,15 +284,17 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     if (__ballot((rk | rv) < 0 || bad || k_big || v_big) == 0) return;
     const int slot = (d + 3) % 3;
     if (rk < 0) xs.ks = xs.km = 0.f;
-    else if (k_big) atomicMax(&sm_ctl[slot].x, exponent(xs.ks, xs.km));
     if (rv < 0 || bad) {
       if (d >= 0 && d * KT + kkey < end) {
         atomicOr(&sm_bad[slot][kkey], rv < 0 ? kOut : nan_bit);
         sm_ctl[slot].z = 1;
       }
       xs.vs = xs.vm = 0.f;
-    } else if (v_big) {
-      atomicMax(&sm_ctl[slot].y, exponent(xs.vs, xs.vm));
+    }
+    const int ek = lane_max(exponent(xs.ks, xs.km)), ev = lane_max(exponent(xs.vs, xs.vm));
+    if (l == 63) {
+      atomicMax(&sm_ctl[slot].x, ek);
+      atomicMax(&sm_ctl[slot].y, ev);
     }
   };
   // Pair d into LDS, and on with what later ones need, in kPieces of code.  The
@@ -385,6 +358,58 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     if (piece == 9) page = page_at(d + 5);
   };
 
+  // the first keys, and the rows of Q meanwhile
+  if (end > 0) {
+    const int p0 = page_at(0), p1 = page_at(1), p2 = page_at(2);
+    page = page_at(3);
+#pragma unroll
+    for (int i = 0; i < KS; ++i) qraw[i] = *(const u32x4*)(src + i * 16);
+    r1 = row_at(0, p0);
+    r2 = row_at(1, p1);
+    r3 = row_at(2, p2);
+    x = codes_of(r1, -1);
+    xs = scales_of(r1, -1);
+    next = scales_of(r2, r1);
+  } else {
+#pragma unroll
+    for (int i = 0; i < KS; ++i) qraw[i] = u32x4{};
+  }
+
+  // q' in fp16, its largest value in [2^10, 2^11); the sign of the scale goes with it
+  f16x8 q[KS];
+  float qm;
+  {
+    const unsigned flip = a.scale2 < 0.f ? 0x80008000u : 0u, keep = a.scale2 == 0.f ? 0u : ~0u;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) qraw[i] = (qraw[i] ^ flip) & keep;
+    float top = 0.f;
+    auto value = [&](int i, int j) __attribute__((always_inline)) {
+      return j & 1 ? bf16hi(qraw[i][j >> 1]) : bf16lo(qraw[i][j >> 1]);
+    };
+    auto convert = [&](auto times) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(times(value(i, j), i, j)));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const int e = (top > 0.f ? min(ilogbf(top), 127) : 0) - 10;
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = slot_code<CB>(j);
+          q[i][j] = (_Float16)ldexpf(times(value(i, c), i, c), -e);
+        }
+      qm = keep == 0u ? 1.f : fmaxf(ldexpf(__builtin_fabsf(a.scale2), e + U), 1.17549435e-38f);
+    };
+    if (a.kdhi) {
+      const float* d = a.kdhi + a.k_first + h * HD + hf * 8;
+      convert([&](float v, int i, int j) __attribute__((always_inline)) { return v * d[i * 16 + j]; });
+    } else {
+      convert([](float v, int, int) __attribute__((always_inline)) { return v; });
+    }
+  }
+
   f32x16 s[NKT];
   f16x8 p[PS];
 #pragma unroll
@@ -443,20 +468,26 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   };
   auto softmax = [&](int t, float f, bool marked) __attribute__((always_inline)) {
     const int k0 = t * KT;
-    if (marked || k0 + KT - 1 > full_hi || k0 < full_lo) {
+    if (k0 + KT - 1 > full_hi || k0 < full_lo) {
+      const int top = min(top_key - k0, KT) - 8 * hf, bottom = max(low_key - k0, 0) - 8 * hf;
+#pragma unroll
+      for (int i = 0; i < NKT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int key = key_of(i, j) - 8 * hf;  // a constant
+          if ((key > top) | (key < bottom)) s[i][j] = -kInf;
+        }
+    }
+    if (marked) {
       const int top = min(top_key - k0, KT), bottom = max(low_key - k0, 0);
 #pragma unroll
       for (int i = 0; i < NKT; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const int key = key_of(i, j);
-          bool seen = key <= top && key >= bottom;
-          if (marked && seen) {
-            const unsigned bad = sm_bad[t % 3][key];
-            if (bad & kOut) seen = false;
-            else nan_groups |= bad;
-          }
-          if (!seen) s[i][j] = -kInf;
+          const unsigned bad = (key > top) | (key < bottom) ? 0u : sm_bad[t % 3][key];
+          if (bad & kOut) s[i][j] = -kInf;
+          nan_groups |= bad;
         }
     }
     float mx = -kInf;
@@ -496,13 +527,6 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     const int nt = (end + KT - 1) / KT;
     if (tid < 3) sm_ctl[tid] = int4{-1000, -1000, 0, 0};
     for (int i = tid; i < 3 * KT; i += 512) (&sm_bad[0][0])[i] = 0;
-    r1 = row_at(0, page_at(0));
-    r2 = row_at(1, page_at(1));
-    r3 = row_at(2, page_at(2));
-    page = page_at(3);
-    x = codes_of(r1, -1);
-    xs = scales_of(r1, -1);
-    next = scales_of(r2, r1);
     __syncthreads();
     check(-1, r1, -1);
     __syncthreads();
@@ -533,7 +557,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   nan_groups |= __shfl_xor(nan_groups, 32);
   if (w0 + n > last) return;
   asm("" : "+v"(r));  // (not kept in other forms through the loop)
-  const int64_t row = (sr.first + r / a.G) * a.H + h * a.G + r % a.G, orow = row * a.nsplit + split;
+  const int64_t row = (sr.first + r / G) * a.H + h * G + r % G, orow = row * a.nsplit + split;
   const bool any = sum > 0.f || sum != sum;
   const float inv = any ? 1.f / sum : 0.f;
   if (a.nsplit > 1) {
@@ -544,11 +568,18 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     if (!any) return;
   }
 #pragma unroll
-  for (int t = 0; t < NCT; ++t)
+  for (int t = 0; t < NCT; ++t) {
+    const int64_t at = a.v_first + h * HD;
+    f32x4 back[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) back[i] = f32x4{1.f, 1.f, 1.f, 1.f};
+    if (a.vdhi) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) back[i] = *(const f32x4*)(a.vdhi + at + t * 32 + i * 8 + hf * 4);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int ch = t * 32 + i * 8 + hf * 4;
-      const int64_t at = a.v_first + h * HD;
       const bool bad = (nan_groups >> (((at + ch) >> a.gshift) - (at >> a.gshift))) & 1;
       f32x4 x;
 #pragma unroll
@@ -558,13 +589,14 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
         x = hf ? f32x4{y0, y1, x[1], x[3]} : f32x4{x[0], x[2], y0, y1};
       }
       if (bad) x = f32x4{1.f, 1.f, 1.f, 1.f} * __builtin_nanf("");
-      if (a.vdhi) x *= *(const f32x4*)(a.vdhi + at + ch);
+      x *= back[i];
       if (a.nsplit > 1)
         *(f32x4*)(a.part + orow * HD + ch) = x;
       else
         *(u32x2*)(a.out + row * HD + ch) =
             u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
     }
+  }
 }
 
 }  // namespace
