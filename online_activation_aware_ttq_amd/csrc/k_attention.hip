@@ -555,6 +555,14 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
         read_words<VB>(vw[j], codes + Sh::CODES + vat + (32 * u + 4 * j << lrb) +
                                   (((off >> 4) ^ vf ^ (j & 3 & (pieces - 1))) << 4) + (off & 15));
       }
+      if (F8 && seen != ~uint64_t(0)) {
+        // (E4M3 has NaN, and the row read for a key that is not there may hold it)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < (VB >= 4 ? VB / 4 : 1); ++i)
+            if (!((seen >> (u * 32 + c * 8 + j)) & 1)) vw[j].w[i] = 0u;
+      }
       f16x8 ps = p;
       if constexpr (kP) ps = p * __builtin_bit_cast(f16x8, sv);
 #pragma unroll

@@ -307,8 +307,11 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     unsigned s1, s16, m;
   } fk, fv;
   auto factors = [&](float s, float m, int y) __attribute__((always_inline)) {
-    const float a = ldexpf(s, -y), b = ldexpf(m, -y - U);
-    return Factors{both(a, a), both(a * 0.0625f, a * 0.0625f), both(b, b)};
+    const float a = ldexpf(s, -y);
+    const _Float16 h = (_Float16)a;
+    // what the scale's 11 bits leave out is made up for in the middle of the codes
+    const float b = ldexpf(m, -y - U) + (F8 ? 0.f : (a - (float)h) * ldexpf((float)(1 << (CB - 1)), -U));
+    return Factors{both(h, h), both((float)h * 0.0625f, (float)h * 0.0625f), both(b, b)};
   };
   auto decode = [&](const unsigned (&code)[CB / 2], int u, const Factors& x, _Float16* dst, int flip, bool odd) __attribute__((always_inline)) {
     unsigned w[2];

@@ -63,7 +63,7 @@ class Cache:
         return [(v * dhi)[:, cut].unflatten(1, (self.KV, self.hd)) for v in (rep(s) * q, rep(m).clone())]
 
 
-def reference(cache, Q, rows, n_keys, shift, scale, window=0):
+def reference(cache, Q, rows, n_keys, shift, scale, window=0, tile=False):
     """Float64 attention of one sequence's rows Q [n, H, hd] over cache rows `rows`
     (its keys, -1: not there), row r at position shift + r; and the bound of the error.
 
@@ -73,7 +73,12 @@ def reference(cache, Q, rows, n_keys, shift, scale, window=0):
     2^-20 of the largest for values far below it, which fp16 holds as subnormals).
     (d) scores: q' is rounded to fp16 (exactly where it is bf16 and no D^{-1/2}
     enters, but for values 2^-14 below its largest), and hd + 8 float32 operations on
-    terms s c q and m sum q; their error moves p by as much relatively."""
+    terms s c q and m sum q; their error moves p by as much relatively.
+    (e) tile (many rows share decoded keys): K is fp16(fp16(s) c + fp16(m)), three
+    roundings of 2^-11 of s c, of m and of their sum, where (d) has them exact; and its
+    unit is such that the largest scale is 2^11 or more of the code's 2^-24, so what
+    fp16 holds as a subnormal is off by 2^-25 of that, 2^-12 of the scale.  V alike:
+    another 2^-11 of m in its sum."""
     n, H, hd = Q.shape
     G = H // cache.KV
     out, tol = torch.zeros(n, H, hd, dtype=torch.float64), torch.zeros(n, H, hd, dtype=torch.float64)
@@ -107,6 +112,12 @@ def reference(cache, Q, rows, n_keys, shift, scale, window=0):
         e_t = abs(scale) * ((HALF["f16"] if cache.dhi[0] is not None else 0.0) * 2 * terms
                        + (hd + 8) * HALF["f32"] * 2 * terms
                        + 2.0 ** -24 * qa.amax(1, keepdim=True) * (ka[:, h // G].abs() + km[:, h // G].abs()).sum(1))
+        if tile:
+            e_v = e_v + HALF["f16"] * p @ vm[:, h // G].abs()
+            dhi = 1.0 if cache.dhi[0] is None else cache.dhi[0].double()[cache.first + h // G * hd:][:hd]
+            top_s = cache.one[1].double().nan_to_num(0.0).amax()
+            e_t = e_t + abs(scale) * (HALF["f16"] * qa @ (ka.abs() + km.abs() + (ka + km).abs())[:, h // G].T
+                                      + 2.0 ** -12 * top_s * (qa * dhi).sum(1, keepdim=True))
         e_t = torch.where(seen, e_t + 2.0 ** -22 * t.abs(), 0.0)
         w = p * torch.expm1(2 * e_t.amax(1, keepdim=True))
         e_s = w @ V.abs() + w.sum(1, keepdim=True) * o.abs()

@@ -1,0 +1,90 @@
+"""Attention over a quantized cache where its rows and keys are divided in other ways:
+many sequences, blocks of several, heads that are no multiple of a workgroup's, page
+tables longer than a workgroup holds, and rows of the cache that are no keys."""
+import random
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def _lens(n, lo, hi, seed):
+    rng = random.Random(seed)
+    return [rng.randint(lo, hi) for _ in range(n)]
+
+
+def _mixed(n, seed):
+    """Lengths and new tokens: whole prompts, chunks of long ones, empty sequences."""
+    rng = random.Random(seed)
+    lens = [rng.choice((0, rng.randint(1, 90), rng.randint(200, 700))) for _ in range(n)]
+    return lens, [rng.randint(0, n) if rng.random() < 0.5 else n for n in lens]
+
+
+MANY = _lens(70, 30, 60, 1)
+FEW, FEW_NEW = _mixed(64, 2)
+ONES = _lens(1100, 1, 40, 3)
+CASES = [
+    # blocks of 256 rows: more sequences than lanes, as many, and a few of which one is long
+    (8, 2, 64, 4, 64, "asym", 16, MANY, MANY, 0, False, False),
+    (4, 2, 64, 4, 32, "sym", 16, FEW, FEW_NEW, 0, True, False),
+    (4, 1, 128, 4, 128, "asym", 16, [700, 64, 1500, 0, 300, 33], [700, 40, 200, 0, 300, 1], 0, False, False),
+    (4, 1, 128, 8, 64, "fp8", 32, [900, 300, 1200], [300, 300, 100], 200, True, True),
+    (2, 1, 256, 4, 64, "intzp", 32, [200, 90], [100, 90], 0, False, False),
+    (2, 1, 256, 8, 256, "asym", 8, [333], [333], 50, True, False),
+    # a few rows of few keys on many workgroups: ranges of a tile
+    (2, 1, 64, 8, 32, "asym", 16, [2600], [70], 0, False, False),
+    # blocks of 16 rows: one a workgroup (more than 2048 of them), and divided evenly
+    (16, 8, 64, 4, 64, "asym", 16, ONES, [1] * 1100, 0, False, False),
+    (6, 3, 64, 4, 32, "sym", 16, [500, 3, 1200, 0, 77], [2, 3, 1, 0, 5], 0, True, False),
+    (10, 5, 128, 8, 128, "asym", 64, [900, 64, 65], [1, 1, 1], 0, False, False),
+    (24, 6, 128, 4, 128, "asym", 16, [1500, 10, 700], [3, 1, 2], 0, False, True),
+    (40, 1, 64, 4, 64, "intzp", 16, [600, 31], [1, 1], 0, False, False),
+    (2, 1, 256, 8, 32, "fp8", 16, [700, 100], [1, 1], 300, True, False),
+    # page tables of more entries than a workgroup holds at a time
+    (2, 1, 64, 8, 32, "fp8", 1, [3000, 1023, 1025], [1, 1, 1], 0, False, False),
+    (8, 4, 128, 4, 128, "asym", 1, [2100], [1], 1500, False, False),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c[:7])) + f"-{len(c[7])}x{max(c[7])}")
+def test_against_float64(case):
+    from test_gpu_attention import _run
+    _run(case)
+
+
+@pytest.mark.parametrize("rows", [1, 9, 40])
+def test_bytes_of_rows_that_are_no_keys(rows):
+    """Every byte of the rows that belong to no key is E4M3's NaN, row 0 among them."""
+    import torch
+    from test_gpu_attention import _call, _i32, _small
+    cache, _ = _small(n_slots=128, bits=8, fmt="fp8")
+    g = torch.Generator(device="cuda").manual_seed(9)
+    Q = torch.randn(rows, 4, 64, generator=g, device="cuda").bfloat16()
+    pages, off, n = _i32([[5, 7, 3, -1]]), _i32([0, rows]), 44
+    want = _call(cache, Q, pages, [n], offsets=off, window=0)
+    assert torch.isfinite(want.float()).all()
+    at = [p * 16 + i for p in (5, 7, 3) for i in range(16)][:n]
+    free = torch.ones(128, dtype=torch.bool, device="cuda")
+    free[at] = False
+    for t in cache.one:
+        t.view(torch.uint8)[free] = 255
+    assert torch.equal(_call(cache, Q, pages, [n], offsets=off, window=0), want)
+
+
+def test_blocks_in_any_order_give_the_same_rows():
+    """The rows of a sequence are the same alone and among others (64 bits of its sums
+    are those of one range of keys here)."""
+    import torch
+    from test_gpu_attention import _call, _i32, _small
+    cache, _ = _small(n_slots=1024, bits=4, fmt="asym")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    lens = [200, 64, 130, 128, 255, 190]
+    Q = torch.randn(sum(lens), 4, 64, generator=g, device="cuda").bfloat16()
+    pages = torch.randperm(64, generator=g, device="cuda")[:16].to(torch.int32)[None].repeat(6, 1).contiguous()
+    off = [0]
+    for n in lens:
+        off.append(off[-1] + n)
+    every = _call(cache, Q, pages, lens, offsets=_i32(off))
+    for i, n in enumerate(lens):
+        one = _call(cache, Q[off[i]:off[i + 1]].contiguous(), pages[i:i + 1].contiguous(), [n], offsets=_i32([0, n]))
+        assert torch.equal(one, every[off[i]:off[i + 1]])
