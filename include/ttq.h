@@ -541,10 +541,13 @@ int ttq_cache_rope(const ttq_heads* hd, int64_t T, int32_t x_type,
  * cache: such keys are not seen) is 0.  Nothing of a key that a row does not see
  * enters it, an infinity or NaN neither; of one that it sees, K's makes the head's
  * row NaN, V's the channels of its group (at least).
- * Products are those of exact codes with q D^{-1/2} and p in 11 bits (fp16, scaled
- * by powers of two); V's scales and offsets enter in 11 bits too.  Scores, sums
- * and the softmax are float32.
- * bits 3 to 8 (others: TTQ_EUNSUPPORTED, as are n_slots from 2^31 on).
+ * Products are those of q D^{-1/2} and p in 11 bits (fp16, scaled by powers of two)
+ * with exact codes, whose scales enter K's in float32 and V's in 11 bits (what these
+ * leave out goes, for the middle of the codes, into the offsets); where a sequence
+ * has 64 and more rows of a K/V head on average, with k and v as fp16 values.
+ * Scores, sums and the softmax are float32.
+ * bits 3 to 8 (others: TTQ_EUNSUPPORTED, as are n_slots from 2^31 on); of a sequence
+ * at most 2^31 - 4097 keys are seen.
  * heads * T up to 2^31 - 1. */
 int ttq_cache_attention_workspace_bytes(const ttq_heads* hd, int64_t T,
                                         int64_t n_seq, int64_t max_pages,

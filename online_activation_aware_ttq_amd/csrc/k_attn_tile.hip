@@ -2,25 +2,37 @@
 // (prompts and chunks of them): tiles of keys, decoded once for 256 rows.
 //
 // A workgroup takes 256 query rows of one K/V head (a token's G heads, then the next
-// token's) and its keys, KT = 8192 / HD at a time.  Its eight waves decode a tile
-// together, (s c + m) in fp16, K as rows and V as columns, into LDS, while they work
-// on the tile before, each for 32 rows:
+// token's) and its keys, KT = 8192 / HD at a time, decoded once for all of them as
+// fp16(s c + m) into LDS rows of K and of V.  Each of its eight waves has 32 rows:
 //   S^T = K q'^T   (32 keys x 32 rows an instruction block).  Key 16s + 8h + 4a + b
 //                  of a block is row 16s + 8a + 4h + b, so that the lane of a row (h
 //                  = lane / 32) ends with the 8 adjacent keys 16s + 8h ..  of it
 //   O^T += V^T P^T that it has to give here: nothing passes between lanes but the
-//                  maximum.
+//                  maximum.  V is transposed as it is read (16 lanes, 4 keys).
 // The sums of p are those of the fp16 values that weight V (v_dot2).
 //
-// fp16's range is kept by powers of two: K and V are decoded as 2^-YK and 2^-YV of
-// what they are, which the workgroup raises, with a tile decoded again, when a scale
-// or offset would leave it; q' as in k_attention.hip.  The maximum of a row follows
-// only steps of 2^8 (p and the sums may be as much larger), so O is seldom scaled.
+// A SIMD has two waves (256 registers each), and a wave's tile is 32 matrix
+// instructions of 32 cycles and about 300 vector ones, 32 of them exponentials.  Left
+// to themselves both waves do the same at the same time.  So half of the waves are
+// half a step behind: while they do their products, the others do the softmax.  The
+// decoding of the next tile is spread between the products, whose operands are read
+// four ahead of them; the order is fixed by hand, for the compiler's waits for each
+// operand before its product (a tile of 64 keys and 128 channels: 3.6 us with waves
+// that decode, multiply and weigh all together, 2.3 so; an order left to the compiler
+// 5.8).  With all that a compute unit's tile is 5000 cycles where the matrix
+// instructions are 2048: a products' phase takes 2200 and the other's 1850 and the
+// two have to wait for each other twice a tile.  LDS is read for 1360 cycles of it and
+// has 500 of conflicts.  64 rows a wave would halve its reads, for twice the registers.
 //
-// What bounds it, a tile of 64 keys and 128 channels: 32 matrix instructions a wave
-// of 32 cycles each, 32 exponentials of 16, about as much other vector work, and 32
-// KiB from LDS a wave (64 of whose rows' reads would halve that, for twice the
-// registers).
+// Besides, a workgroup of one tile takes 21 us: its rows, pages and codes are a chain
+// of loads, and a compute unit holds one workgroup.  2047 x 4 prompts of 32 / 8 heads
+// of 128, 4 bits: 139 us, 450 TFLOP/s of the visible keys.
+//
+// fp16's range is kept by powers of two: K and V are decoded as 2^-YK and 2^-YV of
+// what they are.  A tile's scales are looked at a step before it is decoded, and if
+// one would leave the range all threads raise YK or YV together from that tile on, and
+// O as its first V is used; q' as in k_attention.hip.  The maximum of a row follows
+// only steps of 2^8 (p and the sums may be as much larger), so O is seldom scaled.
 #include <algorithm>
 
 #include "attn.h"

@@ -1574,8 +1574,12 @@ struct AttnPlan {
   bool join = false;
   size_t off_ml = 0, off_pre = 0, total = 0;
 };
-// Rows of a sequence and K/V head from which tiles are decoded for 256 of them, and
-// the workgroups (a compute unit holds one) up to which their keys are divided, down
+// Rows of a sequence and K/V head from which tiles are decoded for 256 of them.  A block
+// of them costs the same however few it has, the other kernel's 16 do not: 1, 8, 32 and
+// 64 sequences (4096, 4096, 1024, 2048 keys, 32 / 8 heads of 128) of 32 rows take 36, 66,
+// 48 and 153 us so, 22, 38, 50 and 101 the other way; of 64 rows 35, 67, 48 and 154, and
+// 28, 52, 78 and 165; of 128 rows 36, 84, 49 and 158, and 30, 81, 119 and 320.
+// And the workgroups (a compute unit holds one) up to which their keys are divided, down
 // to so many keys.
 constexpr int64_t kAttnTileRows = 64, kAttnTileGroups = 256, kAttnTileMinKeys = 512;
 // Workgroups of the other kernel that fill the chip (two a compute unit).  From four
@@ -1601,6 +1605,7 @@ int plan_attention(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t max_pag
   if (h->n_slots > INT32_MAX) return TTQ_EUNSUPPORTED;
   const int64_t room = max_pages * page_tokens;
   P->max_len = max_len > 0 ? std::min(max_len, room) : room;
+  P->max_len = std::min<int64_t>(P->max_len, INT32_MAX - 4096);  // (and some keys ahead: 32 bits)
   const int64_t G = h->heads / h->kv_heads;
   P->tile = T * G >= kAttnTileRows * n_seq;
   const int64_t rows_block = P->tile ? 256 : 16;
