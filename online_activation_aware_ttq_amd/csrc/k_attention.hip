@@ -20,9 +20,19 @@
 // V's operand takes 8 keys of one channel from a lane: it reads HD / 16 adjacent
 // channels of 8 keys and parts them in registers.
 //
-// fp16 holds q' (times a power of two, its largest value in [2^10, 2^11)), p <= 1 and
-// V's scales (divided by 2^Y, Y the wave's so far): 11 bits each, an eighth of what
-// the bf16 result is rounded by.
+// fp16 holds q' (times a power of two, its largest value in [2^10, 2^11)), p up to
+// 2^kLazy and V's scales (divided by 2^Y, Y the wave's so far): 11 bits each, an eighth
+// of what the bf16 result is rounded by; V's offsets are two fp16 values each, which
+// also make up for what a scale's 11 bits leave out, in the middle of its codes.
+//
+// It is bound by memory where there is enough of it to ask for: codes and scales go
+// to LDS without registers, two or three steps ahead, and all steps of all blocks are
+// divided evenly over two workgroups a compute unit.  4 bits, 32 / 8 heads of 128: 64
+// requests of up to 2047 keys 99 us (4.6 TB/s), one of 131071 keys in groups of 64 51 us
+// (3.3 TB/s; groups of 128: 41), 8 requests 36 us (3.0 TB/s).  11 us of each are the chain
+// before the first codes (lengths and their sums, pages, codes) and the join's 4 to 8.
+// Groups of 32 are bound by the products per group and their scales (82 us where groups of
+// 128 take 37).
 //
 // What the maxima and sums of the ranges are is kept in float32 and joined by
 // k_attn_join; with one range the row is written at once.
@@ -137,7 +147,6 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
   constexpr float kSMax = kP ? 200.f : F8 ? 128.f : 60000.f;
   constexpr int kSBits = kP ? 5 : F8 ? 5 : 13;
   constexpr int MU = F8 ? 0 : kP ? 20 : 10;  // V's offsets: 2^MU of O's unit
-  constexpr int kMid = F8 ? 0 : 1 << (CB - 1);
   constexpr float kLazy = 8.f;
   __shared__ __align__(16) float sm_k[NW][2][NG][KS];
   __shared__ __align__(16) _Float16 sm_s[NW][NG][KS], sm_m[NW][F8 ? 1 : 2 * NG][KS];
@@ -462,7 +471,7 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
       const _Float16 s16 = (_Float16)sv;
       sm_s[w][g][kl] = s16;
       if constexpr (!F8) {
-        const float mv = x ? 0.f : fmaf(sv - (float)s16, ldexpf((float)kMid, MU - U), ldexpf(vm[g], MU - U - Y));
+        const float mv = x ? 0.f : fmaf(sv - (float)s16, ldexpf((float)a.mid, MU - U), ldexpf(vm[g], MU - U - Y));
         const _Float16 m16 = (_Float16)mv;
         sm_m[w][g][kl] = m16;
         sm_m[w][NG + g][kl] = (_Float16)(mv - (float)m16);

@@ -314,16 +314,16 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   // barrier ago.
   // (half of the threads begin with the other 8 channels, for the other banks)
   const bool v_odd = tid >> 2 & 1, k_odd = HD > 64 && v_odd;
+  const unsigned mid = (unsigned)a.mid * 0x00010001u, mid16 = mid << 4;  // as codes are: c 2^-24
   constexpr int kPieces = 10;
   struct Factors {
     unsigned s1, s16, m;
   } fk, fv;
   auto factors = [&](float s, float m, int y) __attribute__((always_inline)) {
-    const float a = ldexpf(s, -y);
-    const _Float16 h = (_Float16)a;
-    // what the scale's 11 bits leave out is made up for in the middle of the codes
-    const float b = ldexpf(m, -y - U) + (F8 ? 0.f : (a - (float)h) * ldexpf((float)(1 << (CB - 1)), -U));
-    return Factors{both(h, h), both((float)h * 0.0625f, (float)h * 0.0625f), both(b, b)};
+    // the offset of the middle of the codes, which is small where that of the first is
+    // half the range and would lose so many bits more
+    const float x = ldexpf(s, -y), b = F8 ? 0.f : ldexpf(fmaf(s, (float)a.mid, m), -y - U);
+    return Factors{both(x, x), both(x * 0.0625f, x * 0.0625f), both(b, b)};
   };
   auto decode = [&](const unsigned (&code)[CB / 2], int u, const Factors& x, _Float16* dst, int flip, bool odd) __attribute__((always_inline)) {
     unsigned w[2];
@@ -338,7 +338,11 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     const f16x8 c = codes8<CB, F8>(w[0], w[1]);
     u32x4 v = __builtin_bit_cast(u32x4, c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = fma2(v[i], !F8 && slot_shift<CB>(2 * i) ? x.s16 : x.s1, x.m);
+    for (int i = 0; i < 4; ++i) {
+      const bool by16 = !F8 && slot_shift<CB>(2 * i);
+      if (!F8) v[i] = u2(h2(v[i]) - h2(by16 ? mid16 : mid));  // exact, as is a code
+      v[i] = fma2(v[i], by16 ? x.s16 : x.s1, x.m);
+    }
     *(u32x4*)&dst[(((kch >> 3) + (odd ? 1 - u : u)) ^ flip) * 8] = v;
   };
   auto stage = [&](int d, int piece) __attribute__((always_inline)) {
@@ -529,9 +533,8 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int at = (i & 1) * 8 + 2 * j;
-        v[j] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_pkrtz(
-            __builtin_amdgcn_exp2f(fmaf(s[i >> 1][at], f, -base)),
-            __builtin_amdgcn_exp2f(fmaf(s[i >> 1][at + 1], f, -base))));
+        v[j] = both(__builtin_amdgcn_exp2f(fmaf(s[i >> 1][at], f, -base)),
+                    __builtin_amdgcn_exp2f(fmaf(s[i >> 1][at + 1], f, -base)));
         sum = __builtin_amdgcn_fdot2(h2(v[j]), f16x2{(_Float16)1.f, (_Float16)1.f}, sum, false);
       }
       p[i] = __builtin_bit_cast(f16x8, v);

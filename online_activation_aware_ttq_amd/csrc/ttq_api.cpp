@@ -1703,7 +1703,7 @@ int cache_attention_impl(const ttq_heads* h, int64_t T, int64_t n_seq, int64_t m
              !misaligned(v_scales, 16) && !misaligned(v_mins, 16);
   }
   a.slots = P.slots; a.slot_rows = P.slot_rows;
-  a.nsplit = P.nsplit; a.tiles = P.tiles;
+  a.nsplit = P.nsplit; a.tiles = P.tiles; a.mid = 1 << (f.bits - 1);
   const int cb = container_bits(f.bits);
   st = P.tile ? run(K_ATTN_TILE, s, [&](const Launch& L) {
     return launch_attn_tile(a, h->head_dim, cb, (int)f.qformat, L);

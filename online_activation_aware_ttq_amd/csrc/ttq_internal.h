@@ -861,6 +861,7 @@ struct AttnArgs {
   int64_t slots, slot_rows;   // of a K/V head (slots 0: tiles)
   int nsplit;                 // tiles: ranges of keys
   int64_t tiles;              // blocks of query rows of a K/V head
+  int mid;  // 2^(bits - 1), the middle of the codes
 };
 constexpr int kAttnMaxParts = 2048;  // parts of a row's keys at most
 hipError_t launch_attn_split(const AttnArgs& a, int head_dim, int cb, int qf, int group,

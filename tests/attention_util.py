@@ -63,22 +63,35 @@ class Cache:
         return [(v * dhi)[:, cut].unflatten(1, (self.KV, self.hd)) for v in (rep(s) * q, rep(m).clone())]
 
 
+    def middle(self, rows, which):
+        """What the middle of the codes, 2^(bits - 1), stands for without m: s mid D^{-1/2},
+        as .parts; E4M3: 0."""
+        s = (self.two if which and self.two else self.one)[1]
+        at = (self.first, self.v_first)[which]
+        mid = 0.0 if self.how["qformat"] == "fp8" else 2.0 ** (self.how["bits"] - 1)
+        v = mid * s[rows].double().repeat_interleave(self.group, 1)
+        v = v * (1.0 if self.dhi[which] is None else self.dhi[which].double())
+        return v[:, at:at + self.KV * self.hd].unflatten(1, (self.KV, self.hd))
+
+
 def reference(cache, Q, rows, n_keys, shift, scale, window=0, tile=False):
     """Float64 attention of one sequence's rows Q [n, H, hd] over cache rows `rows`
     (its keys, -1: not there), row r at position shift + r; and the bound of the error.
 
     The bound: (a) the result is rounded once to bf16.  (b) p is rounded to fp16 in
-    the sum and the divisor alike, and for p < 2^-14 by 2^-25.  (c) V's scales,
-    offsets and the products of scales and codes are rounded to fp16 (2^-11 each; and
-    2^-20 of the largest for values far below it, which fp16 holds as subnormals).
+    the sum and the divisor alike, and for p < 2^-14 by 2^-25.
+    (c) V's scales, offsets and the products of scales and codes are rounded to fp16
+    (2^-11 each; and 2^-20 of the largest for values far below it, which fp16 holds as
+    subnormals); what the scale's rounding leaves out is added for the middle of the
+    codes, so that it is off by 2^-11 of s (c - mid), at most s c or s mid.
     (d) scores: q' is rounded to fp16 (exactly where it is bf16 and no D^{-1/2}
     enters, but for values 2^-14 below its largest), and hd + 8 float32 operations on
     terms s c q and m sum q; their error moves p by as much relatively.
-    (e) tile (many rows share decoded keys): K is fp16(fp16(s) c + fp16(m)), three
-    roundings of 2^-11 of s c, of m and of their sum, where (d) has them exact; and its
-    unit is such that the largest scale is 2^11 or more of the code's 2^-24, so what
-    fp16 holds as a subnormal is off by 2^-25 of that, 2^-12 of the scale.  V alike:
-    another 2^-11 of m in its sum."""
+    (e) tile (many rows share decoded keys): K is fp16(fp16(s) (c - mid) + fp16(m +
+    mid s)), three roundings of 2^-11 of s (c - mid), of m + mid s and of their sum,
+    where (d) has them exact; and its unit is such that the largest scale is 2^11 or
+    more of the code's 2^-24, so what fp16 holds as a subnormal is off by 2^-25 of
+    that, 2^-12 of the scale.  V alike."""
     n, H, hd = Q.shape
     G = H // cache.KV
     out, tol = torch.zeros(n, H, hd, dtype=torch.float64), torch.zeros(n, H, hd, dtype=torch.float64)
@@ -88,6 +101,7 @@ def reference(cache, Q, rows, n_keys, shift, scale, window=0, tile=False):
     there = rows >= 0
     at = torch.arange(rows.numel(), device=rows.device)
     (ka, km), (va, vm) = (cache.parts(rows.clamp(min=0), w) for w in (0, 1))
+    k_mid, v_mid = (cache.middle(rows.clamp(min=0), w) for w in (0, 1))
     pos = shift + torch.arange(n, device="cuda")[:, None]
     seen = (at <= pos) & there
     if window:
@@ -105,19 +119,19 @@ def reference(cache, Q, rows, n_keys, shift, scale, window=0, tile=False):
         e_p = 2 * HALF["f16"] * (p @ V.abs() + o.abs())
         e_p = e_p + 2.0 ** -24 * torch.where(seen, torch.exp(top * 0), 0.0).double() @ V.abs() \
             / torch.exp(t - top).sum(1, keepdim=True)
-        e_v = HALF["f16"] * (2 * p @ va[:, h // G].abs() + p @ vm[:, h // G].abs())
-        e_v = e_v + 2.0 ** -20 * torch.where(seen, V.abs().amax(1), 0.0).amax(1, keepdim=True)
+        e_v = HALF["f16"] * p @ (2 * va[:, h // G].abs() + vm[:, h // G].abs() + v_mid[:, h // G])
         qa = q.abs()
         terms = qa @ ka[:, h // G].abs().T + qa.sum(1, keepdim=True) * km[:, h // G].abs().amax(1)
         e_t = abs(scale) * ((HALF["f16"] if cache.dhi[0] is not None else 0.0) * 2 * terms
                        + (hd + 8) * HALF["f32"] * 2 * terms
                        + 2.0 ** -24 * qa.amax(1, keepdim=True) * (ka[:, h // G].abs() + km[:, h // G].abs()).sum(1))
         if tile:
-            e_v = e_v + HALF["f16"] * p @ vm[:, h // G].abs()
+            e_v = HALF["f16"] * p @ ((va - v_mid).abs() + (vm + v_mid).abs() + (va + vm).abs())[:, h // G]
             dhi = 1.0 if cache.dhi[0] is None else cache.dhi[0].double()[cache.first + h // G * hd:][:hd]
             top_s = cache.one[1].double().nan_to_num(0.0).amax()
-            e_t = e_t + abs(scale) * (HALF["f16"] * qa @ (ka.abs() + km.abs() + (ka + km).abs())[:, h // G].T
+            e_t = e_t + abs(scale) * (HALF["f16"] * qa @ ((ka - k_mid).abs() + (km + k_mid).abs() + (ka + km).abs())[:, h // G].T
                                       + 2.0 ** -12 * top_s * (qa * dhi).sum(1, keepdim=True))
+        e_v = e_v + 2.0 ** -20 * torch.where(seen, V.abs().amax(1), 0.0).amax(1, keepdim=True)
         e_t = torch.where(seen, e_t + 2.0 ** -22 * t.abs(), 0.0)
         w = p * torch.expm1(2 * e_t.amax(1, keepdim=True))
         e_s = w @ V.abs() + w.sum(1, keepdim=True) * o.abs()
