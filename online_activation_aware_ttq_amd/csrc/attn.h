@@ -29,6 +29,11 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
+// A scale and offset that are not both finite count as NaN
+__device__ __forceinline__ void finite_or_nan(float& s, float& m) {
+  if (!((__builtin_fabsf(s) <= 3.402823466e38f) & (__builtin_fabsf(m) <= 3.402823466e38f))) s = m = __builtin_nanf("");
+}
+
 // Eight codes of one row (CB bytes, low bits first) as an operand.  4 bits: slots
 // (2i, 2i + 1) are codes (i, i + 4), 16-fold where i is odd (slot_code,
 // slot_shift); 8 bits: in order.

@@ -432,6 +432,9 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
       wave_sync();
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
+        if (F8) km[g] = 0.f;
+        finite_or_nan(ks[g], km[g]);
+        finite_or_nan(vs[g], vm[g]);
         sm_k[w][0][g][kl] = now ? ks[g] : 0.f;
         if (!F8) sm_k[w][1][g][kl] = now ? km[g] : 0.f;
         if (!now) vs[g] = vm[g] = 0.f;

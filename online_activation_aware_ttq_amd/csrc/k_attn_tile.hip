@@ -290,6 +290,8 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   // The scales xs of pair d, K's of row rk and V's of row rv.  Rare: keys in no page,
   // NaN, exponents that are too small.
   auto check = [&](int d, int rk, int rv) __attribute__((always_inline)) {
+    finite_or_nan(xs.ks, xs.km);
+    finite_or_nan(xs.vs, xs.vm);
     const bool bad = nan(xs.vs, xs.vm);
     const bool k_big = ldexpf(xs.ks, -YK) > kSMax || ldexpf(__builtin_fabsf(xs.km), -YK - U) > 30000.f;
     const bool v_big = ldexpf(xs.vs, -YV) > kSMax || ldexpf(__builtin_fabsf(xs.vm), -YV - U) > 30000.f;

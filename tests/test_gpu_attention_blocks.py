@@ -71,6 +71,32 @@ def test_bytes_of_rows_that_are_no_keys(rows):
     assert torch.equal(_call(cache, Q, pages, [n], offsets=off, window=0), want)
 
 
+@pytest.mark.parametrize("fmt,bits", [("asym", 4), ("fp8", 8), ("sym", 8)])
+@pytest.mark.parametrize("rows", [1, 9, 40])
+def test_infinite_scales_stay_with_their_key(fmt, bits, rows):
+    """The newest key's, which only the last row sees: NaN in what it enters, no more."""
+    import torch
+    from test_gpu_attention import _call, _i32, _small
+    cache, _ = _small(n_slots=128, bits=bits, fmt=fmt)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    Q = torch.randn(rows, 4, 64, generator=g, device="cuda").bfloat16()
+    pages, off, n = _i32([[5, 0, 3, 6]]), _i32([0, rows]), 50
+    clean = _call(cache, Q, pages, [n], offsets=off)
+    s, at, gv = cache.one[1], 6 * 16 + 1, cache.v_first // 32 + 2
+    keep = s[at].clone()
+    s[at, gv] = float("inf")
+    got = _call(cache, Q, pages, [n], offsets=off)
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[-1, 2:, :32] = True  # the first group of head 1
+    assert torch.equal(torch.isnan(got.float()), bad) and torch.equal(got[~bad], clean[~bad])
+    s[at] = keep
+    s[at, 0] = float("inf")  # K, head 0
+    got = _call(cache, Q, pages, [n], offsets=off)
+    bad[:] = False
+    bad[-1, :2] = True
+    assert torch.equal(torch.isnan(got.float()), bad) and torch.equal(got[~bad], clean[~bad])
+
+
 def test_blocks_in_any_order_give_the_same_rows():
     """The rows of a sequence are the same alone and among others (64 bits of its sums
     are those of one range of keys here)."""
