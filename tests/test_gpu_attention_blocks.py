@@ -98,8 +98,7 @@ def test_infinite_scales_stay_with_their_key(fmt, bits, rows):
 
 
 def test_blocks_in_any_order_give_the_same_rows():
-    """The rows of a sequence are the same alone and among others (64 bits of its sums
-    are those of one range of keys here)."""
+    """The rows of a sequence are the same alone and among others (few keys: one range)."""
     import torch
     from test_gpu_attention import _call, _i32, _small
     cache, _ = _small(n_slots=1024, bits=4, fmt="asym")
@@ -114,3 +113,78 @@ def test_blocks_in_any_order_give_the_same_rows():
     for i, n in enumerate(lens):
         one = _call(cache, Q[off[i]:off[i + 1]].contiguous(), pages[i:i + 1].contiguous(), [n], offsets=_i32([0, n]))
         assert torch.equal(one, every[off[i]:off[i + 1]])
+
+
+@pytest.mark.parametrize("KV,hd,bits,group", [(8, 128, 4, 128), (8, 128, 4, 64), (4, 64, 8, 32), (2, 256, 8, 64)])
+def test_scales_at_any_alignment(KV, hd, bits, group):
+    """Scales read 16 bytes and 4 bytes at a time give the same bits, and the right ones."""
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    from attention_util import Cache, reference
+    from test_gpu_attention import _i32
+    g = torch.Generator(device="cuda").manual_seed(hd + group)
+    cache = Cache(g, 2048, KV, hd, bits, group, "asym")
+    pages = torch.randperm(128, generator=g, device="cuda").view(2, 64).to(torch.int32)
+    lens = [1000, 333]
+    Q = torch.randn(2, 2 * KV, hd, generator=g, device="cuda").bfloat16()
+
+    def call(c):
+        return ttq.ttq_cache_attention(Q, pages, _i32(lens), *c, page_tokens=16, **cache.kwargs())
+
+    want = call(cache.one)
+    apart = [cache.one[0]]
+    for t in cache.one[1:]:
+        room = torch.empty(t.numel() + 1, device="cuda")
+        room[1:] = t.flatten()
+        apart.append(room[1:].view(t.shape))
+        assert apart[-1].data_ptr() % 16 == 4
+    assert torch.equal(call(apart), want)
+    for i, n in enumerate(lens):
+        t = torch.arange(n, device="cuda")
+        ref, tol = reference(cache, Q[i:i + 1], pages[i].long()[t // 16] * 16 + t % 16, n, n - 1, hd ** -0.5)
+        assert ((want[i:i + 1].double().cpu() - ref).abs() <= tol).all()
+
+
+def test_captured_prompts():
+    """Two graphs of prompts whose keys are divided, replayed at once: the eager call's bits."""
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    from test_gpu_attention import _i32, _small
+    cache, _ = _small(n_slots=4096, KV=2, hd=128, group=128)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    state = []
+    for k in range(2):
+        Q = torch.randn(260, 4, 128, generator=g, device="cuda").bfloat16()
+        pages = torch.randperm(256, generator=g, device="cuda").view(2, 128).to(torch.int32).contiguous()
+        state.append((Q, pages, _i32([2000, 700]), _i32([0, 130, 260]), torch.zeros_like(Q)))
+
+    def call(k, **kw):
+        Q, pages, lens, off, out = state[k]
+        return ttq.ttq_cache_attention(Q, pages, lens, *cache.one, page_tokens=16, offsets=off,
+                                       **cache.kwargs(), **kw)
+
+    call(0)
+    torch.cuda.synchronize()
+    graphs = []
+    for k in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(k, out=state[k][4])
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for step in range(4):
+        for Q, pages, lens, off, out in state:
+            Q.normal_()
+            lens.copy_(_i32([130 + 400 * step, 0 if step == 2 else 2048 - step]))
+            off.copy_(_i32([0, 100 + 10 * step, 250]))
+            out.zero_()
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        got = [st[4].clone() for st in state]
+        for k in range(2):
+            a = call(k, out=torch.zeros_like(got[k]), stream=streams[k].cuda_stream)
+            torch.cuda.synchronize()
+            assert torch.equal(got[k], a) and (got[k][250:] == 0).all()
