@@ -36,6 +36,7 @@
 #include <algorithm>
 
 #include "attn.h"
+#include "block_order.h"
 
 namespace ttq {
 
@@ -98,6 +99,26 @@ __device__ __forceinline__ int lane_max(int x) {
   return max(x, __builtin_amdgcn_update_dpp(x, x, 0x143, 0xc, 0xf, false));
 }
 
+// The lanes of a wave, each with a sequence (block_order.h)
+struct LaneWave {
+  LaneSeq own;
+  template <class F>
+  __device__ __forceinline__ int total(F f) const {
+    return __builtin_amdgcn_readlane(lane_scan(f(own)), 63);
+  }
+  template <class F>
+  __device__ __forceinline__ int owner(F f, int i, int& at) const {
+    const int n = f(own), scan = lane_scan(n);
+    const int lane = __builtin_ctzll(__ballot(scan > i));
+    at = i - __builtin_amdgcn_readlane(scan - n, lane);
+    return lane;
+  }
+  template <class F>
+  __device__ __forceinline__ int of(int lane, F f) const {
+    return __builtin_amdgcn_readlane(f(own), lane);
+  }
+};
+
 // find_block with the blocks in another order, those of the most keys first (to within
 // 256 keys): the last workgroups to begin are then short, where prompts of 2047 and
 // 900 tokens in the order of the batch leave a fifth of the time to a few.  For up to
@@ -105,45 +126,26 @@ __device__ __forceinline__ int lane_max(int x) {
 __device__ __forceinline__ bool find_long_block(const AttnArgs& a, int64_t b, int64_t& seq, SeqRows& s,
                                                 int64_t& r0) {
   const int l = threadIdx.x & 63;
-  int64_t first = 0, rows = 0, shift = 0, len = 0;
+  int64_t first = 0;
+  LaneWave w{};
   if (l < a.n_seq) {
     first = min(max((int64_t)a.offsets[l], (int64_t)0), a.T);
     const int64_t tokens = max(min(max((int64_t)a.offsets[l + 1], (int64_t)0), a.T) - first, (int64_t)0);
-    len = max(a.lens[l], 0);
-    rows = tokens * a.G;
-    shift = len - tokens;
+    w.own.len = max(a.lens[l], 0);
+    w.own.rows = tokens * a.G;
+    w.own.shift = w.own.len - tokens;
   }
-  const int blocks = (int)((rows + 255) >> 8);
-  // blocks of this lane's sequence that see more than x 256 keys: its last ones
-  auto count = [&](int x) __attribute__((always_inline)) {
-    if (x == 0) return blocks;
-    if (len <= (int64_t)x << 8) return 0;
-    const int64_t from = max((((int64_t)x << 8) - shift) * a.G, (int64_t)0) >> 8;
-    return max(blocks - (int)min(from, (int64_t)blocks - 1), 0);
-  };
-  auto total = [&](int x) __attribute__((always_inline)) {
-    return __builtin_amdgcn_readlane(lane_scan(count(x)), 63);
-  };
-  if (b >= total(0)) return false;
-  const int top = 31 - __builtin_clz((unsigned)max((int)(a.max_len >> 8), 1));
-  int x = 0;  // the largest that more than b blocks exceed
-  for (int i = top; i >= 0; --i)
-    if (total(x | 1 << i) > b) x |= 1 << i;
-  const bool last = x + 1 >> (top + 1);
-  const int above = last ? 0 : count(x + 1), n = count(x) - above;
-  const int rest = (int)b - __builtin_amdgcn_readlane(lane_scan(above), 63);
-  const int scan = lane_scan(n);
-  const int from = __builtin_ctzll(__ballot(scan > rest));
+  int from = 0;
+  if (!long_block(w, (int)b, a.max_len, a.G, from, r0)) return false;
   auto of = [&](int64_t v) __attribute__((always_inline)) {
     const unsigned lo = __builtin_amdgcn_readlane((int)v, from), hi = __builtin_amdgcn_readlane((int)(v >> 32), from);
     return (int64_t)((uint64_t)hi << 32 | lo);
   };
   seq = from;
   s.first = of(first);
-  s.rows = (int)of(rows);
-  s.shift = of(shift);
-  s.len = min(min(of(len), a.max_len), a.max_pages << a.pshift);
-  r0 = (of(blocks - count(x)) + rest - of(scan - n)) << 8;
+  s.rows = (int)of(w.own.rows);
+  s.shift = of(w.own.shift);
+  s.len = min(min(of(w.own.len), a.max_len), a.max_pages << a.pshift);
   return true;
 }
 
