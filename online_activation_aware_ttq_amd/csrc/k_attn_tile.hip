@@ -210,8 +210,9 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   const int full_lo = a.window > 0 ? rel(pos_hi - a.window + 1) : 0;
   unsigned r = min(w0 + n, last);
   const int64_t pos = sr.shift + r / G;
-  const int top_key = min(rel(pos), end - 1);
-  const int low_key = a.window > 0 ? rel(pos - a.window + 1) : 0;
+  // this row's, neither far below 0: a tile's first key is taken from them
+  const int top_key = max(min(rel(pos), end - 1), -1);
+  const int low_key = a.window > 0 ? max(rel(pos - a.window + 1), 0) : 0;
   const bf16_t* src = hf * 8 + a.Q + (sr.first + r / G) * a.ldq + (h * G + r % G) * HD;
 
   u32x4 qraw[KS];
