@@ -19,9 +19,10 @@ typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 template <bool F8>
 constexpr int kUnit = F8 ? 0 : 24;
 
-__device__ __forceinline__ unsigned e4m3_pair(unsigned w, bool hi) {
-  return __builtin_bit_cast(unsigned, hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true)
-                                         : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false));
+// (times a power of two)
+__device__ __forceinline__ unsigned e4m3_pair(unsigned w, bool hi, float times = 1.f) {
+  return __builtin_bit_cast(unsigned, hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, times, true)
+                                         : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, times, false));
 }
 
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
@@ -58,6 +59,23 @@ __device__ __forceinline__ constexpr int slot_code(int slot) {
 template <int CB>
 __device__ __forceinline__ constexpr int slot_shift(int slot) {
   return CB == 4 && (slot / 2) & 1 ? 4 : 0;
+}
+
+// The same as normal fp16 values, which a scale can make as small as fp16 goes: codes as
+// 16 + c / 64 (k = k16; nibbles above others: 16 + c / 4), E4M3 as 2^-8 of what they are.
+constexpr unsigned k16 = 0x4c004c00u;
+template <int CB, bool F8>
+__device__ __forceinline__ u32x4 codes8_normal(unsigned w0, unsigned w1, unsigned k) {
+  if constexpr (F8) {
+    return u32x4{e4m3_pair(w0, false, 0x1p-8f), e4m3_pair(w0, true, 0x1p-8f), e4m3_pair(w1, false, 0x1p-8f),
+                 e4m3_pair(w1, true, 0x1p-8f)};
+  } else if constexpr (CB == 8) {
+    return u32x4{__builtin_amdgcn_perm(k | k >> 8, w0, 0x04010400u), __builtin_amdgcn_perm(k | k >> 8, w0, 0x04030402u),
+                 __builtin_amdgcn_perm(k | k >> 8, w1, 0x04010400u), __builtin_amdgcn_perm(k | k >> 8, w1, 0x04030402u)};
+  } else {
+    const unsigned h = w0 >> 8;
+    return u32x4{(w0 & 0x000f000fu) | k, (w0 & 0x00f000f0u) | k, (h & 0x000f000fu) | k, (h & 0x00f000f0u) | k};
+  }
 }
 
 // Channels 4 i .. 4 i + 3 of two keys a and b as pairs (a, b), one a channel; 4 bits:

@@ -28,11 +28,16 @@
 // of loads, and a compute unit holds one workgroup.  4 prompts of up to 2047 tokens, 32 / 8 heads
 // of 128, 4 bits: 125 us a call, 500 TFLOP/s of the visible keys.
 //
-// fp16's range is kept by powers of two: K and V are decoded as 2^-YK and 2^-YV of
-// what they are.  A tile's scales are looked at a step before it is decoded, and if
-// one would leave the range all threads raise YK or YV together from that tile on, and
-// O as its first V is used; q' as in k_attention.hip.  The maximum of a row follows
-// only steps of 2^8 (p and the sums may be as much larger), so O is seldom scaled.
+// fp16's range is kept by powers of two: K and V are decoded as 2^-YK and 2^-YV of what
+// they are, YK and YV a group's (for all keys of the block), which put the newest key
+// that all rows see at 2 to 4; q' is times 2^YK, and as in k_attention.hip.  A key
+// whose groups are all 2^-8 to 4000 in these units (or 0) keeps 11 bits, or 2^-16 of
+// its group's largest value.  Keys of another size, 2^9 and more from that one, are
+// left out of the tiles, and what they give the rows that see them is added from their
+// codes in float32, one after another: so no row depends on the size of a key that it
+// does not see, and a seen one costs the others no bits.
+// The maximum of a row follows only steps of 2^8 (p and the sums may be as much
+// larger), so O is seldom scaled.
 #include <algorithm>
 
 #include "attn.h"
@@ -87,16 +92,6 @@ __device__ __forceinline__ int lane_scan(int x) {
   x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast 15, 31
   x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
   return x;
-}
-
-// Lane 63 is given the largest
-__device__ __forceinline__ int lane_max(int x) {
-  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x111, 0xf, 0xf, false));
-  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x112, 0xf, 0xf, false));
-  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x114, 0xf, 0xf, false));
-  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x118, 0xf, 0xf, false));
-  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x142, 0xa, 0xf, false));
-  return max(x, __builtin_amdgcn_update_dpp(x, x, 0x143, 0xc, 0xf, false));
 }
 
 // The lanes of a wave, each with a sequence (block_order.h)
@@ -157,20 +152,23 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   constexpr int KS = HD / 16;        // steps of 16 channels
   constexpr int PS = KT / 16;        // steps of 16 keys
   constexpr int KP = HD / 16;        // threads that decode a key
-  constexpr int U = kUnit<F8>;
   constexpr float kInf = __builtin_inff();
-  constexpr float kSMax = F8 ? 100.f : 50000.f;  // (k_attention.hip)
-  constexpr int kSBits = F8 ? 4 : 12;
   constexpr float kLazy = 8.f;
+  // sizes of a group in a tile's units; and codes there are (c - mid) / 64 (E4M3: / 256),
+  // so that a group's scale is about as large as its values
+  constexpr float kMost = 4000.f, kLeast = 0x1p-8f;
+  constexpr int kCode = F8 ? 8 : 6;
   // LDS rows are of 16-byte pieces, K's in the order piece ^ key % 8.  Of V, 16 lanes
   // read 32 bytes of 4 keys, the next 16 the 32 bytes beside them: in eight parts of the
   // banks, and the first four in four of half of the banks.
   auto v_flip = [](int key) { return (key & 3) << 1 | (HD == 64 ? 0 : (key & 1) << 3); };
-  constexpr unsigned kOut = 1u << 31;  // the key is in no page of the cache
+  constexpr unsigned kOut = 1u << 31;  // the key is in no page of the cache, or left out
   __shared__ __align__(16) _Float16 sm_k[2][KT * HD];
   __shared__ __align__(16) _Float16 sm_v[2][KT * HD];
   __shared__ unsigned sm_bad[3][KT];  // of a key: groups of V that are NaN; kOut
-  __shared__ int4 sm_ctl[3];          // exponents that K and V ask for; a key is bad
+  __shared__ int sm_ctl[3];           // a key of the tile is in sm_bad
+  __shared__ int sm_y[2][HD / 32];    // YK, YV of 32 channels
+  __shared__ int sm_far;              // keys have been left out
 
   const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = l & 31, hf = l >> 5;
@@ -274,11 +272,20 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     return Scales{a.ks[k], a.km[k], a.vs[v], a.vm[v]};
   };
   auto nan = [](float s, float m) { return s != s || m != m; };
-  auto exponent = [](float s, float m) __attribute__((always_inline)) {
-    int e = -1000;
-    if (s > 0.f) e = ilogbf(s);
-    if (m != 0.f && m == m) e = max(e, ilogbf(m) - U);
-    return e;
+  // the largest value that a group may hold (NaN or infinite if s or m is)
+  auto size_of = [&](float s, float m) __attribute__((always_inline)) {
+    return F8 ? fmaf(m, 0.f, __builtin_fabsf(s) * 448.f)
+              : __builtin_elementwise_maximum(__builtin_fabsf(s) * (float)a.mid,
+                                              __builtin_fabsf(fmaf(s, (float)a.mid, m)));
+  };
+  auto unit_of = [&](float s, float m) __attribute__((always_inline)) {
+    const float x = size_of(s, m);
+    return x > 0.f && x <= 3.402823466e38f ? min(max(__builtin_amdgcn_frexp_expf(x) - 2, -100), 100) : -1;
+  };
+  // Is a group's size one of a tile's, 2^y kLeast to 2^y kMost: as bits of floats
+  auto fits = [&](float s, float m, int y) __attribute__((always_inline)) {
+    const unsigned least = __float_as_uint(kLeast), most = __float_as_uint(kMost);
+    return __float_as_uint(size_of(s, m)) - (least + ((unsigned)y << 23)) <= most - least;
   };
 
   const int late = w >> 2;  // 0: the waves that are ahead, 1: half a step behind
@@ -286,40 +293,47 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   Scales xs, next;   // of pairs d and d + 1
   int r1, r2, r3;    // rows of this thread's key in tiles d + 1, d + 2, d + 3
   int page;          // and its page in tile d + 4
-  int YK = -200, YV = -200, YK_old = -200, YO = -200;
+  int YK = -1, YV = -1;  // of this thread's group
   bool bad_keys = false;  // tile d has keys of sm_bad
-  int4 ctl;
+  int ctl;
+  uint64_t far_k = 0;  // lanes whose key is left out for its K, before its V is there
+
+  // Is a group left out for its size; and of which keys is one (the KP threads of a key
+  // are lanes beside each other)
+  auto far = [&](float s, float m, int y) __attribute__((always_inline)) {
+    return !fits(s, m, y) && size_of(s, m) > 0.f && !nan(s, m);
+  };
+  auto of_key = [&](uint64_t lanes) __attribute__((always_inline)) {
+    return (lanes & (((uint64_t(1) << KP) - 1) << (l & -KP))) != 0;
+  };
 
   // The scales xs of pair d, K's of row rk and V's of row rv.  Rare: keys in no page,
-  // NaN, exponents that are too small.
+  // NaN, and keys of another size than the tile's.
   auto check = [&](int d, int rk, int rv) __attribute__((always_inline)) {
+    const bool usual = fits(xs.ks, xs.km, YK) & fits(xs.vs, xs.vm, YV) & ((rk | rv) >= 0);
+    if ((__ballot(!usual) | far_k) == 0) return;
     finite_or_nan(xs.ks, xs.km);
     finite_or_nan(xs.vs, xs.vm);
     const bool bad = nan(xs.vs, xs.vm);
-    const bool k_big = ldexpf(xs.ks, -YK) > kSMax || ldexpf(__builtin_fabsf(xs.km), -YK - U) > 30000.f;
-    const bool v_big = ldexpf(xs.vs, -YV) > kSMax || ldexpf(__builtin_fabsf(xs.vm), -YV - U) > 30000.f;
-    if (__ballot((rk | rv) < 0 || bad || k_big || v_big) == 0) return;
+    const bool k_far = far(xs.ks, xs.km, YK), v_far = far(xs.vs, xs.vm, YV);
     const int slot = (d + 3) % 3;
+    const bool left = (of_key(far_k) | of_key(__ballot(v_far))) & (rv >= 0);
+    if (d >= 0 && d * KT + kkey < end && (left || bad || rv < 0)) {
+      atomicOr(&sm_bad[slot][kkey], (bad && rv >= 0 ? nan_bit : 0u) | (left || rv < 0 ? kOut : 0u));
+      sm_ctl[slot] = 1;
+      if (left) sm_far = 1;
+    }
     if (rk < 0) xs.ks = xs.km = 0.f;
-    if (rv < 0 || bad) {
-      if (d >= 0 && d * KT + kkey < end) {
-        atomicOr(&sm_bad[slot][kkey], rv < 0 ? kOut : nan_bit);
-        sm_ctl[slot].z = 1;
-      }
-      xs.vs = xs.vm = 0.f;
-    }
-    const int ek = lane_max(exponent(xs.ks, xs.km)), ev = lane_max(exponent(xs.vs, xs.vm));
-    if (l == 63) {
-      atomicMax(&sm_ctl[slot].x, ek);
-      atomicMax(&sm_ctl[slot].y, ev);
-    }
+    if (rv < 0 || bad || v_far) xs.vs = xs.vm = 0.f;
+    far_k = __ballot(k_far);
   };
-  // Pair d into LDS, and on with what later ones need, in kPieces of code.  The
-  // exponents of a pair are those that all its threads agreed on in its check, a
-  // barrier ago.
+  // Pair d into LDS, and on with what later ones need, in kPieces of code.
   // (half of the threads begin with the other 8 channels, for the other banks)
   const bool v_odd = tid >> 2 & 1, k_odd = HD > 64 && v_odd;
-  const unsigned mid = (unsigned)a.mid * 0x00010001u, mid16 = mid << 4;  // as codes are: c 2^-24
+  // (a code in the low bits of 16 counts 1 / 64, a nibble above another 1 / 4)
+  const unsigned mid = (unsigned)a.mid * 0x00010001u + k16, mid16 = ((unsigned)a.mid * 0x00010001u << 4) + k16;
+  unsigned k16v = k16;
+  if constexpr (CB == 4) asm("" : "+v"(k16v));  // (in a register: and and or in one instruction)
   constexpr int kPieces = 10;
   struct Factors {
     unsigned s1, s16, m;
@@ -327,7 +341,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   auto factors = [&](float s, float m, int y) __attribute__((always_inline)) {
     // the offset of the middle of the codes, which is small where that of the first is
     // half the range and would lose so many bits more
-    const float x = ldexpf(s, -y), b = F8 ? 0.f : ldexpf(fmaf(s, (float)a.mid, m), -y - U);
+    const float x = ldexpf(s, kCode - y), b = F8 ? 0.f : ldexpf(fmaf(s, (float)a.mid, m), -y);
     return Factors{both(x, x), both(x * 0.0625f, x * 0.0625f), both(b, b)};
   };
   auto decode = [&](const unsigned (&code)[CB / 2], int u, const Factors& x, _Float16* dst, int flip, bool odd) __attribute__((always_inline)) {
@@ -340,8 +354,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     if (CB == 4) w[1] = 0u;
     // (E4M3 has NaN, and a row that is not this cache's may hold it)
     if (F8 && x.s1 == 0u) w[0] = w[1] = 0u;
-    const f16x8 c = codes8<CB, F8>(w[0], w[1]);
-    u32x4 v = __builtin_bit_cast(u32x4, c);
+    u32x4 v = codes8_normal<CB, F8>(w[0], w[1], k16v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool by16 = !F8 && slot_shift<CB>(2 * i);
@@ -352,10 +365,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   };
   auto stage = [&](int d, int piece) __attribute__((always_inline)) {
     if (piece == 0) {
-      YK_old = YK;
-      YK = max(YK, __builtin_amdgcn_readfirstlane(ctl.x) + 1 - kSBits);
-      YV = max(YV, __builtin_amdgcn_readfirstlane(ctl.y) + 1 - kSBits);
-      bad_keys = __builtin_amdgcn_readfirstlane(ctl.z) != 0;
+      bad_keys = __builtin_amdgcn_readfirstlane(ctl) != 0;
       fk = factors(xs.ks, xs.km, YK);
     }
     if (piece == 1) decode(x.k, 0, fk, &sm_k[(d + 1) & 1][kpos * HD], kpos & 7, k_odd);
@@ -382,49 +392,61 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     if (piece == 9) page = page_at(d + 5);
   };
 
-  // the first keys, and the rows of Q meanwhile
+  // the first keys, the newest that all rows see, and the rows of Q meanwhile
   if (end > 0) {
-    const int p0 = page_at(0), p1 = page_at(1), p2 = page_at(2);
+    const int64_t same = min(max(wg_lo, (int64_t)0), sr.len - 1);
+    const int p0 = page_at(0), p1 = page_at(1), p2 = page_at(2), ps = table[same >> a.pshift];
     page = page_at(3);
 #pragma unroll
     for (int i = 0; i < KS; ++i) qraw[i] = *(const u32x4*)(src + i * 16);
+    const int64_t at = ((int64_t)ps << a.pshift) + (same & pmask);
+    const bool there = ps >= 0 && at < a.n_slots;
+    const Scales unit = scales_of(there ? (int)at : -1, there ? (int)at : -1);
     r1 = row_at(0, p0);
     r2 = row_at(1, p1);
     r3 = row_at(2, p2);
     x = codes_of(r1, -1);
     xs = scales_of(r1, -1);
     next = scales_of(r2, r1);
-  } else {
-#pragma unroll
-    for (int i = 0; i < KS; ++i) qraw[i] = u32x4{};
+    if (there) {
+      YK = unit_of(unit.ks, unit.km);
+      YV = unit_of(unit.vs, unit.vm);
+    }
+    if (kkey == 0) {
+      sm_y[0][kch / 32] = YK;
+      sm_y[1][kch / 32] = YV;
+    }
   }
 
-  // q' in fp16, its largest value in [2^10, 2^11); the sign of the scale goes with it
+  // q' 2^YK in fp16, its largest value in [2^10, 2^11); the sign of the scale goes with it
   f16x8 q[KS];
-  float qm;
-  {
+  float qm = 1.f;
+  auto make_q = [&]() __attribute__((always_inline)) {
     const unsigned flip = a.scale2 < 0.f ? 0x80008000u : 0u, keep = a.scale2 == 0.f ? 0u : ~0u;
 #pragma unroll
     for (int i = 0; i < KS; ++i) qraw[i] = (qraw[i] ^ flip) & keep;
-    float top = 0.f;
     auto value = [&](int i, int j) __attribute__((always_inline)) {
       return j & 1 ? bf16hi(qraw[i][j >> 1]) : bf16lo(qraw[i][j >> 1]);
     };
     auto convert = [&](auto times) __attribute__((always_inline)) {
+      int e = -1000;
 #pragma unroll
-      for (int i = 0; i < KS; ++i)
+      for (int i = 0; i < KS; ++i) {
+        float top = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(times(value(i, j), i, j)));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const int e = (top > 0.f ? min(ilogbf(top), 127) : 0) - 10;
+        if (top > 0.f) e = max(e, min(ilogbf(top), 127) + sm_y[0][i / 2]);
+      }
+      e = max(e, __shfl_xor(e, 32));
+      e = (e == -1000 ? 0 : e) - 10;
 #pragma unroll
       for (int i = 0; i < KS; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int c = slot_code<CB>(j);
-          q[i][j] = (_Float16)ldexpf(times(value(i, c), i, c), -e);
+          q[i][j] = (_Float16)ldexpf(times(value(i, c), i, c), sm_y[0][i / 2] - e);
         }
-      qm = keep == 0u ? 1.f : fmaxf(ldexpf(__builtin_fabsf(a.scale2), e + U), 1.17549435e-38f);
+      if (keep) qm = fminf(fmaxf(ldexpf(__builtin_fabsf(a.scale2), e), 1.17549435e-38f), 3.402823466e38f);
     };
     if (a.kdhi) {
       const float* d = a.kdhi + a.k_first + h * HD + hf * 8;
@@ -432,7 +454,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     } else {
       convert([](float v, int, int) __attribute__((always_inline)) { return v; });
     }
-  }
+  };
 
   f32x16 s[NKT];
   f16x8 p[PS];
@@ -447,13 +469,6 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   auto products = [&](int t, auto score) __attribute__((always_inline)) {
     constexpr int NW = NCT * PS, N = NW + (score ? NKT * KS : 0);
     constexpr int LEAD = 4, NA = HD == 64 ? 2 : 4;
-    const int y = YV;
-    if (y != YO) {  // O in the units of this V
-      const float f = ldexpf(1.f, YO - y);
-#pragma unroll
-      for (int i = 0; i < NCT; ++i) o[i] *= f;
-      YO = y;
-    }
     const _Float16 *vrow[NA], *krow[4];
     // 16 lanes read 4 keys of 16 channels, and each is given a channel of the 4
     const int key = hf * 8 + ((l & 15) >> 2), ch = (l & 16) + (l & 3) * 4;
@@ -524,7 +539,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     mx = __builtin_elementwise_maximum(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
     const float top = mx * f;
     if (__ballot(top > mrun + kLazy)) {
-      const float mnew = fmaxf(mrun, top);
+      const float mnew = top > mrun + kLazy ? top : mrun;  // (by the row's own keys alone)
       const float g = mrun == -kInf ? 0.f : __builtin_amdgcn_exp2f(mrun - mnew);
 #pragma unroll
       for (int i = 0; i < NCT; ++i) o[i] *= g;
@@ -545,12 +560,84 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
       p[i] = __builtin_bit_cast(f16x8, v);
     }
   };
+  // The keys that were left out, each as the one tile of its own: all 32 rows of a wave
+  // at once, a half of the channels a lane, from its codes.
+  auto add_far = [&](int nt) __attribute__((always_inline)) {
+    // 8 channels of row `row` from channel ch on, in units of 2^y, those that f names
+    auto values = [&](const uint8_t* codes, const float* scales, const float* mins, int64_t row, int64_t ch, int y,
+                      auto f, auto& v) __attribute__((always_inline)) {
+      const int64_t g = row * a.groups + (ch >> a.gshift);
+      float sc = scales[g], m = mins[g];
+      finite_or_nan(sc, m);
+      const unsigned* from = (const unsigned*)(codes + row * a.row_bytes + ch * CB / 8);
+      const unsigned w0 = from[0], w1 = CB == 8 ? from[1] : 0u;
+#pragma unroll
+      for (int j = 0; j < (int)(sizeof(v) / sizeof(float)); ++j) {
+        const int at = f(j);
+        const unsigned c = CB == 8 ? (at & 4 ? w1 : w0) >> (at & 3) * 8 & 255u : w0 >> at * 4 & 15u;
+        v[j] = ldexpf(F8 ? sc * __builtin_amdgcn_cvt_f32_fp8((int)c, 0) : fmaf(sc, (float)c, m), -y);
+      }
+      return sc == sc;
+    };
+    const int64_t k_at = a.k_first + h * HD, v_at = a.v_first + h * HD;
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
+      const int mine = row_at(t, page_at(t));
+      Scales sc = scales_of(mine, mine);
+      finite_or_nan(sc.ks, sc.km);
+      finite_or_nan(sc.vs, sc.vm);
+      const bool left = of_key(__ballot(mine >= 0 && (far(sc.ks, sc.km, YK) || far(sc.vs, sc.vm, YV))));
+      __syncthreads();
+      if (kch == 0) sm_bad[0][kkey] = left;
+      __syncthreads();
+#pragma unroll 1
+      for (int i = 0; i < KT; ++i) {
+        const int key = t * KT + i;
+        if (__builtin_amdgcn_readfirstlane(sm_bad[0][i]) == 0) continue;
+        const int64_t row = ((int64_t)table[(lo + key) >> a.pshift] << a.pshift) + ((lo + key) & pmask);
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          float v[8];
+          values(a.kc, a.ks, a.km, row, k_at + i * 16 + hf * 8, sm_y[0][i / 2], [](int j) { return slot_code<CB>(j); }, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x = fmaf((float)q[i][j], v[j], x);
+        }
+        x = (x + __shfl_xor(x, 32)) * qm;
+        const bool seen = key <= top_key && key >= low_key;
+        if (!seen) x = -kInf;
+        const float mnew = x > mrun + kLazy ? x : mrun;
+        const float g = mrun == -kInf ? 0.f : __builtin_amdgcn_exp2f(mrun - mnew);
+        const float p = seen ? __builtin_amdgcn_exp2f(x - (mnew == -kInf ? 0.f : mnew)) : 0.f;
+        if (mnew != mrun) {
+#pragma unroll
+          for (int i = 0; i < NCT; ++i) o[i] *= g;
+          sum *= g;
+          mrun = mnew;
+        }
+        if (hf == 0) sum += p;
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i) {
+          float v[4];
+          const bool good = values(a.vc, a.vs, a.vm, row, v_at + i * 8, sm_y[1][i / 4],
+                                   [&](int j) { return CB == 4 ? slot_code<CB>(j) + 2 * hf : j + 4 * hf; }, v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int at = i % 4 * 4 + j;
+            if (good && p != 0.f) o[i / 4][at] = fmaf(p, v[j], o[i / 4][at]);
+          }
+        }
+      }
+    }
+  };
 
   if (end > 0) {  // uniform over the workgroup
     const int nt = (end + KT - 1) / KT;
-    if (tid < 3) sm_ctl[tid] = int4{-1000, -1000, 0, 0};
+    if (tid < 3) sm_ctl[tid] = 0;
+    if (tid == 0) sm_far = 0;
     for (int i = tid; i < 3 * KT; i += 512) (&sm_bad[0][0])[i] = 0;
     __syncthreads();
+    make_q();
     check(-1, r1, -1);
     __syncthreads();
     ctl = sm_ctl[2];
@@ -566,14 +653,15 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
       __builtin_amdgcn_s_setprio(0);
       if (late && tid - 256 < KT) {   // of pair t - 1, whose slot pair t + 2 takes
         sm_bad[(t + 2) % 3][tid - 256] = 0;
-        if (tid == 256) sm_ctl[(t + 2) % 3] = int4{-1000, -1000, 0, 0};
+        if (tid == 256) sm_ctl[(t + 2) % 3] = 0;
       }
       step_barrier();
-      softmax(t, ldexpf(qm, YK_old), bad_keys);
+      softmax(t, qm, bad_keys);
       step_barrier();
     }
     products(nt, std::false_type{});
     if (!late) step_barrier();
+    if (sm_far) add_far(nt);
   }
 
   sum += __shfl_xor(sum, 32);
@@ -593,6 +681,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
 #pragma unroll
   for (int t = 0; t < NCT; ++t) {
     const int64_t at = a.v_first + h * HD;
+    const int y = any ? sm_y[1][t] : 0;
     f32x4 back[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) back[i] = f32x4{1.f, 1.f, 1.f, 1.f};
@@ -606,7 +695,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
       const bool bad = (nan_groups >> (((at + ch) >> a.gshift) - (at >> a.gshift))) & 1;
       f32x4 x;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = ldexpf(o[t][4 * i + j] * inv, YO + U);
+      for (int j = 0; j < 4; ++j) x[j] = ldexpf(o[t][4 * i + j] * inv, y);
       if constexpr (CB == 4) {  // from slots to codes (slot_code)
         const float y0 = __shfl_xor(hf ? x[0] : x[1], 32), y1 = __shfl_xor(hf ? x[2] : x[3], 32);
         x = hf ? f32x4{y0, y1, x[1], x[3]} : f32x4{x[0], x[2], y0, y1};

@@ -34,3 +34,9 @@ def test_windows_past_the_context_are_none(lens, news, H, KV, hd):
                    2 ** 63 - 1):
         same = torch.equal(call(window), want)
         assert same, window
+
+
+@pytest.mark.parametrize("window", [1, 63, 64, 65, 1999])
+def test_windows_of_a_prompt(window):
+    from test_gpu_attention import _run
+    _run((4, 1, 64, 4, 64, "asym", 16, [2000], [600], window, False, False))
