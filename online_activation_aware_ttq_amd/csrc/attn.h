@@ -25,6 +25,9 @@ __device__ __forceinline__ unsigned e4m3_pair(unsigned w, bool hi, float times =
                                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, times, false));
 }
 
+// A maximum of scores (log2) from which on its rounding is no small part of an exponent
+constexpr float kFarScore = 0x1p18f;
+
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   const unsigned lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
   return (int64_t)((uint64_t)hi << 32 | lo);

@@ -545,7 +545,15 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
       rescale(mrun == -kInf ? 0.f : __builtin_amdgcn_exp2f(mrun - mnew));
       mrun = mnew;
     }
-    const float base = mrun == -kInf ? 0.f : -mrun;
+    // t qm - mrun, rounded once; where mrun is so far from 0 that its own rounding would
+    // be a power of two in p, the product is rounded as it was for mrun
+    float base = mrun == -kInf ? 0.f : -mrun, factor = qm;
+    if (__ballot(__builtin_fabsf(base) > kFarScore)) {
+      factor = 1.f;
+#pragma unroll
+      for (int i = 0; i < 8 * NB; ++i) t[i / 8][i % 8] = t[i / 8][i % 8] * qm + base;
+      base = 0.f;
+    }
     if (any_bad) {  // a scale of V that is NaN: its group, in the rows that see it
 #pragma unroll
       for (int g = 0; g < NG; ++g)
@@ -557,7 +565,7 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
     for (int u = 0; u < NB; ++u) {
       f16x8 p;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = (_Float16)__builtin_amdgcn_exp2f(fmaf(t[u][i], qm, base));
+      for (int i = 0; i < 8; ++i) p[i] = (_Float16)__builtin_amdgcn_exp2f(fmaf(t[u][i], factor, base));
       // V's operands, their scales (of this lane's channels: one group) in p or in V
       const u32x4 sv = *(const u32x4*)&sm_s[w][n * NC / GSE][u * 32 + c * 8];
       Words<VB> vw[8];

@@ -546,7 +546,13 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
       sum *= g;
       mrun = mnew;
     }
-    const float base = mrun == -kInf ? 0.f : mrun;
+    float base = mrun == -kInf ? 0.f : mrun;
+    if (__ballot(__builtin_fabsf(base) > kFarScore)) {  // (k_attention.hip)
+#pragma unroll
+      for (int i = 0; i < 16 * NKT; ++i) s[i / 16][i % 16] = s[i / 16][i % 16] * f - base;
+      f = 1.f;
+      base = 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < PS; ++i) {
       u32x4 v;

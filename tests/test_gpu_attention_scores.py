@@ -1,0 +1,64 @@
+"""Scores of any finite size: one far above the others takes its row, equal ones share it."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows", [1, 9, 200])
+@pytest.mark.parametrize("fmt,bits", [("asym", 4), ("fp8", 8)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_large_scores(rows, fmt, bits, sign):
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    from attention_util import Cache
+    from test_gpu_attention import _i32
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    length, H, KV, hd = 300, 4, 1, 64
+    cache = Cache(g, 320, KV, hd, bits, 64, fmt)
+    pages = torch.randperm(20, generator=g, device="cuda").to(torch.int32)[None]
+    t = torch.arange(length, device="cuda")
+    at = pages[0].long()[t // 16] * 16 + t % 16
+    k, v = (sum(cache.parts(at, w))[:, 0] for w in (0, 1))
+    Q = torch.randn(rows, H, hd, generator=g, device="cuda").bfloat16()
+    pos = length - rows + torch.arange(rows, device="cuda")
+    for big in (1.0, 2.0 ** 18, 2.0 ** 22, 2.0 ** 30, 2.0 ** 60, 2.0 ** 100):
+        q = Q * big
+        out = ttq.ttq_cache_attention(q, pages, _i32([length]), *cache.one, page_tokens=16,
+                                      offsets=_i32([0, rows]), scale=0.125 * sign, **cache.kwargs())
+        assert torch.isfinite(out).all(), big
+        if big == 1:
+            continue
+        x = torch.where((t <= pos[:, None])[:, None], 0.125 * sign * Q.double() @ k.T, -torch.inf)
+        two = x.topk(2, -1)
+        # the largest score's value, where the next is 2^-8 of the largest |score| or more
+        # below it: K in 11 bits moves a score by 3 x 2^-11 of sum |q k| at most
+        room = 6 * 2.0 ** -11 * 0.125 * Q.double().abs() @ k.abs().T
+        clear = two.values[..., 0] - two.values[..., 1] > room.amax(-1)
+        assert clear.float().mean() > 0.3
+        err = (out.double() - v[two.indices[..., 0]]).abs()[clear]
+        assert (err <= 2.0 ** -7 * v.abs().amax(0)).all(), big
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+def test_equal_scores_of_any_size(rows):
+    """All keys alike: the mean of V, whatever the score."""
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    from attention_util import Cache
+    from test_gpu_attention import _i32
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cache = Cache(g, 320, 1, 64, 8, 64, "asym")
+    x = torch.randn(320, cache.d, generator=g, device="cuda")
+    x[:, :64] = 1.5
+    ttq.ttq_cache_write(x, torch.arange(320, device="cuda"), *cache.one, **cache.how)
+    pages = torch.arange(20, dtype=torch.int32, device="cuda")[None]
+    v = sum(cache.parts(torch.arange(300, device="cuda"), 1))[:, 0]
+    pos = 300 - rows + torch.arange(rows, device="cuda")
+    want = torch.stack([v[:p + 1].mean(0) for p in pos.tolist()])[:, None]
+    for big in (1.0, 2.0 ** 20, 2.0 ** 27, -2.0 ** 31, 2.0 ** 90):
+        Q = torch.full((rows, 4, 64), big, dtype=torch.bfloat16, device="cuda")
+        out = ttq.ttq_cache_attention(Q, pages, _i32([300]), *cache.one, page_tokens=16,
+                                      offsets=_i32([0, rows]), **cache.kwargs())
+        # V in 11 bits three times and 2^-16 of the largest, the result in 8
+        tol = 2.0 ** -8 * want.abs() + (3 * 2.0 ** -11 + 2.0 ** -16) * v.abs().amax()
+        assert ((out.double() - want).abs() <= tol).all(), big
