@@ -82,9 +82,9 @@ __device__ __forceinline__ u32x4 codes8_normal(unsigned w0, unsigned w1, unsigne
 }
 
 // Channels 4 i .. 4 i + 3 of two keys a and b as pairs (a, b), one a channel; 4 bits:
-// 16-fold where the channel is odd
+// 16-fold where the channel is odd.  Integers with k (0, or k16 as above) beside them.
 template <int CB, bool F8>
-__device__ __forceinline__ void key_pairs(const unsigned* a, const unsigned* b, int i, unsigned (&out)[4]) {
+__device__ __forceinline__ void key_pairs(const unsigned* a, const unsigned* b, int i, unsigned k, unsigned (&out)[4]) {
   if constexpr (F8) {
     const unsigned lo = __builtin_amdgcn_perm(b[i], a[i], 0x05010400u);
     const unsigned hi = __builtin_amdgcn_perm(b[i], a[i], 0x07030602u);
@@ -93,17 +93,17 @@ __device__ __forceinline__ void key_pairs(const unsigned* a, const unsigned* b, 
     out[2] = e4m3_pair(hi, false);
     out[3] = e4m3_pair(hi, true);
   } else if constexpr (CB == 8) {
-    out[0] = __builtin_amdgcn_perm(b[i], a[i], 0x0c040c00u);
-    out[1] = __builtin_amdgcn_perm(b[i], a[i], 0x0c050c01u);
-    out[2] = __builtin_amdgcn_perm(b[i], a[i], 0x0c060c02u);
-    out[3] = __builtin_amdgcn_perm(b[i], a[i], 0x0c070c03u);
+    out[0] = __builtin_amdgcn_perm(b[i], a[i], 0x0c040c00u) | k;
+    out[1] = __builtin_amdgcn_perm(b[i], a[i], 0x0c050c01u) | k;
+    out[2] = __builtin_amdgcn_perm(b[i], a[i], 0x0c060c02u) | k;
+    out[3] = __builtin_amdgcn_perm(b[i], a[i], 0x0c070c03u) | k;
   } else {
     const unsigned x = __builtin_amdgcn_perm(b[i / 2], a[i / 2], i % 2 ? 0x07060302u : 0x05040100u);
     const unsigned h = x >> 8;
-    out[0] = x & 0x000f000fu;
-    out[1] = x & 0x00f000f0u;
-    out[2] = h & 0x000f000fu;
-    out[3] = h & 0x00f000f0u;
+    out[0] = (x & 0x000f000fu) | k;
+    out[1] = (x & 0x00f000f0u) | k;
+    out[2] = (h & 0x000f000fu) | k;
+    out[3] = (h & 0x00f000f0u) | k;
   }
 }
 

@@ -20,10 +20,13 @@
 // V's operand takes 8 keys of one channel from a lane: it reads HD / 16 adjacent
 // channels of 8 keys and parts them in registers.
 //
-// fp16 holds q' (times a power of two, its largest value in [2^10, 2^11)), p up to
-// 2^kLazy and V's scales (divided by 2^Y, Y the wave's so far): 11 bits each, an eighth
-// of what the bf16 result is rounded by; V's offsets are two fp16 values each, which
-// also make up for what a scale's 11 bits leave out, in the middle of its codes.
+// fp16 holds q' (times a power of two, its largest value in [2^10, 2^11)), p (times
+// 2^kLift) and V's scales (divided by 2^Y): 11 bits each, an eighth of what the bf16 result
+// is rounded by; V's offsets are two fp16 values each, which also make up for what a
+// scale's 11 bits leave out, in the middle of its codes.  Y is a group's, from the newest
+// key that all rows of the block see; a key with a group 2^7 larger or 2^8 smaller
+// than that has no V in the products, and its p v is added in float32: so no row depends on
+// the size of a key that it does not see, and a seen one costs the others no bits.
 //
 // It is bound by memory where there is enough of it to ask for: codes and scales go
 // to LDS without registers, two or three steps ahead, and all steps of all blocks are
@@ -99,6 +102,10 @@ __device__ __forceinline__ float max_rows(float x) {
 __device__ __forceinline__ unsigned mul_pair(unsigned a, unsigned b) {
   return __builtin_bit_cast(unsigned, __builtin_bit_cast(f16x2, a) * __builtin_bit_cast(f16x2, b));
 }
+__device__ __forceinline__ unsigned fma_pair(unsigned a, unsigned b, unsigned c) {
+  return __builtin_bit_cast(unsigned, __builtin_elementwise_fma(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b),
+                                                                __builtin_bit_cast(f16x2, c)));
+}
 
 // A block of 16 query rows and the keys that any of them sees
 struct Item {
@@ -139,15 +146,21 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
   constexpr int KP = KB > 16 ? KB / 16 : 1, KW = KB > 16 ? 16 : KB;  // in pieces
   constexpr int NC = HD / 16;            // channels of V of a lane
   constexpr int VB = NC * CB / 8;
-  constexpr int U = kUnit<F8>;
+  constexpr int U = kUnit<F8>;           // of K's codes
   constexpr float kInf = __builtin_inff();
   constexpr bool kP = NG == 1;           // V's scales go into p, not into V
-  // What a scale times 2^-Y may reach before Y has to grow, and what it is set to
-  // reach: its product with a code (or with p, up to 2^kLazy) stays below 2^16.
-  constexpr float kSMax = kP ? 200.f : F8 ? 128.f : 60000.f;
-  constexpr int kSBits = kP ? 5 : F8 ? 5 : 13;
-  constexpr int MU = F8 ? 0 : kP ? 20 : 10;  // V's offsets: 2^MU of O's unit
-  constexpr float kLazy = 8.f;
+  // V's codes in products: as stored (E4M3, or 2^24 of what they are); integers that are
+  // multiplied by their scales first, as c / 64, so that products are normal fp16 numbers
+  constexpr int UV = F8 ? 0 : kP ? 24 : 6;
+  // p of a row's largest score is 2^kLift to 2^(kLift + kLazy)
+  constexpr float kLazy = 4.f, kLift = 9.f;
+  // A group's size, the larger of its scale and 2^(1 - bits) of its values' middle, in
+  // units of 2^Y: what products take (with p, or with a code, below 2^16; and normal fp16
+  // numbers to 2^-11 of a step, or 2^-20 of the largest p), and 2^kFirst to twice that
+  // for the key that Y is from
+  constexpr float kMost = kP ? 7.5f : F8 ? 128.f : 4000.f, kLeast = kP ? 0x1p-13f : F8 ? 0x1p-12f : 0x1p-8f;
+  constexpr int kFirst = kP ? -5 : F8 ? -2 : 2;
+  constexpr int MU = F8 ? 0 : kP ? 26 : 0;  // V's offsets: 2^MU of O's unit
   __shared__ __align__(16) float sm_k[NW][2][NG][KS];
   __shared__ __align__(16) _Float16 sm_s[NW][NG][KS], sm_m[NW][F8 ? 1 : 2 * NG][KS];
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -155,6 +168,9 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
 
   const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = l & 15, c = l >> 4;
+  const float rmid = 1.f / (float)a.mid;  // (a power of two)
+  unsigned k16v = k16;
+  if constexpr (!kP && CB == 4) asm("" : "+v"(k16v));  // (in a register: and and or in one instruction)
   // A workgroup takes HW neighbouring K/V heads; wave w head w % HW and KS of a step's
   // KS * NW / HW keys.  The steps of all blocks, one block after another, are divided
   // evenly over the workgroups of a head group (a.parts of them), so a range may end
@@ -291,7 +307,7 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
 #pragma unroll
   for (int i = 0; i < NC; ++i) o[i] = om;
   float mrun = -kInf;
-  int Y = -200;
+  int Y[NG];
   unsigned nan_groups = 0;
 
   // LDS of a step: rows of HW heads' codes, K's then V's, key r of 32 in place (r & 7)
@@ -384,6 +400,16 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
     for (int i = 0; i < NC; ++i) o[i] *= f;
     om *= f;
   };
+  // (NaN or infinite if s or m is)
+  auto size_of = [&](float s, float m) __attribute__((always_inline)) {
+    return F8 ? fmaf(m, 0.f, __builtin_fabsf(s))
+              : __builtin_elementwise_maximum(__builtin_fabsf(s), __builtin_fabsf(fmaf(m, rmid, s)));
+  };
+  // 2^y kLeast to 2^y kMost: as bits of floats
+  auto fits = [&](float s, float m, int y) __attribute__((always_inline)) {
+    const unsigned least = __float_as_uint(kLeast), most = __float_as_uint(kMost);
+    return __float_as_uint(size_of(s, m)) - (least + ((unsigned)y << 23)) <= most - least;
+  };
 
   // The pages of as many keys as the table takes, and the first steps of them
   const int64_t epoch = ((int64_t)(Sh::NPAGE - 1) << a.pshift) / step * step;
@@ -398,8 +424,25 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
       if (from + i * step < to) issue(from + i * step, i);
   };
   if (lo < end) {
+    const int64_t same = min(max(pos_lo, (int64_t)0), sr.len - 1);
+    const int page = __builtin_amdgcn_readfirstlane(table[same >> a.pshift]);
     open(lo);
+    const int64_t row = ((int64_t)page << a.pshift) + ((int)same & pmask);
+    const bool there = page >= 0 && row < a.n_slots;
+    const int64_t at = (there ? row : 0) * a.groups + ((a.v_first + h * HD) >> a.gshift);
+    float us[NG], um[NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      us[g] = a.vs[at + g];
+      um[g] = a.vm[at + g];
+    }
     make_q();
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float x = size_of(us[g], um[g]);
+      const int y = there && x > 0.f && x <= 3.402823466e38f ? __builtin_amdgcn_frexp_expf(x) - 1 : 0;
+      Y[g] = __builtin_amdgcn_readfirstlane(min(max(y - kFirst, -100), 100));
+    }
   }
   for (int64_t from = lo; from < end; from += epoch) {
   const int64_t to = min(from + epoch, end);
@@ -416,7 +459,7 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
     const uint8_t* codes = smem + buf * Sh::STEP;
     const int64_t k0 = k1 + sub * KS;
     // scales and offsets of key kl, to where the lanes that need them find them
-    bool now, grow = false, bad = false;
+    bool now, usual = true, bad = false;
     (void)row_of(k0 + kl, page_of(k0 + kl), now);
     float vs[NG], vm[NG];
     {
@@ -434,47 +477,45 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
       for (int g = 0; g < NG; ++g) {
         if (F8) km[g] = 0.f;
         finite_or_nan(ks[g], km[g]);
-        finite_or_nan(vs[g], vm[g]);
         sm_k[w][0][g][kl] = now ? ks[g] : 0.f;
         if (!F8) sm_k[w][1][g][kl] = now ? km[g] : 0.f;
-        if (!now) vs[g] = vm[g] = 0.f;
-        grow |= ldexpf(vs[g], -Y) > kSMax || (!F8 && ldexpf(__builtin_fabsf(vm[g]), MU - U - Y) > 30000.f);
-        bad |= vs[g] != vs[g] || vm[g] != vm[g];
+        usual &= fits(vs[g], vm[g], Y[g]);
       }
     }
     const uint64_t seen = __ballot(now);
-    if (__ballot(grow)) {
-      int top = -1000;
+    // keys whose V is not in the products
+    uint64_t far = 0;
+    if (__ballot(!usual)) {
+      bool other = false;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        if (vs[g] > 0.f) top = max(top, ilogbf(vs[g]));
-        if (vm[g] != 0.f && vm[g] == vm[g]) top = max(top, ilogbf(vm[g]) + MU - U + kSBits - 13);
+        finite_or_nan(vs[g], vm[g]);
+        if (!now) vs[g] = vm[g] = 0.f;
+        bad |= vs[g] != vs[g];
+        other |= size_of(vs[g], vm[g]) > 0.f && !fits(vs[g], vm[g], Y[g]);
       }
+      far = __ballot(other);
+      if (KS == 32) far &= 0xffffffffu;
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) top = max(top, __shfl_xor(top, off));
-      const int y = max(Y, top + 1 - kSBits);
-      const float f = ldexpf(1.f, Y - y);
-#pragma unroll
-      for (int i = 0; i < NC; ++i) o[i] *= f;
-      if (c < 2) om *= f;  // the offsets' rows, not the sum's
-      Y = y;
+      for (int g = 0; g < NG; ++g)
+        if (other && vs[g] == vs[g]) vs[g] = vm[g] = 0.f;
     }
     const bool any_bad = __ballot(bad) != 0;
     uint64_t bad_keys[NG];
     if (any_bad) {
 #pragma unroll
-      for (int g = 0; g < NG; ++g) bad_keys[g] = __ballot(vs[g] != vs[g] || vm[g] != vm[g]);
+      for (int g = 0; g < NG; ++g) bad_keys[g] = __ballot(vs[g] != vs[g]);
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       // V's scale in 11 bits; what it is off is made up for in the middle of the codes
       // by the offset, which is a sum of two fp16 values
-      const bool x = vs[g] != vs[g] || vm[g] != vm[g];
-      const float sv = x ? 0.f : ldexpf(vs[g], -Y);
+      const bool x = vs[g] != vs[g];
+      const float sv = x ? 0.f : ldexpf(vs[g], -Y[g]);
       const _Float16 s16 = (_Float16)sv;
       sm_s[w][g][kl] = s16;
       if constexpr (!F8) {
-        const float mv = x ? 0.f : fmaf(sv - (float)s16, ldexpf((float)a.mid, MU - U), ldexpf(vm[g], MU - U - Y));
+        const float mv = x ? 0.f : fmaf(sv - (float)s16, ldexpf((float)a.mid, MU - UV), ldexpf(vm[g], MU - UV - Y[g]));
         const _Float16 m16 = (_Float16)mv;
         sm_m[w][g][kl] = m16;
         sm_m[w][NG + g][kl] = (_Float16)(mv - (float)m16);
@@ -541,18 +582,19 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
     for (int i = 1; i < 8 * NB; ++i) mx = mx2(mx, t[i / 8][i % 8]);
     mx = max_rows(mx) * qm;
     if (__ballot(mx > mrun + kLazy)) {
-      const float mnew = fmaxf(mrun, mx);
+      const float mnew = mx > mrun + kLazy ? mx : mrun;  // (by the row's own keys alone)
       rescale(mrun == -kInf ? 0.f : __builtin_amdgcn_exp2f(mrun - mnew));
       mrun = mnew;
     }
     // t qm - mrun, rounded once; where mrun is so far from 0 that its own rounding would
     // be a power of two in p, the product is rounded as it was for mrun
-    float base = mrun == -kInf ? 0.f : -mrun, factor = qm;
-    if (__ballot(__builtin_fabsf(base) > kFarScore)) {
+    const float low = mrun == -kInf ? 0.f : mrun;
+    float base = kLift - low, factor = qm;
+    if (__ballot(__builtin_fabsf(low) > kFarScore)) {
       factor = 1.f;
 #pragma unroll
-      for (int i = 0; i < 8 * NB; ++i) t[i / 8][i % 8] = t[i / 8][i % 8] * qm + base;
-      base = 0.f;
+      for (int i = 0; i < 8 * NB; ++i) t[i / 8][i % 8] = t[i / 8][i % 8] * qm - low;
+      base = kLift;
     }
     if (any_bad) {  // a scale of V that is NaN: its group, in the rows that see it
 #pragma unroll
@@ -583,18 +625,56 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
           for (int i = 0; i < (VB >= 4 ? VB / 4 : 1); ++i)
             if (!((seen >> (u * 32 + c * 8 + j)) & 1)) vw[j].w[i] = 0u;
       }
+      // p v of keys that are not in the products, from their codes
+      for (unsigned keys = (unsigned)(far >> (u * 32)); keys; keys &= keys - 1) {
+        const int j = __builtin_ctz(keys);
+        float pj = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pj = i == (j & 7) ? (float)p[i] : pj;
+        pj = __shfl(pj, n + (j >> 3) * 16);
+        const float* sj = (const float*)(codes + 2 * Sh::CODES + 2 * Sh::SCALES) + ((sub * KS + u * 32 + j) << lsg) + hh * NG;
+        const uint8_t* from = codes + Sh::CODES + ((sub * KS + u * 32 + (j & 7) * 4 + (j >> 3)) << lrb);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int ch = (c * 4 + i) * NC, off = hh * HB + ch * CB / 8, g = ch / GSE;
+          float sc = sj[g], m = sj[Sh::SCALES / 4 + g];
+          finite_or_nan(sc, m);
+          int y = Y[0];
+#pragma unroll
+          for (int k = 1; k < NG; ++k) y = g == k ? Y[k] : y;
+          Words<VB> x;
+          read_words<VB>(x, from + (((off >> 4) ^ fold(j)) << 4) + (off & 15));
+#pragma unroll
+          for (int k = 0; k < NC; ++k) {
+            const unsigned code = x.w[k * CB / 32] >> (k * CB % 32) & ((1u << CB) - 1);
+            const float v = F8 ? sc * __builtin_amdgcn_cvt_f32_fp8((int)code, 0) : fmaf(sc, (float)code, m);
+            const float add = ldexpf(v, (CB == 4 && (k & 1) ? 4 : 0) - y - UV);
+            if (pj != 0.f && sc == sc) o[k][i] = fmaf(pj, add, o[k][i]);
+          }
+        }
+      }
       f16x8 ps = p;
       if constexpr (kP) ps = p * __builtin_bit_cast(f16x8, sv);
+      // s (16 + c / 64) - 16 s, rounded once (E4M3: s c)
+      constexpr bool kNormal = !kP && !F8;
+      u32x4 s16 = {0u, 0u, 0u, 0u};
+      if constexpr (kNormal) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s16[j] = mul_pair(sv[j], 0xcc00cc00u);
+      }
+      auto times_scale = [&](unsigned v, int j) __attribute__((always_inline)) {
+        return kNormal ? fma_pair(v, sv[j], s16[j]) : mul_pair(v, sv[j]);
+      };
 #pragma unroll
       for (int i = 0; i < NC / 4; ++i) {
         unsigned vp[4][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) key_pairs<CB, F8>(vw[2 * j].w, vw[2 * j + 1].w, i, vp[j]);
+        for (int j = 0; j < 4; ++j) key_pairs<CB, F8>(vw[2 * j].w, vw[2 * j + 1].w, i, kNormal ? k16v : 0u, vp[j]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const u32x4 v = kP ? u32x4{vp[0][k], vp[1][k], vp[2][k], vp[3][k]}
-                             : u32x4{mul_pair(vp[0][k], sv.x), mul_pair(vp[1][k], sv.y),
-                                     mul_pair(vp[2][k], sv.z), mul_pair(vp[3][k], sv.w)};
+                             : u32x4{times_scale(vp[0][k], 0), times_scale(vp[1][k], 1),
+                                     times_scale(vp[2][k], 2), times_scale(vp[3][k], 3)};
           o[4 * i + k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, v), ps, o[4 * i + k], 0, 0, 0);
         }
       }
@@ -649,12 +729,16 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
     float x[NC];
     const int ch = c * (HD / 4) + i * NC;
     float f = 0.f;
+    int y = 0;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) f = ch / GSE == g ? off[g] : f;
+    for (int g = 0; g < NG; ++g) {
+      f = ch / GSE == g ? off[g] : f;
+      y = any && ch / GSE == g ? Y[g] : y;
+    }
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const float v = o[j][i] * (CB == 4 && (j & 1) ? 0.0625f : 1.f);
-      x[j] = ldexpf((v + ldexpf(f, -MU)) * inv, Y + U) * dv[(i * NC + j) / 4][j % 4];
+      x[j] = ldexpf((v + ldexpf(f, -MU)) * inv, y + UV) * dv[(i * NC + j) / 4][j % 4];
     }
     if (!all) {
       float* dst = a.part + orow * HD + ch;

@@ -12,6 +12,16 @@ FORMS = [
     (4, 1, 128, 8, 128, "fp8", 200, 250, True, False),
     (4, 1, 128, 4, 128, "asym", 200, 200, False, True),
     (2, 1, 256, 4, 64, "intzp", 150, 150, False, False),
+    # ranges of keys: a group a head (a half of two heads' too), and several
+    (4, 2, 128, 4, 128, "asym", 1, 300, False, False),
+    (8, 4, 64, 4, 128, "intzp", 7, 200, False, True),
+    (6, 3, 64, 3, 64, "asym", 9, 150, True, False),
+    (2, 1, 256, 8, 256, "sym", 5, 100, False, False),
+    (4, 1, 128, 8, 128, "fp8", 3, 250, True, False),
+    (4, 2, 128, 4, 32, "asym", 9, 300, False, False),
+    (4, 1, 64, 8, 32, "asym", 1, 200, False, True),
+    (8, 2, 128, 8, 64, "fp8", 12, 333, True, False),
+    (2, 1, 256, 4, 64, "sym", 20, 150, False, False),
 ]
 
 
@@ -51,7 +61,7 @@ def _compare(cache, Q, rows, length, got, scale, window=0, vacuous=0.1):
     err = (got.double() - ref).abs()
     assert torch.isfinite(got).all()
     worst = float((err / tol.clamp(min=1e-300)).max())
-    size = ref.abs().amax(-1, keepdim=True)
+    size = ref.abs().amax(-1, keepdim=True).clamp(min=1e-300)
     share = float((tol / size).median())
     print(f"  largest error {worst:.2f} of its bound, whose median is {share:.4f} of a row's largest", flush=True)
     assert worst <= 1 and share <= vacuous
