@@ -311,7 +311,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   // NaN, and keys of another size than the tile's.
   auto check = [&](int d, int rk, int rv) __attribute__((always_inline)) {
     const bool usual = fits(xs.ks, xs.km, YK) & fits(xs.vs, xs.vm, YV) & ((rk | rv) >= 0);
-    if ((__ballot(!usual) | far_k) == 0) return;
+    if (__builtin_expect((__ballot(!usual) | far_k) == 0, 1)) return;
     finite_or_nan(xs.ks, xs.km);
     finite_or_nan(xs.vs, xs.vm);
     const bool bad = nan(xs.vs, xs.vm);
@@ -418,10 +418,13 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     }
   }
 
-  // q' 2^YK in fp16, its largest value in [2^10, 2^11); the sign of the scale goes with it
+  // q' 2^YK in fp16, its largest value in [2^10, 2^11); the sign of the scale goes with
+  // it.  Eight values at a time first, times a power of two of their own, while YK is on
+  // its way.
   f16x8 q[KS];
+  int qe[KS];
   float qm = 1.f;
-  auto make_q = [&]() __attribute__((always_inline)) {
+  auto convert_q = [&]() __attribute__((always_inline)) {
     const unsigned flip = a.scale2 < 0.f ? 0x80008000u : 0u, keep = a.scale2 == 0.f ? 0u : ~0u;
 #pragma unroll
     for (int i = 0; i < KS; ++i) qraw[i] = (qraw[i] ^ flip) & keep;
@@ -429,24 +432,19 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
       return j & 1 ? bf16hi(qraw[i][j >> 1]) : bf16lo(qraw[i][j >> 1]);
     };
     auto convert = [&](auto times) __attribute__((always_inline)) {
-      int e = -1000;
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         float top = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(times(value(i, j), i, j)));
-        if (top > 0.f) e = max(e, min(ilogbf(top), 127) + sm_y[0][i / 2]);
-      }
-      e = max(e, __shfl_xor(e, 32));
-      e = (e == -1000 ? 0 : e) - 10;
-#pragma unroll
-      for (int i = 0; i < KS; ++i)
+        const int e = top > 3.402823466e38f ? 128 : __builtin_amdgcn_frexp_expf(top);
+        qe[i] = top > 0.f ? e - 11 : -1000;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int c = slot_code<CB>(j);
-          q[i][j] = (_Float16)ldexpf(times(value(i, c), i, c), sm_y[0][i / 2] - e);
+          q[i][j] = (_Float16)ldexpf(times(value(i, c), i, c), 11 - e);
         }
-      if (keep) qm = fminf(fmaxf(ldexpf(__builtin_fabsf(a.scale2), e), 1.17549435e-38f), 3.402823466e38f);
+      }
     };
     if (a.kdhi) {
       const float* d = a.kdhi + a.k_first + h * HD + hf * 8;
@@ -454,6 +452,26 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     } else {
       convert([](float v, int, int) __attribute__((always_inline)) { return v; });
     }
+  };
+  auto join_q = [&]() __attribute__((always_inline)) {
+    int e = -1000;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      qe[i] += sm_y[0][i / 2];
+      e = max(e, qe[i]);
+    }
+    e = max(e, __shfl_xor(e, 32));
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      const float f = ldexpf(1.f, max(qe[i] - e, -40));
+      const unsigned f2 = both(f, f);
+      u32x4 v = __builtin_bit_cast(u32x4, q[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = u2(h2(v[j]) * h2(f2));
+      q[i] = __builtin_bit_cast(f16x8, v);
+    }
+    if (a.scale2 != 0.f && e > -500)
+      qm = fminf(fmaxf(ldexpf(__builtin_fabsf(a.scale2), e), 1.17549435e-38f), 3.402823466e38f);
   };
 
   f32x16 s[NKT];
@@ -641,9 +659,10 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     const int nt = (end + KT - 1) / KT;
     if (tid < 3) sm_ctl[tid] = 0;
     if (tid == 0) sm_far = 0;
+    convert_q();
     for (int i = tid; i < 3 * KT; i += 512) (&sm_bad[0][0])[i] = 0;
     __syncthreads();
-    make_q();
+    join_q();
     check(-1, r1, -1);
     __syncthreads();
     ctl = sm_ctl[2];
@@ -667,7 +686,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     }
     products(nt, std::false_type{});
     if (!late) step_barrier();
-    if (sm_far) add_far(nt);
+    if (__builtin_expect(sm_far != 0, 0)) add_far(nt);
   }
 
   sum += __shfl_xor(sum, 32);
