@@ -294,13 +294,16 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
         q[i][j] = (!F8 && slot_shift<CB>(j)) ? f * (_Float16)0.0625f : f;
       }
     }
+    // (scores of -inf alone would be a row without keys)
+    if (!(top <= 3.402823466e38f)) q[0][0] = (_Float16)__builtin_nanf("");
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       qs[g] += __shfl_xor(qs[g], 16);
       qs[g] += __shfl_xor(qs[g], 32);
       qs[g] = ldexpf(qs[g], -U);
     }
-    qm = sign == 0.f ? 1.f : fmaxf(ldexpf(__builtin_fabsf(a.scale2), e + U), 1.17549435e-38f);
+    // (to what float32 holds: q of 2^100 and more have scores that nothing is near)
+    qm = sign == 0.f ? 1.f : fminf(fmaxf(ldexpf(__builtin_fabsf(a.scale2), e + U), 1.17549435e-38f), 3.402823466e38f);
   };
 
   f32x4 o[NC], om = {0.f, 0.f, 0.f, 0.f};

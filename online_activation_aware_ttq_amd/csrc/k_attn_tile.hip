@@ -437,7 +437,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
         float top = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = fmaxf(top, __builtin_fabsf(times(value(i, j), i, j)));
-        const int e = top > 3.402823466e38f ? 128 : __builtin_amdgcn_frexp_expf(top);
+        const int e = top > 3.402823466e38f ? 129 : __builtin_amdgcn_frexp_expf(top);
         qe[i] = top > 0.f ? e - 11 : -1000;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -445,6 +445,11 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
           q[i][j] = (_Float16)ldexpf(times(value(i, c), i, c), 11 - e);
         }
       }
+      // (scores of -inf alone would be a row without keys)
+      bool inf = false;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) inf |= qe[i] == 129 - 11;
+      if (inf) q[0][0] = (_Float16)__builtin_nanf("");
     };
     if (a.kdhi) {
       const float* d = a.kdhi + a.k_first + h * HD + hf * 8;

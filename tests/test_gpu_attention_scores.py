@@ -21,7 +21,7 @@ def test_large_scores(rows, fmt, bits, sign):
     k, v = (sum(cache.parts(at, w))[:, 0] for w in (0, 1))
     Q = torch.randn(rows, H, hd, generator=g, device="cuda").bfloat16()
     pos = length - rows + torch.arange(rows, device="cuda")
-    for big in (1.0, 2.0 ** 18, 2.0 ** 22, 2.0 ** 30, 2.0 ** 60, 2.0 ** 100):
+    for big in (1.0, 2.0 ** 18, 2.0 ** 22, 2.0 ** 30, 2.0 ** 60, 2.0 ** 100, 2.0 ** 118):
         q = Q * big
         out = ttq.ttq_cache_attention(q, pages, _i32([length]), *cache.one, page_tokens=16,
                                       offsets=_i32([0, rows]), scale=0.125 * sign, **cache.kwargs())
@@ -62,3 +62,41 @@ def test_equal_scores_of_any_size(rows):
         # V in 11 bits three times and 2^-16 of the largest, the result in 8
         tol = 2.0 ** -8 * want.abs() + (3 * 2.0 ** -11 + 2.0 ** -16) * v.abs().amax()
         assert ((out.double() - want).abs() <= tol).all(), big
+
+
+@pytest.mark.parametrize("rows", [1, 9, 200])
+@pytest.mark.parametrize("fmt,bits", [("asym", 4), ("fp8", 8), ("sym", 8)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_infinite_queries_are_nan(rows, fmt, bits, value):
+    """Also where every score would be -inf; a row without keys is 0 all the same."""
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    from attention_util import Cache
+    from test_gpu_attention import _i32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    cache = Cache(g, 320, 2, 64, bits, 64, fmt)
+    x = torch.randn(320, cache.d, generator=g, device="cuda")
+    x[:, :128] = -1 - x[:, :128].abs()
+    ttq.ttq_cache_write(x, torch.arange(320, device="cuda"), *cache.one, **cache.how)
+    pages = torch.arange(20, dtype=torch.int32, device="cuda")[None]
+    Q = torch.randn(rows, 8, 64, generator=g, device="cuda").bfloat16()
+    call = lambda length: ttq.ttq_cache_attention(Q, pages, _i32([length]), *cache.one, page_tokens=16,
+                                                  offsets=_i32([0, rows]), **cache.kwargs())
+    Q[0, 5, 9] = 2.0 ** 127  # the largest finite ones are none
+    clean = call(300)
+    assert torch.isfinite(clean).all()
+    at = rows // 2
+    keep = Q[at, 3, 17].clone()
+    Q[at, 3, 17] = value
+    got = call(300)
+    bad = torch.zeros(rows, 8, dtype=torch.bool, device="cuda")
+    bad[at, 3] = True
+    nan = torch.isnan(got.float())
+    assert nan[bad].all() and not nan[~bad].any()
+    same = torch.equal(got[~bad], clean[~bad])
+    assert same
+    if rows > 1:  # fewer keys than rows: the first rows see none
+        Q[at, 3, 17] = keep
+        Q[0, 3, 17] = value
+        got = call(rows - 1)
+        assert (got[0] == 0).all() and not torch.isnan(got.float()).any()
