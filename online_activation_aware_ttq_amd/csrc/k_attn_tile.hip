@@ -37,7 +37,8 @@
 // codes in float32, one after another: so no row depends on the size of a key that it
 // does not see, and a seen one costs the others no bits.
 // The maximum of a row follows only steps of 2^8 (p and the sums may be as much
-// larger), so O is seldom scaled.
+// larger), so O is seldom scaled; p is 2^7 of what it is, so that fp16 holds the many
+// small ones of a long context, to 2^-32 of the largest.
 #include <algorithm>
 
 #include "attn.h"
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   constexpr int PS = KT / 16;        // steps of 16 keys
   constexpr int KP = HD / 16;        // threads that decode a key
   constexpr float kInf = __builtin_inff();
-  constexpr float kLazy = 8.f;
+  constexpr float kLazy = 8.f, kLift = 7.f;  // p of the largest score: 2^kLift to 2^(kLift + kLazy)
   // sizes of a group in a tile's units; and codes there are (c - mid) / 64 (E4M3: / 256),
   // so that a group's scale is about as large as its values
   constexpr float kMost = 4000.f, kLeast = 0x1p-8f;
@@ -569,12 +570,13 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
       sum *= g;
       mrun = mnew;
     }
-    float base = mrun == -kInf ? 0.f : mrun;
-    if (__ballot(__builtin_fabsf(base) > kFarScore)) {  // (k_attention.hip)
+    const float low = mrun == -kInf ? 0.f : mrun;
+    float base = low - kLift;
+    if (__ballot(__builtin_fabsf(low) > kFarScore)) {  // (k_attention.hip)
 #pragma unroll
-      for (int i = 0; i < 16 * NKT; ++i) s[i / 16][i % 16] = s[i / 16][i % 16] * f - base;
+      for (int i = 0; i < 16 * NKT; ++i) s[i / 16][i % 16] = s[i / 16][i % 16] * f - low;
       f = 1.f;
-      base = 0.f;
+      base = -kLift;
     }
 #pragma unroll
     for (int i = 0; i < PS; ++i) {
@@ -637,7 +639,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
         if (!seen) x = -kInf;
         const float mnew = x > mrun + kLazy ? x : mrun;
         const float g = mrun == -kInf ? 0.f : __builtin_amdgcn_exp2f(mrun - mnew);
-        const float p = seen ? __builtin_amdgcn_exp2f(x - (mnew == -kInf ? 0.f : mnew)) : 0.f;
+        const float p = seen ? __builtin_amdgcn_exp2f(x - (mnew == -kInf ? 0.f : mnew) + kLift) : 0.f;
         if (mnew != mrun) {
 #pragma unroll
           for (int i = 0; i < NCT; ++i) o[i] *= g;

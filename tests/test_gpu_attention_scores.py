@@ -100,3 +100,32 @@ def test_infinite_queries_are_nan(rows, fmt, bits, value):
         Q[0, 3, 17] = value
         got = call(rows - 1)
         assert (got[0] == 0).all() and not torch.isnan(got.float()).any()
+
+
+@pytest.mark.parametrize("rows", [1, 70])
+@pytest.mark.parametrize("group", [32, 64])
+def test_many_small_weights_add_up(rows, group):
+    """One key far above thousands of equal ones, which together make the result: their p
+    is 2^-25.6 of its."""
+    import math
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    from attention_util import Cache
+    from test_gpu_attention import _i32
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n, D = 16000, 25.6
+    cache = Cache(g, n, 1, 64, 8, group, "asym")
+    x = torch.zeros(n, cache.d, device="cuda")
+    x[:, 64:128] = 1.0       # V of all keys but one, which is 0 and has the large score
+    x[70, :64], x[70, 64:128] = 1.0, 0.0
+    ttq.ttq_cache_write(x, torch.arange(n, device="cuda"), *cache.one, **cache.how)
+    Q = torch.ones(rows, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out = ttq.ttq_cache_attention(Q, torch.arange(n // 16, dtype=torch.int32, device="cuda")[None], _i32([n]),
+                                  *cache.one, page_tokens=16, offsets=_i32([0, rows]),
+                                  scale=D * math.log(2) / 64, **cache.kwargs())
+    w = (n - rows + torch.arange(rows, device="cuda").double()) * 2.0 ** -D
+    want = (w / (1 + w))[:, None, None]
+    # p: 2^-25 of 2^7 times the largest, all the same way; the score's float32 roundings
+    # (70 of 2^-24 D, as powers of two); the result's 8 bits
+    tol = 2.0 ** (D - 32) + 70 * 2.0 ** -24 * D + 2.0 ** -8
+    assert ((out.double() - want).abs() <= tol * want).all(), float((out.double() / want - 1).abs().max())
