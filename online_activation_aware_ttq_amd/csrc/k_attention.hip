@@ -238,7 +238,10 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
   for (; left > 0 && block < a.tiles; ++block) {
   Item it;
   const int64_t steps = find_item(a, block, step, it);
-  if (steps == 0) continue;
+  if (steps == 0) {
+    if (a.parts == 0) return;  // (uniform; the next block has its own workgroup)
+    continue;
+  }
   const int64_t todo = min(steps - skip, left);
   const bool all = todo == steps && lg == 0;  // the block's keys are all this wave's
   const int64_t lo = it.lo + skip * step, hi = it.hi;
