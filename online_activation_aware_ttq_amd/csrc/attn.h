@@ -25,6 +25,15 @@ __device__ __forceinline__ unsigned e4m3_pair(unsigned w, bool hi, float times =
                                          : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, times, false));
 }
 
+// Workgroups of a launch, which has fewer than 2^32 threads along x; some of the last row
+// are too many.  (A multiple of 8 in a row, for the dies.  Fewer than 2^31 of them: blocks
+// of a K/V head times K/V heads are T heads / 16 and n_seq kv_heads at most, 2^27 + 2^30.)
+inline dim3 attn_grid(int64_t n) {
+  const int64_t x = int64_t(1) << 21;
+  return n <= x ? dim3((unsigned)n) : dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+__device__ __forceinline__ unsigned attn_group() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // A maximum of scores (log2) from which on its rounding is no small part of an exponent
 constexpr float kFarScore = 0x1p18f;
 

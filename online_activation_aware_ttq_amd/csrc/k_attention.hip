@@ -181,9 +181,10 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
   // then reads the lines that their scales share once (a part's scales of four heads
   // are 16 bytes of a line).
   const int64_t count = a.parts > 0 ? a.parts : a.tiles, even = (count & ~int64_t(7)) * hgroups;
-  const int64_t in_die = blockIdx.x / 8, rest = blockIdx.x - even;
-  const int64_t part = blockIdx.x < even ? in_die / hgroups * 8 + blockIdx.x % 8 : (count & ~int64_t(7)) + rest / hgroups;
-  const int h0 = (int)(blockIdx.x < even ? in_die % hgroups : rest % hgroups) << lh;
+  const unsigned group = attn_group();
+  const int64_t in_die = group / 8, rest = group - even;
+  const int64_t part = group < even ? in_die / hgroups * 8 + group % 8 : (count & ~int64_t(7)) + rest / hgroups;
+  const int h0 = (int)(group < even ? in_die % hgroups : rest % hgroups) << lh;
   const int hh = w & (HW - 1), sub = w >> lh, h = h0 + hh;
   int64_t block, left, skip;  // the first block, the steps to do, those of it to leave out
   if (a.parts > 0) {
@@ -213,14 +214,14 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
     }
     total = uniform64(total);
     const int64_t per = (total + a.parts - 1) / a.parts, begin = part * per;
-    if (tid == 0 && blockIdx.x == 0) a.pre[0] = 0;
+    if (tid == 0 && group == 0) a.pre[0] = 0;
     for (int i = b0; i < min((int64_t)(b0 + each), a.tiles); ++i) {
       const int64_t next = run + pre[i + 1];
       if (run <= begin && begin < next) {
         sm_first = i;
         sm_skip = begin - run;
       }
-      if (blockIdx.x == 0) a.pre[i + 1] = next;
+      if (group == 0) a.pre[i + 1] = next;
       run = next;
     }
     __syncthreads();
@@ -768,7 +769,8 @@ __global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a) {
   __shared__ float sm_w[kAttnMaxParts], sm_red[2][NT / 64];
   __shared__ __align__(16) float sm[SB][HD];
   const int tid = threadIdx.x, l = tid & 63, w = tid >> 6;
-  const int64_t row = blockIdx.x, t = row / a.H;
+  const int64_t row = attn_group(), t = row / a.H;
+  if (t >= a.T) return;
   if (a.offsets && (t >= a.offsets[a.n_seq] || t < a.offsets[0])) return;  // uniform
   // its parts: rows base + s stride
   int64_t base = row * a.nsplit, stride = 1;
@@ -888,7 +890,7 @@ hipError_t go_split(const AttnArgs& a, const Launch& L) {
       hipFuncAttributeMaxDynamicSharedMemorySize, Sh::LDS);
   if (attr != hipSuccess) return attr;
   const int64_t groups = (a.parts > 0 ? a.parts : a.tiles) * (a.KV >> a.hw_shift);
-  return ext_launch(k_attn_split<HD, GSE, CB, F8, LH>, dim3((unsigned)groups), dim3(64 * Sh::NW),
+  return ext_launch(k_attn_split<HD, GSE, CB, F8, LH>, attn_grid(groups), dim3(64 * Sh::NW),
                     Sh::LDS, L, a);
 }
 
@@ -925,7 +927,7 @@ hipError_t launch_attn_split(const AttnArgs& a, int head_dim, int cb, int qf, in
 
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, const Launch& L) {
   const int64_t rows = a.T * a.H;
-  const dim3 grid((unsigned)rows);
+  const dim3 grid = attn_grid(rows);
   const bool merge = a.slots == 0 && a.nsplit <= 16;
   // many parts of a row: more of them side by side
   const bool wide = a.parts > 64 * a.tiles;

@@ -173,10 +173,12 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
 
   const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = l & 31, hf = l >> 5;
-  const int h = (int)(blockIdx.x % a.KV);
-  const unsigned bs = blockIdx.x / a.KV, nsplit = (unsigned)a.nsplit;
+  const unsigned group = attn_group();
+  const int h = (int)(group % a.KV);
+  const unsigned bs = group / a.KV, nsplit = (unsigned)a.nsplit;
   const int split = (int)(bs % nsplit);
   const int64_t block = bs / nsplit;
+  if (block >= a.tiles) return;
   int64_t seq, r0;
   SeqRows sr;
   if (!(a.offsets && a.n_seq <= 64 ? find_long_block(a, block, seq, sr, r0)
@@ -746,7 +748,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
 }  // namespace
 
 hipError_t launch_attn_tile(const AttnArgs& a, int head_dim, int cb, int qf, const Launch& L) {
-  const dim3 grid((unsigned)(a.tiles * a.nsplit * a.KV)), blk(512);
+  const dim3 grid = attn_grid(a.tiles * a.nsplit * a.KV), blk(512);
 #define TTQ_AT(HDV)                                                                        \
   if (head_dim == HDV) {                                                                   \
     if (qf == QF_FP8) return ext_launch(k_attn_tile<HDV, 8, true>, grid, blk, 0, L, a);    \
