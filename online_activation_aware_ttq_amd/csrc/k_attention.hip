@@ -761,8 +761,9 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
 }
 
 // One workgroup joins the parts of a row: out = sum_s w_s l_s o_s / sum_s w_s l_s,
-// w_s = exp(m_s - max m), o_s the mean of part s.  The weights first, all at once;
-// then HD / 4 lanes a part, NT / (HD / 4) parts side by side.
+// w_s = exp(m_s - max m), o_s the mean of part s.  The weights first, all at once, and
+// divided by their sum (o_s may be as large as float32 goes); then HD / 4 lanes a part,
+// NT / (HD / 4) parts side by side.
 template <int HD, int NT>
 __global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a) {
   constexpr int LN = HD / 4, SB = NT / LN;
@@ -829,12 +830,13 @@ __global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a) {
   total = 0.f;
 #pragma unroll
   for (int i = 0; i < NT / 64; ++i) total += sm_red[1][i];
+  const float inv = total == 0.f ? 0.f : 1.f / total;
   const int c = tid % LN * 4, s0 = tid / LN;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   const float* p = a.part + base * HD + c;
 #pragma unroll 4
   for (int s = s0; s < count; s += SB) {
-    const float g = sm_w[s];
+    const float g = sm_w[s] * inv;
     if (g == 0.f) continue;
     const f32x4 v = *(const f32x4*)(p + s * stride * HD);
 #pragma unroll
@@ -849,12 +851,14 @@ __global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a) {
       x[0] += sm[i][2 * tid];
       x[1] += sm[i][2 * tid + 1];
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    *(unsigned*)(a.out + row * HD + 2 * tid) = pack_bf16(x[0] * inv, x[1] * inv);
+    *(unsigned*)(a.out + row * HD + 2 * tid) = pack_bf16(x[0], x[1]);
   }
 }
 
-// The same where all rows have the same few parts beside each other: 4 channels a thread
+// The same where all rows have the same few parts beside each other (kMerge at most): 4
+// channels a thread.  Weights are divided by a power of two that keeps their sum below 1
+// until it is known.
+constexpr int kMerge = 16;
 template <int HD>
 __global__ __launch_bounds__(256) void k_attn_merge(AttnArgs a) {
   constexpr int LN = HD / 4;
@@ -864,14 +868,18 @@ __global__ __launch_bounds__(256) void k_attn_merge(AttnArgs a) {
   if (a.offsets && (t >= a.offsets[a.n_seq] || t < a.offsets[0])) return;
   const float* ml = a.ml + row * a.nsplit * 2;
   const float* p = a.part + row * a.nsplit * HD + c;
-  float mx = -__builtin_inff();
-  for (int s = 0; s < a.nsplit; ++s) mx = fmaxf(mx, ml[2 * s]);
+  float mx = -__builtin_inff(), most = 0.f;
+  for (int s = 0; s < a.nsplit; ++s) {
+    mx = fmaxf(mx, ml[2 * s]);
+    most = fmaxf(most, ml[2 * s + 1]);
+  }
+  const float unit = ldexpf(1.f, -4 - __builtin_amdgcn_frexp_expf(most));
   float total = 0.f;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int s = 0; s < a.nsplit; ++s) {
     const float sum = ml[2 * s + 1];
-    const float f = sum > 0.f || sum != sum ? __builtin_amdgcn_exp2f(ml[2 * s] - mx) * sum : 0.f;
+    const float f = sum > 0.f || sum != sum ? __builtin_amdgcn_exp2f(ml[2 * s] - mx) * (sum * unit) : 0.f;
     if (f == 0.f) continue;  // (a part without keys has written no row)
     total += f;
     const f32x4 v = *(const f32x4*)(p + s * HD);
@@ -928,7 +936,7 @@ hipError_t launch_attn_split(const AttnArgs& a, int head_dim, int cb, int qf, in
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, const Launch& L) {
   const int64_t rows = a.T * a.H;
   const dim3 grid = attn_grid(rows);
-  const bool merge = a.slots == 0 && a.nsplit <= 16;
+  const bool merge = a.slots == 0 && a.nsplit <= kMerge;
   // many parts of a row: more of them side by side
   const bool wide = a.parts > 64 * a.tiles;
 #define TTQ_AJ(HDV)                                                                        \

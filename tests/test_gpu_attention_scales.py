@@ -128,3 +128,23 @@ def test_sizes_far_apart_in_a_window(form):
     cache, Q, pages, rows = _make(form, 8, 2.0, 8.0)
     got = _call(cache, Q, pages, form[7], scale=2.0 ** -8, window=40)
     _compare(cache, Q, rows, form[7], got, 2.0 ** -8, window=40)
+
+
+@pytest.mark.parametrize("size", [1e-36, 1.0, 1e33, 3e37])
+@pytest.mark.parametrize("length,n,H", [(20000, 1, 2), (20000, 70, 1), (900, 9, 2)])
+def test_values_as_large_as_float32_goes(length, n, H, size):
+    """Ranges of many keys joined: the mean of V is as large as V is."""
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    from attention_util import Cache
+    g = torch.Generator(device="cuda").manual_seed(2)
+    cache = Cache(g, -(-length // 16) * 16, 1, 64, 8, 64, "asym")
+    x = torch.randn(cache.one[0].shape[0], cache.d, generator=g, device="cuda")
+    x[:, 64:] = x[:, 64:].clamp(-3, 3) * size
+    ttq.ttq_cache_write(x, torch.arange(x.shape[0], device="cuda"), *cache.one, **cache.how)
+    Q = torch.randn(n, H, 64, generator=g, device="cuda").bfloat16()
+    pages = torch.arange(x.shape[0] // 16, dtype=torch.int32, device="cuda")[None]
+    got = _call(cache, Q, pages, length)
+    # (the mean of 20000 values of both signs is 141 times smaller than they are, to which
+    # the bound, 0.0015 of them, goes: 0.21 of it)
+    _compare(cache, Q, torch.arange(length, device="cuda"), length, got, 0.125, vacuous=0.3)
