@@ -148,3 +148,29 @@ def test_values_as_large_as_float32_goes(length, n, H, size):
     # (the mean of 20000 values of both signs is 141 times smaller than they are, to which
     # the bound, 0.0015 of them, goes: 0.21 of it)
     _compare(cache, Q, torch.arange(length, device="cuda"), length, got, 0.125, vacuous=0.3)
+
+
+@pytest.mark.parametrize("rows", [9, 200])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 14, 2.0 ** -40])
+def test_without_the_key_that_units_are_from(rows, size):
+    """The newest pages are in no cache, so that no unit comes from them: any size is right."""
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    from attention_util import Cache, reference
+    from test_gpu_attention import _i32
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    cache = Cache(g, 512, 2, 64, 4, 64, "asym")
+    for t in cache.one[1:]:
+        t[:, cache.v_first // 64:] *= size
+    length = 400
+    pages = torch.randperm(32, generator=g, device="cuda")[:25].to(torch.int32)
+    for p in range(25):  # every page that a block's first row is in
+        if p % 2 or p > 20:
+            pages[p] = -1
+    Q = torch.randn(rows, 8, 64, generator=g, device="cuda").bfloat16()
+    out = ttq.ttq_cache_attention(Q, pages[None], _i32([length]), *cache.one, page_tokens=16,
+                                  offsets=_i32([0, rows]), **cache.kwargs())
+    t = torch.arange(length, device="cuda")
+    at = torch.where(pages[t // 16] >= 0, pages[t // 16].long() * 16 + t % 16, -1)
+    ref, tol = reference(cache, Q, at, length, length - rows, 0.125, tile=rows * 4 >= 64)
+    assert ((out.double().cpu() - ref).abs() <= tol).all()
