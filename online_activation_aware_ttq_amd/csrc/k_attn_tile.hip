@@ -533,7 +533,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   };
   auto softmax = [&](int t, float f, bool marked) __attribute__((always_inline)) {
     const int k0 = t * KT;
-    if (k0 + KT - 1 > full_hi || k0 < full_lo) {
+    if (__builtin_expect(k0 + KT - 1 > full_hi || k0 < full_lo, 0)) {
       const int top = min(top_key - k0, KT) - 8 * hf, bottom = max(low_key - k0, 0) - 8 * hf;
 #pragma unroll
       for (int i = 0; i < NKT; ++i)
@@ -543,7 +543,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
           if ((key > top) | (key < bottom)) s[i][j] = -kInf;
         }
     }
-    if (marked) {
+    if (__builtin_expect(marked, 0)) {
       const int top = min(top_key - k0, KT), bottom = max(low_key - k0, 0);
 #pragma unroll
       for (int i = 0; i < NKT; ++i)
