@@ -540,12 +540,18 @@ int ttq_cache_rope(const ttq_heads* hd, int64_t T, int32_t x_type,
  * A row that sees no key (an empty or negative length, or every page outside the
  * cache: such keys are not seen) is 0.  Nothing of a key that a row does not see
  * enters it, an infinity or NaN neither; of one that it sees, K's makes the head's
- * row NaN, V's the channels of its group (at least).
+ * row NaN, V's the channels of its group (at least).  A query that is not finite makes
+ * its head's row NaN.  (E4M3 codes are finite, as ttq_cache_write stores them.)
  * Products are those of q D^{-1/2} and p in 11 bits (fp16, scaled by powers of two)
  * with exact codes, whose scales enter K's in float32 and V's in 11 bits (what these
  * leave out goes, for the middle of the codes, into the offsets); where a sequence
  * has 64 and more rows of a K/V head on average, with k and v as fp16 values.
- * Scores, sums and the softmax are float32.
+ * Scores, sums and the softmax are float32; weights of less than 2^-32 of a row's
+ * largest may count as 0.  The sizes of keys may be any that float32 holds, side by
+ * side: those with a group about 2^8 larger or smaller than the others' cost time (each
+ * is added by itself), no bits.  Nor do they pass into rows that do not see them, but
+ * that roundings may follow one key's size where a window is shorter than the 16 (256)
+ * rows of a K/V head that are done together.
  * bits 3 to 8 (others: TTQ_EUNSUPPORTED, as are n_slots from 2^31 on); of a sequence
  * at most 2^31 - 4097 keys are seen.
  * heads * T up to 2^31 - 1. */

@@ -23,19 +23,20 @@
 // fp16 holds q' (times a power of two, its largest value in [2^10, 2^11)), p (times
 // 2^kLift) and V's scales (divided by 2^Y): 11 bits each, an eighth of what the bf16 result
 // is rounded by; V's offsets are two fp16 values each, which also make up for what a
-// scale's 11 bits leave out, in the middle of its codes.  Y is a group's, from the newest
-// key that all rows of the block see; a key with a group 2^7 larger or 2^8 smaller
+// scale's 11 bits leave out, in the middle of its codes.  Y is a group's, from the median of
+// the first keys that all rows of the block see; a key with a group 2^7 larger or 2^8 smaller
 // than that has no V in the products, and its p v is added in float32: so no row depends on
 // the size of a key that it does not see, and a seen one costs the others no bits.
 //
 // It is bound by memory where there is enough of it to ask for: codes and scales go
 // to LDS without registers, two or three steps ahead, and all steps of all blocks are
 // divided evenly over two workgroups a compute unit.  4 bits, 32 / 8 heads of 128: 64
-// requests of up to 2047 keys 99 us (4.6 TB/s), one of 131071 keys in groups of 64 51 us
-// (3.3 TB/s; groups of 128: 41), 8 requests 36 us (3.0 TB/s).  11 us of each are the chain
+// requests of up to 8192 keys 100 us (4.6 TB/s), one of 131071 keys in groups of 64 52 us
+// (3.2 TB/s; groups of 128: 41), 8 requests 36 us (3.0 TB/s).  11 us of each are the chain
 // before the first codes (lengths and their sums, pages, codes) and the join's 4 to 8.
-// Groups of 32 are bound by the products per group and their scales (82 us where groups of
-// 128 take 37).
+// Groups of 32 are bound by the products per group and their scales (8 requests of 32 heads:
+// 79 us where groups of 128 take 35).  A key that is added by itself takes a wave about
+// 0.4 us (16 requests of 8192 keys, one in a hundred such: 104 us, 39 without).
 //
 // What the maxima and sums of the ranges are is kept in float32 and joined by
 // k_attn_join; with one range the row is written at once.
@@ -315,6 +316,7 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
   for (int i = 0; i < NC; ++i) o[i] = om;
   float mrun = -kInf;
   int Y[NG];
+  bool no_unit = true;
   unsigned nan_groups = 0;
 
   // LDS of a step: rows of HW heads' codes, K's then V's, key r of 32 in place (r & 7)
@@ -341,7 +343,8 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
   // this wave's part of a step: 1 KiB of codes an instruction, and 4 / NW of the
   // arrays of scales, 64 values an instruction or, where a key's values are whole 16
   // bytes (a.wide), four times as many: a load of 4 bytes a lane takes the address
-  // units as long (context 131071, groups of 64: 72 us without, 44 with)
+  // units as long (64 requests: groups of 64 142 us so, 133 with 16 bytes; of 32 297 and
+  // 263; context 131071, groups of 64: 55 either way)
   constexpr int NQ = KS * HB / 1024, NI = KS * NW * NG / 64, NA = 4 / NW;
   constexpr int PER = 2 * NQ + NA * NI, NIW = (NI + 3) / 4, PERW = 2 * NQ + NA * NIW;
   const int lsg = lh + __builtin_ctz((unsigned)NG);  // log2 of a key's scales
@@ -431,25 +434,8 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
       if (from + i * step < to) issue(from + i * step, i);
   };
   if (lo < end) {
-    const int64_t same = min(max(pos_lo, (int64_t)0), sr.len - 1);
-    const int page = __builtin_amdgcn_readfirstlane(table[same >> a.pshift]);
     open(lo);
-    const int64_t row = ((int64_t)page << a.pshift) + ((int)same & pmask);
-    const bool there = page >= 0 && row < a.n_slots;
-    const int64_t at = (there ? row : 0) * a.groups + ((a.v_first + h * HD) >> a.gshift);
-    float us[NG], um[NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      us[g] = a.vs[at + g];
-      um[g] = a.vm[at + g];
-    }
     make_q();
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const float x = size_of(us[g], um[g]);
-      const int y = there && x > 0.f && x <= 3.402823466e38f ? __builtin_amdgcn_frexp_expf(x) - 1 : 0;
-      Y[g] = __builtin_amdgcn_readfirstlane(min(max(y - kFirst, -100), 100));
-    }
   }
   for (int64_t from = lo; from < end; from += epoch) {
   const int64_t to = min(from + epoch, end);
@@ -486,10 +472,31 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
         finite_or_nan(ks[g], km[g]);
         sm_k[w][0][g][kl] = now ? ks[g] : 0.f;
         if (!F8) sm_k[w][1][g][kl] = now ? km[g] : 0.f;
-        usual &= fits(vs[g], vm[g], Y[g]);
       }
     }
     const uint64_t seen = __ballot(now);
+    if (__builtin_expect(no_unit, 0)) {
+      // The first keys there are: of each group the median of their sizes, of keys that
+      // all rows see if there are some
+      const int64_t key = k0 + kl;
+      const uint64_t common = __ballot(now && key <= pos_lo && (a.window == 0 || key > pos_hi - a.window));
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const float x = size_of(vs[g], vm[g]);
+        const uint64_t sized = __ballot(now && x > 0.f && x <= 3.402823466e38f);
+        const uint64_t of = sized & common ? sized & common : sized;
+        const int e = __builtin_amdgcn_frexp_expf(x) - 1;
+        int y = -256;
+#pragma unroll
+        for (int bit = 256; bit > 0; bit >>= 1) {
+          if (2 * __builtin_popcountll(__ballot(e >= y + bit) & of) > __builtin_popcountll(of)) y += bit;
+        }
+        Y[g] = of ? min(max(y - kFirst, -100), 100) : -kFirst;
+        no_unit &= of == 0;
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) usual &= fits(vs[g], vm[g], Y[g]);
     // keys whose V is not in the products
     uint64_t far = 0;
     if (__ballot(!usual)) {

@@ -3,7 +3,7 @@
 //
 // A workgroup takes 256 query rows of one K/V head (a token's G heads, then the next
 // token's) and its keys, KT = 8192 / HD at a time, decoded once for all of them as
-// fp16(s c + m) into LDS rows of K and of V.  Each of its eight waves has 32 rows:
+// fp16(s (c - mid) + (m + mid s)) into LDS rows of K and of V.  Each of its eight waves has 32 rows:
 //   S^T = K q'^T   (32 keys x 32 rows an instruction block).  Key 16s + 8h + 4a + b
 //                  of a block is row 16s + 8a + 4h + b, so that the lane of a row (h
 //                  = lane / 32) ends with the 8 adjacent keys 16s + 8h ..  of it
@@ -26,16 +26,18 @@
 //
 // Besides, a workgroup of one tile takes 21 us: its rows, pages and codes are a chain
 // of loads, and a compute unit holds one workgroup.  4 prompts of up to 2047 tokens, 32 / 8 heads
-// of 128, 4 bits: 125 us a call, 500 TFLOP/s of the visible keys.
+// of 128, 4 bits: 121 us a call, 518 TFLOP/s of the visible keys.
 //
 // fp16's range is kept by powers of two: K and V are decoded as 2^-YK and 2^-YV of what
-// they are, YK and YV a group's (for all keys of the block), which put the newest key
-// that all rows see at 2 to 4; q' is times 2^YK, and as in k_attention.hip.  A key
-// whose groups are all 2^-8 to 4000 in these units (or 0) keeps 11 bits, or 2^-16 of
-// its group's largest value.  Keys of another size, 2^9 and more from that one, are
-// left out of the tiles, and what they give the rows that see them is added from their
+// they are, YK and YV a group's (for all keys of the block), which put the median of a
+// few keys that all rows see at 2 to 4; q' is times 2^YK, and as in k_attention.hip.  A
+// key whose groups are all 2^-8 to 4000 in these units (or 0) keeps 11 bits, or 2^-16 of
+// its group's largest value.  Keys of another size, 2^9 and more from that, are left out
+// of the tiles, and what they give the rows that see them is added from their
 // codes in float32, one after another: so no row depends on the size of a key that it
-// does not see, and a seen one costs the others no bits.
+// does not see, and a seen one costs the others no bits.  That is slow, about 7 us a key
+// of a workgroup, most of it waiting for its codes (4 prompts of 2048 tokens whose V is
+// 2^+-2 apart: 390 us, 261 where they are alike; 2^+-8 apart: 12.8 ms).
 // The maximum of a row follows only steps of 2^8 (p and the sums may be as much
 // larger), so O is seldom scaled; p is 2^7 of what it is, so that fp16 holds the many
 // small ones of a long context, to 2^-32 of the largest.
@@ -159,6 +161,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   // so that a group's scale is about as large as its values
   constexpr float kMost = 4000.f, kLeast = 0x1p-8f;
   constexpr int kCode = F8 ? 8 : 6;
+  constexpr int kNoUnit = 1000;  // (of a key that is not there, or 0; if all are, -1)
   // LDS rows are of 16-byte pieces, K's in the order piece ^ key % 8.  Of V, 16 lanes
   // read 32 bytes of 4 keys, the next 16 the 32 bytes beside them: in eight parts of the
   // banks, and the first four in four of half of the banks.
@@ -283,7 +286,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   };
   auto unit_of = [&](float s, float m) __attribute__((always_inline)) {
     const float x = size_of(s, m);
-    return x > 0.f && x <= 3.402823466e38f ? min(max(__builtin_amdgcn_frexp_expf(x) - 2, -100), 100) : -1;
+    return x > 0.f && x <= 3.402823466e38f ? min(max(__builtin_amdgcn_frexp_expf(x) - 2, -100), 100) : kNoUnit;
   };
   // Is a group's size one of a tile's, 2^y kLeast to 2^y kMost: as bits of floats
   auto fits = [&](float s, float m, int y) __attribute__((always_inline)) {
@@ -395,30 +398,40 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     if (piece == 9) page = page_at(d + 5);
   };
 
-  // the first keys, the newest that all rows see, and the rows of Q meanwhile
+  // the first keys, and the rows of Q meanwhile
   if (end > 0) {
-    const int64_t same = min(max(wg_lo, (int64_t)0), sr.len - 1);
-    const int p0 = page_at(0), p1 = page_at(1), p2 = page_at(2), ps = table[same >> a.pshift];
+    const int p0 = page_at(0), p1 = page_at(1), p2 = page_at(2);
     page = page_at(3);
 #pragma unroll
     for (int i = 0; i < KS; ++i) qraw[i] = *(const u32x4*)(src + i * 16);
-    const int64_t at = ((int64_t)ps << a.pshift) + (same & pmask);
-    const bool there = ps >= 0 && at < a.n_slots;
-    const Scales unit = scales_of(there ? (int)at : -1, there ? (int)at : -1);
+    if (w == 0) {
+      // The units, by 64 / KP keys over the range that all rows see: of each group the
+      // key in the middle of their sizes
+      const int64_t to = min(max(wg_lo, (int64_t)0), sr.len - 1);
+      const int64_t from = a.window > 0 ? min(max(wg_hi - a.window + 1, (int64_t)0), to) : 0;
+      const int64_t key = to - (to - from) * kkey / (64 / KP);
+      const int64_t at = ((int64_t)table[key >> a.pshift] << a.pshift) + (key & pmask);
+      const int row = at >= 0 && at < a.n_slots ? (int)at : -1;
+      const Scales unit = scales_of(row, row);
+      int e[2] = {row >= 0 ? unit_of(unit.ks, unit.km) : kNoUnit, row >= 0 ? unit_of(unit.vs, unit.vm) : kNoUnit};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        int below = 0, valid = 0;
+#pragma unroll
+        for (int j = 0; j < 64 / KP; ++j) {
+          const int x = __shfl(e[i], j * KP + l % KP);
+          below += x < e[i] || (x == e[i] && j < kkey);
+          valid += x != kNoUnit;
+        }
+        if (below == (valid > 0 ? (valid - 1) / 2 : 0)) sm_y[i][kch / 32] = e[i] == kNoUnit ? -1 : e[i];
+      }
+    }
     r1 = row_at(0, p0);
     r2 = row_at(1, p1);
     r3 = row_at(2, p2);
     x = codes_of(r1, -1);
     xs = scales_of(r1, -1);
     next = scales_of(r2, r1);
-    if (there) {
-      YK = unit_of(unit.ks, unit.km);
-      YV = unit_of(unit.vs, unit.vm);
-    }
-    if (kkey == 0) {
-      sm_y[0][kch / 32] = YK;
-      sm_y[1][kch / 32] = YV;
-    }
   }
 
   // q' 2^YK in fp16, its largest value in [2^10, 2^11); the sign of the scale goes with
@@ -671,6 +684,8 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     convert_q();
     for (int i = tid; i < 3 * KT; i += 512) (&sm_bad[0][0])[i] = 0;
     __syncthreads();
+    YK = sm_y[0][kch / 32];
+    YV = sm_y[1][kch / 32];
     join_q();
     check(-1, r1, -1);
     __syncthreads();

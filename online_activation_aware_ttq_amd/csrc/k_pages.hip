@@ -13,8 +13,10 @@
 // t and find their sequence by bisection in LDS.
 //
 // It is bound by latency, a chain of dependent loads, two running sums and the
-// barriers between them: 8 sequences 5.4 us, prompts of 65536 rows 10.9, and 4.2 for the
-// second launch that deals more than 4096 rows to the whole chip.
+// barriers between them: 8 sequences 5.4 us.  100 prompts of 65536 rows together take 10.9:
+// one chunk too, but a thread deals out several pages, one after another, each a bisection
+// and two accesses that wait for each other; and 4.3 for the second launch that deals more
+// than 4096 rows to the whole chip.
 #include <algorithm>
 
 #include "ttq_internal.h"

@@ -17,8 +17,9 @@
 // same channels of a head in each of its chunks, so it needs its 8 (interleaved:
 // 4) angles once; a chunk is asked for while the one before is worked on (42 -> 38 us).
 //
-// 4096 rows of 32 / 8 heads of 128 to 4 bits: 38 us, 2.9 TB/s of what it has to read and
-// write; waves wait for memory 60 % of their time, vector units are busy 20 %.  One row:
+// 4096 rows of 32 / 8 heads of 128 to 4 bits: 38 us, 2.3 TB/s of the 89 MB that it has to
+// read and write (a copy reaches 4.8); waves wait for memory 45 % of their time, with one
+// chunk of 16 bytes a lane on its way, and issue vector instructions 23 % of it.  One row:
 // 6 us, most of it the launch, the angles in float64 and two loads after one another.
 #include <algorithm>
 
