@@ -36,7 +36,7 @@
 // before the first codes (lengths and their sums, pages, codes) and the join's 4 to 8.
 // Groups of 32 are bound by the products per group and their scales (8 requests of 32 heads:
 // 79 us where groups of 128 take 35).  A key that is added by itself takes a wave about
-// 0.4 us (16 requests of 8192 keys, one in a hundred such: 104 us, 39 without).
+// 1.5 us (16 requests of 8192 keys, 32 / 8 heads: 40 us, 53 with one such key in 64).
 //
 // What the maxima and sums of the ranges are is kept in float32 and joined by
 // k_attn_join; with one range the row is written at once.
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
   // A group's size, the larger of its scale and 2^(1 - bits) of its values' middle, in
   // units of 2^Y: what products take (with p, or with a code, below 2^16; and normal fp16
   // numbers to 2^-11 of a step, or 2^-20 of the largest p), and 2^kFirst to twice that
-  // for the key that Y is from
+  // for the size that Y is from
   constexpr float kMost = kP ? 7.5f : F8 ? 128.f : 4000.f, kLeast = kP ? 0x1p-13f : F8 ? 0x1p-12f : 0x1p-8f;
   constexpr int kFirst = kP ? -5 : F8 ? -2 : 2;
   constexpr int MU = F8 ? 0 : kP ? 26 : 0;  // V's offsets: 2^MU of O's unit

@@ -35,9 +35,9 @@
 // its group's largest value.  Keys of another size, 2^9 and more from that, are left out
 // of the tiles, and what they give the rows that see them is added from their
 // codes in float32, one after another: so no row depends on the size of a key that it
-// does not see, and a seen one costs the others no bits.  That is slow, about 7 us a key
-// of a workgroup, most of it waiting for its codes (4 prompts of 2048 tokens whose V is
-// 2^+-2 apart: 390 us, 261 where they are alike; 2^+-8 apart: 12.8 ms).
+// does not see, and a seen one costs the others no bits.  That is slow, about 12 us a key
+// of a workgroup, most of it waiting for its codes (4 prompts of 2048 tokens, 32 / 8 heads of
+// 128: 242 us, with one such token in 1024 297, with one in 64 1080).
 // The maximum of a row follows only steps of 2^8 (p and the sums may be as much
 // larger), so O is seldom scaled; p is 2^7 of what it is, so that fp16 holds the many
 // small ones of a long context, to 2^-32 of the largest.
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   __shared__ unsigned sm_bad[3][KT];  // of a key: groups of V that are NaN; kOut
   __shared__ int sm_ctl[3];           // a key of the tile is in sm_bad
   __shared__ int sm_y[2][HD / 32];    // YK, YV of 32 channels
-  __shared__ int sm_far;              // keys have been left out
+  __shared__ unsigned sm_far[33];     // tiles (mod 1024) that have left out keys, a bit each; any
 
   const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = l & 31, hf = l >> 5;
@@ -327,7 +327,10 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     if (d >= 0 && d * KT + kkey < end && (left || bad || rv < 0)) {
       atomicOr(&sm_bad[slot][kkey], (bad && rv >= 0 ? nan_bit : 0u) | (left || rv < 0 ? kOut : 0u));
       sm_ctl[slot] = 1;
-      if (left) sm_far = 1;
+      if (left) {
+        atomicOr(&sm_far[d >> 5 & 31], 1u << (d & 31));
+        sm_far[32] = 1;
+      }
     }
     if (rk < 0) xs.ks = xs.km = 0.f;
     if (rv < 0 || bad || v_far) xs.vs = xs.vm = 0.f;
@@ -628,6 +631,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     const int64_t k_at = a.k_first + h * HD, v_at = a.v_first + h * HD;
 #pragma unroll 1
     for (int t = 0; t < nt; ++t) {
+      if ((__builtin_amdgcn_readfirstlane(sm_far[t >> 5 & 31]) >> (t & 31) & 1) == 0) continue;
       const int mine = row_at(t, page_at(t));
       Scales sc = scales_of(mine, mine);
       finite_or_nan(sc.ks, sc.km);
@@ -680,7 +684,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
   if (end > 0) {  // uniform over the workgroup
     const int nt = (end + KT - 1) / KT;
     if (tid < 3) sm_ctl[tid] = 0;
-    if (tid == 0) sm_far = 0;
+    if (tid < 33) sm_far[tid] = 0;
     convert_q();
     for (int i = tid; i < 3 * KT; i += 512) (&sm_bad[0][0])[i] = 0;
     __syncthreads();
@@ -710,7 +714,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     }
     products(nt, std::false_type{});
     if (!late) step_barrier();
-    if (__builtin_expect(sm_far != 0, 0)) add_far(nt);
+    if (__builtin_expect(sm_far[32] != 0, 0)) add_far(nt);
   }
 
   sum += __shfl_xor(sum, 32);
