@@ -174,3 +174,28 @@ def test_without_the_key_that_units_are_from(rows, size):
     at = torch.where(pages[t // 16] >= 0, pages[t // 16].long() * 16 + t % 16, -1)
     ref, tol = reference(cache, Q, at, length, length - rows, 0.125, tile=rows * 4 >= 64)
     assert ((out.double().cpu() - ref).abs() <= tol).all()
+
+
+def test_keys_of_another_size_in_a_long_context():
+    """More tiles than there are marks for them, of a workgroup that has them all."""
+    import torch
+    from attention_bounds import by_key
+    from attention_util import Cache
+    g = torch.Generator(device="cuda").manual_seed(4)
+    length, n = 140000, 33000
+    cache = Cache(g, length + 16 - length % 16, 1, 64, 4, 64, "asym")
+    far = torch.tensor([130, 131, 128 * 1024 + 5, 128 * 1025 + 2, 128 * 40, length - n], device="cuda")
+    for t in cache.one[1:]:
+        t[far] *= 2.0 ** 11
+        t[far[:3], 0] *= 2.0 ** -22  # K of some small, their V large
+    Q = torch.randn(n, 1, 64, generator=g, device="cuda").bfloat16()
+    pages = torch.arange(cache.one[0].shape[0] // 16, dtype=torch.int32, device="cuda")[None]
+    got = _call(cache, Q, pages, length, scale=2.0 ** -12)
+    rows = torch.arange(length, device="cuda")
+    for a, b in ((0, 2), (15000, 15002), (n - 2, n)):
+        end = length - n + b
+        ref, tol = by_key(cache, Q[a:b], rows[:end], end - (b - a), 2.0 ** -12, tile=True)
+        err = (got[a:b].double() - ref).abs()
+        worst = float((err / tol).max())
+        print(f"  rows {a}..: largest error {worst:.2f} of its bound", flush=True)
+        assert worst <= 1 and float((tol / ref.abs().amax(-1, keepdim=True)).median()) <= 0.3
