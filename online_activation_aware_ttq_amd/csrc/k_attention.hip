@@ -604,11 +604,12 @@ __global__ __launch_bounds__(64 * (HD * CB == 2048 ? 2 : 4), HD * CB == 2048 ? 1
     // be a power of two in p, the product is rounded as it was for mrun
     const float low = mrun == -kInf ? 0.f : mrun;
     float base = kLift - low, factor = qm;
-    if (__ballot(__builtin_fabsf(low) > kFarScore)) {
-      factor = 1.f;
+    const bool far_row = __builtin_fabsf(low) > kFarScore;
+    if (__ballot(far_row)) {
 #pragma unroll
-      for (int i = 0; i < 8 * NB; ++i) t[i / 8][i % 8] = t[i / 8][i % 8] * qm - low;
-      base = kLift;
+      for (int i = 0; i < 8 * NB; ++i) t[i / 8][i % 8] = far_row ? t[i / 8][i % 8] * qm - low : t[i / 8][i % 8];
+      base = far_row ? kLift : base;
+      factor = far_row ? 1.f : qm;
     }
     if (any_bad) {  // a scale of V that is NaN: its group, in the rows that see it
 #pragma unroll

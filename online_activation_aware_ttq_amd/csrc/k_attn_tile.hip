@@ -590,11 +590,12 @@ __global__ __launch_bounds__(512, 2) void k_attn_tile(AttnArgs a) {
     }
     const float low = mrun == -kInf ? 0.f : mrun;
     float base = low - kLift;
-    if (__ballot(__builtin_fabsf(low) > kFarScore)) {  // (k_attention.hip)
+    const bool far_row = __builtin_fabsf(low) > kFarScore;
+    if (__ballot(far_row)) {  // (k_attention.hip)
 #pragma unroll
-      for (int i = 0; i < 16 * NKT; ++i) s[i / 16][i % 16] = s[i / 16][i % 16] * f - low;
-      f = 1.f;
-      base = -kLift;
+      for (int i = 0; i < 16 * NKT; ++i) s[i / 16][i % 16] = far_row ? s[i / 16][i % 16] * f - low : s[i / 16][i % 16];
+      f = far_row ? 1.f : f;
+      base = far_row ? -kLift : base;
     }
 #pragma unroll
     for (int i = 0; i < PS; ++i) {

@@ -129,3 +129,27 @@ def test_many_small_weights_add_up(rows, group):
     # (70 of 2^-24 D, as powers of two); the result's 8 bits
     tol = 2.0 ** (D - 32) + 70 * 2.0 ** -24 * D + 2.0 ** -8
     assert ((out.double() - want).abs() <= tol * want).all(), float((out.double() / want - 1).abs().max())
+
+
+@pytest.mark.parametrize("rows", [9, 200])
+@pytest.mark.parametrize("fmt,bits", [("asym", 4), ("fp8", 8)])
+def test_large_scores_of_one_row_are_its_own(rows, fmt, bits):
+    """Queries of one head of one row 2^30 times larger: the others keep their bits."""
+    import torch
+    import online_activation_aware_ttq_amd as ttq
+    from attention_util import Cache
+    from test_gpu_attention import _i32
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    cache = Cache(g, 3008, 2, 128, bits, 128, fmt)
+    pages = torch.randperm(188, generator=g, device="cuda").to(torch.int32)[None]
+    Q = torch.randn(rows, 8, 128, generator=g, device="cuda").bfloat16()
+    call = lambda: ttq.ttq_cache_attention(Q, pages, _i32([3000]), *cache.one, page_tokens=16,
+                                           offsets=_i32([0, rows]), **cache.kwargs())
+    clean = call()
+    other = torch.ones(rows, 8, dtype=torch.bool, device="cuda")
+    for at in range(0, rows, 5):
+        Q[at, at % 8] *= 2.0 ** 30
+        other[at, at % 8] = False
+    got = call()
+    same = torch.equal(got[other], clean[other])
+    assert same and torch.isfinite(got).all()
