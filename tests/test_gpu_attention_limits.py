@@ -31,3 +31,14 @@ def test_more_rows_than_a_launch_has_along_x(n_seq, news, KV, hd):
         same = bool((out.view(n_seq, news, KV, hd)[at:at + 10000] == out[:news]).all())
         assert same, at
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("case", [
+    # one row a sequence of so many heads of a K/V head that tiles are decoded for them
+    (64, 1, 64, 4, 64, "asym", 16, [500, 31, 0], [1, 1, 1], 0, False, False),
+    (150, 1, 128, 8, 64, "fp8", 32, [900], [1], 100, True, False),
+    (300, 1, 64, 4, 32, "sym", 16, [70, 257], [1, 1], 0, False, True),
+], ids=lambda c: "-".join(map(str, c[:6])))
+def test_many_heads_of_a_row(case):
+    from test_gpu_attention import _run
+    _run(case)
