@@ -548,10 +548,11 @@ int ttq_cache_rope(const ttq_heads* hd, int64_t T, int32_t x_type,
  * has 64 and more rows of a K/V head on average, with k and v as fp16 values.
  * Scores, sums and the softmax are float32; weights of less than 2^-32 of a row's
  * largest may count as 0.  The sizes of keys may be any that float32 holds, side by
- * side: those with a group about 2^8 larger or smaller than the others' cost time (each
- * is added by itself), no bits.  Nor do they pass into rows that do not see them, but
- * that roundings may follow one key's size where a window is shorter than the 16 (256)
- * rows of a K/V head that are done together.
+ * side up to 2^100 apart (a row that sees one further above may be infinite): those with
+ * a group about 2^8 larger or smaller than the others' cost time (each is added by
+ * itself), no bits.  Nor do they pass into rows that do not see them, but that roundings
+ * may follow their size where a window is shorter than the 16 (256) rows of a K/V head
+ * that are done together.
  * bits 3 to 8 (others: TTQ_EUNSUPPORTED, as are n_slots from 2^31 on); of a sequence
  * at most 2^31 - 4097 keys are seen.
  * heads * T up to 2^31 - 1. */

@@ -199,3 +199,18 @@ def test_keys_of_another_size_in_a_long_context():
         worst = float((err / tol).max())
         print(f"  rows {a}..: largest error {worst:.2f} of its bound", flush=True)
         assert worst <= 1 and float((tol / ref.abs().amax(-1, keepdim=True)).median()) <= 0.3
+
+
+@pytest.mark.parametrize("form", FORMS, ids=_id)
+def test_sizes_2_to_100_apart(form):
+    """All keys 2^-60, one of the oldest and one of the newest 2^40 of what they were."""
+    cache, Q, pages, rows = _make(form, 9, 0.0, 0.0)
+    width = cache.KV * cache.hd
+    a = cache.v_first // cache.group
+    cut = slice(a, a + max(1, width // cache.group))
+    for t in (cache.two or cache.one)[1:]:
+        t[:, cut] *= 2.0 ** -60
+        t[rows[1], cut] *= 2.0 ** 100
+        t[rows[-1], cut] *= 2.0 ** 100
+    got = _call(cache, Q, pages, form[7])
+    _compare(cache, Q, rows, form[7], got, form[2] ** -0.5)
